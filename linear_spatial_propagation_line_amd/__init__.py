@@ -540,3 +540,17 @@ def propagate_backward(x, logits, lam, u, grad_out, dirs: int = ALL, group_rows:
     _check(L.gspn_propagate_backward_shared_ws(args[0], args[1], cl, *args[2:], ws_ptr, ws_len,
                                                sptr))
     return grads
+
+
+_TOKENS = ("causal_conv", "causal_conv_backward", "selective_scan", "selective_scan_saved",
+           "selective_scan_backward", "cross_attention", "cross_attention_backward")
+
+
+def __getattr__(name):
+    """The token-sequence operators (tokens.py), imported on first use so
+    that importing the package does not import torch."""
+    if name in _TOKENS:
+        from . import tokens
+        globals().update({n: getattr(tokens, n) for n in _TOKENS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

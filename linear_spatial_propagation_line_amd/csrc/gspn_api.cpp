@@ -672,6 +672,19 @@ gspn_status run_bwd(gspn::BwdProblem pr, const BChecked& chk, void* ws, hipStrea
 
 }  // namespace
 
+namespace gspn {
+
+// for the entry points outside this file
+gspn_status set_error(gspn_status s, const char* detail) { return fail(s, detail); }
+void clear_error() { g_last_error.clear(); }
+void trace_begin(Tracer* tr) {
+  tr->events = g_trace_events;
+  tr->pairs = g_trace_pairs;
+}
+void trace_end(const Tracer& tr) { keep_trace(tr); }
+
+}  // namespace gspn
+
 extern "C" {
 
 gspn_status gspn_propagate(const void* x, const void* const w_logits[3], const void* lambda,

@@ -1,0 +1,222 @@
+// Tiles shared by the cross attention kernels (gspn_attn.hip,
+// gspn_attn_bwd.hip): 32 x 32 products on matrix cores whose result feeds the
+// next product from registers.
+//
+// Every product is taken as X = M1 M2^T or X = M1^T W with 32 x 32 results
+// (v_mfma_f32_32x32x16_bf16, or four v_mfma_f32_32x32x2_f32 for fp32):
+// lane l holds column l % 32 of the result, rows (i % 4) + 8 (i / 4) + 4 (l / 32)
+// in its 16 registers i. A result W[row][col] is then already a B operand
+// (lane: one column, consecutive contraction rows) if the contraction runs
+// over its rows in the order in which the registers hold them; the other
+// operand, M1^T, is read from LDS in that same order, for bf16 by the
+// transposing LDS read. So probabilities and score gradients never pass
+// through LDS.
+#pragma once
+
+#include "gspn_mfma.hpp"
+#include "gspn_tokens.hpp"
+
+namespace gspn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// The rows that share one key head: row r of (entry, key head) is query
+// r % Lq of head hk * share + r / Lq.
+struct RowMap {
+  int64_t batch, row, head;   // strides in elements
+};
+
+template <typename T> struct Mma;
+
+template <> struct Mma<bf16_t> {
+  static constexpr int kChunk = 16;    // contraction length of one fragment pair
+  static constexpr int kPer = 8;       // elements a lane holds of it
+  typedef bf16x8 Frag;
+  __device__ static __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Mma<float> {
+  static constexpr int kChunk = 8;
+  static constexpr int kPer = 4;
+  typedef f32x4 Frag;
+  __device__ static __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[k], b[k], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// LDS row pitch in bytes: 16 bytes of padding spread a column of 16-byte
+// pieces over the banks
+template <typename T, int EP> constexpr int tile_pitch() { return EP * static_cast<int>(sizeof(T)) + 16; }
+
+// 16 bytes of row values e0 .. : whole when `wide`, else value by value with
+// the row's end honoured (a value past E is 0)
+template <typename T>
+__device__ __forceinline__ u32x4 load16(const T* row, int e0, int E, bool wide) {
+  constexpr int kPer = 16 / sizeof(T);
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (wide) {
+    if (e0 < E) v = *reinterpret_cast<const u32x4*>(row + e0);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (e0 + k < E) {
+        if constexpr (sizeof(T) == 4) v[k] = __float_as_uint(to_f32(row[e0 + k]));
+        else v[k / 2] |= static_cast<uint32_t>(row[e0 + k].bits) << (16 * (k & 1));
+      }
+    }
+  }
+  return v;
+}
+
+// a lane's fragments of one row in global memory (zeros when !keep)
+template <typename T, int EP>
+__device__ __forceinline__ void row_frags(const T* row, bool keep, int E, bool wide,
+                                          typename Mma<T>::Frag (&f)[EP / Mma<T>::kChunk]) {
+  const int hh = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int j = 0; j < EP / Mma<T>::kChunk; ++j) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (keep) v = load16(row, j * Mma<T>::kChunk + hh * Mma<T>::kPer, E, wide);
+    f[j] = __builtin_bit_cast(typename Mma<T>::Frag, v);
+  }
+}
+
+// fragment j of the lane's row (row0 + l % 32) of an LDS tile
+template <typename T, int EP>
+__device__ __forceinline__ typename Mma<T>::Frag tile_frag(const char* tile, int row0, int j, int lane) {
+  return *reinterpret_cast<const typename Mma<T>::Frag*>(
+      tile + (row0 + (lane & 31)) * tile_pitch<T, EP>() + j * 32 + (lane >> 5) * 16);
+}
+
+// X[32 rows of the tile][32 lane columns] = tile rows . the lanes' fragments
+template <typename T, int EP>
+__device__ __forceinline__ f32x16 tile_dot(const char* tile, int row0,
+                                           const typename Mma<T>::Frag (&f)[EP / Mma<T>::kChunk],
+                                           int lane) {
+  f32x16 x = {};
+#pragma unroll
+  for (int j = 0; j < EP / Mma<T>::kChunk; ++j)
+    x = Mma<T>::mma(tile_frag<T, EP>(tile, row0, j, lane), f[j], x);
+  return x;
+}
+
+// acc[et][32 e of slab et][lane column] += tile rows^T W, W[32 rows][lane
+// column] in the result layout above
+template <int EP>
+__device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
+                                           f32x16 (&acc)[EP / 32], int lane, bf16_t) {
+  const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
+  constexpr int pitch = tile_pitch<bf16_t, EP>();
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    u32x4 p;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = pack_bf16x2(w[8 * kb + 2 * k], w[8 * kb + 2 * k + 1]);
+    const bf16x8 b = __builtin_bit_cast(bf16x8, p);
+    const char* q = tile + (row0 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
+#pragma unroll
+    for (int et = 0; et < EP / 32; ++et) {
+      const v4i16 lo = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64));
+      const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
+      const bf16x8 a = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+      acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[et], 0, 0, 0);
+    }
+  }
+}
+template <int EP>
+__device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
+                                           f32x16 (&acc)[EP / 32], int lane, float) {
+  constexpr int pitch = tile_pitch<float, EP>();
+  const char* q = tile + (row0 + 4 * (lane >> 5)) * pitch + (lane & 31) * 4;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+#pragma unroll
+    for (int et = 0; et < EP / 32; ++et) {
+      const float a = *reinterpret_cast<const float*>(q + ((i & 3) + 8 * (i >> 2)) * pitch + et * 128);
+      acc[et] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, w[i], acc[et], 0, 0, 0);
+    }
+  }
+}
+
+// the other half-wavefront's value of the same column
+__device__ __forceinline__ float other_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// A lane column of acc (EP values of one row) times f into row[0 .. E), or
+// zeros when !live, whatever acc holds; nothing when !keep. Halves of the
+// wavefront swap register groups so that each lane stores 8 adjacent values;
+// `wide` needs E % 8 == 0 and a 16-byte aligned row.
+template <typename T, int EP>
+__device__ __forceinline__ void store_col(T* row, bool keep, bool live, int E, bool wide,
+                                          const f32x16 (&acc)[EP / 32], float f, int lane) {
+  const int hh = lane >> 5;
+#pragma unroll
+  for (int et = 0; et < EP / 32; ++et) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[et][8 * h + k] * f),
+                                                        __float_as_uint(acc[et][8 * h + 4 + k] * f),
+                                                        false, false);
+        v[k] = live ? __uint_as_float(r[0]) : 0.0f;
+        v[4 + k] = live ? __uint_as_float(r[1]) : 0.0f;
+      }
+      const int e0 = et * 32 + h * 16 + hh * 8;
+      if (!keep || e0 >= E) continue;
+      if (wide) {
+        run_st<8>(row, e0, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (e0 + k < E) Store<T>::put(row, e0 + k, v[k]);
+      }
+    }
+  }
+}
+
+// Rows of a [rows][E] operand on their way into an LDS tile of ROWS rows, by
+// THREADS threads: 16-byte pieces held in registers between the load and the
+// write.
+template <typename T, int EP, int ROWS, int THREADS> struct Stage {
+  static constexpr int kPieces = EP * static_cast<int>(sizeof(T)) / 16;   // of one row
+  static constexpr int kEach = (ROWS * kPieces + THREADS - 1) / THREADS;
+  u32x4 v[kEach];
+  __device__ static __forceinline__ int row(int tid, int i) { return (tid + i * THREADS) / kPieces; }
+  __device__ static __forceinline__ int e0(int tid, int i) {
+    return (tid + i * THREADS) % kPieces * (16 / static_cast<int>(sizeof(T)));
+  }
+  // at(r): the row's address, or null for a row of zeros
+  template <typename F> __device__ __forceinline__ void load(int tid, int E, bool wide, F&& at) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      const int r = row(tid, i);
+      if (r < ROWS) {
+        const T* p = at(r);
+        if (p) v[i] = load16(p, e0(tid, i), E, wide);
+      }
+    }
+  }
+  // keep(r): whether the row's values are kept (zeros otherwise)
+  template <typename F> __device__ __forceinline__ void write(char* tile, int tid, F&& keep) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = row(tid, i);
+      if (r < ROWS)
+        *reinterpret_cast<u32x4*>(tile + r * tile_pitch<T, EP>() + e0(tid, i) * static_cast<int>(sizeof(T))) =
+            keep(r) ? v[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+};
+
+// the kernels' EP for a head of E values
+inline int attn_ep(int64_t E) { return E <= 32 ? 32 : (E <= 64 ? 64 : (E <= 96 ? 96 : 128)); }
+
+}  // namespace gspn

@@ -1,0 +1,334 @@
+// Cross attention, backward. With P from the forward pass's lse and
+// D[row] = sum_e grad_out out:
+//
+//   dV = P^T dO,   dS = P (dO V^T - D),   dQ = scale dS K,   dK = scale dS^T Q
+//
+// Two passes recompute P: one owns keys (a wavefront 32 of them, their K and
+// V fragments and their dK, dV in registers) and walks the rows, one owns
+// rows and walks the keys. Each sum then has one owner, so nothing is added
+// atomically; where few keys leave the chip idle, the rows of the first pass
+// are split and the parts added in order.
+#include "gspn_attn.hpp"
+
+namespace gspn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T> struct BwdP {
+  const T *q, *k, *v, *gy, *out;
+  RowMap qm, km, vm, gm;
+  const uint8_t* mask;
+  int64_t mask_batch;
+  const float* lse;
+  float* delta;        // [B][Hq][Lq]
+  T *dq, *dk, *dv;
+  float* part;         // [2][splits][B][Lk][Hkv][E], or null
+  int64_t B, Lq, Lk, rows;
+  int Hq, Hkv, share, E, splits, key_tiles, row_tiles, tiles_each;
+  float c, scale;      // scale * log2(e), scale
+  bool wide_q, wide_kv, wide_g, wide_dq, wide_dkv;
+};
+
+template <typename T> struct Row {
+  int64_t h, q;
+};
+template <typename T> __device__ __forceinline__ Row<T> row_of(const BwdP<T>& a, int hk, int64_t r) {
+  const int64_t hs = r / a.Lq;
+  return Row<T>{hk * a.share + hs, r - hs * a.Lq};
+}
+
+// delta[b][h][q] = sum_e grad_out out: 16 lanes per row
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
+  const int64_t i = (blockIdx.x * int64_t(kThreads) + threadIdx.x) / 16;
+  const int64_t total = a.B * a.Hq * a.Lq;
+  const int64_t ic = i < total ? i : total - 1;
+  const int64_t q = ic % a.Lq, bh = ic / a.Lq, b = bh / a.Hq, h = bh - b * a.Hq;
+  const T* g = a.gy + b * a.gm.batch + q * a.gm.row + h * a.gm.head;
+  const T* o = a.out + ((b * a.Lq + q) * a.Hq + h) * a.E;
+  float s = 0.0f;
+  for (int e = threadIdx.x % 16; e < a.E; e += 16) s = __builtin_fmaf(ld1(g + e), ld1(o + e), s);
+#pragma unroll
+  for (int m = 8; m >= 1; m /= 2) s += __shfl_xor(s, m);
+  if (i < total && threadIdx.x % 16 == 0) a.delta[i] = s;
+}
+
+// ---- dK, dV: 128 keys per workgroup, rows 32 at a time through LDS ----------
+template <typename T, int EP>
+__global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
+  extern __shared__ __align__(16) char lds[];
+  constexpr int TR = 32;
+  char* qt = lds;
+  char* gt = lds + TR * tile_pitch<T, EP>();
+  float* st = reinterpret_cast<float*>(lds + 2 * TR * tile_pitch<T, EP>());   // lse, delta
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hh = lane >> 5;
+  int64_t blk = blockIdx.x;
+  const int kt = static_cast<int>(blk % a.key_tiles);
+  blk /= a.key_tiles;
+  const int split = static_cast<int>(blk % a.splits);
+  const int64_t bh = blk / a.splits, b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const int64_t key = static_cast<int64_t>(kt) * 128 + wave * 32 + (lane & 31);
+  const bool in = key < a.Lk;
+  const bool keep = in && (!a.mask || a.mask[b * a.mask_batch + key] != 0);
+
+  typename Mma<T>::Frag kf[EP / Mma<T>::kChunk], vf[EP / Mma<T>::kChunk];
+  row_frags<T, EP>(a.k + b * a.km.batch + key * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
+  row_frags<T, EP>(a.v + b * a.vm.batch + key * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
+
+  f32x16 dk[EP / 32] = {}, dv[EP / 32] = {};
+  const int t_first = split * a.tiles_each;
+  const int t_last = t_first + a.tiles_each < a.row_tiles ? t_first + a.tiles_each : a.row_tiles;
+  Stage<T, EP, TR, kThreads> qs, gs;
+  float stat = 0.0f;
+  auto fetch = [&](int t) {
+    const int64_t r0 = static_cast<int64_t>(t) * TR;
+    qs.load(tid, a.E, a.wide_q, [&](int i) -> const T* {
+      if (r0 + i >= a.rows) return nullptr;
+      const Row<T> w = row_of(a, hk, r0 + i);
+      return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
+    });
+    gs.load(tid, a.E, a.wide_g, [&](int i) -> const T* {
+      if (r0 + i >= a.rows) return nullptr;
+      const Row<T> w = row_of(a, hk, r0 + i);
+      return a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head;
+    });
+    if (tid < 2 * TR) {
+      // rows past the end get lse = +inf, hence P = 0; the rows of one key
+      // head are adjacent in lse and delta
+      const int64_t r = r0 + (tid & (TR - 1));
+      const int64_t at = (b * a.Hq + hk * a.share) * a.Lq + r;
+      stat = tid < TR ? (r < a.rows ? a.lse[at] * kLog2e : INFINITY) : (r < a.rows ? a.delta[at] : 0.0f);
+    }
+  };
+  if (t_first < t_last) fetch(t_first);
+  for (int t = t_first; t < t_last; ++t) {
+    qs.write(qt, tid, [](int) { return true; });
+    gs.write(gt, tid, [](int) { return true; });
+    if (tid < 2 * TR) st[tid] = stat;
+    __syncthreads();
+    if (t + 1 < t_last) fetch(t + 1);
+    const f32x16 x = tile_dot<T, EP>(qt, 0, kf, lane);
+    const f32x16 y = tile_dot<T, EP>(gt, 0, vf, lane);
+    float p[16], ds[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = (i & 3) + 8 * (i >> 2) + 4 * hh;
+      p[i] = keep ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -st[r])) : 0.0f;
+      ds[i] = keep ? p[i] * (y[i] - st[TR + r]) : 0.0f;
+    }
+    tile_accum<EP>(gt, 0, p, dv, lane, T{});
+    tile_accum<EP>(qt, 0, ds, dk, lane, T{});
+    __syncthreads();
+  }
+  const int64_t at = ((b * a.Lk + key) * a.Hkv + hk) * a.E;
+  if (a.part) {
+    const int64_t n = a.B * a.Lk * a.Hkv * a.E;
+    store_col<float, EP>(a.part + split * n + at, in, keep, a.E, a.E % 8 == 0, dk, a.scale, lane);
+    store_col<float, EP>(a.part + (a.splits + split) * n + at, in, keep, a.E, a.E % 8 == 0, dv, 1.0f, lane);
+  } else {
+    store_col<T, EP>(a.dk + at, in, keep, a.E, a.wide_dkv, dk, a.scale, lane);
+    store_col<T, EP>(a.dv + at, in, keep, a.E, a.wide_dkv, dv, 1.0f, lane);
+  }
+}
+
+// the row splits' parts of dK and dV, added in order
+template <typename T>
+__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(BwdP<T> a) {
+  const int64_t n = a.B * a.Lk * a.Hkv * a.E;
+  const int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+  if (i >= 2 * n) return;
+  const bool second = i >= n;
+  const int64_t k = second ? i - n : i;
+  const float* p = a.part + (second ? a.splits * n : 0) + k;
+  float s = 0.0f;
+  for (int j = 0; j < a.splits; ++j) s += p[j * n];
+  Store<T>::put(second ? a.dv : a.dk, k, s);
+}
+
+// ---- dQ: 128 rows per workgroup, keys 32 at a time through LDS --------------
+template <typename T, int EP>
+__global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
+  extern __shared__ __align__(16) char lds[];
+  constexpr int TK = 32;
+  char* kt = lds;
+  char* vt = lds + TK * tile_pitch<T, EP>();
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int rts = static_cast<int>((a.rows + 127) / 128);
+  const int rt = static_cast<int>(blockIdx.x % rts);
+  const int64_t bh = blockIdx.x / rts, b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const int64_t r = static_cast<int64_t>(rt) * 128 + wave * 32 + (lane & 31);
+  const bool row_ok = r < a.rows;
+  const Row<T> w = row_of(a, hk, row_ok ? r : a.rows - 1);
+  typename Mma<T>::Frag qf[EP / Mma<T>::kChunk], gf[EP / Mma<T>::kChunk];
+  row_frags<T, EP>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
+  row_frags<T, EP>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, row_ok, a.E, a.wide_g, gf);
+  const int64_t at = (b * a.Hq + w.h) * a.Lq + w.q;
+  const float lse = row_ok ? a.lse[at] * kLog2e : INFINITY, delta = row_ok ? a.delta[at] : 0.0f;
+
+  const T* kp = a.k + b * a.km.batch + hk * a.km.head;
+  const T* vp = a.v + b * a.vm.batch + hk * a.vm.head;
+  const uint8_t* mp = a.mask ? a.mask + b * a.mask_batch : nullptr;
+  auto kept = [&](int64_t key) { return key < a.Lk && (!mp || mp[key] != 0); };
+  f32x16 dq[EP / 32] = {};
+  Stage<T, EP, TK, kThreads> ks, vs;
+  const int tiles = static_cast<int>((a.Lk + TK - 1) / TK);
+  auto fetch = [&](int t) {
+    const int64_t k0 = static_cast<int64_t>(t) * TK;
+    ks.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? kp + (k0 + i) * a.km.row : nullptr; });
+    vs.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? vp + (k0 + i) * a.vm.row : nullptr; });
+  };
+  if (tiles > 0) fetch(0);
+  for (int t = 0; t < tiles; ++t) {
+    const int64_t k0 = static_cast<int64_t>(t) * TK;
+    ks.write(kt, tid, [&](int i) { return kept(k0 + i); });
+    vs.write(vt, tid, [&](int i) { return kept(k0 + i); });
+    __syncthreads();
+    if (t + 1 < tiles) fetch(t + 1);
+    const uint32_t bits = static_cast<uint32_t>(__ballot(kept(k0 + (lane & 31))));
+    if (bits != 0) {
+      const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
+      const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
+      const uint32_t mine = bits >> (4 * (lane >> 5));
+      float ds[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -lse));
+        ds[i] = (mine >> ((i & 3) + 8 * (i >> 2))) & 1u ? p * (y[i] - delta) : 0.0f;
+      }
+      tile_accum<EP>(kt, 0, ds, dq, lane, T{});
+    }
+    __syncthreads();
+  }
+  store_col<T, EP>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
+}
+
+// ---- host -------------------------------------------------------------------
+struct BwdCut {
+  int key_tiles, row_tiles, splits, tiles_each;
+};
+// the rows of the dK, dV pass are split until about 512 workgroups run
+BwdCut cut_bwd(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv) {
+  BwdCut k;
+  k.key_tiles = static_cast<int>(cdiv(Lk, 128));
+  k.row_tiles = static_cast<int>(cdiv(Lq * (Hq / Hkv), 32));
+  const int64_t groups = std::max<int64_t>(1, B * Hkv * k.key_tiles);
+  int64_t splits = 1;
+  if (groups < 256) splits = std::min<int64_t>(k.row_tiles, cdiv(512, groups));
+  splits = std::max<int64_t>(1, splits);
+  k.tiles_each = static_cast<int>(cdiv(std::max(1, k.row_tiles), splits));
+  k.splits = static_cast<int>(cdiv(std::max(1, k.row_tiles), k.tiles_each));
+  return k;
+}
+
+template <typename K> hipError_t more_lds(K kern, int bytes) {
+  if (bytes <= 65536) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename T, int EP>
+hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
+  hipError_t e;
+  if (p.rows > 0) {
+    tr->before(stream, "attn_delta", p.B);
+    hipLaunchKernelGGL(attn_delta_kernel<T>,
+                       dim3(static_cast<unsigned>(cdiv(p.B * p.Hq * p.Lq, kThreads / 16))),
+                       dim3(kThreads), 0, stream, p);
+    tr->after(stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (p.Lk > 0) {
+    auto kern = attn_dkv_kernel<T, EP>;
+    constexpr int bytes = 2 * 32 * tile_pitch<T, EP>() + 64 * 4;
+    if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
+    tr->before(stream, "attn_dkv", p.B * p.Hkv);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * p.splits * p.key_tiles)),
+                       dim3(kThreads), bytes, stream, p);
+    tr->after(stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (p.part) {
+      tr->before(stream, "attn_dkv_join", p.B * p.Hkv);
+      hipLaunchKernelGGL(attn_dkv_join_kernel<T>,
+                         dim3(static_cast<unsigned>(cdiv(2 * p.B * p.Lk * p.Hkv * p.E, kThreads))),
+                         dim3(kThreads), 0, stream, p);
+      tr->after(stream);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  if (p.rows > 0) {
+    auto kern = attn_dq_kernel<T, EP>;
+    constexpr int bytes = 2 * 32 * tile_pitch<T, EP>();
+    if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
+    tr->before(stream, "attn_dq", p.B * p.Hkv);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * cdiv(p.rows, 128))),
+                       dim3(kThreads), bytes, stream, p);
+    tr->after(stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t bwd_dt(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws, hipStream_t stream,
+                  Tracer* tr) {
+  BwdP<T> p{};
+  const BwdCut k = cut_bwd(a.B, a.Lq, a.Lk, a.Hq, a.Hkv);
+  p.q = static_cast<const T*>(a.q.p); p.qm = {a.q.batch, a.q.row, a.q.head};
+  p.k = static_cast<const T*>(a.k.p); p.km = {a.k.batch, a.k.row, a.k.head};
+  p.v = static_cast<const T*>(a.v.p); p.vm = {a.v.batch, a.v.row, a.v.head};
+  p.gy = static_cast<const T*>(g.grad_out.p);
+  p.gm = {g.grad_out.batch, g.grad_out.row, g.grad_out.head};
+  p.out = static_cast<const T*>(a.out);
+  p.mask = a.mask; p.mask_batch = a.mask_batch;
+  p.lse = a.lse;
+  p.dq = static_cast<T*>(g.q); p.dk = static_cast<T*>(g.k); p.dv = static_cast<T*>(g.v);
+  p.B = a.B; p.Lq = a.Lq; p.Lk = a.Lk;
+  p.Hq = static_cast<int>(a.Hq); p.Hkv = static_cast<int>(a.Hkv);
+  p.share = p.Hq / p.Hkv;
+  p.rows = a.Lq * p.share;
+  p.E = static_cast<int>(a.E);
+  p.splits = k.splits; p.key_tiles = k.key_tiles; p.row_tiles = k.row_tiles;
+  p.tiles_each = k.tiles_each;
+  p.scale = a.scale;
+  p.c = a.scale * kLog2e;
+  p.delta = static_cast<float*>(ws);
+  if (k.splits > 1)
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + up256(static_cast<size_t>(a.B * a.Hq * a.Lq) * 4));
+  constexpr int per = 16 / sizeof(T);
+  const bool whole = a.E % per == 0, eight = a.E % 8 == 0;
+  const size_t es = sizeof(T);
+  p.wide_q = whole && wide_ok(a.q.p, 16, es, {a.q.batch, a.q.row, a.q.head});
+  p.wide_kv = whole && wide_ok(a.k.p, 16, es, {a.k.batch, a.k.row, a.k.head}) &&
+              wide_ok(a.v.p, 16, es, {a.v.batch, a.v.row, a.v.head});
+  p.wide_g = whole && wide_ok(p.gy, 16, es, {p.gm.batch, p.gm.row, p.gm.head});
+  p.wide_dq = eight && wide_ok(p.dq, 16, es, {});
+  p.wide_dkv = eight && wide_ok(p.dk, 16, es, {}) && wide_ok(p.dv, 16, es, {});
+  switch (attn_ep(a.E)) {
+    case 32: return bwd_ep<T, 32>(p, stream, tr);
+    case 64: return bwd_ep<T, 64>(p, stream, tr);
+    case 96: return bwd_ep<T, 96>(p, stream, tr);
+    default: return bwd_ep<T, 128>(p, stream, tr);
+  }
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E) {
+  if (B == 0) return 0;
+  const BwdCut k = cut_bwd(B, Lq, Lk, Hq, Hkv);
+  size_t n = up256(static_cast<size_t>(B * Hq * Lq) * sizeof(float));
+  if (k.splits > 1) n += static_cast<size_t>(2 * k.splits * B * Lk * Hkv * E) * sizeof(float);
+  return n;
+}
+
+hipError_t launch_attn_bwd(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws,
+                           hipStream_t stream, Tracer* tr) {
+  if (a.dtype == GSPN_F32) return bwd_dt<float>(a, g, ws, stream, tr);
+  return bwd_dt<bf16_t>(a, g, ws, stream, tr);
+}
+
+}  // namespace gspn

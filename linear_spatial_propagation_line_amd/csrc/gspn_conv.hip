@@ -1,0 +1,384 @@
+// Short causal convolution over tokens, forward and backward.
+//
+//   pre[t] = bias + sum_{j<K} w[j] xx[t + j],  xx = state ++ x,  out = silu(pre)
+//   dpre   = grad_out * silu'(pre)
+//   dxx[s] = sum_j w[j] dpre[s - j],  dw[j] = sum_t dpre[t] xx[t + j],  db = sum_t dpre[t]
+//
+// Bound by memory: 2 K + 5 operations against 2 elements moved per value
+// (forward), so the work is to move each row once in wide accesses. A lane
+// owns V adjacent channels (16 bytes) and walks a run of tokens with the last
+// K - 1 rows in registers, so each row is read once per run plus K - 1 rows
+// of the run before; rows are loaded kAhead at a time, which keeps that many
+// 16-byte loads in flight per lane.
+#include "gspn_tokens.hpp"
+
+namespace gspn {
+
+namespace {
+
+constexpr int kRun = 32;     // tokens one lane walks
+constexpr int kAhead = 8;    // rows loaded together
+
+template <typename T> struct ConvP {
+  const T* x; int64_t xb, xr;
+  const T* gy; int64_t gb, gr;
+  const T* w; const T* bias; const T* state; const int32_t* lens;
+  T* out; T* state_out;
+  T* dx; T* dstate; float* part;
+  int64_t L, C;
+  int64_t runs;       // runs of kRun tokens per entry (at least 1)
+  int64_t ctiles;     // tiles of 64 * V channels
+  int silu;
+};
+
+// V values at p, widened
+template <int V> __device__ __forceinline__ void ldv(const float* p, float* d) {
+  if constexpr (V == 1) d[0] = p[0];
+  else run_ld<V>(p, 0, d);
+}
+template <int V> __device__ __forceinline__ void ldv(const bf16_t* p, float* d) {
+  if constexpr (V == 1) d[0] = to_f32(p[0]);
+  else run_ld<V>(p, 0, d);
+}
+template <int V, typename T> __device__ __forceinline__ void stv(T* p, const float* d) {
+  if constexpr (V == 1) Store<T>::put(p, 0, d[0]);
+  else run_st<V>(p, 0, d);
+}
+
+// row t of xx without the K - 1 offset: x[t] for 0 <= t < n, the state for
+// t < 0 (zeros without one); rows past n are not read
+template <int K, int V, typename T>
+__device__ __forceinline__ void row_at(const ConvP<T>& a, int64_t b, int64_t c, int64_t t,
+                                       int64_t n, float* d) {
+  if (t >= 0 && t < n) {
+    ldv<V>(a.x + b * a.xb + t * a.xr + c, d);
+  } else if (t < 0 && a.state) {
+    ldv<V>(a.state + (b * (K - 1) + (t + K - 1)) * a.C + c, d);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) d[e] = 0.0f;
+  }
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
+  // four runs of one channel tile per workgroup, one per wavefront
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rgroups = (a.runs + 3) / 4;
+  int64_t i = blockIdx.x;
+  const int64_t ct = i % a.ctiles;
+  i /= a.ctiles;
+  const int64_t rg = i % rgroups, b = i / rgroups;
+  const int64_t run = rg * 4 + wave, c = (ct * 64 + lane) * V;
+  if (run >= a.runs || c >= a.C) return;
+  const int64_t n = seq_len(a.lens, b, a.L);
+  const int64_t t0 = run * kRun, t1 = t0 + kRun < a.L ? t0 + kRun : a.L;
+
+  float w[K][V], bias[V], win[K - 1 > 0 ? K - 1 : 1][V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][e] = ld1(a.w + (c + e) * K + j);
+    bias[e] = a.bias ? ld1(a.bias + c + e) : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j]);
+  // the run that reads the old state also writes the new one (they may be
+  // the same memory): rows n - (K - 1) .. n - 1 of state ++ x
+  if (run == 0 && a.state_out) {
+    float last[K - 1 > 0 ? K - 1 : 1][V];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, n - (K - 1) + j, n, last[j]);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) stv<V>(a.state_out + (b * (K - 1) + j) * a.C + c, last[j]);
+  }
+  T* o = a.out + (b * a.L + t0) * a.C + c;
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    float r[kAhead][V];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) row_at<K, V>(a, b, c, t + k, n, r[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t + k < t1) {
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float s = bias[e];
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
+          s = __builtin_fmaf(w[K - 1][e], r[k][e], s);
+          if (a.silu) s *= sigmoid_f32(s);
+          y[e] = t + k < n ? s : 0.0f;
+        }
+        stv<V>(o, y);
+        o += a.C;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
+        if (K > 1) win[K > 1 ? K - 2 : 0][e] = r[k][e];
+      }
+    }
+  }
+}
+
+// A run of kRun tokens computes dpre for its own tokens and the K - 1 after
+// them (which its dx needs too); dw and db take its own tokens only. The
+// partial sums of the workgroup's four runs are joined in LDS, in run order,
+// into row (b, group of runs) of part: [K + 1][C], taps first, then the bias.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
+  __shared__ float acc[3][(K + 1) * V][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rgroups = (a.runs + 3) / 4;
+  int64_t i = blockIdx.x;
+  const int64_t ct = i % a.ctiles;
+  i /= a.ctiles;
+  const int64_t rg = i % rgroups, b = i / rgroups;
+  const int64_t run = rg * 4 + wave, c = (ct * 64 + lane) * V;
+  const bool live = run < a.runs && c < a.C;
+
+  float w[K][V], bias[V], win[K][V], dp[K][V], dw[K][V], db[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    db[e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][e] = dp[j][e] = 0.0f;
+  }
+  if (live) {
+    const int64_t n = seq_len(a.lens, b, a.L);
+    const int64_t t0 = run * kRun, t1 = t0 + kRun < a.L ? t0 + kRun : a.L;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][e] = ld1(a.w + (c + e) * K + j);
+      bias[e] = a.bias ? ld1(a.bias + c + e) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j + 1]);
+    const T* gp = a.gy + b * a.gb + c;
+    for (int64_t t = t0; t < t1 + K - 1; t += kAhead) {
+      float r[kAhead][V], gy[kAhead][V];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool in = t + k < n;   // rows past the end give dpre = 0
+        row_at<K, V>(a, b, c, in ? t + k : n, n, r[k]);
+        if (in) ldv<V>(gp + (t + k) * a.gr, gy[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t tt = t + k;
+        if (tt < t1 + K - 1) {
+          float o[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) win[j][e] = win[j + 1][e];
+            win[K - 1][e] = r[k][e];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) dp[j][e] = dp[j + 1][e];
+            float s = bias[e];
+#pragma unroll
+            for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
+            float d = 1.0f;
+            if (a.silu) {
+              const float sg = sigmoid_f32(s);
+              d = sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
+            }
+            d = tt < n ? d * gy[k][e] : 0.0f;
+            dp[K - 1][e] = d;
+            if (tt < t1 && tt < n) {
+              db[e] += d;
+#pragma unroll
+              for (int j = 0; j < K; ++j) dw[j][e] = __builtin_fmaf(d, win[j][e], dw[j][e]);
+            }
+            // dxx of row s = tt - (K - 1): w[j] meets dpre[s + K - 1 - j]
+            o[e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
+          }
+          const int64_t s = tt - (K - 1);
+          if (s >= t0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
+            stv<V>(a.dx + (b * a.L + s) * a.C + c, o);
+          } else if (run == 0 && a.dstate) {
+            stv<V>(a.dstate + (b * (K - 1) + s + K - 1) * a.C + c, o);
+          }
+        }
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) acc[wave - 1][j * V + e][lane] = dw[j][e];
+      acc[wave - 1][K * V + e][lane] = db[e];
+    }
+  }
+  __syncthreads();
+  if (wave == 0 && c < a.C) {
+    float* p = a.part + (b * rgroups + rg) * (K + 1) * a.C + c;
+#pragma unroll
+    for (int j = 0; j <= K; ++j) {
+      float s[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s[e] = j < K ? dw[j < K ? j : 0][e] : db[e];
+#pragma unroll
+        for (int q = 0; q < 3; ++q) s[e] += acc[q][j * V + e][lane];
+      }
+      // part is fp32 and its rows need not be 16-byte aligned
+#pragma unroll
+      for (int e = 0; e < V; ++e) p[j * a.C + e] = s[e];
+    }
+  }
+}
+
+// columns of part summed over its rows; the taps' sums go to dw [C][K] and
+// the last C columns to db
+template <typename T>
+__global__ __launch_bounds__(512) void conv_reduce_kernel(const float* part, int64_t rows, int64_t C,
+                                                          int K, T* dw, T* db) {
+  __shared__ float acc[8][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t cols = (K + 1) * C, i = blockIdx.x * int64_t(64) + lane;
+  float s = 0.0f;
+  if (i < cols)
+    for (int64_t r = wave; r < rows; r += 8) s += part[r * cols + i];
+  acc[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && i < cols) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += acc[q][lane];
+    const int64_t j = i / C, c = i - j * C;
+    if (j < K) Store<T>::put(dw, c * K + j, s);
+    else if (db) Store<T>::put(db, c, s);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(512) void reduce_rows_kernel(const float* part, int64_t rows,
+                                                          int64_t cols, T* out) {
+  __shared__ float acc[8][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i = blockIdx.x * int64_t(64) + lane;
+  float s = 0.0f;
+  if (i < cols)
+    for (int64_t r = wave; r < rows; r += 8) s += part[r * cols + i];
+  acc[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && i < cols) {
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += acc[q][lane];
+    Store<T>::put(out, i, s);
+  }
+}
+
+template <typename T> ConvP<T> conv_params(const gspn_conv_args& a) {
+  ConvP<T> p{};
+  p.x = static_cast<const T*>(a.x.p);
+  p.xb = a.x.batch;
+  p.xr = a.x.row;
+  p.w = static_cast<const T*>(a.weight);
+  p.bias = static_cast<const T*>(a.bias);
+  p.state = static_cast<const T*>(a.state);
+  p.lens = a.lens;
+  p.out = static_cast<T*>(a.out);
+  p.state_out = static_cast<T*>(a.state_out);
+  p.L = a.L;
+  p.C = a.C;
+  p.runs = std::max<int64_t>(1, cdiv(a.L, kRun));
+  p.silu = a.silu;
+  return p;
+}
+
+template <typename T, int K>
+hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, hipStream_t stream,
+                   Tracer* tr) {
+  constexpr int V = 16 / sizeof(T);
+  ConvP<T> p = conv_params<T>(a);
+  const size_t es = sizeof(T);
+  bool wide = a.C % V == 0 && wide_ok(a.x.p, 16, es, {a.x.batch, a.x.row}) &&
+              (!a.state || wide_ok(a.state, 16, es, {}));
+  if (g) {
+    p.gy = static_cast<const T*>(g->grad_out.p);
+    p.gb = g->grad_out.batch;
+    p.gr = g->grad_out.row;
+    p.dx = static_cast<T*>(g->x);
+    p.dstate = static_cast<T*>(g->state);
+    p.part = static_cast<float*>(ws);
+    wide = wide && wide_ok(p.gy, 16, es, {p.gb, p.gr}) && wide_ok(p.dx, 16, es, {}) &&
+           (!p.dstate || wide_ok(p.dstate, 16, es, {}));
+  } else {
+    wide = wide && wide_ok(p.out, 16, es, {}) && (!p.state_out || wide_ok(p.state_out, 16, es, {}));
+  }
+  p.ctiles = cdiv(a.C, 64 * (wide ? V : 1));
+  const int64_t rgroups = cdiv(p.runs, 4);
+  const dim3 grid(static_cast<unsigned>(a.B * rgroups * p.ctiles));
+  const char* name = g ? "conv_bwd" : "conv_fwd";
+  tr->before(stream, name, a.B);
+  if (a.B > 0) {
+    if (g) {
+      if (wide) hipLaunchKernelGGL((conv_bwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((conv_bwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);
+    } else {
+      if (wide) hipLaunchKernelGGL((conv_fwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((conv_fwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);
+    }
+  }
+  tr->after(stream);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !g) return e;
+  const int64_t cols = (K + 1) * a.C;
+  tr->before(stream, "conv_reduce", a.B);
+  hipLaunchKernelGGL(conv_reduce_kernel<T>, dim3(static_cast<unsigned>(cdiv(cols, 64))), dim3(512),
+                     0, stream, p.part, a.B * rgroups, a.C, K, static_cast<T*>(g->weight),
+                     static_cast<T*>(g->bias));
+  tr->after(stream);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t conv_k(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, hipStream_t stream,
+                  Tracer* tr) {
+  switch (a.K) {
+    case 1: return conv_dt<T, 1>(a, g, ws, stream, tr);
+    case 2: return conv_dt<T, 2>(a, g, ws, stream, tr);
+    case 3: return conv_dt<T, 3>(a, g, ws, stream, tr);
+    default: return conv_dt<T, 4>(a, g, ws, stream, tr);
+  }
+}
+
+}  // namespace
+
+template <typename T>
+hipError_t reduce_rows(const float* part, int64_t rows, int64_t cols, T* out, hipStream_t stream,
+                       Tracer* tr) {
+  tr->before(stream, "reduce_rows", rows);
+  hipLaunchKernelGGL(reduce_rows_kernel<T>, dim3(static_cast<unsigned>(cdiv(cols, 64))), dim3(512),
+                     0, stream, part, rows, cols, out);
+  tr->after(stream);
+  return hipGetLastError();
+}
+template hipError_t reduce_rows<float>(const float*, int64_t, int64_t, float*, hipStream_t, Tracer*);
+
+size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t K) {
+  const int64_t rgroups = cdiv(std::max<int64_t>(1, cdiv(L, kRun)), 4);
+  return static_cast<size_t>(B * rgroups * (K + 1) * C) * sizeof(float);
+}
+
+hipError_t launch_conv(const gspn_conv_args& a, hipStream_t stream, Tracer* tr) {
+  if (a.dtype == GSPN_F32) return conv_k<float>(a, nullptr, nullptr, stream, tr);
+  return conv_k<bf16_t>(a, nullptr, nullptr, stream, tr);
+}
+
+hipError_t launch_conv_bwd(const gspn_conv_args& a, const gspn_conv_grads& g, void* ws,
+                           hipStream_t stream, Tracer* tr) {
+  if (a.dtype == GSPN_F32) return conv_k<float>(a, &g, ws, stream, tr);
+  return conv_k<bf16_t>(a, &g, ws, stream, tr);
+}
+
+}  // namespace gspn

@@ -75,6 +75,14 @@ struct Tracer {
   }
 };
 
+// The calling thread's error text and launch trace, for entry points outside
+// gspn_api.cpp: set_error returns `s`; trace_begin hands the tracer the
+// caller's events, trace_end keeps what it recorded.
+gspn_status set_error(gspn_status s, const char* detail);
+void clear_error();
+void trace_begin(Tracer* tr);
+void trace_end(const Tracer& tr);
+
 // plane-resident path (gspn_plane.hip)
 bool plane_fits(int64_t H, int64_t W);
 int plane_seg(int64_t H, int64_t W);

@@ -1,0 +1,96 @@
+// Internal interface and device helpers of the token-sequence operators
+// (causal convolution, selective scan, cross attention).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gspn_device.hpp"
+#include "gspn_launch.hpp"
+#include "gspn_tokens.h"
+
+namespace gspn {
+
+// Validated problems go to the launchers as the ABI's own argument structs.
+size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t K);
+hipError_t launch_conv(const gspn_conv_args& a, hipStream_t stream, Tracer* tr);
+hipError_t launch_conv_bwd(const gspn_conv_args& a, const gspn_conv_grads& g, void* ws,
+                           hipStream_t stream, Tracer* tr);
+
+constexpr int kScanSave = 32;   // tokens between saved states
+size_t scan_saved_bytes(int64_t B, int64_t L, int64_t C, int64_t N);
+size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G);
+hipError_t launch_scan(const gspn_scan_args& a, void* ws, hipStream_t stream, Tracer* tr);
+size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G);
+hipError_t launch_scan_bwd(const gspn_scan_args& a, const gspn_scan_grads& g, void* ws,
+                           hipStream_t stream, Tracer* tr);
+
+size_t attn_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E);
+hipError_t launch_attn(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr);
+size_t attn_bwd_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv,
+                                int64_t E);
+hipError_t launch_attn_bwd(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws,
+                           hipStream_t stream, Tracer* tr);
+
+// out[i] = sum over r < rows of part[r * cols + i], in row order within each
+// of eight interleaved row sets whose sums are then added in order; rows = 0
+// writes zeros (gspn_conv.hip)
+template <typename T>
+hipError_t reduce_rows(const float* part, int64_t rows, int64_t cols, T* out, hipStream_t stream,
+                       Tracer* tr);
+
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// a host-side check that a pointer and the strides used with it keep
+// `bytes`-wide accesses aligned
+inline bool wide_ok(const void* p, size_t bytes, size_t es, std::initializer_list<int64_t> strides) {
+  if (reinterpret_cast<uintptr_t>(p) % bytes) return false;
+  for (const int64_t s : strides)
+    if ((static_cast<uint64_t>(s) * es) % bytes) return false;
+  return true;
+}
+
+// ---- device helpers ---------------------------------------------------------
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T> __device__ __forceinline__ float ld1(const T* p) { return to_f32(*p); }
+template <typename T> __device__ __forceinline__ void st1(T* p, float v) { Store<T>::put(p, 0, v); }
+
+// sigmoid(v); the exponent is capped so that the denominator stays finite (at
+// the cap the result is below 2^-125), NaN stays NaN through the callers'
+// products with v
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return recip(1.0f + __builtin_amdgcn_exp2f(fminf(v * -kLog2e, 125.0f)));
+}
+
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1]. The
+// logarithm is 2 atanh(s), s = e / (2 + e) <= 1/3, by its power series up to
+// s^15 (the next term is below 2^-27 of the sum), which keeps the relative
+// precision that log(1 + e) loses for small e.
+__device__ __forceinline__ float softplus_f32(float v) {
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+  const float s = e * recip(2.0f + e);
+  const float q = s * s;
+  float p = __builtin_fmaf(q, 1.0f / 15.0f, 1.0f / 13.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 11.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 9.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 7.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 5.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 3.0f);
+  p = __builtin_fmaf(q, p, 1.0f);
+  return fmaxf(v, 0.0f) + 2.0f * s * p;
+}
+
+// length of entry b: lens[b] clamped to 0 .. L, or L
+__device__ __forceinline__ int64_t seq_len(const int32_t* lens, int64_t b, int64_t L) {
+  if (!lens) return L;
+  const int64_t n = lens[b];
+  return n < 0 ? 0 : (n > L ? L : n);
+}
+
+}  // namespace gspn

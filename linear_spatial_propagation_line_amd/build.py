@@ -21,8 +21,8 @@ SOURCES = ["gspn_api.cpp", "gspn_plane.hip", "gspn_stream.hip", "gspn_tpipe.hip"
            "gspn_bwd_band.hip", "gspn_dirs.hip",
            "gspn_prologue.hip", "gspn_bwd_tpipe.hip", "gspn_groups.cpp",
            "gspn_calib.hip", "gspn_fused.hip", "gspn_strip.hip",
-           "gspn_tok_api.cpp", "gspn_conv.hip", "gspn_scan.hip", "gspn_attn.hip",
-           "gspn_attn_bwd.hip"]
+           "tokens/gspn_tok_api.cpp", "tokens/gspn_conv.hip", "tokens/gspn_scan.hip",
+           "tokens/gspn_attn.hip", "tokens/gspn_attn_bwd.hip"]
 ARCH = os.environ.get("GSPN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [
@@ -30,7 +30,7 @@ FLAGS = [
     "-Wall", "-Werror=return-type",
     # keep the compiler from forming packed-fp32 instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-I", INCLUDE, "-I", CSRC,
+    "-I", INCLUDE, "-I", CSRC, "-I", os.path.join(CSRC, "tokens"),
 ]
 
 
@@ -43,6 +43,7 @@ def _hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    os.makedirs(os.path.dirname(obj), exist_ok=True)
     cmd = [_hipcc(), *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

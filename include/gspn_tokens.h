@@ -111,7 +111,7 @@ size_t gspn_causal_conv_backward_workspace_bytes(int64_t B, int64_t L, int64_t C
  *   N 1 .. 32, G >= 1 dividing C (GSPN_E_SHAPE)
  *   out [B, L, C]       in dtype
  *   saved               NULL, or gspn_selective_scan_saved_bytes() bytes,
- *                       256-byte aligned: receives the states at every 32nd
+ *                       256-byte aligned: receives the states at every 16th
  *                       token, which the backward pass of the same arguments
  *                       then takes instead of finding them again
  * A call with L = 1 and state_out = state is one step of a serving loop.

@@ -13,15 +13,21 @@
 //   dA[n]    = sum over entries and tokens of d_t m_t[n]
 //
 // Bound by the vector ALU: per token, channel and state one exponential
-// (quarter rate), two products and two multiply-adds, against 8 bytes moved
-// per token and channel. So a lane owns one channel with all its N states in
-// registers, 64 adjacent channels per wavefront: the states need no exchange
-// between lanes, every row of x, dt, z is one coalesced access, and B_t, C_t
-// are the same for the whole wavefront. They are read by scalar loads into
-// scalar registers, where they cost the vector ALU nothing, from an fp32
-// copy padded to NP states (pack_kernel).
+// (8.3 cycles per wavefront on this chip), two products and two multiply-adds
+// (4.1 each), against 8 bytes moved per token and channel. So a lane owns one
+// channel, 64 adjacent channels per workgroup, and states stay in registers;
+// every row of x, dt, z is one coalesced access; B_t and C_t are the same for
+// a whole wavefront and are read by scalar loads into scalar registers, where
+// they cost the vector ALU nothing, from an fp32 copy (pack_kernel).
 //
-// Few channels do not fill the chip: the token axis is then cut into
+// The four wavefronts of a workgroup share the channels and split the states.
+// That gives four times the wavefronts of one lane holding all states, and the
+// work that is per token and channel rather than per state (softplus, gate,
+// conversions) is split as well: for 16 tokens at a time each wavefront
+// prepares four tokens into LDS, runs its own states over all 16, and finishes
+// four tokens from the four partial results.
+//
+// Few channels still do not fill the chip: the token axis is then cut into
 // segments. A first pass finds each segment's state from zero and its sum of
 // d (the product of its decays is exp(A sum d): one exponential), a small
 // kernel carries states across segments, and the full pass starts every
@@ -33,11 +39,11 @@ namespace gspn {
 
 namespace {
 
-typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef const __attribute__((address_space(4))) f32x8* cvec8;
-
-constexpr int kStepMax = 4;   // up to this many tokens: the single-token kernel
-constexpr int kSub = 8;       // tokens loaded together; divides kScanSave
+constexpr int kStepMax = 4;             // up to this many tokens: the single-token kernel
+constexpr int kW = 4;                   // wavefronts of a workgroup
+constexpr int kS = kScanSave;           // tokens prepared together
+constexpr int kOwn = kS / kW;           // of which each wavefront prepares these
+constexpr int kThreads = 64 * kW;
 
 template <typename T> struct ScanP {
   const T *x, *dt, *z, *gy;
@@ -49,63 +55,60 @@ template <typename T> struct ScanP {
   T* out;
   float* state_out;
   float* saved;        // [B][chunks][NP][C]
-  float* pack;         // [B][G][L][2][NP]
+  float* pack;         // [B][G][kW][Lp][2][NS]
   float* sum_d;        // [B][segs][C]
   float* carry;        // [B][segs][NP][C]: local results, then carried-in values
   // backward
   T *dx, *ddt, *dz;
-  float* partA;        // [B * segs][NP][C]
+  float* partA;        // [B * segs][C][N]
   float* partD;        // [B * segs][C], then the same for dt_bias
-  float* partBC;       // [B][G][tiles][L][2][NP]
+  float* partBC;       // [B][G][tiles][Lp][kW][2][NS]
   float* dstate;
-  int64_t B, L, C, G, Cg, chunks;
+  int64_t B, L, Lp, C, G, Cg, chunks;   // Lp: L rounded up to whole chunks
   int N, tiles, segs, segChunks, softplus;
 };
 
-// ---- B and C as fp32 rows of NP states, zeros past N ------------------------
-template <typename T, int NP>
+// ---- B and C as fp32, zeros past N states and past the entry's tokens --------
+template <typename T, int NS>
 __global__ __launch_bounds__(256) void pack_kernel(ScanP<T> a) {
   int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
-  const int n = static_cast<int>(i % (2 * NP));
-  i /= 2 * NP;
-  const int64_t t = i % a.L;
-  i /= a.L;
+  const int n = static_cast<int>(i % (2 * NS));
+  i /= 2 * NS;
+  const int w = static_cast<int>(i % kW);     // reads of a token's states stay adjacent
+  i /= kW;
+  const int64_t t = i % a.Lp;
+  i /= a.Lp;
   const int64_t g = i % a.G, b = i / a.G;
   if (b >= a.B) return;
-  const int k = n % NP;
+  const int k = w * NS + n % NS;
   float v = 0.0f;
   if (k < a.N && t < seq_len(a.lens, b, a.L))
-    v = n < NP ? ld1(a.Bm + b * a.bb + t * a.br + g * a.bh + k)
+    v = n < NS ? ld1(a.Bm + b * a.bb + t * a.br + g * a.bh + k)
                : ld1(a.Cm + b * a.cb + t * a.cr + g * a.ch + k);
-  a.pack[((b * a.G + g) * a.L + t) * (2 * NP) + n] = v;
+  a.pack[(((b * a.G + g) * kW + w) * a.Lp + t) * (2 * NS) + n] = v;
 }
 
-template <int NP> struct BCRow {
-  float b[NP], c[NP];
-};
-// token t's B and C, uniform over the wavefront: scalar loads
-template <int NP>
-__device__ __forceinline__ void load_bc(const float* pack, int64_t t, float (&b)[NP], float (&c)[NP]) {
-  const cvec8 q = (cvec8)(uintptr_t)(pack + t * (2 * NP));
+// a token's B and C of this wavefront's states: uniform, by scalar loads
+template <int NS>
+__device__ __forceinline__ void load_bc(const float* pack, int64_t t, float (&b)[NS], float (&c)[NS]) {
+  typedef const __attribute__((address_space(4))) float* cptr;
+  const cptr q = (cptr)(uintptr_t)(pack + t * (2 * NS));
 #pragma unroll
-  for (int k = 0; k < NP / 8; ++k) {
-    const f32x8 u = q[k], v = q[NP / 8 + k];
+  for (int n = 0; n < NS; ++n) b[n] = q[n];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      b[8 * k + e] = u[e];
-      c[8 * k + e] = v[e];
-    }
-  }
+  for (int n = 0; n < NS; ++n) c[n] = q[NS + n];
 }
 
-// where a wavefront works: entry b, group g, its channel, its segment
+// where a workgroup works: entry b, group g, the lane's channel, its segment
 template <typename T> struct Place {
-  int64_t b, g, seg, c, t0, t1, n;
-  int tile;
+  int64_t b, g, seg, c, t0, t1, end;   // tokens t0 .. t1 - 1, padding t1 .. end - 1
+  int tile, lane, w;
   bool live;
 };
 template <typename T> __device__ __forceinline__ Place<T> place(const ScanP<T>& a) {
   Place<T> p;
+  p.lane = threadIdx.x & 63;
+  p.w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t i = blockIdx.x;
   p.tile = static_cast<int>(i % a.tiles);
   i /= a.tiles;
@@ -113,13 +116,14 @@ template <typename T> __device__ __forceinline__ Place<T> place(const ScanP<T>& 
   i /= a.G;
   p.seg = i % a.segs;
   p.b = i / a.segs;
-  const int64_t k = p.tile * int64_t(64) + threadIdx.x;
+  const int64_t k = p.tile * int64_t(64) + p.lane;
   p.live = k < a.Cg;
   p.c = p.g * a.Cg + (p.live ? k : a.Cg - 1);   // idle lanes read the last channel
-  p.n = seq_len(a.lens, p.b, a.L);
-  p.t0 = p.seg * a.segChunks * kScanSave;
-  p.t1 = p.t0 + a.segChunks * kScanSave;
-  if (p.t1 > p.n) p.t1 = p.n;
+  const int64_t n = seq_len(a.lens, p.b, a.L);
+  p.t0 = p.seg * a.segChunks * kS;
+  p.end = p.t0 + a.segChunks * kS;
+  if (p.end > a.L) p.end = a.L;
+  p.t1 = p.end < n ? p.end : n;
   return p;
 }
 
@@ -128,99 +132,180 @@ template <typename T> __device__ __forceinline__ float step_size(const ScanP<T>&
   return a.softplus ? softplus_f32(v) : v;
 }
 
+// this wavefront's states of the lane's channel: A log2(e), zero past N
+template <typename T, int NS>
+__device__ __forceinline__ void load_A(const ScanP<T>& a, const Place<T>& p, float (&A2)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    A2[n] = p.w * NS + n < a.N ? a.A[p.c * a.N + p.w * NS + n] * kLog2e : 0.0f;
+}
+
 // ---- forward ----------------------------------------------------------------
-// kSummary: only the segment's end state from zero and its sum of d
-template <typename T, int NP, bool kSummary>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanP<T> a) {
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanP<T> a) {
+  __shared__ float sd[kS][64], sx[kS][64], sy[kW][kS][64];   // d, d x, partial y
   const Place<T> p = place(a);
+  const int lane = p.lane, w = p.w;
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
-  float A2[NP], h[NP];
+  float A2[NS], h[NS];
+  load_A(a, p, A2);
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    A2[n] = n < a.N ? a.A[p.c * a.N + n] * kLog2e : 0.0f;
+  for (int n = 0; n < NS; ++n) {
     h[n] = 0.0f;
-  }
-  if constexpr (!kSummary) {
-    if (a.segs > 1) {
-#pragma unroll
-      for (int n = 0; n < NP; ++n) h[n] = a.carry[((p.b * a.segs + p.seg) * NP + n) * a.C + p.c];
-    } else if (a.state) {
-#pragma unroll
-      for (int n = 0; n < NP; ++n)
-        if (n < a.N) h[n] = a.state[(p.b * a.C + p.c) * a.N + n];
-    }
+    const int k = w * NS + n;
+    if (a.segs > 1) h[n] = a.carry[((p.b * a.segs + p.seg) * (kW * NS) + k) * a.C + p.c];
+    else if (a.state && k < a.N) h[n] = a.state[(p.b * a.C + p.c) * a.N + k];
   }
   const T* xp = a.x + p.b * a.xb + p.c;
   const T* dp = a.dt + p.b * a.db + p.c;
   const T* zp = a.z ? a.z + p.b * a.zb + p.c : nullptr;
-  const float* pack = a.pack + (p.b * a.G + p.g) * a.L * (2 * NP);
+  const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
   T* op = a.out + p.b * a.L * a.C + p.c;
-  float sum_d = 0.0f;
 
-  T rx[kSub], rd[kSub], rz[kSub];
-  auto fetch = [&](int64_t t) {
+  T rx[kOwn], rd[kOwn], rz[kOwn];
+  auto fetch = [&](int64_t c0) {
 #pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      const int64_t u = t + k < p.t1 ? t + k : p.t1 - 1;
+    for (int k = 0; k < kOwn; ++k) {
+      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
       rx[k] = xp[u * a.xr];
       rd[k] = dp[u * a.dr];
-      if (!kSummary && zp) rz[k] = zp[u * a.zr];
+      if (zp) rz[k] = zp[u * a.zr];
     }
   };
   if (p.t0 < p.t1) fetch(p.t0);
-  for (int64_t t = p.t0; t < p.t1; t += kSub) {
-    float x[kSub], d[kSub], z[kSub];
+  for (int64_t c0 = p.t0; c0 < p.t1; c0 += kS) {
+    float x[kOwn], gate[kOwn];
 #pragma unroll
-    for (int k = 0; k < kSub; ++k) {
+    for (int k = 0; k < kOwn; ++k) {
+      // a token past the end has d = 0, which leaves the states as they are
+      const bool in = c0 + w * kOwn + k < p.t1;
       x[k] = to_f32(rx[k]);
-      d[k] = to_f32(rd[k]);
-      if (!kSummary && zp) z[k] = to_f32(rz[k]);
-    }
-    if (t + kSub < p.t1) fetch(t + kSub);
-    if constexpr (!kSummary) {
-      if (a.saved && t % kScanSave == 0 && p.live) {
-        float* s = a.saved + (p.b * a.chunks + t / kScanSave) * NP * a.C + p.c;
-#pragma unroll
-        for (int n = 0; n < NP; ++n) s[n * a.C] = h[n];
+      const float d = in ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
+      sd[w * kOwn + k][lane] = d;
+      sx[w * kOwn + k][lane] = in ? d * x[k] : 0.0f;
+      gate[k] = 1.0f;
+      if (zp) {
+        const float z = to_f32(rz[k]);
+        gate[k] = z * sigmoid_f32(z);
       }
     }
+    if (a.saved && p.live) {
+      float* s = a.saved + ((p.b * a.chunks + c0 / kS) * (kW * NS) + w * NS) * a.C + p.c;
 #pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      if (t + k < p.t1) {
-        float Bt[NP], Ct[NP];
-        load_bc<NP>(pack, t + k, Bt, Ct);
-        const float dk = step_size(a, d[k], bias), dx = dk * x[k];
-        float y = Dc * x[k];
+      for (int n = 0; n < NS; ++n) s[n * a.C] = h[n];
+    }
+    lds_barrier();
+    if (c0 + kS < p.t1) fetch(c0 + kS);
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          const float e = __builtin_amdgcn_exp2f(dk * A2[n]);
-          h[n] = __builtin_fmaf(e, h[n], dx * Bt[n]);
-          if constexpr (!kSummary) y = __builtin_fmaf(Ct[n], h[n], y);
-        }
-        if constexpr (kSummary) {
-          sum_d += dk;
-        } else {
-          if (zp) y *= z[k] * sigmoid_f32(z[k]);
-          if (p.live) Store<T>::put(op, (t + k) * a.C, y);
-        }
+    for (int k = 0; k < kS; ++k) {
+      float Bt[NS], Ct[NS];
+      load_bc<NS>(pack, c0 + k, Bt, Ct);
+      const float d = sd[k][lane], dx = sx[k][lane];
+      float y = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+        h[n] = __builtin_fmaf(e, h[n], dx * Bt[n]);
+        y = __builtin_fmaf(Ct[n], h[n], y);
       }
+      sy[w][k][lane] = y;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int64_t t = c0 + w * kOwn + k;
+      float y = Dc * x[k];
+#pragma unroll
+      for (int q = 0; q < kW; ++q) y += sy[q][w * kOwn + k][lane];
+      if (p.live && t < p.t1) Store<T>::put(op, t * a.C, y * gate[k]);
     }
   }
   if (!p.live) return;
-  if constexpr (kSummary) {
-    a.sum_d[(p.b * a.segs + p.seg) * a.C + p.c] = sum_d;
+  for (int64_t t = (p.t1 > p.t0 ? p.t1 : p.t0) + w; t < p.end; t += kW) Store<T>::put(op, t * a.C, 0.0f);
+  if (a.segs == 1 && a.state_out) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) a.carry[((p.b * a.segs + p.seg) * NP + n) * a.C + p.c] = h[n];
-  } else {
-    // padding of this segment
-    const int64_t end = p.seg + 1 == a.segs ? a.L : (p.seg + 1) * a.segChunks * kScanSave;
-    for (int64_t t = p.t1 > p.t0 ? p.t1 : p.t0; t < end; ++t) Store<T>::put(op, t * a.C, 0.0f);
-    if (a.segs == 1 && a.state_out) {
+    for (int n = 0; n < NS; ++n)
+      if (w * NS + n < a.N) a.state_out[(p.b * a.C + p.c) * a.N + w * NS + n] = h[n];
+  }
+}
+
+// First pass over a segment: its end state from zero and its sum of d
+// (kReverse false), or, from its last token back, the g that it hands to the
+// segment before it, from zero behind it (kReverse true).
+template <typename T, int NS, bool kReverse>
+__global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
+  // d, and d x (forward) or grad_out silu(z) (reverse); two chunks' worth, so
+  // that one barrier per chunk is enough
+  __shared__ float sd[2][kS][64], sx[2][kS][64];
+  __shared__ float sum[kW][64];
+  const Place<T> p = place(a);
+  const int lane = p.lane, w = p.w;
+  const float bias = a.bias ? a.bias[p.c] : 0.0f;
+  float A2[NS], h[NS], sum_d = 0.0f;
+  load_A(a, p, A2);
 #pragma unroll
-      for (int n = 0; n < NP; ++n)
-        if (n < a.N) a.state_out[(p.b * a.C + p.c) * a.N + n] = h[n];
+  for (int n = 0; n < NS; ++n) h[n] = 0.0f;
+  const T* dp = a.dt + p.b * a.db + p.c;
+  const T* xp = kReverse ? a.gy + p.b * a.gb + p.c : a.x + p.b * a.xb + p.c;
+  const int64_t xr = kReverse ? a.gr : a.xr;
+  const T* zp = kReverse && a.z ? a.z + p.b * a.zb + p.c : nullptr;
+  const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
+  T rx[kOwn], rd[kOwn], rz[kOwn];
+  auto fetch = [&](int64_t c0) {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
+      rx[k] = xp[u * xr];
+      rd[k] = dp[u * a.dr];
+      if (zp) rz[k] = zp[u * a.zr];
+    }
+  };
+  const int64_t chunks = p.t1 > p.t0 ? (p.t1 - p.t0 + kS - 1) / kS : 0;
+  auto start = [&](int64_t i) { return p.t0 + (kReverse ? chunks - 1 - i : i) * kS; };
+  if (chunks > 0) fetch(start(0));
+  for (int64_t i = 0; i < chunks; ++i) {
+    const int64_t c0 = start(i);
+    const int buf = i & 1;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const bool in = c0 + w * kOwn + k < p.t1;
+      const float d = in ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
+      float v = to_f32(rx[k]);
+      if constexpr (kReverse) {
+        if (zp) {
+          const float z = to_f32(rz[k]);
+          v *= z * sigmoid_f32(z);
+        }
+      } else {
+        v *= d;
+      }
+      sum_d += d;
+      sd[buf][w * kOwn + k][lane] = d;
+      sx[buf][w * kOwn + k][lane] = in ? v : 0.0f;
+    }
+    lds_barrier();
+    if (i + 1 < chunks) fetch(start(i + 1));
+#pragma unroll
+    for (int j = 0; j < kS; ++j) {
+      const int k = kReverse ? kS - 1 - j : j;
+      float Bt[NS], Ct[NS];
+      load_bc<NS>(pack, c0 + k, Bt, Ct);
+      const float d = sd[buf][k][lane], v = sx[buf][k][lane];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+        if constexpr (kReverse) h[n] = e * __builtin_fmaf(Ct[n], v, h[n]);
+        else h[n] = __builtin_fmaf(e, h[n], v * Bt[n]);
+      }
     }
   }
+  sum[w][lane] = sum_d;
+  __syncthreads();
+  if (!p.live) return;
+  const int64_t s = p.b * a.segs + p.seg;
+  if (w == 0) a.sum_d[s * a.C + p.c] = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) a.carry[(s * (kW * NS) + w * NS + n) * a.C + p.c] = h[n];
 }
 
 // Carries over the segments of one (entry, state): carry holds the segments'
@@ -277,7 +362,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanP<T> a) {
       for (int k = 0; k < 4; ++k) h[k] = a.state[si + k];
     }
   }
-  if (a.saved && live) {   // the state before token 0; the launch covers all padded states
+  if (a.saved && live) {   // the state before token 0, padding states (zeros) included
 #pragma unroll
     for (int k = 0; k < 4; ++k) a.saved[(b * 4 * P + n0 + k) * a.C + c] = h[k];
   }
@@ -319,332 +404,289 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanP<T> a) {
 }
 
 // ---- backward ---------------------------------------------------------------
-// the segment's g from zero behind it, and its sum of d
-template <typename T, int NP>
-__global__ __launch_bounds__(64) void scan_adj_kernel(ScanP<T> a) {
-  const Place<T> p = place(a);
-  const float bias = a.bias ? a.bias[p.c] : 0.0f;
-  float A2[NP], g[NP];
+// Sums each of M values over the wavefront's 64 lanes by halving: while more
+// than one value is left, a step joins two values into one register, each
+// half of the lanes keeping one of them, so M values take about 2 M + 6
+// operations instead of 6 M. Lane l ends with value wave_sum_index<M>(l).
+template <int D> __device__ __forceinline__ float partner_add(float a, float b) {
+  // a + the value of b in the partner lane, for partners within 16 lanes
+  constexpr int ctrl = D == 8 ? 0x128 : (D == 4 ? 0x141 : (D == 2 ? 0x4e : 0xb1));   // ror 8, half mirror, quads
+  return a + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(b), ctrl, 0xf, 0xf, true));
+}
+template <int M, int D> __device__ __forceinline__ void wave_halve(float (&v)[M], int count, int lane) {
+  // `count` (a compile-time constant after unrolling) values are left
+  if (count > 1) {
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    A2[n] = n < a.N ? a.A[p.c * a.N + n] * kLog2e : 0.0f;
-    g[n] = 0.0f;
-  }
-  const T* dp = a.dt + p.b * a.db + p.c;
-  const T* zp = a.z ? a.z + p.b * a.zb + p.c : nullptr;
-  const T* gp = a.gy + p.b * a.gb + p.c;
-  const float* pack = a.pack + (p.b * a.G + p.g) * a.L * (2 * NP);
-  float sum_d = 0.0f;
-  T rd[kSub], rz[kSub], rg[kSub];
-  auto fetch = [&](int64_t t) {   // tokens t, t - 1, ...
-#pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      const int64_t u = t - k > p.t0 ? t - k : p.t0;
-      rd[k] = dp[u * a.dr];
-      rg[k] = gp[u * a.gr];
-      if (zp) rz[k] = zp[u * a.zr];
-    }
-  };
-  if (p.t0 < p.t1) fetch(p.t1 - 1);
-  for (int64_t t = p.t1 - 1; t >= p.t0; t -= kSub) {
-    float d[kSub], z[kSub], gy[kSub];
-#pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      d[k] = to_f32(rd[k]);
-      gy[k] = to_f32(rg[k]);
-      if (zp) z[k] = to_f32(rz[k]);
-    }
-    if (t - kSub >= p.t0) fetch(t - kSub);
-#pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      if (t - k >= p.t0) {
-        float Bt[NP], Ct[NP];
-        load_bc<NP>(pack, t - k, Bt, Ct);
-        const float dk = step_size(a, d[k], bias);
-        const float gz = zp ? gy[k] * (z[k] * sigmoid_f32(z[k])) : gy[k];
-        sum_d += dk;
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-          g[n] = __builtin_amdgcn_exp2f(dk * A2[n]) * __builtin_fmaf(Ct[n], gz, g[n]);
+    for (int i = 0; i < M / 2; ++i) {
+      if (i < count / 2) {
+        const int k = i + count / 2;
+        if constexpr (D == 32 || D == 16) {
+          const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[k < M ? k : 0]), false, false)
+                                 : __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[k < M ? k : 0]), false, false);
+          v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        } else {
+          const bool hi = lane & D;
+          const float o = v[k < M ? k : 0];
+          v[i] = partner_add<D>(hi ? o : v[i], hi ? v[i] : o);
+        }
       }
     }
+  } else if constexpr (D == 32 || D == 16) {
+    const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(__float_as_uint(v[0]), __float_as_uint(v[0]), false, false)
+                           : __builtin_amdgcn_permlane16_swap(__float_as_uint(v[0]), __float_as_uint(v[0]), false, false);
+    v[0] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  } else {
+    v[0] = partner_add<D>(v[0], v[0]);
   }
-  if (!p.live) return;
-  a.sum_d[(p.b * a.segs + p.seg) * a.C + p.c] = sum_d;
-#pragma unroll
-  for (int n = 0; n < NP; ++n) a.carry[((p.b * a.segs + p.seg) * NP + n) * a.C + p.c] = g[n];
-}
-
-// Sums each of M values over the wavefront's 64 lanes by halving: a step
-// joins two values into one register, each half of the lanes keeping one of
-// them, so M values take about 2 M operations instead of 6 M. Lane l ends
-// with value wave_sum_index<M>(l).
-__device__ __forceinline__ float dpp_add(float a, float b, int which) {
-  // a + the value of b in the partner lane
-  int m;
-  switch (which) {
-    case 8: m = __builtin_amdgcn_update_dpp(0, __float_as_int(b), 0x128, 0xf, 0xf, true); break;   // row_ror:8
-    case 4: m = __builtin_amdgcn_update_dpp(0, __float_as_int(b), 0x141, 0xf, 0xf, true); break;   // half mirror
-    case 2: m = __builtin_amdgcn_update_dpp(0, __float_as_int(b), 0x4e, 0xf, 0xf, true); break;    // quad 2 3 0 1
-    default: m = __builtin_amdgcn_update_dpp(0, __float_as_int(b), 0xb1, 0xf, 0xf, true); break;   // quad 1 0 3 2
-  }
-  return a + __int_as_float(m);
 }
 template <int M> __device__ __forceinline__ float wave_sum(float (&v)[M], int lane) {
-  static_assert(M == 16 || M == 32 || M == 64, "");
-#pragma unroll
-  for (int i = 0; i < M / 2; ++i) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + M / 2]), false, false);
-    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < M / 4; ++i) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + M / 4]), false, false);
-    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < M / 8; ++i) {
-    const bool hi = lane & 8;
-    v[i] = dpp_add(hi ? v[i + M / 8] : v[i], hi ? v[i] : v[i + M / 8], 8);
-  }
-#pragma unroll
-  for (int i = 0; i < M / 16; ++i) {
-    const bool hi = lane & 4;
-    v[i] = dpp_add(hi ? v[i + M / 16] : v[i], hi ? v[i] : v[i + M / 16], 4);
-  }
-  if constexpr (M >= 32) {
-#pragma unroll
-    for (int i = 0; i < M / 32; ++i) {
-      const bool hi = lane & 2;
-      v[i] = dpp_add(hi ? v[i + M / 32] : v[i], hi ? v[i] : v[i + M / 32], 2);
-    }
-  } else {
-    v[0] = dpp_add(v[0], v[0], 2);
-  }
-  if constexpr (M >= 64) {
-    const bool hi = lane & 1;
-    v[0] = dpp_add(hi ? v[1] : v[0], hi ? v[0] : v[1], 1);
-  } else {
-    v[0] = dpp_add(v[0], v[0], 1);
-  }
+  static_assert(M == 2 || M == 4 || M == 8 || M == 16, "");
+  wave_halve<M, 32>(v, M, lane);
+  wave_halve<M, 16>(v, M / 2, lane);
+  wave_halve<M, 8>(v, M / 4, lane);
+  wave_halve<M, 4>(v, M / 8, lane);
+  wave_halve<M, 2>(v, M / 16, lane);
+  wave_halve<M, 1>(v, M / 32, lane);
   return v[0];
 }
 template <int M> __device__ __forceinline__ int wave_sum_index(int lane) {
-  int i = (lane & 32 ? M / 2 : 0) + (lane & 16 ? M / 4 : 0) + (lane & 8 ? M / 8 : 0) +
-          (lane & 4 ? M / 16 : 0);
-  if (M >= 32) i += lane & 2 ? M / 32 : 0;
-  if (M >= 64) i += lane & 1;
+  int i = 0, left = M;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) {
+    if (left > 1) {
+      left /= 2;
+      i += lane & d ? left : 0;
+    }
+  }
   return i;
 }
 
 // The backward pass of one segment, from its last token to its first, given
-// g carried in from behind it. Chunks of kScanSave tokens start from their
-// saved state: a walk forward leaves the state before each block of TS
-// tokens in LDS, then the blocks are taken in reverse, each recomputing its
-// states into registers before walking back over them.
-template <typename T, int NP, int TS>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanP<T> a) {
-  constexpr int kBlocks = kScanSave / TS;
-  __shared__ float mid[kBlocks - 1][NP][64];
+// g carried in from behind it, 16 tokens at a time: each wavefront prepares
+// four tokens, runs its states forward from the saved ones (states and decays
+// stay in registers; with eight states per wavefront the decays are computed
+// again), walks back over them, and finishes four tokens.
+template <typename T, int NS>
+__global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
+  constexpr bool kKeep = NS <= 4;    // decays kept: 16 NS registers
+  __shared__ float sd[kS][64], sx[kS][64], sg[kS][64];                    // d, d x, gy
+  __shared__ float sy[kW][kS][64], su[kW][kS][64], sv[kW][kS][64];        // partial y, sum g B, sum A m
   const Place<T> p = place(a);
-  const int lane = threadIdx.x;
+  const int lane = p.lane, w = p.w;
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
-  float A2[NP], g[NP], dA[NP], dD = 0.0f, dbias = 0.0f;
+  float A2[NS], g[NS], dA[NS], dD = 0.0f, dbias = 0.0f;
+  load_A(a, p, A2);
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    A2[n] = n < a.N ? a.A[p.c * a.N + n] * kLog2e : 0.0f;
+  for (int n = 0; n < NS; ++n) {
+    const int k = w * NS + n;
     dA[n] = 0.0f;
     g[n] = 0.0f;
-  }
-  if (a.segs > 1) {
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-      if (n < a.N) g[n] = a.carry[((p.b * a.segs + p.seg) * NP + n) * a.C + p.c];
-  } else if (a.gstate) {
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-      if (n < a.N) g[n] = a.gstate[(p.b * a.C + p.c) * a.N + n];
+    if (k < a.N) {
+      if (a.segs > 1) g[n] = a.carry[((p.b * a.segs + p.seg) * (kW * NS) + k) * a.C + p.c];
+      else if (a.gstate) g[n] = a.gstate[(p.b * a.C + p.c) * a.N + k];
+    }
   }
   const T* xp = a.x + p.b * a.xb + p.c;
   const T* dp = a.dt + p.b * a.db + p.c;
   const T* zp = a.z ? a.z + p.b * a.zb + p.c : nullptr;
   const T* gp = a.gy + p.b * a.gb + p.c;
   const int64_t row0 = p.b * a.L * a.C + p.c;
-  const float* pack = a.pack + (p.b * a.G + p.g) * a.L * (2 * NP);
-  float* part = a.partBC + ((p.b * a.G + p.g) * a.tiles + p.tile) * a.L * (2 * NP);
-  const int slot = wave_sum_index<2 * NP>(lane);
-  const bool writer = (lane & (NP == 8 ? 3 : NP == 16 ? 1 : 0)) == 0;
+  const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
+  float* part = a.partBC + (((p.b * a.G + p.g) * a.tiles + p.tile) * a.Lp * kW + w) * (2 * NS);
+  const int slot = wave_sum_index<2 * NS>(lane);
+  // one of the lanes that end with the same value stores it
+  const bool writer = (lane & (64 / (2 * NS) - 1)) == 0;
 
-  // padding of this segment
-  {
-    const int64_t end = p.seg + 1 == a.segs ? a.L : (p.seg + 1) * a.segChunks * kScanSave;
-    for (int64_t t = p.t1 > p.t0 ? p.t1 : p.t0; t < end; ++t) {
-      if (p.live) {
-        Store<T>::put(a.dx, row0 + t * a.C, 0.0f);
-        Store<T>::put(a.ddt, row0 + t * a.C, 0.0f);
-        if (a.dz) Store<T>::put(a.dz, row0 + t * a.C, 0.0f);
-      }
-      if (lane < 2 * NP) part[t * (2 * NP) + lane] = 0.0f;
+  for (int64_t t = (p.t1 > p.t0 ? p.t1 : p.t0) + w; t < p.end; t += kW) {
+    if (p.live) {
+      Store<T>::put(a.dx, row0 + t * a.C, 0.0f);
+      Store<T>::put(a.ddt, row0 + t * a.C, 0.0f);
+      if (a.dz) Store<T>::put(a.dz, row0 + t * a.C, 0.0f);
     }
   }
+  // whole chunks of padding; a chunk that holds a token is written below
+  for (int64_t t = p.t1 > p.t0 ? (p.t1 + kS - 1) / kS * kS : p.t0; t < p.end; ++t)
+    if (lane < 2 * NS) part[t * (kW * 2 * NS) + lane] = 0.0f;
 
-  const int64_t last = p.t1 > p.t0 ? (p.t1 - 1) / kScanSave : -1, first = p.t0 / kScanSave;
-  for (int64_t ck = last; ck >= first; --ck) {
-    const int64_t c0 = ck * kScanSave, c1 = c0 + kScanSave < p.t1 ? c0 + kScanSave : p.t1;
-    const int nb = static_cast<int>((c1 - c0 + TS - 1) / TS);   // blocks of this chunk
-    float h0[NP];
-    {
-      const float* s = a.saved + (p.b * a.chunks + ck) * NP * a.C + p.c;
+  T rx[kOwn], rd[kOwn], rz[kOwn], rg[kOwn];
+  float rh[NS];
+  auto fetch = [&](int64_t c0) {
 #pragma unroll
-      for (int n = 0; n < NP; ++n) h0[n] = s[n * a.C];
+    for (int k = 0; k < kOwn; ++k) {
+      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
+      rx[k] = xp[u * a.xr];
+      rd[k] = dp[u * a.dr];
+      rg[k] = gp[u * a.gr];
+      if (zp) rz[k] = zp[u * a.zr];
     }
-    for (int blk = 0; blk + 1 < nb; ++blk) {
-      const int64_t t = c0 + blk * TS;
+    const float* s = a.saved + ((p.b * a.chunks + c0 / kS) * (kW * NS) + w * NS) * a.C + p.c;
 #pragma unroll
-      for (int n = 0; n < NP; ++n) mid[blk][n][lane] = h0[n];
-      float x[TS], d[TS];
+    for (int n = 0; n < NS; ++n) rh[n] = s[n * a.C];
+  };
+  const int64_t chunks = p.t1 > p.t0 ? (p.t1 - p.t0 + kS - 1) / kS : 0;
+  if (chunks > 0) fetch(p.t0 + (chunks - 1) * kS);
+  for (int64_t i = chunks - 1; i >= 0; --i) {
+    const int64_t c0 = p.t0 + i * kS;
+    float x[kOwn], d[kOwn], slope[kOwn], gz[kOwn], gsl[kOwn];   // gsl: grad_out silu'(z)
 #pragma unroll
-      for (int k = 0; k < TS; ++k) {
-        x[k] = to_f32(xp[(t + k) * a.xr]);
-        d[k] = to_f32(dp[(t + k) * a.dr]);
+    for (int k = 0; k < kOwn; ++k) {
+      const bool in = c0 + w * kOwn + k < p.t1;
+      const float v = to_f32(rd[k]) + bias;
+      x[k] = to_f32(rx[k]);
+      slope[k] = 1.0f;
+      d[k] = a.softplus ? softplus_f32(v, &slope[k]) : v;
+      gz[k] = to_f32(rg[k]);
+      gsl[k] = 0.0f;
+      if (zp) {
+        const float z = to_f32(rz[k]), s = sigmoid_f32(z);
+        gsl[k] = gz[k] * (s * __builtin_fmaf(z, 1.0f - s, 1.0f));
+        gz[k] *= z * s;
       }
-#pragma unroll
-      for (int k = 0; k < TS; ++k) {
-        float Bt[NP], Ct[NP];
-        load_bc<NP>(pack, t + k, Bt, Ct);
-        const float dk = step_size(a, d[k], bias), dx = dk * x[k];
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-          h0[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[n]), h0[n], dx * Bt[n]);
-      }
+      const int r = w * kOwn + k;
+      // idle lanes and tokens past the end add nothing to any sum
+      const bool on = in && p.live;
+      sd[r][lane] = in ? d[k] : 0.0f;
+      sx[r][lane] = on ? d[k] * x[k] : 0.0f;
+      sg[r][lane] = on ? gz[k] : 0.0f;
     }
-    for (int blk = nb - 1; blk >= 0; --blk) {
-      const int64_t t = c0 + blk * TS;
-      if (blk + 1 < nb) {
+    float h[kS + 1][NS], e[kKeep ? kS : 1][NS];
 #pragma unroll
-        for (int n = 0; n < NP; ++n) h0[n] = mid[blk][n][lane];
+    for (int n = 0; n < NS; ++n) h[0][n] = rh[n];
+    lds_barrier();
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      float Bt[NS], Ct[NS];
+      load_bc<NS>(pack, c0 + k, Bt, Ct);
+      const float dk = sd[k][lane], dx = sx[k][lane];
+      float y = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const float f = __builtin_amdgcn_exp2f(dk * A2[n]);
+        if constexpr (kKeep) e[k][n] = f;
+        h[k + 1][n] = __builtin_fmaf(f, h[k][n], dx * Bt[n]);
+        y = __builtin_fmaf(Ct[n], h[k + 1][n], y);
       }
-      float x[TS], raw[TS], d[TS], z[TS], gy[TS], y[TS], h[TS + 1][NP];
+      sy[w][k][lane] = y;
+    }
 #pragma unroll
-      for (int k = 0; k < TS; ++k) {
-        const int64_t u = t + k < c1 ? t + k : c1 - 1;
-        x[k] = to_f32(xp[u * a.xr]);
-        raw[k] = to_f32(dp[u * a.dr]) + bias;
-        gy[k] = to_f32(gp[u * a.gr]);
-        z[k] = zp ? to_f32(zp[u * a.zr]) : 0.0f;
-        y[k] = Dc * x[k];
+    for (int k = kS - 1; k >= 0; --k) {
+      // the chunk before: late enough that half of the states are done with
+      if (k == kS / 2 && i > 0) fetch(c0 - kS);
+      float Bt[NS], Ct[NS], bc[2 * NS];
+      load_bc<NS>(pack, c0 + k, Bt, Ct);
+      const float dk = sd[k][lane], dx = sx[k][lane], gk = sg[k][lane];
+      float du = 0.0f, dd = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        g[n] = __builtin_fmaf(Ct[n], gk, g[n]);
+        const float back = g[n] * (kKeep ? e[kKeep ? k : 0][n] : __builtin_amdgcn_exp2f(dk * A2[n]));
+        const float m = back * h[k][n];
+        du = __builtin_fmaf(g[n], Bt[n], du);
+        dd = __builtin_fmaf(m, A2[n], dd);
+        dA[n] = __builtin_fmaf(m, dk, dA[n]);
+        bc[n] = dx * g[n];
+        bc[NS + n] = gk * h[k + 1][n];
+        g[n] = back;
       }
+      su[w][k][lane] = du;
+      sv[w][k][lane] = dd;
+      const float s = wave_sum<2 * NS>(bc, lane);
+      if (writer) part[(c0 + k) * (kW * 2 * NS) + slot] = s;
+    }
+    lds_barrier();
 #pragma unroll
-      for (int n = 0; n < NP; ++n) h[0][n] = h0[n];
+    for (int k = 0; k < kOwn; ++k) {
+      const int r = w * kOwn + k;
+      const int64_t t = c0 + r;
+      float y = Dc * x[k], du = 0.0f, dd = 0.0f;
 #pragma unroll
-      for (int k = 0; k < TS; ++k) {
-        d[k] = a.softplus ? softplus_f32(raw[k]) : raw[k];
-        if (t + k < c1) {
-          float Bt[NP], Ct[NP];
-          load_bc<NP>(pack, t + k, Bt, Ct);
-          const float dx = d[k] * x[k];
-#pragma unroll
-          for (int n = 0; n < NP; ++n) {
-            h[k + 1][n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[k] * A2[n]), h[k][n], dx * Bt[n]);
-            y[k] = __builtin_fmaf(Ct[n], h[k + 1][n], y[k]);
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < NP; ++n) h[k + 1][n] = h[k][n];
-        }
+      for (int q = 0; q < kW; ++q) {
+        y += sy[q][r][lane];
+        du += su[q][r][lane];
+        dd += sv[q][r][lane];
       }
-#pragma unroll
-      for (int k = TS - 1; k >= 0; --k) {
-        if (t + k < c1) {
-          float Bt[NP], Ct[NP];
-          load_bc<NP>(pack, t + k, Bt, Ct);
-          float gz = gy[k];
-          if (zp) {
-            const float sg = sigmoid_f32(z[k]);
-            gz = gy[k] * (z[k] * sg);
-            if (p.live)
-              Store<T>::put(a.dz, row0 + (t + k) * a.C,
-                            gy[k] * y[k] * (sg * __builtin_fmaf(z[k], 1.0f - sg, 1.0f)));
-          }
-          const float dx = d[k] * x[k];
-          float du = 0.0f, dd = 0.0f, bc[2 * NP];
-#pragma unroll
-          for (int n = 0; n < NP; ++n) {
-            g[n] = __builtin_fmaf(Ct[n], gz, g[n]);
-            const float back = g[n] * __builtin_amdgcn_exp2f(d[k] * A2[n]);
-            const float m = back * h[k][n];
-            du = __builtin_fmaf(g[n], Bt[n], du);
-            dd = __builtin_fmaf(m, A2[n], dd);
-            dA[n] = __builtin_fmaf(m, d[k], dA[n]);
-            bc[n] = p.live ? dx * g[n] : 0.0f;
-            bc[NP + n] = p.live ? gz * h[k + 1][n] : 0.0f;
-            g[n] = back;
-          }
-          float ddt = __builtin_fmaf(x[k], du, dd * kLn2);
-          if (a.softplus) ddt *= sigmoid_f32(raw[k]);
-          dbias += ddt;
-          dD = __builtin_fmaf(gz, x[k], dD);
-          if (p.live) {
-            Store<T>::put(a.dx, row0 + (t + k) * a.C, __builtin_fmaf(Dc, gz, d[k] * du));
-            Store<T>::put(a.ddt, row0 + (t + k) * a.C, ddt);
-          }
-          const float s = wave_sum<2 * NP>(bc, lane);
-          if (writer) part[(t + k) * (2 * NP) + slot] = s;
+      if (t < p.t1) {
+        const float ddt = __builtin_fmaf(x[k], du, dd * kLn2) * slope[k];
+        dbias += ddt;
+        dD = __builtin_fmaf(gz[k], x[k], dD);
+        if (p.live) {
+          Store<T>::put(a.dx, row0 + t * a.C, __builtin_fmaf(Dc, gz[k], d[k] * du));
+          Store<T>::put(a.ddt, row0 + t * a.C, ddt);
+          if (a.dz) Store<T>::put(a.dz, row0 + t * a.C, y * gsl[k]);
         }
       }
     }
   }
+  __syncthreads();
+  sd[w][lane] = dD;
+  sx[w][lane] = dbias;
+  __syncthreads();
   if (!p.live) return;
   const int64_t pi = p.b * a.segs + p.seg;
+  if (w == 0) {
+    a.partD[pi * a.C + p.c] = sd[0][lane] + sd[1][lane] + sd[2][lane] + sd[3][lane];
+    a.partD[(a.B * a.segs + pi) * a.C + p.c] = sx[0][lane] + sx[1][lane] + sx[2][lane] + sx[3][lane];
+  }
 #pragma unroll
-  for (int n = 0; n < NP; ++n)
-    if (n < a.N) a.partA[(pi * a.C + p.c) * a.N + n] = dA[n];
-  a.partD[pi * a.C + p.c] = dD;
-  a.partD[(a.B * a.segs + pi) * a.C + p.c] = dbias;
-  if (a.segs == 1 && a.dstate) {
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-      if (n < a.N) a.dstate[(p.b * a.C + p.c) * a.N + n] = g[n];
+  for (int n = 0; n < NS; ++n) {
+    const int k = w * NS + n;
+    if (k < a.N) {
+      a.partA[(pi * a.C + p.c) * a.N + k] = dA[n];
+      if (a.segs == 1 && a.dstate) a.dstate[(p.b * a.C + p.c) * a.N + k] = g[n];
+    }
   }
 }
 
 // dB, dC: the channel tiles' sums added in tile order
-template <typename T, int NP>
+template <typename T, int NS>
 __global__ __launch_bounds__(256) void reduce_bc_kernel(ScanP<T> a, T* dB, T* dC) {
   int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
-  const int n = static_cast<int>(i % (2 * NP));
-  i /= 2 * NP;
+  const int n = static_cast<int>(i % (kW * 2 * NS));
+  i /= kW * 2 * NS;
   const int64_t t = i % a.L;
   i /= a.L;   // entry and group
   if (i >= a.B * a.G) return;
-  const float* q = a.partBC + (i * a.tiles * a.L + t) * (2 * NP) + n;
+  const float* q = a.partBC + (i * a.tiles * a.Lp + t) * (kW * 2 * NS) + n;
   float s = 0.0f;
-  for (int k = 0; k < a.tiles; ++k) s += q[k * a.L * (2 * NP)];
+  for (int k = 0; k < a.tiles; ++k) s += q[k * a.Lp * (kW * 2 * NS)];
   const int64_t b = i / a.G, g = i - b * a.G;
-  const int m = n % NP;
-  if (m < a.N) Store<T>::put(n < NP ? dB : dC, ((b * a.L + t) * a.G + g) * a.N + m, s);
+  const int m = n / (2 * NS) * NS + n % NS;
+  if (m < a.N) Store<T>::put(n % (2 * NS) < NS ? dB : dC, ((b * a.L + t) * a.G + g) * a.N + m, s);
 }
 
 // ---- host -------------------------------------------------------------------
-int scan_np(int64_t N) { return N <= 8 ? 8 : (N <= 16 ? 16 : 32); }
+// states per wavefront: 1, 2, 4 or 8
+int scan_ns(int64_t N) { return N <= 4 ? 1 : (N <= 8 ? 2 : (N <= 16 ? 4 : 8)); }
+int scan_np(int64_t N) { return kW * scan_ns(N); }
 
 struct Cut {
   int64_t chunks;
   int tiles, segs, segChunks;
 };
-// Segments of the token axis. Cutting doubles the work (the first pass), so
-// it pays when the whole-axis wavefronts would leave more than half of the
-// chip's 4 SIMDs per compute unit idle; then as many segments as give two
-// wavefronts per SIMD, of at least one chunk.
-Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t G) {
+// Segments of the token axis. Cutting adds the first pass, so it pays only
+// where whole-axis workgroups would leave compute units idle or unevenly
+// loaded: the estimate is, for each number of segments, the workgroups of the
+// fullest compute unit times a workgroup's tokens times the cycles per token
+// (per state 25 forward, 70 backward, 21 in the first pass, and what does not
+// depend on the states), a quarter more where a compute unit has one
+// workgroup only, and the two extra launches.
+Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
   Cut k;
-  k.chunks = std::max<int64_t>(1, cdiv(L, kScanSave));
+  k.chunks = std::max<int64_t>(1, cdiv(L, kS));
   k.tiles = static_cast<int>(cdiv(C / G, 64));
-  const int64_t waves = std::max<int64_t>(1, B * G * k.tiles), simds = 1024;
+  const int64_t groups = std::max<int64_t>(1, B * G * k.tiles);
+  const double ns = scan_ns(N), full = bwd ? 70 * ns + 150 : 25 * ns + 50, first = 21 * ns + 30;
+  double best = 0;
   k.segChunks = static_cast<int>(k.chunks);
-  if (waves < simds / 2) {
-    const int64_t want = std::min<int64_t>(k.chunks, cdiv(2 * simds, waves));
-    k.segChunks = static_cast<int>(cdiv(k.chunks, want));
+  for (int64_t s = 1; s <= std::min<int64_t>(k.chunks, 128); ++s) {
+    const int64_t each = cdiv(k.chunks, s), segs = cdiv(k.chunks, each), per = cdiv(groups * segs, 256);
+    const double cost = per * each * kS * (full + (segs > 1 ? first : 0.0)) * (1.0 + 0.25 / per) +
+                        (segs > 1 ? 20000.0 + 40.0 * segs : 0.0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      k.segChunks = static_cast<int>(each);
+    }
+    if (per >= 16) break;
   }
   k.segs = static_cast<int>(cdiv(k.chunks, k.segChunks));
   return k;
@@ -656,30 +698,31 @@ struct Space {
 Space scan_space(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
   Space s{};
   if (!bwd && L <= kStepMax) return s;
-  const Cut k = cut_scan(B, L, C, G);
-  const int64_t np = scan_np(N);
+  const Cut f = cut_scan(B, L, C, N, G, false), k = cut_scan(B, L, C, N, G, true);
+  const int64_t np = scan_np(N), Lp = k.chunks * kS;
   size_t at = 0;
   auto take = [&](int64_t floats) {
     const size_t here = at;
     at += up256(static_cast<size_t>(floats) * sizeof(float));
     return here;
   };
-  s.pack = take(B * G * L * 2 * np);
-  if (k.segs > 1) {
-    s.sum_d = take(B * k.segs * C);
-    s.carry = take(B * k.segs * np * C);
+  const int64_t segs = bwd ? std::max(f.segs, k.segs) : f.segs;
+  s.pack = take(B * G * Lp * 2 * np);
+  if (segs > 1) {
+    s.sum_d = take(B * segs * C);
+    s.carry = take(B * segs * np * C);
   }
   if (bwd) {
     s.saved = take(B * k.chunks * np * C);   // used when the caller kept none
     s.partA = take(B * k.segs * C * N);
     s.partD = take(2 * B * k.segs * C);
-    s.partBC = take(B * G * k.tiles * L * 2 * np);
+    s.partBC = take(B * G * k.tiles * Lp * 2 * np);
   }
   s.total = at;
   return s;
 }
 
-template <typename T> ScanP<T> scan_params(const gspn_scan_args& a) {
+template <typename T> ScanP<T> scan_params(const gspn_scan_args& a, bool bwd) {
   ScanP<T> p{};
   p.x = static_cast<const T*>(a.x.p); p.xb = a.x.batch; p.xr = a.x.row;
   p.dt = static_cast<const T*>(a.dt.p); p.db = a.dt.batch; p.dr = a.dt.row;
@@ -693,8 +736,9 @@ template <typename T> ScanP<T> scan_params(const gspn_scan_args& a) {
   p.B = a.B; p.L = a.L; p.C = a.C; p.G = a.G; p.Cg = a.C / a.G;
   p.N = static_cast<int>(a.N);
   p.softplus = a.softplus;
-  const Cut k = cut_scan(a.B, a.L, a.C, a.G);
+  const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, bwd);
   p.chunks = k.chunks; p.tiles = k.tiles; p.segs = k.segs; p.segChunks = k.segChunks;
+  p.Lp = k.chunks * kS;
   return p;
 }
 
@@ -711,34 +755,39 @@ float* at_bytes(void* ws, size_t off) { return reinterpret_cast<float*>(static_c
   } while (0)
 
 // the forward passes over whole prompts; p.saved set: states are kept
-template <typename T, int NP>
+template <typename T, int NS>
 hipError_t scan_passes(const ScanP<T>& p, hipStream_t stream, Tracer* tr) {
   const int64_t grid = p.B * p.segs * p.G * p.tiles;
   if (p.segs > 1) {
-    GSPN_LAUNCH("scan_summary", p.B, (scan_fwd_kernel<T, NP, true>), grid, 64, p);
-    GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, NP, false>), p.B * p.N * cdiv(p.C, 64), 64, p,
+    GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, false>), grid, kThreads, p);
+    GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, kW * NS, false>), p.B * p.N * cdiv(p.C, 64), 64, p,
                 p.state, p.state_out);
   }
-  GSPN_LAUNCH("scan_fwd", p.B, (scan_fwd_kernel<T, NP, false>), grid, 64, p);
+  GSPN_LAUNCH("scan_fwd", p.B, (scan_fwd_kernel<T, NS>), grid, kThreads, p);
   return hipSuccess;
 }
 
-template <typename T, int NP>
-hipError_t scan_fwd_np(const gspn_scan_args& a, void* ws, hipStream_t stream, Tracer* tr) {
-  ScanP<T> p = scan_params<T>(a);
+template <typename T, int NS> hipError_t run_pack(const ScanP<T>& p, hipStream_t stream, Tracer* tr) {
+  GSPN_LAUNCH("scan_pack", p.B, (pack_kernel<T, NS>), cdiv(p.B * p.G * p.Lp * kW * 2 * NS, 256), 256, p);
+  return hipSuccess;
+}
+
+template <typename T, int NS>
+hipError_t scan_fwd_ns(const gspn_scan_args& a, void* ws, hipStream_t stream, Tracer* tr) {
+  ScanP<T> p = scan_params<T>(a, false);
   const Space s = scan_space(a.B, a.L, a.C, a.N, a.G, false);
   p.pack = at_bytes(ws, s.pack);
   p.sum_d = at_bytes(ws, s.sum_d);
   p.carry = at_bytes(ws, s.carry);
-  GSPN_LAUNCH("scan_pack", p.B, (pack_kernel<T, NP>), cdiv(p.B * p.G * p.L * 2 * NP, 256), 256, p);
-  return scan_passes<T, NP>(p, stream, tr);
+  const hipError_t e = run_pack<T, NS>(p, stream, tr);
+  return e != hipSuccess ? e : scan_passes<T, NS>(p, stream, tr);
 }
 
 template <typename T>
 hipError_t scan_fwd_dt(const gspn_scan_args& a, void* ws, hipStream_t stream, Tracer* tr) {
   if (a.L <= kStepMax) {
-    const ScanP<T> p = scan_params<T>(a);
-    const int lanes = a.N <= 4 && !a.saved ? 1 : scan_np(a.N) / 4;
+    const ScanP<T> p = scan_params<T>(a, false);
+    const int lanes = scan_np(a.N) / 4;
     const int64_t grid = a.B * cdiv(a.C, 256 / lanes);
     switch (lanes) {
       case 1: GSPN_LAUNCH("scan_step", a.B, (scan_step_kernel<T, 1>), grid, 256, p); break;
@@ -748,17 +797,18 @@ hipError_t scan_fwd_dt(const gspn_scan_args& a, void* ws, hipStream_t stream, Tr
     }
     return hipSuccess;
   }
-  switch (scan_np(a.N)) {
-    case 8: return scan_fwd_np<T, 8>(a, ws, stream, tr);
-    case 16: return scan_fwd_np<T, 16>(a, ws, stream, tr);
-    default: return scan_fwd_np<T, 32>(a, ws, stream, tr);
+  switch (scan_ns(a.N)) {
+    case 1: return scan_fwd_ns<T, 1>(a, ws, stream, tr);
+    case 2: return scan_fwd_ns<T, 2>(a, ws, stream, tr);
+    case 4: return scan_fwd_ns<T, 4>(a, ws, stream, tr);
+    default: return scan_fwd_ns<T, 8>(a, ws, stream, tr);
   }
 }
 
-template <typename T, int NP>
-hipError_t scan_bwd_np(const gspn_scan_args& a, const gspn_scan_grads& g, void* ws,
+template <typename T, int NS>
+hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* ws,
                        hipStream_t stream, Tracer* tr) {
-  ScanP<T> p = scan_params<T>(a);
+  ScanP<T> p = scan_params<T>(a, true);
   const Space s = scan_space(a.B, a.L, a.C, a.N, a.G, true);
   p.pack = at_bytes(ws, s.pack);
   p.sum_d = at_bytes(ws, s.sum_d);
@@ -772,35 +822,38 @@ hipError_t scan_bwd_np(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
   p.ddt = static_cast<T*>(g.dt);
   p.dz = static_cast<T*>(g.z);
   p.dstate = g.state;
-  const bool any = p.B > 0 && p.L > 0;
   const int64_t grid = p.B * p.segs * p.G * p.tiles;
-  if (any) {
-    GSPN_LAUNCH("scan_pack", p.B, (pack_kernel<T, NP>), cdiv(p.B * p.G * p.L * 2 * NP, 256), 256, p);
-    if (!p.saved) {
-      // find the states again: the forward passes, their output into dx
-      // (written again below)
-      ScanP<T> f = p;
-      f.saved = p.saved = at_bytes(ws, s.saved);
-      f.out = p.dx;
-      f.z = nullptr;
-      f.state_out = nullptr;
-      const hipError_t e = scan_passes<T, NP>(f, stream, tr);
-      if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (p.B > 0) {
+    if (p.L > 0) {
+      if ((e = run_pack<T, NS>(p, stream, tr)) != hipSuccess) return e;
+      if (!p.saved) {
+        // find the states again: the forward passes, their output into dx
+        // (written again below)
+        ScanP<T> f = p;
+        const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, false);
+        f.segs = k.segs;
+        f.segChunks = k.segChunks;
+        f.saved = p.saved = at_bytes(ws, s.saved);
+        f.out = p.dx;
+        f.z = nullptr;
+        f.state_out = nullptr;
+        if ((e = scan_passes<T, NS>(f, stream, tr)) != hipSuccess) return e;
+      }
+      if (p.segs > 1) {
+        GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, true>), grid, kThreads, p);
+        GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, kW * NS, true>), p.B * p.N * cdiv(p.C, 64), 64, p,
+                    p.gstate, p.dstate);
+      }
     }
-    if (p.segs > 1) {
-      GSPN_LAUNCH("scan_adjoint", p.B, (scan_adj_kernel<T, NP>), grid, 64, p);
-      GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, NP, true>), p.B * p.N * cdiv(p.C, 64), 64, p,
-                  p.gstate, p.dstate);
-    }
+    GSPN_LAUNCH("scan_bwd", p.B, (scan_bwd_kernel<T, NS>), grid, kThreads, p);
+    if (p.L > 0)
+      GSPN_LAUNCH("scan_reduce_bc", p.B, (reduce_bc_kernel<T, NS>),
+                  cdiv(p.B * p.G * p.L * kW * 2 * NS, 256), 256, p, static_cast<T*>(g.Bm),
+                  static_cast<T*>(g.Cm));
   }
-  if (p.B > 0)
-    GSPN_LAUNCH("scan_bwd", p.B, (scan_bwd_kernel<T, NP, NP == 32 ? 4 : 8>), grid, 64, p);
-  if (any)
-    GSPN_LAUNCH("scan_reduce_bc", p.B, (reduce_bc_kernel<T, NP>),
-                cdiv(p.B * p.G * p.L * 2 * NP, 256), 256, p, static_cast<T*>(g.Bm),
-                static_cast<T*>(g.Cm));
   const int64_t rows = p.B * p.segs;
-  hipError_t e = reduce_rows<float>(p.partA, rows, p.C * p.N, g.A, stream, tr);
+  e = reduce_rows<float>(p.partA, rows, p.C * p.N, g.A, stream, tr);
   if (e == hipSuccess && g.D) e = reduce_rows<float>(p.partD, rows, p.C, g.D, stream, tr);
   if (e == hipSuccess && g.dt_bias)
     e = reduce_rows<float>(p.partD + rows * p.C, rows, p.C, g.dt_bias, stream, tr);
@@ -810,17 +863,18 @@ hipError_t scan_bwd_np(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
 template <typename T>
 hipError_t scan_bwd_dt(const gspn_scan_args& a, const gspn_scan_grads& g, void* ws,
                        hipStream_t stream, Tracer* tr) {
-  switch (scan_np(a.N)) {
-    case 8: return scan_bwd_np<T, 8>(a, g, ws, stream, tr);
-    case 16: return scan_bwd_np<T, 16>(a, g, ws, stream, tr);
-    default: return scan_bwd_np<T, 32>(a, g, ws, stream, tr);
+  switch (scan_ns(a.N)) {
+    case 1: return scan_bwd_ns<T, 1>(a, g, ws, stream, tr);
+    case 2: return scan_bwd_ns<T, 2>(a, g, ws, stream, tr);
+    case 4: return scan_bwd_ns<T, 4>(a, g, ws, stream, tr);
+    default: return scan_bwd_ns<T, 8>(a, g, ws, stream, tr);
   }
 }
 
 }  // namespace
 
 size_t scan_saved_bytes(int64_t B, int64_t L, int64_t C, int64_t N) {
-  return static_cast<size_t>(B * std::max<int64_t>(1, cdiv(L, kScanSave)) * scan_np(N) * C) *
+  return static_cast<size_t>(B * std::max<int64_t>(1, cdiv(L, kS)) * scan_np(N) * C) *
          sizeof(float);
 }
 size_t scan_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G) {

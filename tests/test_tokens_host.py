@@ -132,7 +132,7 @@ def test_workspace_sizes(L):
     assert w(4, 1, 256, 16, 1, 1) == 0 and w(4, 4, 256, 16, 1, 1) == 0      # single tokens
     assert w(4, 64, 256, 16, 1, 1) > 0 and w(4, 64, 256, 40, 1, 1) == 0     # 0 for what the call refuses
     s = L.gspn_selective_scan_saved_bytes
-    assert s(2, 64, 10, 16) == 2 * 2 * 16 * 10 * 4 and s(2, 65, 10, 9) == 2 * 3 * 16 * 10 * 4
+    assert s(2, 64, 10, 16) == 2 * 4 * 16 * 10 * 4 and s(2, 65, 10, 9) == 2 * 5 * 16 * 10 * 4
     a = L.gspn_cross_attention_workspace_bytes
     assert a(2, 1 << 20, 77, 4, 4, 64, 1) == 0                               # rows enough: nothing split
     assert a(2, 1, 8192, 4, 4, 64, 1) > 0

@@ -29,9 +29,10 @@
 //
 // Few channels still do not fill the chip: the token axis is then cut into
 // segments. A first pass finds each segment's state from zero and its sum of
-// d (the product of its decays is exp(A sum d): one exponential), a small
-// kernel carries states across segments, and the full pass starts every
-// segment from its carried state.
+// d (the product of its decays is exp(A sum d): one exponential), and the full
+// pass folds the segments before its own into the state that it starts from.
+#include <cmath>
+
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 
@@ -57,7 +58,7 @@ template <typename T> struct ScanP {
   float* saved;        // [B][chunks][NP][C]
   float* pack;         // [B][G][kW][Lp][2][NS]
   float* sum_d;        // [B][segs][C]
-  float* carry;        // [B][segs][NP][C]: local results, then carried-in values
+  float* carry;        // [B][segs][NP][C]: the segments' local results
   // backward
   T *dx, *ddt, *dz;
   float* partA;        // [B * segs][C][N]
@@ -88,37 +89,81 @@ __global__ __launch_bounds__(256) void pack_kernel(ScanP<T> a) {
   a.pack[(((b * a.G + g) * kW + w) * a.Lp + t) * (2 * NS) + n] = v;
 }
 
-// a token's B and C of this wavefront's states: uniform, by scalar loads
-template <int NS>
-__device__ __forceinline__ void load_bc(const float* pack, int64_t t, float (&b)[NS], float (&c)[NS]) {
+// The per-token operands of kB tokens: B and C of this wavefront's states,
+// uniform over the wavefront, by scalar loads, and values of the lane's channel
+// from LDS. Both count in one counter that a scalar load lets be waited for
+// only as a whole. So a batch is loaded while the one before is computed with,
+// and waited for once: wait_lds_scalar(), issue the next, compute.
+template <int NS> struct Batch {
+  static constexpr int kB = NS == 1 ? 4 : (NS <= 4 ? 2 : 1);   // 16 scalar registers, held twice
+  float b[kB][NS], c[kB][NS];
+};
+__device__ __forceinline__ void wait_lds_scalar() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));   // lgkmcnt(0) alone
+  __builtin_amdgcn_sched_barrier(0);
+}
+// tokens t .. t + kB - 1 (rows are adjacent in pack)
+template <int NS> __device__ __forceinline__ void load_batch(const float* pack, int64_t t, Batch<NS>& o) {
+  constexpr int kB = Batch<NS>::kB;
+  const float* row = pack + t * (2 * NS);
+  asm volatile("" : "+s"(row));   // keeps the loads here, and apart from other loads of these rows
   typedef const __attribute__((address_space(4))) float* cptr;
-  const cptr q = (cptr)(uintptr_t)(pack + t * (2 * NS));
+  const cptr q = (cptr)(uintptr_t)row;
 #pragma unroll
-  for (int n = 0; n < NS; ++n) b[n] = q[n];
+  for (int k = 0; k < kB; ++k) {
 #pragma unroll
-  for (int n = 0; n < NS; ++n) c[n] = q[NS + n];
+    for (int n = 0; n < NS; ++n) {
+      o.b[k][n] = q[k * 2 * NS + n];
+      o.c[k][n] = q[k * 2 * NS + NS + n];
+    }
+  }
+}
+
+// Four token rows of a [B, L, C] input, starting at token t and clamped to
+// the last one: uniform row addresses, the lane's channel as the offset.
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* base, int64_t stride, int64_t t, int64_t last,
+                                          uint32_t c, T (&r)[kOwn]) {
+  const T* row = base + (t < last ? t : last) * stride;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    r[k] = row[c];
+    row += t + k < last ? stride : 0;
+  }
+}
+
+// The kernel's arguments, read again from where the launch put them: keeping
+// all of them in scalar registers through the loops would crowd out B and C.
+template <typename T> using Args = const __attribute__((address_space(4))) ScanP<T>*;
+template <typename T> __device__ __forceinline__ Args<T> args_again() {
+  uint64_t k = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(k));
+  return reinterpret_cast<Args<T>>(k);
 }
 
 // where a workgroup works: entry b, group g, the lane's channel, its segment
 template <typename T> struct Place {
-  int64_t b, g, seg, c, t0, t1, end;   // tokens t0 .. t1 - 1, padding t1 .. end - 1
+  int64_t b, g, seg, t0, t1, end;   // tokens t0 .. t1 - 1, padding t1 .. end - 1
+  uint32_t c;
   int tile, lane, w;
   bool live;
 };
-template <typename T> __device__ __forceinline__ Place<T> place(const ScanP<T>& a) {
+template <typename T>
+__device__ __forceinline__ Place<T> place(const ScanP<T>& a, int segs, int first_seg) {
   Place<T> p;
   p.lane = threadIdx.x & 63;
   p.w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t i = blockIdx.x;
+  uint32_t i = blockIdx.x;
   p.tile = static_cast<int>(i % a.tiles);
   i /= a.tiles;
-  p.g = i % a.G;
-  i /= a.G;
-  p.seg = i % a.segs;
-  p.b = i / a.segs;
+  p.g = i % static_cast<uint32_t>(a.G);
+  i /= static_cast<uint32_t>(a.G);
+  p.seg = first_seg + i % segs;
+  p.b = i / segs;
   const int64_t k = p.tile * int64_t(64) + p.lane;
   p.live = k < a.Cg;
-  p.c = p.g * a.Cg + (p.live ? k : a.Cg - 1);   // idle lanes read the last channel
+  p.c = static_cast<uint32_t>(p.g * a.Cg + (p.live ? k : a.Cg - 1));   // idle lanes read the last channel
   const int64_t n = seq_len(a.lens, p.b, a.L);
   p.t0 = p.seg * a.segChunks * kS;
   p.end = p.t0 + a.segChunks * kS;
@@ -140,89 +185,133 @@ __device__ __forceinline__ void load_A(const ScanP<T>& a, const Place<T>& p, flo
     A2[n] = p.w * NS + n < a.N ? a.A[p.c * a.N + p.w * NS + n] * kLog2e : 0.0f;
 }
 
+// What the segments before this one (after it: kReverse) hand to it, folded
+// in order from their local results and sums of d; `from` is the state
+// before all of them, or null.
+template <typename T, int NS, bool kReverse>
+__device__ __forceinline__ void carried_in(const ScanP<T>& a, const Place<T>& p, const float* from,
+                                           const float (&A2)[NS], float (&h)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    const int k = p.w * NS + n;
+    h[n] = from && k < a.N ? from[(p.b * a.C + p.c) * a.N + k] : 0.0f;
+  }
+  const int count = static_cast<int>(kReverse ? a.segs - 1 - p.seg : p.seg);
+  constexpr int kAt = 8;   // segments loaded together
+  for (int i = 0; i < count; i += kAt) {
+    float local[kAt][NS], sum[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int q = i + j < count ? i + j : count - 1;
+      const int64_t s = p.b * a.segs + (kReverse ? a.segs - 1 - q : q);
+      sum[j] = a.sum_d[s * a.C + p.c];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) local[j][n] = a.carry[(s * (kW * NS) + p.w * NS + n) * a.C + p.c];
+    }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      if (i + j < count) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+          h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[n] * sum[j]), h[n], local[j][n]);
+      }
+    }
+  }
+  // have the values here, so that no wait for them is left inside the loops
+#pragma unroll
+  for (int n = 0; n < NS; ++n) asm volatile("" : "+v"(h[n]));
+}
+
 // ---- forward ----------------------------------------------------------------
 template <typename T, int NS>
 __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanP<T> a) {
+  constexpr int kB = Batch<NS>::kB;
   __shared__ float sd[kS][64], sx[kS][64], sy[kW][kS][64];   // d, d x, partial y
-  const Place<T> p = place(a);
+  const Place<T> p = place(a, a.segs, 0);
   const int lane = p.lane, w = p.w;
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
   float A2[NS], h[NS];
   load_A(a, p, A2);
-#pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    h[n] = 0.0f;
-    const int k = w * NS + n;
-    if (a.segs > 1) h[n] = a.carry[((p.b * a.segs + p.seg) * (kW * NS) + k) * a.C + p.c];
-    else if (a.state && k < a.N) h[n] = a.state[(p.b * a.C + p.c) * a.N + k];
-  }
-  const T* xp = a.x + p.b * a.xb + p.c;
-  const T* dp = a.dt + p.b * a.db + p.c;
-  const T* zp = a.z ? a.z + p.b * a.zb + p.c : nullptr;
+  carried_in<T, NS, false>(a, p, a.state, A2, h);
+  const bool zp = a.z != nullptr, keep = a.saved != nullptr;
   const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
-  T* op = a.out + p.b * a.L * a.C + p.c;
 
   T rx[kOwn], rd[kOwn], rz[kOwn];
   auto fetch = [&](int64_t c0) {
-#pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
-      rx[k] = xp[u * a.xr];
-      rd[k] = dp[u * a.dr];
-      if (zp) rz[k] = zp[u * a.zr];
-    }
+    const Args<T> k = args_again<T>();
+    load_rows(k->x + p.b * k->xb, k->xr, c0 + w * kOwn, p.t1 - 1, p.c, rx);
+    load_rows(k->dt + p.b * k->db, k->dr, c0 + w * kOwn, p.t1 - 1, p.c, rd);
+    if (zp) load_rows(k->z + p.b * k->zb, k->zr, c0 + w * kOwn, p.t1 - 1, p.c, rz);
   };
   if (p.t0 < p.t1) fetch(p.t0);
   for (int64_t c0 = p.t0; c0 < p.t1; c0 += kS) {
+    const int left = static_cast<int>(p.t1 - c0 < kS ? p.t1 - c0 : kS) - w * kOwn;   // own tokens here
     float x[kOwn], gate[kOwn];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
       // a token past the end has d = 0, which leaves the states as they are
-      const bool in = c0 + w * kOwn + k < p.t1;
       x[k] = to_f32(rx[k]);
-      const float d = in ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
+      const float d = k < left ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
       sd[w * kOwn + k][lane] = d;
-      sx[w * kOwn + k][lane] = in ? d * x[k] : 0.0f;
+      sx[w * kOwn + k][lane] = k < left ? d * x[k] : 0.0f;
       gate[k] = 1.0f;
       if (zp) {
         const float z = to_f32(rz[k]);
         gate[k] = z * sigmoid_f32(z);
       }
     }
-    if (a.saved && p.live) {
-      float* s = a.saved + ((p.b * a.chunks + c0 / kS) * (kW * NS) + w * NS) * a.C + p.c;
+    if (keep && p.live) {
+      const Args<T> k = args_again<T>();
+      float* s = k->saved + ((p.b * k->chunks + c0 / kS) * (kW * NS) + w * NS) * k->C;
 #pragma unroll
-      for (int n = 0; n < NS; ++n) s[n * a.C] = h[n];
+      for (int n = 0; n < NS; ++n) s[n * k->C + p.c] = h[n];
     }
     lds_barrier();
     if (c0 + kS < p.t1) fetch(c0 + kS);
+    Batch<NS> bc[2];
+    float d[2][kB], dx[2][kB];
+    auto issue = [&](int q) {
+      load_batch<NS>(pack, c0 + q * kB, bc[q & 1]);
 #pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      float Bt[NS], Ct[NS];
-      load_bc<NS>(pack, c0 + k, Bt, Ct);
-      const float d = sd[k][lane], dx = sx[k][lane];
-      float y = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
-        h[n] = __builtin_fmaf(e, h[n], dx * Bt[n]);
-        y = __builtin_fmaf(Ct[n], h[n], y);
+      for (int k = 0; k < kB; ++k) {
+        d[q & 1][k] = sd[q * kB + k][lane];
+        dx[q & 1][k] = sx[q * kB + k][lane];
       }
-      sy[w][k][lane] = y;
+    };
+    issue(0);
+#pragma unroll
+    for (int q = 0; q < kS / kB; ++q) {
+      wait_lds_scalar();
+      if (q + 1 < kS / kB) issue(q + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        float y = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float e = __builtin_amdgcn_exp2f(d[q & 1][k] * A2[n]);
+          h[n] = __builtin_fmaf(e, h[n], dx[q & 1][k] * bc[q & 1].b[k][n]);
+          y = __builtin_fmaf(bc[q & 1].c[k][n], h[n], y);
+        }
+        sy[w][q * kB + k][lane] = y;
+      }
     }
     lds_barrier();
+    const Args<T> again = args_again<T>();
+    T* o = again->out + (p.b * again->L + c0 + w * kOwn) * again->C;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      const int64_t t = c0 + w * kOwn + k;
       float y = Dc * x[k];
 #pragma unroll
       for (int q = 0; q < kW; ++q) y += sy[q][w * kOwn + k][lane];
-      if (p.live && t < p.t1) Store<T>::put(op, t * a.C, y * gate[k]);
+      if (p.live && k < left) Store<T>::put(o, p.c, y * gate[k]);
+      o += again->C;
     }
   }
   if (!p.live) return;
-  for (int64_t t = (p.t1 > p.t0 ? p.t1 : p.t0) + w; t < p.end; t += kW) Store<T>::put(op, t * a.C, 0.0f);
-  if (a.segs == 1 && a.state_out) {
+  T* op = a.out + p.b * a.L * a.C;
+  for (int64_t t = (p.t1 > p.t0 ? p.t1 : p.t0) + w; t < p.end; t += kW) Store<T>::put(op + t * a.C, p.c, 0.0f);
+  if (p.seg == a.segs - 1 && a.state_out) {
 #pragma unroll
     for (int n = 0; n < NS; ++n)
       if (w * NS + n < a.N) a.state_out[(p.b * a.C + p.c) * a.N + w * NS + n] = h[n];
@@ -231,34 +320,35 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanP<T> a) {
 
 // First pass over a segment: its end state from zero and its sum of d
 // (kReverse false), or, from its last token back, the g that it hands to the
-// segment before it, from zero behind it (kReverse true).
+// segment before it, from zero behind it (kReverse true). The segment that
+// hands nothing on is left out.
 template <typename T, int NS, bool kReverse>
 __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
   // d, and d x (forward) or grad_out silu(z) (reverse); two chunks' worth, so
   // that one barrier per chunk is enough
+  constexpr int kB = Batch<NS>::kB;
   __shared__ float sd[2][kS][64], sx[2][kS][64];
   __shared__ float sum[kW][64];
-  const Place<T> p = place(a);
+  const Place<T> p = place(a, a.segs - 1, kReverse ? 1 : 0);
   const int lane = p.lane, w = p.w;
   const float bias = a.bias ? a.bias[p.c] : 0.0f;
   float A2[NS], h[NS], sum_d = 0.0f;
   load_A(a, p, A2);
 #pragma unroll
-  for (int n = 0; n < NS; ++n) h[n] = 0.0f;
-  const T* dp = a.dt + p.b * a.db + p.c;
-  const T* xp = kReverse ? a.gy + p.b * a.gb + p.c : a.x + p.b * a.xb + p.c;
+  for (int n = 0; n < NS; ++n) {
+    h[n] = 0.0f;
+    asm volatile("" : "+v"(A2[n]));   // loaded before the loop
+  }
+  const T* dp = a.dt + p.b * a.db;
+  const T* xp = kReverse ? a.gy + p.b * a.gb : a.x + p.b * a.xb;
   const int64_t xr = kReverse ? a.gr : a.xr;
-  const T* zp = kReverse && a.z ? a.z + p.b * a.zb + p.c : nullptr;
+  const T* zp = kReverse && a.z ? a.z + p.b * a.zb : nullptr;
   const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
   T rx[kOwn], rd[kOwn], rz[kOwn];
   auto fetch = [&](int64_t c0) {
-#pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
-      rx[k] = xp[u * xr];
-      rd[k] = dp[u * a.dr];
-      if (zp) rz[k] = zp[u * a.zr];
-    }
+    load_rows(xp, xr, c0 + w * kOwn, p.t1 - 1, p.c, rx);
+    load_rows(dp, a.dr, c0 + w * kOwn, p.t1 - 1, p.c, rd);
+    if (zp) load_rows(zp, a.zr, c0 + w * kOwn, p.t1 - 1, p.c, rz);
   };
   const int64_t chunks = p.t1 > p.t0 ? (p.t1 - p.t0 + kS - 1) / kS : 0;
   auto start = [&](int64_t i) { return p.t0 + (kReverse ? chunks - 1 - i : i) * kS; };
@@ -266,10 +356,10 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
   for (int64_t i = 0; i < chunks; ++i) {
     const int64_t c0 = start(i);
     const int buf = i & 1;
+    const int left = static_cast<int>(p.t1 - c0 < kS ? p.t1 - c0 : kS) - w * kOwn;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      const bool in = c0 + w * kOwn + k < p.t1;
-      const float d = in ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
+      const float d = k < left ? step_size(a, to_f32(rd[k]), bias) : 0.0f;
       float v = to_f32(rx[k]);
       if constexpr (kReverse) {
         if (zp) {
@@ -281,21 +371,36 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
       }
       sum_d += d;
       sd[buf][w * kOwn + k][lane] = d;
-      sx[buf][w * kOwn + k][lane] = in ? v : 0.0f;
+      sx[buf][w * kOwn + k][lane] = k < left ? v : 0.0f;
     }
     lds_barrier();
     if (i + 1 < chunks) fetch(start(i + 1));
+    Batch<NS> bc[2];
+    float d[2][kB], v[2][kB];
+    auto issue = [&](int q) {   // batches in the order of the walk
+      const int t = kReverse ? kS - (q + 1) * kB : q * kB;
+      load_batch<NS>(pack, c0 + t, bc[q & 1]);
 #pragma unroll
-    for (int j = 0; j < kS; ++j) {
-      const int k = kReverse ? kS - 1 - j : j;
-      float Bt[NS], Ct[NS];
-      load_bc<NS>(pack, c0 + k, Bt, Ct);
-      const float d = sd[buf][k][lane], v = sx[buf][k][lane];
+      for (int k = 0; k < kB; ++k) {
+        d[q & 1][k] = sd[buf][t + k][lane];
+        v[q & 1][k] = sx[buf][t + k][lane];
+      }
+    };
+    issue(0);
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
-        if constexpr (kReverse) h[n] = e * __builtin_fmaf(Ct[n], v, h[n]);
-        else h[n] = __builtin_fmaf(e, h[n], v * Bt[n]);
+    for (int q = 0; q < kS / kB; ++q) {
+      wait_lds_scalar();
+      if (q + 1 < kS / kB) issue(q + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        const int k = kReverse ? kB - 1 - j : j;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float e = __builtin_amdgcn_exp2f(d[q & 1][k] * A2[n]);
+          if constexpr (kReverse) h[n] = e * __builtin_fmaf(bc[q & 1].c[k][n], v[q & 1][k], h[n]);
+          else h[n] = __builtin_fmaf(e, h[n], v[q & 1][k] * bc[q & 1].b[k][n]);
+        }
       }
     }
   }
@@ -306,30 +411,6 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
   if (w == 0) a.sum_d[s * a.C + p.c] = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
 #pragma unroll
   for (int n = 0; n < NS; ++n) a.carry[(s * (kW * NS) + w * NS + n) * a.C + p.c] = h[n];
-}
-
-// Carries over the segments of one (entry, state): carry holds the segments'
-// local results and receives the value each segment starts from. kReverse
-// runs from the last segment to the first (the backward pass's g).
-template <typename T, int NP, bool kReverse>
-__global__ __launch_bounds__(64) void carry_kernel(ScanP<T> a, const float* from, float* to) {
-  int64_t i = blockIdx.x;
-  const int64_t ctiles = (a.C + 63) / 64;
-  const int64_t c = (i % ctiles) * 64 + threadIdx.x;
-  i /= ctiles;
-  const int n = static_cast<int>(i % a.N);
-  const int64_t b = i / a.N;
-  if (c >= a.C) return;
-  const float A2 = a.A[c * a.N + n] * kLog2e;
-  float h = from ? from[(b * a.C + c) * a.N + n] : 0.0f;
-  for (int k = 0; k < a.segs; ++k) {
-    const int64_t s = b * a.segs + (kReverse ? a.segs - 1 - k : k);
-    float* q = a.carry + (s * NP + n) * a.C + c;
-    const float local = *q;
-    *q = h;
-    h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.sum_d[s * a.C + c]), h, local);
-  }
-  if (to) to[(b * a.C + c) * a.N + n] = h;
 }
 
 // ---- few tokens: the serving step -------------------------------------------
@@ -471,37 +552,29 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
   constexpr bool kKeep = NS <= 4;    // decays kept: 16 NS registers
   __shared__ float sd[kS][64], sx[kS][64], sg[kS][64];                    // d, d x, gy
   __shared__ float sy[kW][kS][64], su[kW][kS][64], sv[kW][kS][64];        // partial y, sum g B, sum A m
-  const Place<T> p = place(a);
+  constexpr int kB = Batch<NS>::kB;
+  const Place<T> p = place(a, a.segs, 0);
   const int lane = p.lane, w = p.w;
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
   float A2[NS], g[NS], dA[NS], dD = 0.0f, dbias = 0.0f;
   load_A(a, p, A2);
+  carried_in<T, NS, true>(a, p, a.gstate, A2, g);
 #pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    const int k = w * NS + n;
-    dA[n] = 0.0f;
-    g[n] = 0.0f;
-    if (k < a.N) {
-      if (a.segs > 1) g[n] = a.carry[((p.b * a.segs + p.seg) * (kW * NS) + k) * a.C + p.c];
-      else if (a.gstate) g[n] = a.gstate[(p.b * a.C + p.c) * a.N + k];
-    }
-  }
-  const T* xp = a.x + p.b * a.xb + p.c;
-  const T* dp = a.dt + p.b * a.db + p.c;
-  const T* zp = a.z ? a.z + p.b * a.zb + p.c : nullptr;
-  const T* gp = a.gy + p.b * a.gb + p.c;
-  const int64_t row0 = p.b * a.L * a.C + p.c;
+  for (int n = 0; n < NS; ++n) dA[n] = 0.0f;
+  const bool zp = a.z != nullptr;
   const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
   float* part = a.partBC + (((p.b * a.G + p.g) * a.tiles + p.tile) * a.Lp * kW + w) * (2 * NS);
-  const int slot = wave_sum_index<2 * NS>(lane);
-  // one of the lanes that end with the same value stores it
-  const bool writer = (lane & (64 / (2 * NS) - 1)) == 0;
+  // kSame lanes end a sum with the same value, so each of them keeps another
+  // token's and one store writes kSame tokens
+  constexpr int kSame = 32 / NS < kS ? 32 / NS : kS;
+  const int slot = wave_sum_index<2 * NS>(lane), turn = lane & (32 / NS - 1);
 
   for (int64_t t = (p.t1 > p.t0 ? p.t1 : p.t0) + w; t < p.end; t += kW) {
     if (p.live) {
-      Store<T>::put(a.dx, row0 + t * a.C, 0.0f);
-      Store<T>::put(a.ddt, row0 + t * a.C, 0.0f);
-      if (a.dz) Store<T>::put(a.dz, row0 + t * a.C, 0.0f);
+      const int64_t at = (p.b * a.L + t) * a.C + p.c;
+      Store<T>::put(a.dx, at, 0.0f);
+      Store<T>::put(a.ddt, at, 0.0f);
+      if (zp) Store<T>::put(a.dz, at, 0.0f);
     }
   }
   // whole chunks of padding; a chunk that holds a token is written below
@@ -511,26 +584,24 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
   T rx[kOwn], rd[kOwn], rz[kOwn], rg[kOwn];
   float rh[NS];
   auto fetch = [&](int64_t c0) {
+    const Args<T> k = args_again<T>();
+    load_rows(k->x + p.b * k->xb, k->xr, c0 + w * kOwn, p.t1 - 1, p.c, rx);
+    load_rows(k->dt + p.b * k->db, k->dr, c0 + w * kOwn, p.t1 - 1, p.c, rd);
+    load_rows(k->gy + p.b * k->gb, k->gr, c0 + w * kOwn, p.t1 - 1, p.c, rg);
+    if (zp) load_rows(k->z + p.b * k->zb, k->zr, c0 + w * kOwn, p.t1 - 1, p.c, rz);
+    const float* s = k->saved + ((p.b * k->chunks + c0 / kS) * (kW * NS) + w * NS) * k->C;
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      const int64_t t = c0 + w * kOwn + k, u = t < p.t1 ? t : p.t1 - 1;
-      rx[k] = xp[u * a.xr];
-      rd[k] = dp[u * a.dr];
-      rg[k] = gp[u * a.gr];
-      if (zp) rz[k] = zp[u * a.zr];
-    }
-    const float* s = a.saved + ((p.b * a.chunks + c0 / kS) * (kW * NS) + w * NS) * a.C + p.c;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) rh[n] = s[n * a.C];
+    for (int n = 0; n < NS; ++n) rh[n] = s[n * k->C + p.c];
   };
   const int64_t chunks = p.t1 > p.t0 ? (p.t1 - p.t0 + kS - 1) / kS : 0;
   if (chunks > 0) fetch(p.t0 + (chunks - 1) * kS);
   for (int64_t i = chunks - 1; i >= 0; --i) {
     const int64_t c0 = p.t0 + i * kS;
+    const int left = static_cast<int>(p.t1 - c0 < kS ? p.t1 - c0 : kS) - w * kOwn;
     float x[kOwn], d[kOwn], slope[kOwn], gz[kOwn], gsl[kOwn];   // gsl: grad_out silu'(z)
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      const bool in = c0 + w * kOwn + k < p.t1;
+      const bool in = k < left;
       const float v = to_f32(rd[k]) + bias;
       x[k] = to_f32(rx[k]);
       slope[k] = 1.0f;
@@ -553,51 +624,78 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[0][n] = rh[n];
     lds_barrier();
+    Batch<NS> bc[2];
+    float bd[2][kB], bx[2][kB], bg[2][kB];
+    auto issue = [&](int q, int buf) {   // batch q of the chunk's tokens
+      load_batch<NS>(pack, c0 + q * kB, bc[buf]);
 #pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      float Bt[NS], Ct[NS];
-      load_bc<NS>(pack, c0 + k, Bt, Ct);
-      const float dk = sd[k][lane], dx = sx[k][lane];
-      float y = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const float f = __builtin_amdgcn_exp2f(dk * A2[n]);
-        if constexpr (kKeep) e[k][n] = f;
-        h[k + 1][n] = __builtin_fmaf(f, h[k][n], dx * Bt[n]);
-        y = __builtin_fmaf(Ct[n], h[k + 1][n], y);
+      for (int k = 0; k < kB; ++k) {
+        bd[buf][k] = sd[q * kB + k][lane];
+        bx[buf][k] = sx[q * kB + k][lane];
+        bg[buf][k] = sg[q * kB + k][lane];
       }
-      sy[w][k][lane] = y;
+    };
+    constexpr int kQ = kS / kB;
+    issue(0, 0);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      wait_lds_scalar();
+      // after the last batch the walk back begins, with the same one
+      if (q + 1 < kQ) issue(q + 1, (q + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        float y = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const int t = q * kB + k;
+          const float f = __builtin_amdgcn_exp2f(bd[q & 1][k] * A2[n]);
+          if constexpr (kKeep) e[t][n] = f;
+          h[t + 1][n] = __builtin_fmaf(f, h[t][n], bx[q & 1][k] * bc[q & 1].b[k][n]);
+          y = __builtin_fmaf(bc[q & 1].c[k][n], h[t + 1][n], y);
+        }
+        sy[w][q * kB + k][lane] = y;
+      }
     }
+    float held = 0.0f;
 #pragma unroll
-    for (int k = kS - 1; k >= 0; --k) {
+    for (int q = kQ - 1; q >= 0; --q) {
+      if (q < kQ - 1) wait_lds_scalar();
       // the chunk before: late enough that half of the states are done with
-      if (k == kS / 2 && i > 0) fetch(c0 - kS);
-      float Bt[NS], Ct[NS], bc[2 * NS];
-      load_bc<NS>(pack, c0 + k, Bt, Ct);
-      const float dk = sd[k][lane], dx = sx[k][lane], gk = sg[k][lane];
-      float du = 0.0f, dd = 0.0f;
+      if (q == kQ / 2 - 1 && i > 0) fetch(c0 - kS);
+      if (q > 0) issue(q - 1, (q - 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        g[n] = __builtin_fmaf(Ct[n], gk, g[n]);
-        const float back = g[n] * (kKeep ? e[kKeep ? k : 0][n] : __builtin_amdgcn_exp2f(dk * A2[n]));
-        const float m = back * h[k][n];
-        du = __builtin_fmaf(g[n], Bt[n], du);
-        dd = __builtin_fmaf(m, A2[n], dd);
-        dA[n] = __builtin_fmaf(m, dk, dA[n]);
-        bc[n] = dx * g[n];
-        bc[NS + n] = gk * h[k + 1][n];
-        g[n] = back;
+      for (int k = kB - 1; k >= 0; --k) {
+        const int t = q * kB + k;
+        const float dk = bd[q & 1][k], dx = bx[q & 1][k], gk = bg[q & 1][k];
+        float du = 0.0f, dd = 0.0f, v[2 * NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          g[n] = __builtin_fmaf(bc[q & 1].c[k][n], gk, g[n]);
+          const float back = g[n] * (kKeep ? e[kKeep ? t : 0][n] : __builtin_amdgcn_exp2f(dk * A2[n]));
+          const float m = back * h[t][n];
+          du = __builtin_fmaf(g[n], bc[q & 1].b[k][n], du);
+          dd = __builtin_fmaf(m, A2[n], dd);
+          dA[n] = __builtin_fmaf(m, dk, dA[n]);
+          v[n] = dx * g[n];
+          v[NS + n] = gk * h[t + 1][n];
+          g[n] = back;
+        }
+        su[w][t][lane] = du;
+        sv[w][t][lane] = dd;
+        const float sum = wave_sum<2 * NS>(v, lane);
+        held = turn == t % kSame ? sum : held;
+        if (t % kSame == 0 && turn < kSame) part[(c0 + t + turn) * (kW * 2 * NS) + slot] = held;
       }
-      su[w][k][lane] = du;
-      sv[w][k][lane] = dd;
-      const float s = wave_sum<2 * NS>(bc, lane);
-      if (writer) part[(c0 + k) * (kW * 2 * NS) + slot] = s;
     }
     lds_barrier();
+    const Args<T> again = args_again<T>();
+    const int64_t row = (p.b * again->L + c0 + w * kOwn) * again->C;
+    T *dxp = again->dx + row, *ddtp = again->ddt + row, *dzp = again->dz + row;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
       const int r = w * kOwn + k;
-      const int64_t t = c0 + r;
       float y = Dc * x[k], du = 0.0f, dd = 0.0f;
 #pragma unroll
       for (int q = 0; q < kW; ++q) {
@@ -605,16 +703,19 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
         du += su[q][r][lane];
         dd += sv[q][r][lane];
       }
-      if (t < p.t1) {
+      if (k < left) {
         const float ddt = __builtin_fmaf(x[k], du, dd * kLn2) * slope[k];
         dbias += ddt;
         dD = __builtin_fmaf(gz[k], x[k], dD);
         if (p.live) {
-          Store<T>::put(a.dx, row0 + t * a.C, __builtin_fmaf(Dc, gz[k], d[k] * du));
-          Store<T>::put(a.ddt, row0 + t * a.C, ddt);
-          if (a.dz) Store<T>::put(a.dz, row0 + t * a.C, y * gsl[k]);
+          Store<T>::put(dxp, p.c, __builtin_fmaf(Dc, gz[k], d[k] * du));
+          Store<T>::put(ddtp, p.c, ddt);
+          if (zp) Store<T>::put(dzp, p.c, y * gsl[k]);
         }
       }
+      dxp += again->C;
+      ddtp += again->C;
+      dzp += again->C;
     }
   }
   __syncthreads();
@@ -632,7 +733,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
     const int k = w * NS + n;
     if (k < a.N) {
       a.partA[(pi * a.C + p.c) * a.N + k] = dA[n];
-      if (a.segs == 1 && a.dstate) a.dstate[(p.b * a.C + p.c) * a.N + k] = g[n];
+      if (p.seg == 0 && a.dstate) a.dstate[(p.b * a.C + p.c) * a.N + k] = g[n];
     }
   }
 }
@@ -659,29 +760,37 @@ __global__ __launch_bounds__(256) void reduce_bc_kernel(ScanP<T> a, T* dB, T* dC
 int scan_ns(int64_t N) { return N <= 4 ? 1 : (N <= 8 ? 2 : (N <= 16 ? 4 : 8)); }
 int scan_np(int64_t N) { return kW * scan_ns(N); }
 
+constexpr int64_t kMaxSegs = 64;
 struct Cut {
   int64_t chunks;
   int tiles, segs, segChunks;
 };
 // Segments of the token axis. Cutting adds the first pass, so it pays only
 // where whole-axis workgroups would leave compute units idle or unevenly
-// loaded: the estimate is, for each number of segments, the workgroups of the
-// fullest compute unit times a workgroup's tokens times the cycles per token
-// (per state 25 forward, 70 backward, 21 in the first pass, and what does not
-// depend on the states), a quarter more where a compute unit has one
-// workgroup only, and the two extra launches.
-Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
+// loaded. For each number of segments the time is estimated as the workgroups
+// on the fullest compute unit times a workgroup's tokens times the cycles
+// that a token takes (measured on full compute units, with four states per
+// wavefront: 190 forward, 127 in a first pass, 647 backward), a quarter more
+// where one workgroup has a compute unit to itself, plus what every
+// workgroup spends before its first token and on folding the segments before
+// its own. With padded entries the work is taken to be half of the tokens
+// once there are segments to leave out.
+// Both sides of the choice, bf16, 16 states (forward): 1 x 8192 x 2304 takes
+// 1150 us whole; 16 x 2048 x 2304 ragged takes 415 us whole.
+Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool ragged, bool bwd) {
   Cut k;
   k.chunks = std::max<int64_t>(1, cdiv(L, kS));
   k.tiles = static_cast<int>(cdiv(C / G, 64));
   const int64_t groups = std::max<int64_t>(1, B * G * k.tiles);
-  const double ns = scan_ns(N), full = bwd ? 70 * ns + 150 : 25 * ns + 50, first = 21 * ns + 30;
+  const double ns = scan_ns(N), full = bwd ? 125 * ns + 147 : 35 * ns + 50, first = 24 * ns + 30;
   double best = 0;
   k.segChunks = static_cast<int>(k.chunks);
-  for (int64_t s = 1; s <= std::min<int64_t>(k.chunks, 128); ++s) {
-    const int64_t each = cdiv(k.chunks, s), segs = cdiv(k.chunks, each), per = cdiv(groups * segs, 256);
-    const double cost = per * each * kS * (full + (segs > 1 ? first : 0.0)) * (1.0 + 0.25 / per) +
-                        (segs > 1 ? 20000.0 + 40.0 * segs : 0.0);
+  for (int64_t s = 1; s <= std::min<int64_t>(k.chunks, kMaxSegs); ++s) {
+    const int64_t each = cdiv(k.chunks, s), segs = cdiv(k.chunks, each);
+    const double part = ragged ? 0.5 + 0.5 / segs : 1.0;
+    const double per = std::ceil(groups * segs * part / 256), per1 = std::ceil(groups * (segs - 1) * part / 256);
+    const double cost = per * (each * kS * full * (1.0 + 0.25 / per) + 4000.0 + 30.0 * segs) +
+                        (segs > 1 ? per1 * (each * kS * first * (1.0 + 0.25 / per1) + 3000.0) + 8000.0 : 0.0);
     if (s == 1 || cost < best) {
       best = cost;
       k.segChunks = static_cast<int>(each);
@@ -691,6 +800,10 @@ Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
   k.segs = static_cast<int>(cdiv(k.chunks, k.segChunks));
   return k;
 }
+// most segments that any call of this shape may use, for its workspace
+int64_t most_segs(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
+  return std::max(cut_scan(B, L, C, N, G, false, bwd).segs, cut_scan(B, L, C, N, G, true, bwd).segs);
+}
 
 struct Space {
   size_t pack, sum_d, carry, saved, partA, partD, partBC, total;
@@ -698,7 +811,7 @@ struct Space {
 Space scan_space(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd) {
   Space s{};
   if (!bwd && L <= kStepMax) return s;
-  const Cut f = cut_scan(B, L, C, N, G, false), k = cut_scan(B, L, C, N, G, true);
+  const Cut k = cut_scan(B, L, C, N, G, false, bwd);
   const int64_t np = scan_np(N), Lp = k.chunks * kS;
   size_t at = 0;
   auto take = [&](int64_t floats) {
@@ -706,7 +819,8 @@ Space scan_space(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd
     at += up256(static_cast<size_t>(floats) * sizeof(float));
     return here;
   };
-  const int64_t segs = bwd ? std::max(f.segs, k.segs) : f.segs;
+  const int64_t fsegs = most_segs(B, L, C, N, G, false), bsegs = bwd ? most_segs(B, L, C, N, G, true) : 1;
+  const int64_t segs = std::max(fsegs, bsegs);
   s.pack = take(B * G * Lp * 2 * np);
   if (segs > 1) {
     s.sum_d = take(B * segs * C);
@@ -714,8 +828,8 @@ Space scan_space(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool bwd
   }
   if (bwd) {
     s.saved = take(B * k.chunks * np * C);   // used when the caller kept none
-    s.partA = take(B * k.segs * C * N);
-    s.partD = take(2 * B * k.segs * C);
+    s.partA = take(B * bsegs * C * N);
+    s.partD = take(2 * B * bsegs * C);
     s.partBC = take(B * G * k.tiles * Lp * 2 * np);
   }
   s.total = at;
@@ -736,7 +850,7 @@ template <typename T> ScanP<T> scan_params(const gspn_scan_args& a, bool bwd) {
   p.B = a.B; p.L = a.L; p.C = a.C; p.G = a.G; p.Cg = a.C / a.G;
   p.N = static_cast<int>(a.N);
   p.softplus = a.softplus;
-  const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, bwd);
+  const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, a.lens != nullptr, bwd);
   p.chunks = k.chunks; p.tiles = k.tiles; p.segs = k.segs; p.segChunks = k.segChunks;
   p.Lp = k.chunks * kS;
   return p;
@@ -759,9 +873,8 @@ template <typename T, int NS>
 hipError_t scan_passes(const ScanP<T>& p, hipStream_t stream, Tracer* tr) {
   const int64_t grid = p.B * p.segs * p.G * p.tiles;
   if (p.segs > 1) {
-    GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, false>), grid, kThreads, p);
-    GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, kW * NS, false>), p.B * p.N * cdiv(p.C, 64), 64, p,
-                p.state, p.state_out);
+    GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, false>), grid / p.segs * (p.segs - 1),
+                kThreads, p);
   }
   GSPN_LAUNCH("scan_fwd", p.B, (scan_fwd_kernel<T, NS>), grid, kThreads, p);
   return hipSuccess;
@@ -831,7 +944,7 @@ hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
         // find the states again: the forward passes, their output into dx
         // (written again below)
         ScanP<T> f = p;
-        const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, false);
+        const Cut k = cut_scan(a.B, a.L, a.C, a.N, a.G, a.lens != nullptr, false);
         f.segs = k.segs;
         f.segChunks = k.segChunks;
         f.saved = p.saved = at_bytes(ws, s.saved);
@@ -841,9 +954,8 @@ hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
         if ((e = scan_passes<T, NS>(f, stream, tr)) != hipSuccess) return e;
       }
       if (p.segs > 1) {
-        GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, true>), grid, kThreads, p);
-        GSPN_LAUNCH("scan_carry", p.B, (carry_kernel<T, kW * NS, true>), p.B * p.N * cdiv(p.C, 64), 64, p,
-                    p.gstate, p.dstate);
+        GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, true>), grid / p.segs * (p.segs - 1),
+                    kThreads, p);
       }
     }
     GSPN_LAUNCH("scan_bwd", p.B, (scan_bwd_kernel<T, NS>), grid, kThreads, p);

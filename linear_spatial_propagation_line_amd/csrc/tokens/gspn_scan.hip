@@ -789,8 +789,8 @@ Cut cut_scan(int64_t B, int64_t L, int64_t C, int64_t N, int64_t G, bool ragged,
     const int64_t each = cdiv(k.chunks, s), segs = cdiv(k.chunks, each);
     const double part = ragged ? 0.5 + 0.5 / segs : 1.0;
     const double per = std::ceil(groups * segs * part / 256), per1 = std::ceil(groups * (segs - 1) * part / 256);
-    const double cost = per * (each * kS * full * (1.0 + 0.25 / per) + 4000.0 + 30.0 * segs) +
-                        (segs > 1 ? per1 * (each * kS * first * (1.0 + 0.25 / per1) + 3000.0) + 8000.0 : 0.0);
+    const double cost = (per + 0.7) * each * kS * full + std::ceil(per / 4) * (4000.0 + 100.0 * segs) +
+                        (segs > 1 ? (per1 + 0.7) * each * kS * first + std::ceil(per1 / 4) * 4000.0 + 8000.0 : 0.0);
     if (s == 1 || cost < best) {
       best = cost;
       k.segChunks = static_cast<int>(each);

@@ -1,10 +1,10 @@
 // Cross attention, forward: out = softmax(scale q k^T over the kept keys) v.
 //
 // One pass over the keys with the running maximum and sum of the softmax: a
-// wavefront holds 32 query rows (their fragments and the 32 x E result stay
-// in registers) and takes 32 keys at a time, X^T = K Q^T, probabilities, then
-// O^T += V^T P^T, with one lane per query row, so that the row's maximum and
-// sum need one exchange between half-wavefronts. The query heads that share
+// wavefront holds query rows in tiles of 32 (their fragments and the 32 x E
+// result stay in registers) and takes 32 keys at a time, X^T = K Q^T,
+// probabilities, then O^T += V^T P^T, with one lane per query row, so that the
+// row's maximum and sum need one exchange between half-wavefronts. The query heads that share
 // a key head are rows of one problem, so their K and V are read once.
 #include "gspn_attn.hpp"
 
@@ -29,138 +29,321 @@ template <typename T> struct AttnP {
   bool wide_q, wide_kv, wide_o;
 };
 
-// WR wavefronts take different rows; with WR = 1 the four wavefronts take
-// different keys of the same 32 rows, each as a split of its own.
-template <typename T, int EP, int WR, int TK>
+// Query row r of (entry b, key head hk), clamped to the last row
+struct QRow {
+  int64_t h, q;
+};
+template <typename T> __device__ __forceinline__ QRow q_row(const AttnP<T>& a, int hk, uint32_t r) {
+  const uint32_t rc = r < a.rows ? r : static_cast<uint32_t>(a.rows) - 1;
+  const uint32_t hs = rc / static_cast<uint32_t>(a.Lq);
+  return QRow{static_cast<int64_t>(hk) * a.share + hs, static_cast<int64_t>(rc - hs * static_cast<uint32_t>(a.Lq))};
+}
+template <typename T> struct Keys {   // K, V and the kept keys of one (entry, key head)
+  const T *k, *v;
+  const uint8_t* mask;
+  __device__ __forceinline__ Keys(const AttnP<T>& a, int64_t b, int hk)
+      : k(a.k + b * a.km.batch + hk * a.km.head), v(a.v + b * a.vm.batch + hk * a.vm.head),
+        mask(a.mask ? a.mask + b * a.mask_batch : nullptr) {}
+  __device__ __forceinline__ bool kept(const AttnP<T>& a, int64_t key) const {
+    return key < a.Lk && (!mask || mask[key] != 0);
+  }
+};
+
+// One step of the running softmax over 32 keys: w becomes the probabilities
+// (unnormalised, base 2 exponent against m), m and l follow, and the result
+// so far is rescaled when the maximum moved.
+template <int N>
+__device__ __forceinline__ void softmax_step(float (&w)[16], float c, float& m, float& l, f32x16 (&o)[N]) {
+  float top = w[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) top = fmaxf(top, w[i]);
+  top = column_max(top) * c;
+  if (__any(top > m)) {
+    const float mn = fmaxf(m, top);
+    const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int et = 0; et < N; ++et) o[et] *= f;
+  }
+  const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], c, -base));
+    l += w[i];
+  }
+}
+
+// ---- long key axes, many rows -------------------------------------------------
+// Four wavefronts of 32 rows each; K and V pass through LDS 64 (fp32: 32)
+// keys at a time.
+template <typename T, int EP, int TK>
 __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   extern __shared__ __align__(16) char lds[];
-  constexpr int kKeysEach = WR == 1 ? TK / 4 : TK;   // keys of a tile that one wavefront takes
   char* kt = lds;
   char* vt = lds + TK * tile_pitch<T, EP>();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int64_t blk = blockIdx.x;
+  uint32_t blk = blockIdx.x;
   const int rt = static_cast<int>(blk % a.row_tiles);
   blk /= a.row_tiles;
   const int split = static_cast<int>(blk % a.splits);
   const int64_t bh = blk / a.splits, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
-
-  const int64_t r = (static_cast<int64_t>(rt) * WR + (WR == 1 ? 0 : wave)) * 32 + (lane & 31);
+  const uint32_t r = (static_cast<uint32_t>(rt) * 4 + wave) * 32 + (lane & 31);
   const bool row_ok = r < a.rows;
-  const int64_t rc = row_ok ? r : a.rows - 1;
-  const int64_t hs = rc / a.Lq, qi = rc - hs * a.Lq;
-  const int64_t h = hk * a.share + hs;
+  const QRow w_ = q_row(a, hk, r);
+  const Keys<T> keys(a, b, hk);
 
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
-  row_frags<T, EP>(a.q + b * a.qm.batch + qi * a.qm.row + h * a.qm.head, row_ok, a.E, a.wide_q, qf);
-
-  const T* kp = a.k + b * a.km.batch + hk * a.km.head;
-  const T* vp = a.v + b * a.vm.batch + hk * a.vm.head;
-  const uint8_t* mp = a.mask ? a.mask + b * a.mask_batch : nullptr;
-  auto kept = [&](int64_t key) { return key < a.Lk && (!mp || mp[key] != 0); };
-
+  row_frags<T, EP>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
   f32x16 o[EP / 32] = {};
   float m = -INFINITY, l = 0.0f;
   const int t_first = split * a.tiles_each;
   const int t_last = t_first + a.tiles_each < a.key_tiles ? t_first + a.tiles_each : a.key_tiles;
-
   Stage<T, EP, TK, kThreads> ks, vs;
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? kp + (k0 + i) * a.km.row : nullptr; });
-    vs.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? vp + (k0 + i) * a.vm.row : nullptr; });
+    ks.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.k + (k0 + i) * a.km.row : nullptr; });
+    vs.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.v + (k0 + i) * a.vm.row : nullptr; });
   };
   if (t_first < t_last) fetch(t_first);
   for (int t = t_first; t < t_last; ++t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.write(kt, tid, [&](int i) { return kept(k0 + i); });
-    vs.write(vt, tid, [&](int i) { return kept(k0 + i); });
+    ks.write(kt, tid, [&](int i) { return keys.kept(a, k0 + i); });
+    vs.write(vt, tid, [&](int i) { return keys.kept(a, k0 + i); });
     __syncthreads();
     if (t + 1 < t_last) fetch(t + 1);
 #pragma unroll
-    for (int s = 0; s < kKeysEach / 32; ++s) {
-      const int row0 = (WR == 1 ? wave * kKeysEach : 0) + s * 32;
-      const uint32_t bits = static_cast<uint32_t>(__ballot(kept(k0 + row0 + (lane & 31))));
+    for (int s = 0; s < TK / 32; ++s) {
+      const uint32_t bits = static_cast<uint32_t>(__ballot(keys.kept(a, k0 + s * 32 + (lane & 31))));
       if (bits == 0) continue;
-      const f32x16 x = tile_dot<T, EP>(kt, row0, qf, lane);
+      const f32x16 x = tile_dot<T, EP>(kt, s * 32, qf, lane);
       float w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = x[i];
-      if (bits != 0xffffffffu) {
-        const uint32_t mine = bits >> (4 * (lane >> 5));
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = (mine >> ((i & 3) + 8 * (i >> 2))) & 1u ? w[i] : -INFINITY;
-      }
-      float top = w[0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, w[i]);
-      top = fmaxf(top, other_half(top)) * a.c;
-      if (__any(top > m)) {
-        const float mn = fmaxf(m, top);
-        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int et = 0; et < EP / 32; ++et) o[et] *= f;
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], a.c, -base));
-        l += w[i];
-      }
-      tile_accum<EP>(vt, row0, w, o, lane, T{});
+      drop_keys(w, bits, lane);
+      softmax_step(w, a.c, m, l, o);
+      tile_accum<EP>(vt, s * 32, w, o, lane, T{});
     }
     __syncthreads();
   }
-  l += other_half(l);
-  const int64_t n = a.rows;
-  if (WR == 1 || a.splits > 1) {
-    const int64_t sp = WR == 1 ? split * 4 + wave : split;
-    const int64_t at = (sp * a.B * a.Hkv + bh) * n + r;
+  l = column_sum(l);
+  if (a.splits > 1) {
+    const int64_t at = (split * a.B * a.Hkv + bh) * a.rows + r;
     store_col<float, EP>(a.part + at * EP, row_ok, true, EP, true, o, 1.0f, lane);
     if (row_ok && lane < 32) {
       a.part_ml[at * 2] = m;
       a.part_ml[at * 2 + 1] = l;
     }
   } else {
-    const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    store_col<T, EP>(a.out + ((b * a.Lq + qi) * a.Hq + h) * a.E, row_ok, true, a.E, a.wide_o, o, f, lane);
-    if (a.lse && row_ok && lane < 32)
-      a.lse[(b * a.Hq + h) * a.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    store_col<T, EP>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
+                     softmax_scale(l), lane);
+    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
   }
 }
 
-// Joins the splits of a row: one wavefront per row, lanes over the values.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnP<T> a, int parts, int EP) {
+// ---- at most 128 keys -----------------------------------------------------------
+// All keys of an (entry, key head) stay in LDS while each wavefront walks row
+// tiles of its own, with no barrier after the keys are staged: all scores of
+// a row are in registers, so its maximum is known before the first exponential.
+// Bound by the rows' bytes (q in, out back); the next tile's q is loaded ahead.
+template <typename T, int EP, int NT>
+__global__ __launch_bounds__(kThreads) void attn_short_kernel(AttnP<T> a) {
+  extern __shared__ __align__(16) char lds[];
+  char* kt = lds;
+  char* vt = lds + NT * 32 * tile_pitch<T, EP>();
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t bh = blockIdx.x / a.splits, part = blockIdx.x % a.splits;   // splits: of the rows
+  const int64_t b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const Keys<T> keys(a, b, hk);
+  uint32_t bits[NT];
+  {
+    Stage<T, EP, NT * 32, kThreads> ks;
+    ks.load(tid, a.E, a.wide_kv, [&](int i) { return keys.kept(a, i) ? keys.k + i * a.km.row : nullptr; });
+    ks.write(kt, tid, [](int) { return true; });
+    ks.load(tid, a.E, a.wide_kv, [&](int i) { return keys.kept(a, i) ? keys.v + i * a.vm.row : nullptr; });
+    ks.write(vt, tid, [](int) { return true; });
+#pragma unroll
+    for (int s = 0; s < NT; ++s) bits[s] = static_cast<uint32_t>(__ballot(keys.kept(a, s * 32 + (lane & 31))));
+  }
+  __syncthreads();
+  const int t_last = (part + 1) * a.tiles_each < static_cast<uint32_t>(a.row_tiles) ? (part + 1) * a.tiles_each : a.row_tiles;
+  typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+  auto fetch = [&](int t) {
+    const uint32_t r = static_cast<uint32_t>(t) * 32 + (lane & 31);
+    const QRow w = q_row(a, hk, r);
+    row_frags<T, EP>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, r < a.rows, a.E, a.wide_q, qf);
+  };
+  int t = part * a.tiles_each + wave;
+  if (t < t_last) fetch(t);
+  for (; t < t_last; t += 4) {
+    const uint32_t r = static_cast<uint32_t>(t) * 32 + (lane & 31);
+    const bool row_ok = r < a.rows;
+    const QRow w_ = q_row(a, hk, r);
+    float w[NT][16], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      const f32x16 x = tile_dot<T, EP>(kt, s * 32, qf, lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[s][i] = x[i];
+    }
+    if (t + 4 < t_last) fetch(t + 4);
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      drop_keys(w[s], bits[s], lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, w[s][i]);
+    }
+    m = column_max(m) * a.c;
+    const float base = m == -INFINITY ? 0.0f : m;
+    f32x16 o[EP / 32] = {};
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        w[s][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[s][i], a.c, -base));
+        l += w[s][i];
+      }
+      tile_accum<EP>(vt, s * 32, w[s], o, lane, T{});
+    }
+    l = column_sum(l);
+    store_col<T, EP>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
+                     softmax_scale(l), lane);
+    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
+  }
+}
+
+// ---- at most 32 rows share a key head, more keys ---------------------------------
+// Bound by the bytes of K and V. Each wavefront walks 32 keys at a time of its
+// own through its own part of LDS, without barriers, so that wavefronts drift
+// apart and loads stay in flight; the four are joined at the end, and the
+// workgroups of an (entry, key head) by attn_join_kernel.
+template <typename T, int EP>
+__global__ __launch_bounds__(kThreads) void attn_few_kernel(AttnP<T> a) {
+  extern __shared__ __align__(16) char lds[];
+  constexpr int kMine = 2 * 32 * tile_pitch<T, EP>();
+  static_assert(kMine >= 32 * EP * 4, "the result fits where the tiles were");
+  __shared__ float sm[4][32], sl[4][32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  char* kt = lds + wave * kMine;
+  char* vt = kt + 32 * tile_pitch<T, EP>();
+  const uint32_t bh = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits;
+  const int64_t b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const uint32_t r = lane & 31;
+  const QRow w_ = q_row(a, hk, r);
+  const Keys<T> keys(a, b, hk);
+  typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+  row_frags<T, EP>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, r < a.rows, a.E, a.wide_q, qf);
+  f32x16 o[EP / 32] = {};
+  float m = -INFINITY, l = 0.0f;
+  const int t_last = (split + 1) * a.tiles_each < a.key_tiles ? (split + 1) * a.tiles_each : a.key_tiles;
+  Stage<T, EP, 32, 64> ks, vs;
+  bool keep = false;   // of key lane % 32
+  auto fetch = [&](int t) {
+    const int64_t k0 = static_cast<int64_t>(t) * 32;
+    keep = keys.kept(a, k0 + (lane & 31));
+    ks.load(lane, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.k + (k0 + i) * a.km.row : nullptr; });
+    vs.load(lane, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.v + (k0 + i) * a.vm.row : nullptr; });
+  };
+  int t = split * a.tiles_each + wave;
+  if (t < t_last) fetch(t);
+  for (; t < t_last; t += 4) {
+    const uint32_t bits = static_cast<uint32_t>(__ballot(keep));
+    ks.write(kt, lane, [&](int i) { return (bits >> i) & 1u; });
+    vs.write(vt, lane, [&](int i) { return (bits >> i) & 1u; });
+    lds_wave_sync();
+    if (t + 4 < t_last) fetch(t + 4);
+    if (bits != 0) {
+      const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
+      float w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = x[i];
+      drop_keys(w, bits, lane);
+      softmax_step(w, a.c, m, l, o);
+      tile_accum<EP>(vt, 0, w, o, lane, T{});
+    }
+    lds_wave_sync();
+  }
+  l = column_sum(l);
+  float* mine = reinterpret_cast<float*>(kt);
+#pragma unroll
+  for (int et = 0; et < EP / 32; ++et) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine[(lane & 31) * EP + et * 32 + (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5)] = o[et][i];
+  }
+  if (lane < 32) {
+    sm[wave][lane] = m;
+    sl[wave][lane] = l;
+  }
+  __syncthreads();
+  const int rows = static_cast<int>(a.rows);
+  for (int i = tid; i < rows * EP; i += kThreads) {
+    const int row = i / EP, e = i - row * EP;
+    float top = sm[0][row];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) top = fmaxf(top, sm[q][row]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float v = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float f = __builtin_amdgcn_exp2f(sm[q][row] - base);
+      sum = __builtin_fmaf(f, sl[q][row], sum);
+      v = __builtin_fmaf(f, reinterpret_cast<const float*>(lds + q * kMine)[i], v);
+    }
+    const QRow u = q_row(a, hk, row);
+    if (a.splits > 1) {
+      const int64_t at = (static_cast<int64_t>(split) * a.B * a.Hkv + bh) * rows + row;
+      a.part[at * EP + e] = v;
+      if (e == 0) {
+        a.part_ml[at * 2] = top;
+        a.part_ml[at * 2 + 1] = sum;
+      }
+    } else {
+      if (e < a.E) Store<T>::put(a.out, ((b * a.Lq + u.q) * a.Hq + u.h) * a.E + e, v * softmax_scale(sum));
+      if (e == 0 && a.lse) a.lse[(b * a.Hq + u.h) * a.Lq + u.q] = softmax_lse(top, sum);
+    }
+  }
+}
+
+// Joins the at most 64 parts of a row, in order: one wavefront per row, lane s
+// holding part s's maximum and sum, lanes over the values.
+template <typename T, int EP>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnP<T> a) {
   const int lane = threadIdx.x & 63;
   const int64_t i = blockIdx.x * int64_t(kThreads / 64) + (threadIdx.x >> 6);
   const int64_t total = a.B * a.Hkv * a.rows;
   if (i >= total) return;
-  const int64_t bh = i / a.rows, r = i - bh * a.rows;
-  const int64_t b = bh / a.Hkv, hs = r / a.Lq, qi = r - hs * a.Lq;
-  const int64_t h = (bh - b * a.Hkv) * a.share + hs;
-  float m = -INFINITY;
-  for (int s = 0; s < parts; ++s) m = fmaxf(m, a.part_ml[(s * total + i) * 2]);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, v[2] = {0.0f, 0.0f};
-  for (int s = 0; s < parts; ++s) {
-    const int64_t at = s * total + i;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[at * 2] - base);
-    l = __builtin_fmaf(f, a.part_ml[at * 2 + 1], l);
+  const int64_t bh = i / a.rows, b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const QRow u = q_row(a, hk, static_cast<uint32_t>(i - bh * a.rows));
+  const bool in = lane < a.splits;
+  const float pm = in ? a.part_ml[(lane * total + i) * 2] : -INFINITY;
+  float m = pm;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (lane + 64 * k < EP) v[k] = __builtin_fmaf(f, a.part[at * EP + lane + 64 * k], v[k]);
+  for (int d = 32; d >= 1; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
+  const float f = __builtin_amdgcn_exp2f(pm - (m == -INFINITY ? 0.0f : m));
+  float l = in ? f * a.part_ml[(lane * total + i) * 2 + 1] : 0.0f;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) l += __shfl_xor(l, d);
+  constexpr int kV = (EP + 63) / 64;
+  float v[kV] = {};
+  const float* p = a.part + i * EP + lane;
+#pragma unroll 8
+  for (int s = 0; s < a.splits; ++s) {
+    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+      if (lane + 64 * k < EP) v[k] = __builtin_fmaf(fs, p[s * total * EP + 64 * k], v[k]);
   }
-  const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const float scale = softmax_scale(l);
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < kV; ++k)
     if (lane + 64 * k < a.E)
-      Store<T>::put(a.out, ((b * a.Lq + qi) * a.Hq + h) * a.E + lane + 64 * k, v[k] * f);
-  if (a.lse && lane == 0)
-    a.lse[(b * a.Hq + h) * a.Lq + qi] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+      Store<T>::put(a.out, ((b * a.Lq + u.q) * a.Hq + u.h) * a.E + lane + 64 * k, v[k] * scale);
+  if (a.lse && lane == 0) a.lse[(b * a.Hq + u.h) * a.Lq + u.q] = softmax_lse(m, l);
 }
 
 // out = 0, lse = -inf when there is no key at all
@@ -172,26 +355,46 @@ __global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n,
 }
 
 // ---- host -------------------------------------------------------------------
+enum class AttnPlan { kShort, kFew, kRows };
 struct AttnCut {
-  bool few;          // at most 32 rows share a key head: wavefronts over keys
-  int tk, splits, parts, key_tiles, row_tiles, tiles_each;
+  AttnPlan plan;
+  int splits, parts, key_tiles, row_tiles, tiles_each;
 };
-// With few rows the wavefronts take different keys; the key axis is split
-// further until about two workgroups per compute unit run.
 AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, size_t es) {
   AttnCut k{};
-  const int64_t rows = Lq * (Hq / Hkv);
-  k.few = rows <= 32;
-  k.tk = k.few ? 128 : (es == 2 ? 64 : 32);
-  k.key_tiles = static_cast<int>(cdiv(Lk, k.tk));
-  k.row_tiles = static_cast<int>(cdiv(rows, k.few ? 32 : 128));
-  const int64_t groups = std::max<int64_t>(1, B * Hkv * k.row_tiles);
+  const int64_t rows = Lq * (Hq / Hkv), heads = std::max<int64_t>(1, B * Hkv);
   int64_t splits = 1;
-  if (groups < 256) splits = std::min<int64_t>(k.key_tiles, cdiv(512, groups));
-  splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
-  k.tiles_each = static_cast<int>(cdiv(std::max(1, k.key_tiles), splits));
-  k.splits = static_cast<int>(cdiv(std::max(1, k.key_tiles), k.tiles_each));
-  k.parts = k.few ? 4 * k.splits : (k.splits > 1 ? k.splits : 0);
+  if (Lk <= 128) {
+    // Row tiles of 32; a workgroup's four wavefronts take up to 32 each, so
+    // that staging the keys is a small part, but all compute units get some.
+    k.plan = AttnPlan::kShort;
+    k.row_tiles = static_cast<int>(cdiv(rows, 32));
+    const int64_t each = std::max<int64_t>(4, std::min<int64_t>(128, heads * k.row_tiles / 1024));
+    splits = cdiv(k.row_tiles, each);
+    k.tiles_each = static_cast<int>(cdiv(k.row_tiles, splits));
+    k.splits = static_cast<int>(cdiv(k.row_tiles, k.tiles_each));
+    return k;
+  }
+  if (rows <= 32) {
+    // Keys in tiles of 32, four at a time per workgroup; about four
+    // workgroups per compute unit keep enough loads in flight.
+    k.plan = AttnPlan::kFew;
+    k.key_tiles = static_cast<int>(cdiv(Lk, 32));
+    splits = std::max<int64_t>(1, std::min<int64_t>(64, std::min<int64_t>(cdiv(k.key_tiles, 8), cdiv(1024, heads))));
+    k.tiles_each = static_cast<int>(cdiv(cdiv(k.key_tiles, splits), 4) * 4);
+    k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
+  } else {
+    // Few row tiles: the key axis is split until about two workgroups per
+    // compute unit run.
+    k.plan = AttnPlan::kRows;
+    k.key_tiles = static_cast<int>(cdiv(Lk, es == 2 ? 64 : 32));
+    k.row_tiles = static_cast<int>(cdiv(rows, 128));
+    const int64_t groups = heads * k.row_tiles;
+    if (groups < 256) splits = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(k.key_tiles, 64), cdiv(512, groups)));
+    k.tiles_each = static_cast<int>(cdiv(k.key_tiles, splits));
+    k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
+  }
+  k.parts = k.splits > 1 ? k.splits : 0;
   return k;
 }
 
@@ -220,17 +423,15 @@ template <typename T> AttnP<T> attn_params(const gspn_attn_args& a, const AttnCu
   return p;
 }
 
-template <typename T, int EP, int WR, int TK>
-hipError_t run_fwd(const AttnP<T>& p, hipStream_t stream, Tracer* tr) {
-  auto kern = attn_fwd_kernel<T, EP, WR, TK>;
-  constexpr int bytes = 2 * TK * tile_pitch<T, EP>();
+template <typename T>
+hipError_t run(void (*kern)(AttnP<T>), const char* name, int bytes, int64_t grid, const AttnP<T>& p,
+               hipStream_t stream, Tracer* tr) {
   if (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
   }
-  const int64_t grid = p.B * p.Hkv * p.splits * p.row_tiles;
-  tr->before(stream, "attn_fwd", p.B * p.Hkv);
+  tr->before(stream, name, p.B * p.Hkv);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, stream, p);
   tr->after(stream);
   return hipGetLastError();
@@ -240,19 +441,29 @@ template <typename T, int EP>
 hipError_t attn_ep_run(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr) {
   const AttnCut k = cut_attn(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, sizeof(T));
   AttnP<T> p = attn_params<T>(a, k);
-  const int64_t total = p.B * p.Hkv * p.rows;
+  const int64_t heads = p.B * p.Hkv, total = heads * p.rows;
   if (k.parts) {
     p.part = static_cast<float*>(ws);
     p.part_ml = p.part + k.parts * total * EP;
   }
-  hipError_t e = k.few ? run_fwd<T, EP, 1, 128>(p, stream, tr)
-                       : run_fwd<T, EP, 4, sizeof(T) == 2 ? 64 : 32>(p, stream, tr);
+  constexpr int row = 2 * tile_pitch<T, EP>();   // LDS bytes of a key's K and V
+  hipError_t e;
+  if (k.plan == AttnPlan::kShort) {
+    switch ((p.Lk + 31) / 32) {
+      case 1: return run<T>(attn_short_kernel<T, EP, 1>, "attn_short", 32 * row, heads * k.splits, p, stream, tr);
+      case 2: return run<T>(attn_short_kernel<T, EP, 2>, "attn_short", 64 * row, heads * k.splits, p, stream, tr);
+      case 3: return run<T>(attn_short_kernel<T, EP, 3>, "attn_short", 96 * row, heads * k.splits, p, stream, tr);
+      default: return run<T>(attn_short_kernel<T, EP, 4>, "attn_short", 128 * row, heads * k.splits, p, stream, tr);
+    }
+  }
+  if (k.plan == AttnPlan::kFew) {
+    e = run<T>(attn_few_kernel<T, EP>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
+  } else {
+    constexpr int TK = sizeof(T) == 2 ? 64 : 32;
+    e = run<T>(attn_fwd_kernel<T, EP, TK>, "attn_fwd", TK * row, heads * k.splits * k.row_tiles, p, stream, tr);
+  }
   if (e != hipSuccess || !k.parts) return e;
-  tr->before(stream, "attn_join", total);
-  hipLaunchKernelGGL(attn_join_kernel<T>, dim3(static_cast<unsigned>(cdiv(total, kThreads / 64))),
-                     dim3(kThreads), 0, stream, p, k.parts, EP);
-  tr->after(stream);
-  return hipGetLastError();
+  return run<T>(attn_join_kernel<T, EP>, "attn_join", 0, cdiv(total, kThreads / 64), p, stream, tr);
 }
 
 template <typename T> hipError_t attn_dt(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr) {

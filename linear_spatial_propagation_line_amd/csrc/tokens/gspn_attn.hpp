@@ -141,10 +141,30 @@ __device__ __forceinline__ void tile_accum(const char* tile, int row0, const flo
   }
 }
 
-// the other half-wavefront's value of the same column
-__device__ __forceinline__ float other_half(float v) {
+// a column's maximum and sum over both half-wavefronts
+__device__ __forceinline__ float column_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// scores of 32 keys with the dropped ones (bits: kept keys) at -inf
+__device__ __forceinline__ void drop_keys(float (&w)[16], uint32_t bits, int lane) {
+  if (bits != 0xffffffffu) {
+    const uint32_t mine = bits >> (4 * (lane >> 5));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = (mine >> ((i & 3) + 8 * (i >> 2))) & 1u ? w[i] : -INFINITY;
+  }
+}
+
+// 1 / l for the softmax's sum: 0 for a row that kept no key, NaN stays NaN
+__device__ __forceinline__ float softmax_scale(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+// the log of the softmax's sum from the running maximum (base 2) and sum
+__device__ __forceinline__ float softmax_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // A lane column of acc (EP values of one row) times f into row[0 .. E), or

@@ -44,21 +44,29 @@ template <typename T> struct Keys {   // K, V and the kept keys of one (entry, k
   __device__ __forceinline__ Keys(const AttnP<T>& a, int64_t b, int hk)
       : k(a.k + b * a.km.batch + hk * a.km.head), v(a.v + b * a.vm.batch + hk * a.vm.head),
         mask(a.mask ? a.mask + b * a.mask_batch : nullptr) {}
+  __device__ __forceinline__ int64_t clamp(const AttnP<T>& a, int64_t key) const {
+    return key < a.Lk ? key : a.Lk - 1;
+  }
   __device__ __forceinline__ bool kept(const AttnP<T>& a, int64_t key) const {
     return key < a.Lk && (!mask || mask[key] != 0);
   }
 };
 
+// The running maximum may lag behind the true one by this much (base 2): the
+// probabilities then reach 2^8, which neither fp32 sums nor bf16 operands
+// mind, and the result so far is rescaled only when it has to be.
+constexpr float kLag = 8.0f;
+
 // One step of the running softmax over 32 keys: w becomes the probabilities
 // (unnormalised, base 2 exponent against m), m and l follow, and the result
-// so far is rescaled when the maximum moved.
+// so far is rescaled when the maximum moved far.
 template <int N>
 __device__ __forceinline__ void softmax_step(float (&w)[16], float c, float& m, float& l, f32x16 (&o)[N]) {
   float top = w[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) top = fmaxf(top, w[i]);
   top = column_max(top) * c;
-  if (__any(top > m)) {
+  if (__any(top > m + kLag)) {
     const float mn = fmaxf(m, top);
     const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
     m = mn;
@@ -77,7 +85,7 @@ __device__ __forceinline__ void softmax_step(float (&w)[16], float c, float& m, 
 // ---- long key axes, many rows -------------------------------------------------
 // Four wavefronts of 32 rows each; K and V pass through LDS 64 (fp32: 32)
 // keys at a time.
-template <typename T, int EP, int TK>
+template <typename T, int EP, int TK, bool FULL>
 __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   extern __shared__ __align__(16) char lds[];
   char* kt = lds;
@@ -95,16 +103,18 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   const Keys<T> keys(a, b, hk);
 
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
-  row_frags<T, EP>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
+  row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, true, a.E, a.wide_q, qf);
   f32x16 o[EP / 32] = {};
   float m = -INFINITY, l = 0.0f;
-  const int t_first = split * a.tiles_each;
-  const int t_last = t_first + a.tiles_each < a.key_tiles ? t_first + a.tiles_each : a.key_tiles;
+  int64_t k_lo, k_hi;
+  key_range(keys.mask, a.Lk, tid, &k_lo, &k_hi);
+  const int t_first = max(split * a.tiles_each, static_cast<int>(k_lo / TK));
+  const int t_last = min((split + 1) * a.tiles_each, static_cast<int>((k_hi + TK - 1) / TK));
   Stage<T, EP, TK, kThreads> ks, vs;
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.k + (k0 + i) * a.km.row : nullptr; });
-    vs.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.v + (k0 + i) * a.vm.row : nullptr; });
+    ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.k + keys.clamp(a, k0 + i) * a.km.row; });
+    vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, k0 + i) * a.vm.row; });
   };
   if (t_first < t_last) fetch(t_first);
   for (int t = t_first; t < t_last; ++t) {
@@ -130,15 +140,170 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   l = column_sum(l);
   if (a.splits > 1) {
     const int64_t at = (split * a.B * a.Hkv + bh) * a.rows + r;
-    store_col<float, EP>(a.part + at * EP, row_ok, true, EP, true, o, 1.0f, lane);
+    store_col<float, EP, true>(a.part + at * EP, row_ok, true, EP, true, o, 1.0f, lane);
     if (row_ok && lane < 32) {
       a.part_ml[at * 2] = m;
       a.part_ml[at * 2 + 1] = l;
     }
   } else {
-    store_col<T, EP>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
+    store_col<T, EP, FULL>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
                      softmax_scale(l), lane);
     if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
+  }
+}
+
+// ---- long key axes, rows enough to fill the chip, bf16 ---------------------------
+// 64 rows per wavefront in two column tiles, so that every K or V fragment read
+// from LDS feeds two products: with one, the reads alone (1 KB per 32-cycle
+// product and SIMD) would take all of LDS's 128 bytes per cycle. One wavefront
+// per SIMD then holds everything (256 registers of results and queries at
+// E = 128), so products and exponentials have to overlap inside it: the
+// products of P and V lag one subtile of 32 keys behind, and those of K and Q
+// run one ahead, of the exponentials that stand between them.
+template <int EP>
+__global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a) {
+  using T = bf16_t;
+  extern __shared__ __align__(16) char lds[];
+  constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int rt = static_cast<int>(blk % a.row_tiles);
+  const int64_t bh = blk / a.row_tiles, b = bh / a.Hkv;
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const Keys<T> keys(a, b, hk);
+  const uint32_t r0 = (static_cast<uint32_t>(rt) * 4 + wave) * 64 + (lane & 31);
+  Mma<T>::Frag qf[2][EP / 16];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const QRow w = q_row(a, hk, r0 + 32 * u);
+    row_frags<T, EP, true>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, EP, true, qf[u]);
+  }
+  int64_t k_lo, k_hi;
+  key_range(keys.mask, a.Lk, tid, &k_lo, &k_hi);
+  const int t0 = static_cast<int>(k_lo / 64), t1 = static_cast<int>((k_hi + 63) / 64);
+
+  f32x16 o[2][kN] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  Stage<T, EP, 64, kThreads> ks, vs;
+  bool keep = false;
+  auto fetch = [&](int t) {
+    const int64_t k0 = static_cast<int64_t>(t) * 64;
+    keep = keys.kept(a, k0 + lane);
+    ks.template load<true>(tid, EP, true, [&](int i) { return keys.k + keys.clamp(a, k0 + i) * a.km.row; });
+    vs.template load<true>(tid, EP, true, [&](int i) { return keys.v + keys.clamp(a, k0 + i) * a.vm.row; });
+  };
+  uint64_t bits = 0, bits_next = 0;   // kept keys of this tile and of the one in staging
+  auto stage = [&](int t) {
+    bits_next = __ballot(keep);
+    char* k = lds + (t & 1) * 2 * kTile;
+    ks.write(k, tid, [&](int i) { return (bits_next >> i) & 1u; });
+    vs.write(k + kTile, tid, [&](int i) { return (bits_next >> i) & 1u; });
+  };
+  f32x16 x[2];          // scores of the subtile at hand
+  uint32_t p[2][8];     // probabilities of the subtile before, as bf16 pairs
+  auto scores = [&](int t, int s) {
+    const char* k = lds + (t & 1) * 2 * kTile;
+    x[0] = f32x16{};
+    x[1] = f32x16{};
+#pragma unroll
+    for (int j = 0; j < EP / 16; ++j) {
+      const Mma<T>::Frag f = tile_frag<T, EP>(k, s * 32, j, lane);
+      x[0] = Mma<T>::mma(f, qf[0][j], x[0]);
+      x[1] = Mma<T>::mma(f, qf[1][j], x[1]);
+    }
+  };
+  auto values = [&](int t, int s) {   // o += V^T P of subtile s of tile t
+    const char* v = lds + (t & 1) * 2 * kTile + kTile;
+    const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
+    constexpr int pitch = tile_pitch<T, EP>();
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const char* q = v + (s * 32 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
+      const bf16x8 p0 = __builtin_bit_cast(bf16x8, u32x4{p[0][4 * kb], p[0][4 * kb + 1], p[0][4 * kb + 2], p[0][4 * kb + 3]});
+      const bf16x8 p1 = __builtin_bit_cast(bf16x8, u32x4{p[1][4 * kb], p[1][4 * kb + 1], p[1][4 * kb + 2], p[1][4 * kb + 3]});
+#pragma unroll
+      for (int et = 0; et < kN; ++et) {
+        const v4i16 lo = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64));
+        const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
+        const bf16x8 f = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+        o[0][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p0, o[0][et], 0, 0, 0);
+        o[1][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p1, o[1][et], 0, 0, 0);
+      }
+    }
+  };
+  if (t0 < t1) {
+    fetch(t0);
+    stage(t0);
+    __syncthreads();
+    if (t0 + 1 < t1) fetch(t0 + 1);
+    scores(t0, 0);
+  }
+  for (int t = t0; t < t1; ++t) {
+    bits = bits_next;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float w[2][16];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[u][i] = x[u][i];
+        drop_keys(w[u], static_cast<uint32_t>(bits >> (32 * s)), lane);
+      }
+      // the subtile before: its values are in this tile's buffer or the other
+      if (s == 1) values(t, 0);
+      else if (t > t0) values(t - 1, 1);
+      float top[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        top[u] = w[u][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top[u] = fmaxf(top[u], w[u][i]);
+        top[u] = column_max(top[u]) * a.c;
+      }
+      if (s == 0) {
+        // all wavefronts are through with the other buffer
+        lds_barrier();
+        if (t + 1 < t1) stage(t + 1);
+        if (t + 2 < t1) fetch(t + 2);
+      } else {
+        lds_barrier();   // and now it holds the next tile
+      }
+      if (__any(top[0] > m[0] + kLag || top[1] > m[1] + kLag)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float mn = fmaxf(m[u], top[u]);
+          const float f = __builtin_amdgcn_exp2f(m[u] - (mn == -INFINITY ? 0.0f : mn));
+          m[u] = mn;
+          l[u] *= f;
+#pragma unroll
+          for (int et = 0; et < kN; ++et) o[u][et] *= f;
+        }
+      }
+      if (s == 0) scores(t, 1);
+      else if (t + 1 < t1) scores(t + 1, 0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float base = m[u] == -INFINITY ? 0.0f : m[u];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          w[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[u][i], a.c, -base));
+          l[u] += w[u][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[u][i] = pack_bf16x2(w[u][2 * i], w[u][2 * i + 1]);
+      }
+    }
+  }
+  if (t0 < t1) values(t1 - 1, 1);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t r = r0 + 32 * u;
+    const bool row_ok = r < a.rows;
+    const QRow w = q_row(a, hk, r);
+    const float sum = column_sum(l[u]);
+    store_col<T, EP, true>(a.out + ((b * a.Lq + w.q) * a.Hq + w.h) * EP, row_ok, true, EP, true, o[u],
+                           softmax_scale(sum), lane);
+    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w.h) * a.Lq + w.q] = softmax_lse(m[u], sum);
   }
 }
 
@@ -147,68 +312,76 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
 // tiles of its own, with no barrier after the keys are staged: all scores of
 // a row are in registers, so its maximum is known before the first exponential.
 // Bound by the rows' bytes (q in, out back); the next tile's q is loaded ahead.
-template <typename T, int EP, int NT>
-__global__ __launch_bounds__(kThreads) void attn_short_kernel(AttnP<T> a) {
+template <typename T, int EP, int NT, bool FULL>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_kernel(AttnP<T> a) {
   extern __shared__ __align__(16) char lds[];
   char* kt = lds;
   char* vt = lds + NT * 32 * tile_pitch<T, EP>();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const uint32_t bh = blockIdx.x / a.splits, part = blockIdx.x % a.splits;   // splits: of the rows
+  // adjacent workgroups take the heads of the same rows, which share lines
+  // and memory pages; splits: of the rows
+  const uint32_t heads = static_cast<uint32_t>(a.B) * a.Hkv, bh = blockIdx.x % heads, part = blockIdx.x / heads;
   const int64_t b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const Keys<T> keys(a, b, hk);
-  uint32_t bits[NT];
+  __shared__ __align__(16) float bias[NT * 32];   // 0 for a kept key, -inf for a dropped one
   {
     Stage<T, EP, NT * 32, kThreads> ks;
-    ks.load(tid, a.E, a.wide_kv, [&](int i) { return keys.kept(a, i) ? keys.k + i * a.km.row : nullptr; });
-    ks.write(kt, tid, [](int) { return true; });
-    ks.load(tid, a.E, a.wide_kv, [&](int i) { return keys.kept(a, i) ? keys.v + i * a.vm.row : nullptr; });
-    ks.write(vt, tid, [](int) { return true; });
-#pragma unroll
-    for (int s = 0; s < NT; ++s) bits[s] = static_cast<uint32_t>(__ballot(keys.kept(a, s * 32 + (lane & 31))));
+    Stage<T, EP, NT * 32, kThreads> vs;
+    ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.k + keys.clamp(a, i) * a.km.row; });
+    vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, i) * a.vm.row; });
+    ks.write(kt, tid, [&](int i) { return keys.kept(a, i); });
+    vs.write(vt, tid, [&](int i) { return keys.kept(a, i); });
+    if (tid < NT * 32) bias[tid] = keys.kept(a, tid) ? 0.0f : -INFINITY;
   }
   __syncthreads();
   const int t_last = (part + 1) * a.tiles_each < static_cast<uint32_t>(a.row_tiles) ? (part + 1) * a.tiles_each : a.row_tiles;
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+  int E = a.E;
+  QRow next;
   auto fetch = [&](int t) {
-    const uint32_t r = static_cast<uint32_t>(t) * 32 + (lane & 31);
-    const QRow w = q_row(a, hk, r);
-    row_frags<T, EP>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, r < a.rows, a.E, a.wide_q, qf);
+    next = q_row(a, hk, static_cast<uint32_t>(t) * 32 + (lane & 31));
+    row_frags<T, EP, FULL>(a.q + b * a.qm.batch + next.q * a.qm.row + next.h * a.qm.head, true, E, a.wide_q, qf);
   };
   int t = part * a.tiles_each + wave;
   if (t < t_last) fetch(t);
   for (; t < t_last; t += 4) {
-    const uint32_t r = static_cast<uint32_t>(t) * 32 + (lane & 31);
-    const bool row_ok = r < a.rows;
-    const QRow w_ = q_row(a, hk, r);
+    // The keys' fragments and the comparisons with E are the same for every
+    // tile; kept in registers they would cost the occupancy that hides the
+    // rows' latency, so they are taken anew.
+    asm volatile("" : "+s"(E) : : "memory");
+    const bool row_ok = static_cast<uint32_t>(t) * 32 + (lane & 31) < a.rows;
+    const QRow w_ = next;
     float w[NT][16], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
       const f32x16 x = tile_dot<T, EP>(kt, s * 32, qf, lane);
+      // dropped keys are zeros in LDS, so x is finite there
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[s][i] = x[i];
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(bias + s * 32 + 8 * j + 4 * (lane >> 5));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[s][4 * j + i] = __builtin_fmaf(x[4 * j + i], a.c, y[i]);
+          m = fmaxf(m, w[s][4 * j + i]);
+        }
+      }
     }
     if (t + 4 < t_last) fetch(t + 4);
-#pragma unroll
-    for (int s = 0; s < NT; ++s) {
-      drop_keys(w[s], bits[s], lane);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = fmaxf(m, w[s][i]);
-    }
-    m = column_max(m) * a.c;
+    m = column_max(m);
     const float base = m == -INFINITY ? 0.0f : m;
     f32x16 o[EP / 32] = {};
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        w[s][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[s][i], a.c, -base));
+        w[s][i] = __builtin_amdgcn_exp2f(w[s][i] - base);
         l += w[s][i];
       }
       tile_accum<EP>(vt, s * 32, w[s], o, lane, T{});
     }
     l = column_sum(l);
-    store_col<T, EP>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
+    store_col<T, EP, FULL>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, E, a.wide_o, o,
                      softmax_scale(l), lane);
     if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
   }
@@ -219,7 +392,7 @@ __global__ __launch_bounds__(kThreads) void attn_short_kernel(AttnP<T> a) {
 // own through its own part of LDS, without barriers, so that wavefronts drift
 // apart and loads stay in flight; the four are joined at the end, and the
 // workgroups of an (entry, key head) by attn_join_kernel.
-template <typename T, int EP>
+template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads) void attn_few_kernel(AttnP<T> a) {
   extern __shared__ __align__(16) char lds[];
   constexpr int kMine = 2 * 32 * tile_pitch<T, EP>();
@@ -236,17 +409,17 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(AttnP<T> a) {
   const QRow w_ = q_row(a, hk, r);
   const Keys<T> keys(a, b, hk);
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
-  row_frags<T, EP>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, r < a.rows, a.E, a.wide_q, qf);
+  row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, true, a.E, a.wide_q, qf);
   f32x16 o[EP / 32] = {};
   float m = -INFINITY, l = 0.0f;
-  const int t_last = (split + 1) * a.tiles_each < a.key_tiles ? (split + 1) * a.tiles_each : a.key_tiles;
+  const int t_last = min((split + 1) * a.tiles_each, a.key_tiles);
   Stage<T, EP, 32, 64> ks, vs;
   bool keep = false;   // of key lane % 32
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * 32;
     keep = keys.kept(a, k0 + (lane & 31));
-    ks.load(lane, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.k + (k0 + i) * a.km.row : nullptr; });
-    vs.load(lane, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? keys.v + (k0 + i) * a.vm.row : nullptr; });
+    ks.template load<FULL>(lane, a.E, a.wide_kv, [&](int i) { return keys.k + keys.clamp(a, k0 + i) * a.km.row; });
+    vs.template load<FULL>(lane, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, k0 + i) * a.vm.row; });
   };
   int t = split * a.tiles_each + wave;
   if (t < t_last) fetch(t);
@@ -355,7 +528,7 @@ __global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n,
 }
 
 // ---- host -------------------------------------------------------------------
-enum class AttnPlan { kShort, kFew, kRows };
+enum class AttnPlan { kShort, kFew, kRows };   // kRows: attn_wide or attn_fwd
 struct AttnCut {
   AttnPlan plan;
   int splits, parts, key_tiles, row_tiles, tiles_each;
@@ -437,31 +610,45 @@ hipError_t run(void (*kern)(AttnP<T>), const char* name, int bytes, int64_t grid
   return hipGetLastError();
 }
 
+template <typename T, int EP, bool FULL>
+hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Tracer* tr) {
+  constexpr int row = 2 * tile_pitch<T, EP>();   // LDS bytes of a key's K and V
+  const int64_t heads = p.B * p.Hkv;
+  if (k.plan == AttnPlan::kShort) {
+    switch ((p.Lk + 31) / 32) {
+      case 1: return run<T>(attn_short_kernel<T, EP, 1, FULL>, "attn_short", 32 * row, heads * k.splits, p, stream, tr);
+      case 2: return run<T>(attn_short_kernel<T, EP, 2, FULL>, "attn_short", 64 * row, heads * k.splits, p, stream, tr);
+      case 3: return run<T>(attn_short_kernel<T, EP, 3, FULL>, "attn_short", 96 * row, heads * k.splits, p, stream, tr);
+      default: return run<T>(attn_short_kernel<T, EP, 4, FULL>, "attn_short", 128 * row, heads * k.splits, p, stream, tr);
+    }
+  }
+  if (k.plan == AttnPlan::kFew)
+    return run<T>(attn_few_kernel<T, EP, FULL>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
+  if constexpr (FULL && sizeof(T) == 2) {
+    // a workgroup of the wide kernel takes 256 rows and a compute unit
+    if (heads * cdiv(p.rows, 256) >= 192) {
+      p.row_tiles = static_cast<int>(cdiv(p.rows, 256));
+      return run<T>(attn_wide_kernel<EP>, "attn_wide", 128 * row, heads * p.row_tiles, p, stream, tr);
+    }
+  }
+  constexpr int TK = sizeof(T) == 2 ? 64 : 32;
+  return run<T>(attn_fwd_kernel<T, EP, TK, FULL>, "attn_fwd", TK * row, heads * k.splits * k.row_tiles, p, stream, tr);
+}
+
 template <typename T, int EP>
 hipError_t attn_ep_run(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr) {
   const AttnCut k = cut_attn(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, sizeof(T));
   AttnP<T> p = attn_params<T>(a, k);
-  const int64_t heads = p.B * p.Hkv, total = heads * p.rows;
+  const int64_t total = p.B * p.Hkv * p.rows;
   if (k.parts) {
     p.part = static_cast<float*>(ws);
     p.part_ml = p.part + k.parts * total * EP;
   }
-  constexpr int row = 2 * tile_pitch<T, EP>();   // LDS bytes of a key's K and V
+  // whole 16-byte pieces everywhere and no padding of the head
+  const bool full = p.E == EP && p.wide_q && p.wide_kv && p.wide_o;
   hipError_t e;
-  if (k.plan == AttnPlan::kShort) {
-    switch ((p.Lk + 31) / 32) {
-      case 1: return run<T>(attn_short_kernel<T, EP, 1>, "attn_short", 32 * row, heads * k.splits, p, stream, tr);
-      case 2: return run<T>(attn_short_kernel<T, EP, 2>, "attn_short", 64 * row, heads * k.splits, p, stream, tr);
-      case 3: return run<T>(attn_short_kernel<T, EP, 3>, "attn_short", 96 * row, heads * k.splits, p, stream, tr);
-      default: return run<T>(attn_short_kernel<T, EP, 4>, "attn_short", 128 * row, heads * k.splits, p, stream, tr);
-    }
-  }
-  if (k.plan == AttnPlan::kFew) {
-    e = run<T>(attn_few_kernel<T, EP>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
-  } else {
-    constexpr int TK = sizeof(T) == 2 ? 64 : 32;
-    e = run<T>(attn_fwd_kernel<T, EP, TK>, "attn_fwd", TK * row, heads * k.splits * k.row_tiles, p, stream, tr);
-  }
+  if (full) e = attn_plan_run<T, EP, true>(p, k, stream, tr);
+  else e = attn_plan_run<T, EP, false>(p, k, stream, tr);
   if (e != hipSuccess || !k.parts) return e;
   return run<T>(attn_join_kernel<T, EP>, "attn_join", 0, cdiv(total, kThreads / 64), p, stream, tr);
 }

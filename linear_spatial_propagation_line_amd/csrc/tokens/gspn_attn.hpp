@@ -52,10 +52,12 @@ template <> struct Mma<float> {
 template <typename T, int EP> constexpr int tile_pitch() { return EP * static_cast<int>(sizeof(T)) + 16; }
 
 // 16 bytes of row values e0 .. : whole when `wide`, else value by value with
-// the row's end honoured (a value past E is 0)
-template <typename T>
+// the row's end honoured (a value past E is 0). FULL: the row holds all the
+// values that a tile has room for and is 16-byte aligned, no questions asked.
+template <typename T, bool FULL>
 __device__ __forceinline__ u32x4 load16(const T* row, int e0, int E, bool wide) {
   constexpr int kPer = 16 / sizeof(T);
+  if constexpr (FULL) return *reinterpret_cast<const u32x4*>(row + e0);
   u32x4 v = {0u, 0u, 0u, 0u};
   if (wide) {
     if (e0 < E) v = *reinterpret_cast<const u32x4*>(row + e0);
@@ -71,15 +73,21 @@ __device__ __forceinline__ u32x4 load16(const T* row, int e0, int E, bool wide) 
   return v;
 }
 
-// a lane's fragments of one row in global memory (zeros when !keep)
-template <typename T, int EP>
+// a lane's fragments of one row in global memory (zeros when !keep; with FULL
+// the row is always read, so it has to be one that exists)
+template <typename T, int EP, bool FULL>
 __device__ __forceinline__ void row_frags(const T* row, bool keep, int E, bool wide,
                                           typename Mma<T>::Frag (&f)[EP / Mma<T>::kChunk]) {
   const int hh = (threadIdx.x & 63) >> 5;
 #pragma unroll
   for (int j = 0; j < EP / Mma<T>::kChunk; ++j) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (keep) v = load16(row, j * Mma<T>::kChunk + hh * Mma<T>::kPer, E, wide);
+    if constexpr (FULL) {
+      const u32x4 u = load16<T, true>(row, j * Mma<T>::kChunk + hh * Mma<T>::kPer, E, wide);
+      v = keep ? u : v;
+    } else if (keep) {
+      v = load16<T, false>(row, j * Mma<T>::kChunk + hh * Mma<T>::kPer, E, wide);
+    }
     f[j] = __builtin_bit_cast(typename Mma<T>::Frag, v);
   }
 }
@@ -160,6 +168,47 @@ __device__ __forceinline__ void drop_keys(float (&w)[16], uint32_t bits, int lan
   }
 }
 
+// The first and one past the last key of [0, Lk) that the mask keeps (0, 0 if
+// none), found by the whole workgroup; tiles outside need not be looked at.
+__device__ __forceinline__ void key_range(const uint8_t* mask, int64_t Lk, int tid, int64_t* first,
+                                          int64_t* last) {
+  __shared__ int lo[4], hi[4];
+  int a = static_cast<int>(Lk), b = 0;
+  if (mask) {
+    for (int k = tid; k < Lk; k += 256) {
+      const bool on = mask[k] != 0;
+      a = on && k < a ? k : a;
+      b = on ? k + 1 : b;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d /= 2) {
+      const int u = __shfl_xor(a, d), v = __shfl_xor(b, d);
+      a = u < a ? u : a;
+      b = v > b ? v : b;
+    }
+    if ((tid & 63) == 0) {
+      lo[tid >> 6] = a;
+      hi[tid >> 6] = b;
+    }
+    __syncthreads();
+    a = min(min(lo[0], lo[1]), min(lo[2], lo[3]));
+    b = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
+  } else {
+    a = 0;
+    b = static_cast<int>(Lk);
+  }
+  *first = a < b ? a : 0;
+  *last = b;
+}
+
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own: the
+// logical block of a launch of n blocks such that each XCD works on
+// neighbours, which read the same keys.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t blk, uint32_t n) {
+  const uint32_t each = n / 8, left = n % 8, x = blk % 8;
+  return x * each + (x < left ? x : left) + blk / 8;
+}
+
 // 1 / l for the softmax's sum: 0 for a row that kept no key, NaN stays NaN
 __device__ __forceinline__ float softmax_scale(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
 // the log of the softmax's sum from the running maximum (base 2) and sum
@@ -171,7 +220,7 @@ __device__ __forceinline__ float softmax_lse(float m, float l) {
 // zeros when !live, whatever acc holds; nothing when !keep. Halves of the
 // wavefront swap register groups so that each lane stores 8 adjacent values;
 // `wide` needs E % 8 == 0 and a 16-byte aligned row.
-template <typename T, int EP>
+template <typename T, int EP, bool FULL>
 __device__ __forceinline__ void store_col(T* row, bool keep, bool live, int E, bool wide,
                                           const f32x16 (&acc)[EP / 32], float f, int lane) {
   const int hh = lane >> 5;
@@ -189,8 +238,8 @@ __device__ __forceinline__ void store_col(T* row, bool keep, bool live, int E, b
         v[4 + k] = live ? __uint_as_float(r[1]) : 0.0f;
       }
       const int e0 = et * 32 + h * 16 + hh * 8;
-      if (!keep || e0 >= E) continue;
-      if (wide) {
+      if (!keep || (!FULL && e0 >= E)) continue;
+      if (FULL || wide) {
         run_st<8>(row, e0, v);
       } else {
 #pragma unroll
@@ -207,21 +256,18 @@ __device__ __forceinline__ void store_col(T* row, bool keep, bool live, int E, b
 template <typename T, int EP, int ROWS, int THREADS> struct Stage {
   static constexpr int kPieces = EP * static_cast<int>(sizeof(T)) / 16;   // of one row
   static constexpr int kEach = (ROWS * kPieces + THREADS - 1) / THREADS;
+  static constexpr bool kExact = ROWS * kPieces % THREADS == 0;
   u32x4 v[kEach];
   __device__ static __forceinline__ int row(int tid, int i) { return (tid + i * THREADS) / kPieces; }
   __device__ static __forceinline__ int e0(int tid, int i) {
     return (tid + i * THREADS) % kPieces * (16 / static_cast<int>(sizeof(T)));
   }
-  // at(r): the row's address, or null for a row of zeros
-  template <typename F> __device__ __forceinline__ void load(int tid, int E, bool wide, F&& at) {
+  // at(r): the address of row r of the tile, which has to exist
+  template <bool FULL, typename F> __device__ __forceinline__ void load(int tid, int E, bool wide, F&& at) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      v[i] = u32x4{0u, 0u, 0u, 0u};
       const int r = row(tid, i);
-      if (r < ROWS) {
-        const T* p = at(r);
-        if (p) v[i] = load16(p, e0(tid, i), E, wide);
-      }
+      v[i] = load16<T, FULL>(at(kExact || r < ROWS ? r : ROWS - 1), e0(tid, i), E, wide);
     }
   }
   // keep(r): whether the row's values are kept (zeros otherwise)
@@ -229,7 +275,7 @@ template <typename T, int EP, int ROWS, int THREADS> struct Stage {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int r = row(tid, i);
-      if (r < ROWS)
+      if (kExact || r < ROWS)
         *reinterpret_cast<u32x4*>(tile + r * tile_pitch<T, EP>() + e0(tid, i) * static_cast<int>(sizeof(T))) =
             keep(r) ? v[i] : u32x4{0u, 0u, 0u, 0u};
     }

@@ -75,8 +75,8 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   const bool keep = in && (!a.mask || a.mask[b * a.mask_batch + key] != 0);
 
   typename Mma<T>::Frag kf[EP / Mma<T>::kChunk], vf[EP / Mma<T>::kChunk];
-  row_frags<T, EP>(a.k + b * a.km.batch + key * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
-  row_frags<T, EP>(a.v + b * a.vm.batch + key * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
+  row_frags<T, EP, false>(a.k + b * a.km.batch + key * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
+  row_frags<T, EP, false>(a.v + b * a.vm.batch + key * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
 
   f32x16 dk[EP / 32] = {}, dv[EP / 32] = {};
   const int t_first = split * a.tiles_each;
@@ -85,14 +85,12 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   float stat = 0.0f;
   auto fetch = [&](int t) {
     const int64_t r0 = static_cast<int64_t>(t) * TR;
-    qs.load(tid, a.E, a.wide_q, [&](int i) -> const T* {
-      if (r0 + i >= a.rows) return nullptr;
-      const Row<T> w = row_of(a, hk, r0 + i);
+    qs.template load<false>(tid, a.E, a.wide_q, [&](int i) -> const T* {
+      const Row<T> w = row_of(a, hk, r0 + i < a.rows ? r0 + i : a.rows - 1);
       return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
     });
-    gs.load(tid, a.E, a.wide_g, [&](int i) -> const T* {
-      if (r0 + i >= a.rows) return nullptr;
-      const Row<T> w = row_of(a, hk, r0 + i);
+    gs.template load<false>(tid, a.E, a.wide_g, [&](int i) -> const T* {
+      const Row<T> w = row_of(a, hk, r0 + i < a.rows ? r0 + i : a.rows - 1);
       return a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head;
     });
     if (tid < 2 * TR) {
@@ -105,8 +103,9 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   };
   if (t_first < t_last) fetch(t_first);
   for (int t = t_first; t < t_last; ++t) {
-    qs.write(qt, tid, [](int) { return true; });
-    gs.write(gt, tid, [](int) { return true; });
+    const int64_t left = a.rows - static_cast<int64_t>(t) * TR;
+    qs.write(qt, tid, [&](int i) { return i < left; });
+    gs.write(gt, tid, [&](int i) { return i < left; });
     if (tid < 2 * TR) st[tid] = stat;
     __syncthreads();
     if (t + 1 < t_last) fetch(t + 1);
@@ -126,11 +125,11 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   const int64_t at = ((b * a.Lk + key) * a.Hkv + hk) * a.E;
   if (a.part) {
     const int64_t n = a.B * a.Lk * a.Hkv * a.E;
-    store_col<float, EP>(a.part + split * n + at, in, keep, a.E, a.E % 8 == 0, dk, a.scale, lane);
-    store_col<float, EP>(a.part + (a.splits + split) * n + at, in, keep, a.E, a.E % 8 == 0, dv, 1.0f, lane);
+    store_col<float, EP, false>(a.part + split * n + at, in, keep, a.E, a.E % 8 == 0, dk, a.scale, lane);
+    store_col<float, EP, false>(a.part + (a.splits + split) * n + at, in, keep, a.E, a.E % 8 == 0, dv, 1.0f, lane);
   } else {
-    store_col<T, EP>(a.dk + at, in, keep, a.E, a.wide_dkv, dk, a.scale, lane);
-    store_col<T, EP>(a.dv + at, in, keep, a.E, a.wide_dkv, dv, 1.0f, lane);
+    store_col<T, EP, false>(a.dk + at, in, keep, a.E, a.wide_dkv, dk, a.scale, lane);
+    store_col<T, EP, false>(a.dv + at, in, keep, a.E, a.wide_dkv, dv, 1.0f, lane);
   }
 }
 
@@ -164,8 +163,8 @@ __global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
   const bool row_ok = r < a.rows;
   const Row<T> w = row_of(a, hk, row_ok ? r : a.rows - 1);
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk], gf[EP / Mma<T>::kChunk];
-  row_frags<T, EP>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
-  row_frags<T, EP>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, row_ok, a.E, a.wide_g, gf);
+  row_frags<T, EP, false>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
+  row_frags<T, EP, false>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, row_ok, a.E, a.wide_g, gf);
   const int64_t at = (b * a.Hq + w.h) * a.Lq + w.q;
   const float lse = row_ok ? a.lse[at] * kLog2e : INFINITY, delta = row_ok ? a.delta[at] : 0.0f;
 
@@ -178,8 +177,8 @@ __global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
   const int tiles = static_cast<int>((a.Lk + TK - 1) / TK);
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? kp + (k0 + i) * a.km.row : nullptr; });
-    vs.load(tid, a.E, a.wide_kv, [&](int i) { return k0 + i < a.Lk ? vp + (k0 + i) * a.vm.row : nullptr; });
+    ks.template load<false>(tid, a.E, a.wide_kv, [&](int i) { return kp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.km.row; });
+    vs.template load<false>(tid, a.E, a.wide_kv, [&](int i) { return vp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.vm.row; });
   };
   if (tiles > 0) fetch(0);
   for (int t = 0; t < tiles; ++t) {
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
     }
     __syncthreads();
   }
-  store_col<T, EP>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
+  store_col<T, EP, false>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
 }
 
 // ---- host -------------------------------------------------------------------

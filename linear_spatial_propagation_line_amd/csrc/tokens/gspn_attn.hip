@@ -38,6 +38,27 @@ template <typename T> __device__ __forceinline__ QRow q_row(const AttnP<T>& a, i
   const uint32_t hs = rc / static_cast<uint32_t>(a.Lq);
   return QRow{static_cast<int64_t>(hk) * a.share + hs, static_cast<int64_t>(rc - hs * static_cast<uint32_t>(a.Lq))};
 }
+// The addresses of 32 adjacent rows starting at row r0 of (entry b, key head
+// hk): one division for all of them unless the queries are few
+template <typename T> struct RowTile {
+  uint32_t r0, h, q, Lq;
+  int64_t b;
+  int hk;
+  __device__ __forceinline__ RowTile(const AttnP<T>& a, int64_t b_, int hk_, uint32_t r0_)
+      : r0(r0_), Lq(static_cast<uint32_t>(a.Lq)), b(b_), hk(hk_) {
+    h = r0 / Lq;
+    q = r0 - h * Lq;
+    h += hk * a.share;
+  }
+  // (head, query) of row i of the tile, clamped to the last row
+  __device__ __forceinline__ QRow at(const AttnP<T>& a, int i) const {
+    const uint32_t left = static_cast<uint32_t>(a.rows) - 1 - r0;
+    const uint32_t k = static_cast<uint32_t>(i) < left ? i : left;
+    if (Lq < 32) return q_row(a, hk, r0 + k);
+    const uint32_t u = q + k;
+    return u < Lq ? QRow{h, u} : QRow{static_cast<int64_t>(h) + 1, u - Lq};
+  }
+};
 template <typename T> struct Keys {   // K, V and the kept keys of one (entry, key head)
   const T *k, *v;
   const uint8_t* mask;
@@ -335,13 +356,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     if (tid < NT * 32) bias[tid] = keys.kept(a, tid) ? 0.0f : -INFINITY;
   }
   __syncthreads();
-  const int t_last = (part + 1) * a.tiles_each < static_cast<uint32_t>(a.row_tiles) ? (part + 1) * a.tiles_each : a.row_tiles;
-  typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+  // Rows pass through LDS in both directions, so that every access to memory
+  // is of whole 128-byte lines: fragments straight from memory take a line in
+  // four 32-byte parts, and with the lines of all wavefronts in flight the
+  // first-level cache does not hold one that long.
+  constexpr int kRow = tile_pitch<T, EP>();
+  char* mine = lds + 2 * NT * 32 * kRow + wave * 32 * kRow;
+  const int t_last = min((part + 1) * a.tiles_each, static_cast<uint32_t>(a.row_tiles));
   int E = a.E;
-  QRow next;
+  Stage<T, EP, 32, 64> qs;
   auto fetch = [&](int t) {
-    next = q_row(a, hk, static_cast<uint32_t>(t) * 32 + (lane & 31));
-    row_frags<T, EP, FULL>(a.q + b * a.qm.batch + next.q * a.qm.row + next.h * a.qm.head, true, E, a.wide_q, qf);
+    const RowTile<T> rows(a, b, hk, static_cast<uint32_t>(t) * 32);
+    qs.template load<FULL>(lane, E, a.wide_q, [&](int i) {
+      const QRow w = rows.at(a, i);
+      return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
+    });
   };
   int t = part * a.tiles_each + wave;
   if (t < t_last) fetch(t);
@@ -350,8 +379,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     // tile; kept in registers they would cost the occupancy that hides the
     // rows' latency, so they are taken anew.
     asm volatile("" : "+s"(E) : : "memory");
-    const bool row_ok = static_cast<uint32_t>(t) * 32 + (lane & 31) < a.rows;
-    const QRow w_ = next;
+    const RowTile<T> rows(a, b, hk, static_cast<uint32_t>(t) * 32);
+    qs.write(mine, lane, [](int) { return true; });
+    lds_wave_sync();
+    typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+#pragma unroll
+    for (int j = 0; j < EP / Mma<T>::kChunk; ++j) qf[j] = tile_frag<T, EP>(mine, 0, j, lane);
+    if (t + 4 < t_last) fetch(t + 4);
     float w[NT][16], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
@@ -367,7 +401,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
         }
       }
     }
-    if (t + 4 < t_last) fetch(t + 4);
     m = column_max(m);
     const float base = m == -INFINITY ? 0.0f : m;
     f32x16 o[EP / 32] = {};
@@ -381,9 +414,39 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
       tile_accum<EP>(vt, s * 32, w[s], o, lane, T{});
     }
     l = column_sum(l);
-    store_col<T, EP, FULL>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, E, a.wide_o, o,
-                     softmax_scale(l), lane);
-    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
+    if (a.lse && lane < 32 && rows.r0 + lane < a.rows) {
+      const QRow u = rows.at(a, lane);
+      a.lse[(b * a.Hq + u.h) * a.Lq + u.q] = softmax_lse(m, l);
+    }
+    const float f = softmax_scale(l);
+    lds_wave_sync();   // the queries' fragments have been read
+    T* to = reinterpret_cast<T*>(mine + (lane & 31) * kRow) + 4 * (lane >> 5);
+#pragma unroll
+    for (int et = 0; et < EP / 32; ++et) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v[4] = {o[et][4 * j] * f, o[et][4 * j + 1] * f, o[et][4 * j + 2] * f, o[et][4 * j + 3] * f};
+        V4<T>::store(to, et * 32 + 8 * j, v);
+      }
+    }
+    lds_wave_sync();
+    using St = Stage<T, EP, 32, 64>;
+#pragma unroll
+    for (int i = 0; i < St::kEach; ++i) {
+      const int row = St::row(lane, i), e0 = St::e0(lane, i);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kRow + e0 * static_cast<int>(sizeof(T)));
+      if (rows.r0 + row >= a.rows) continue;
+      const QRow u = rows.at(a, row);
+      T* out = a.out + ((b * a.Lq + u.q) * a.Hq + u.h) * E;
+      if (FULL || (a.wide_o && e0 < E)) {
+        *reinterpret_cast<u32x4*>(out + e0) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16 / static_cast<int>(sizeof(T)); ++k)
+          if (e0 + k < E) out[e0 + k] = reinterpret_cast<const T*>(mine + row * kRow)[e0 + k];
+      }
+    }
+    lds_wave_sync();   // before the next tile's queries go there
   }
 }
 
@@ -616,10 +679,10 @@ hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Trac
   const int64_t heads = p.B * p.Hkv;
   if (k.plan == AttnPlan::kShort) {
     switch ((p.Lk + 31) / 32) {
-      case 1: return run<T>(attn_short_kernel<T, EP, 1, FULL>, "attn_short", 32 * row, heads * k.splits, p, stream, tr);
-      case 2: return run<T>(attn_short_kernel<T, EP, 2, FULL>, "attn_short", 64 * row, heads * k.splits, p, stream, tr);
-      case 3: return run<T>(attn_short_kernel<T, EP, 3, FULL>, "attn_short", 96 * row, heads * k.splits, p, stream, tr);
-      default: return run<T>(attn_short_kernel<T, EP, 4, FULL>, "attn_short", 128 * row, heads * k.splits, p, stream, tr);
+      case 1: return run<T>(attn_short_kernel<T, EP, 1, FULL>, "attn_short", 160 * row, heads * k.splits, p, stream, tr);
+      case 2: return run<T>(attn_short_kernel<T, EP, 2, FULL>, "attn_short", 192 * row, heads * k.splits, p, stream, tr);
+      case 3: return run<T>(attn_short_kernel<T, EP, 3, FULL>, "attn_short", 160 * row, heads * k.splits, p, stream, tr);
+      default: return run<T>(attn_short_kernel<T, EP, 4, FULL>, "attn_short", 192 * row, heads * k.splits, p, stream, tr);
     }
   }
   if (k.plan == AttnPlan::kFew)

@@ -29,36 +29,6 @@ template <typename T> struct AttnP {
   bool wide_q, wide_kv, wide_o;
 };
 
-// Query row r of (entry b, key head hk), clamped to the last row
-struct QRow {
-  int64_t h, q;
-};
-template <typename T> __device__ __forceinline__ QRow q_row(const AttnP<T>& a, int hk, uint32_t r) {
-  const uint32_t rc = r < a.rows ? r : static_cast<uint32_t>(a.rows) - 1;
-  const uint32_t hs = rc / static_cast<uint32_t>(a.Lq);
-  return QRow{static_cast<int64_t>(hk) * a.share + hs, static_cast<int64_t>(rc - hs * static_cast<uint32_t>(a.Lq))};
-}
-// The addresses of 32 adjacent rows starting at row r0 of (entry b, key head
-// hk): one division for all of them unless the queries are few
-template <typename T> struct RowTile {
-  uint32_t r0, h, q, Lq;
-  int64_t b;
-  int hk;
-  __device__ __forceinline__ RowTile(const AttnP<T>& a, int64_t b_, int hk_, uint32_t r0_)
-      : r0(r0_), Lq(static_cast<uint32_t>(a.Lq)), b(b_), hk(hk_) {
-    h = r0 / Lq;
-    q = r0 - h * Lq;
-    h += hk * a.share;
-  }
-  // (head, query) of row i of the tile, clamped to the last row
-  __device__ __forceinline__ QRow at(const AttnP<T>& a, int i) const {
-    const uint32_t left = static_cast<uint32_t>(a.rows) - 1 - r0;
-    const uint32_t k = static_cast<uint32_t>(i) < left ? i : left;
-    if (Lq < 32) return q_row(a, hk, r0 + k);
-    const uint32_t u = q + k;
-    return u < Lq ? QRow{h, u} : QRow{static_cast<int64_t>(h) + 1, u - Lq};
-  }
-};
 template <typename T> struct Keys {   // K, V and the kept keys of one (entry, key head)
   const T *k, *v;
   const uint8_t* mask;
@@ -366,9 +336,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
   int E = a.E;
   Stage<T, EP, 32, 64> qs;
   auto fetch = [&](int t) {
-    const RowTile<T> rows(a, b, hk, static_cast<uint32_t>(t) * 32);
+    const RowTile rows(a, hk, static_cast<uint32_t>(t) * 32);
     qs.template load<FULL>(lane, E, a.wide_q, [&](int i) {
-      const QRow w = rows.at(a, i);
+      const QRow w = rows.at(i);
       return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
     });
   };
@@ -379,7 +349,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     // tile; kept in registers they would cost the occupancy that hides the
     // rows' latency, so they are taken anew.
     asm volatile("" : "+s"(E) : : "memory");
-    const RowTile<T> rows(a, b, hk, static_cast<uint32_t>(t) * 32);
+    const RowTile rows(a, hk, static_cast<uint32_t>(t) * 32);
     qs.write(mine, lane, [](int) { return true; });
     lds_wave_sync();
     typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
@@ -415,7 +385,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     }
     l = column_sum(l);
     if (a.lse && lane < 32 && rows.r0 + lane < a.rows) {
-      const QRow u = rows.at(a, lane);
+      const QRow u = rows.at(lane);
       a.lse[(b * a.Hq + u.h) * a.Lq + u.q] = softmax_lse(m, l);
     }
     const float f = softmax_scale(l);
@@ -436,7 +406,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
       const int row = St::row(lane, i), e0 = St::e0(lane, i);
       const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kRow + e0 * static_cast<int>(sizeof(T)));
       if (rows.r0 + row >= a.rows) continue;
-      const QRow u = rows.at(a, row);
+      const QRow u = rows.at(row);
       T* out = a.out + ((b * a.Lq + u.q) * a.Hq + u.h) * E;
       if (FULL || (a.wide_o && e0 < E)) {
         *reinterpret_cast<u32x4*>(out + e0) = v;

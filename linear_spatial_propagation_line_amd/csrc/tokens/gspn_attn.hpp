@@ -20,10 +20,42 @@ namespace gspn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// The rows that share one key head: row r of (entry, key head) is query
-// r % Lq of head hk * share + r / Lq.
 struct RowMap {
   int64_t batch, row, head;   // strides in elements
+};
+
+// The rows that share one key head: row r of (entry, key head hk) is query
+// r % Lq of head hk * share + r / Lq; P is a problem with Lq, share and rows.
+struct QRow {
+  int64_t h, q;
+};
+template <typename P> __device__ __forceinline__ QRow q_row(const P& a, int hk, uint32_t r) {
+  const uint32_t rc = r < a.rows ? r : static_cast<uint32_t>(a.rows) - 1;   // clamped to the last
+  const uint32_t hs = rc / static_cast<uint32_t>(a.Lq);
+  return QRow{static_cast<int64_t>(hk) * a.share + hs, static_cast<int64_t>(rc - hs * static_cast<uint32_t>(a.Lq))};
+}
+// 32 adjacent rows starting at row r0: one division for all of them unless
+// the queries are few
+struct RowTile {
+  uint32_t r0, h, q, Lq, left, share, hk;
+  template <typename P>
+  __device__ __forceinline__ RowTile(const P& a, int hk_, uint32_t r0_)
+      : r0(r0_), Lq(static_cast<uint32_t>(a.Lq)), left(static_cast<uint32_t>(a.rows) - 1 - r0_),
+        share(a.share), hk(hk_) {
+    h = r0 / Lq;
+    q = r0 - h * Lq;
+    h += hk * share;
+  }
+  // row i of the tile, clamped to the last row
+  __device__ __forceinline__ QRow at(int i) const {
+    const uint32_t k = static_cast<uint32_t>(i) < left ? i : left;
+    if (Lq < 32) {
+      const uint32_t hs = (r0 + k) / Lq;
+      return QRow{static_cast<int64_t>(hk) * share + hs, static_cast<int64_t>(r0 + k - hs * Lq)};
+    }
+    const uint32_t u = q + k;
+    return u < Lq ? QRow{h, u} : QRow{static_cast<int64_t>(h) + 1, u - Lq};
+  }
 };
 
 template <typename T> struct Mma;

@@ -28,16 +28,8 @@ template <typename T> struct BwdP {
   int64_t B, Lq, Lk, rows;
   int Hq, Hkv, share, E, splits, key_tiles, row_tiles, tiles_each;
   float c, scale;      // scale * log2(e), scale
-  bool wide_q, wide_kv, wide_g, wide_dq, wide_dkv;
+  bool wide_q, wide_kv, wide_g, wide_dq, wide_dkv, full;
 };
-
-template <typename T> struct Row {
-  int64_t h, q;
-};
-template <typename T> __device__ __forceinline__ Row<T> row_of(const BwdP<T>& a, int hk, int64_t r) {
-  const int64_t hs = r / a.Lq;
-  return Row<T>{hk * a.share + hs, r - hs * a.Lq};
-}
 
 // delta[b][h][q] = sum_e grad_out out: 16 lanes per row
 template <typename T>
@@ -56,15 +48,15 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 }
 
 // ---- dK, dV: 128 keys per workgroup, rows 32 at a time through LDS ----------
-template <typename T, int EP>
-__global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
+template <typename T, int EP, bool FULL>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
   constexpr int TR = 32;
   char* qt = lds;
   char* gt = lds + TR * tile_pitch<T, EP>();
   float* st = reinterpret_cast<float*>(lds + 2 * TR * tile_pitch<T, EP>());   // lse, delta
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hh = lane >> 5;
-  int64_t blk = blockIdx.x;
+  uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int kt = static_cast<int>(blk % a.key_tiles);
   blk /= a.key_tiles;
   const int split = static_cast<int>(blk % a.splits);
@@ -72,25 +64,28 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const int64_t key = static_cast<int64_t>(kt) * 128 + wave * 32 + (lane & 31);
   const bool in = key < a.Lk;
-  const bool keep = in && (!a.mask || a.mask[b * a.mask_batch + key] != 0);
+  const int64_t kc = in ? key : a.Lk - 1;
+  const bool keep = in && (!a.mask || a.mask[b * a.mask_batch + kc] != 0);
 
   typename Mma<T>::Frag kf[EP / Mma<T>::kChunk], vf[EP / Mma<T>::kChunk];
-  row_frags<T, EP, false>(a.k + b * a.km.batch + key * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
-  row_frags<T, EP, false>(a.v + b * a.vm.batch + key * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
+  row_frags<T, EP, FULL>(a.k + b * a.km.batch + kc * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
+  row_frags<T, EP, FULL>(a.v + b * a.vm.batch + kc * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
 
   f32x16 dk[EP / 32] = {}, dv[EP / 32] = {};
+  // nothing to add up where the workgroup's keys are all dropped
   const int t_first = split * a.tiles_each;
-  const int t_last = t_first + a.tiles_each < a.row_tiles ? t_first + a.tiles_each : a.row_tiles;
+  const int t_last = __syncthreads_or(keep) ? min(t_first + a.tiles_each, a.row_tiles) : t_first;
   Stage<T, EP, TR, kThreads> qs, gs;
   float stat = 0.0f;
   auto fetch = [&](int t) {
     const int64_t r0 = static_cast<int64_t>(t) * TR;
-    qs.template load<false>(tid, a.E, a.wide_q, [&](int i) -> const T* {
-      const Row<T> w = row_of(a, hk, r0 + i < a.rows ? r0 + i : a.rows - 1);
+    const RowTile rows(a, hk, static_cast<uint32_t>(r0));
+    qs.template load<FULL>(tid, a.E, a.wide_q, [&](int i) {
+      const QRow w = rows.at(i);
       return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
     });
-    gs.template load<false>(tid, a.E, a.wide_g, [&](int i) -> const T* {
-      const Row<T> w = row_of(a, hk, r0 + i < a.rows ? r0 + i : a.rows - 1);
+    gs.template load<FULL>(tid, a.E, a.wide_g, [&](int i) {
+      const QRow w = rows.at(i);
       return a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head;
     });
     if (tid < 2 * TR) {
@@ -125,11 +120,11 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_kernel(BwdP<T> a) {
   const int64_t at = ((b * a.Lk + key) * a.Hkv + hk) * a.E;
   if (a.part) {
     const int64_t n = a.B * a.Lk * a.Hkv * a.E;
-    store_col<float, EP, false>(a.part + split * n + at, in, keep, a.E, a.E % 8 == 0, dk, a.scale, lane);
-    store_col<float, EP, false>(a.part + (a.splits + split) * n + at, in, keep, a.E, a.E % 8 == 0, dv, 1.0f, lane);
+    store_col<float, EP, FULL>(a.part + split * n + at, in, keep, a.E, a.E % 8 == 0, dk, a.scale, lane);
+    store_col<float, EP, FULL>(a.part + (a.splits + split) * n + at, in, keep, a.E, a.E % 8 == 0, dv, 1.0f, lane);
   } else {
-    store_col<T, EP, false>(a.dk + at, in, keep, a.E, a.wide_dkv, dk, a.scale, lane);
-    store_col<T, EP, false>(a.dv + at, in, keep, a.E, a.wide_dkv, dv, 1.0f, lane);
+    store_col<T, EP, FULL>(a.dk + at, in, keep, a.E, a.wide_dkv, dk, a.scale, lane);
+    store_col<T, EP, FULL>(a.dv + at, in, keep, a.E, a.wide_dkv, dv, 1.0f, lane);
   }
 }
 
@@ -148,23 +143,24 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(BwdP<T> a) {
 }
 
 // ---- dQ: 128 rows per workgroup, keys 32 at a time through LDS --------------
-template <typename T, int EP>
-__global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
+template <typename T, int EP, bool FULL>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
   constexpr int TK = 32;
   char* kt = lds;
   char* vt = lds + TK * tile_pitch<T, EP>();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rts = static_cast<int>((a.rows + 127) / 128);
-  const int rt = static_cast<int>(blockIdx.x % rts);
-  const int64_t bh = blockIdx.x / rts, b = bh / a.Hkv;
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int rt = static_cast<int>(blk % rts);
+  const int64_t bh = blk / rts, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const int64_t r = static_cast<int64_t>(rt) * 128 + wave * 32 + (lane & 31);
   const bool row_ok = r < a.rows;
-  const Row<T> w = row_of(a, hk, row_ok ? r : a.rows - 1);
+  const QRow w = q_row(a, hk, static_cast<uint32_t>(r));
   typename Mma<T>::Frag qf[EP / Mma<T>::kChunk], gf[EP / Mma<T>::kChunk];
-  row_frags<T, EP, false>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, row_ok, a.E, a.wide_q, qf);
-  row_frags<T, EP, false>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, row_ok, a.E, a.wide_g, gf);
+  row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, a.E, a.wide_q, qf);
+  row_frags<T, EP, FULL>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, true, a.E, a.wide_g, gf);
   const int64_t at = (b * a.Hq + w.h) * a.Lq + w.q;
   const float lse = row_ok ? a.lse[at] * kLog2e : INFINITY, delta = row_ok ? a.delta[at] : 0.0f;
 
@@ -174,19 +170,21 @@ __global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
   auto kept = [&](int64_t key) { return key < a.Lk && (!mp || mp[key] != 0); };
   f32x16 dq[EP / 32] = {};
   Stage<T, EP, TK, kThreads> ks, vs;
-  const int tiles = static_cast<int>((a.Lk + TK - 1) / TK);
+  int64_t k_lo, k_hi;
+  key_range(mp, a.Lk, tid, &k_lo, &k_hi);
+  const int t_first = static_cast<int>(k_lo / TK), t_last = static_cast<int>((k_hi + TK - 1) / TK);
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.template load<false>(tid, a.E, a.wide_kv, [&](int i) { return kp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.km.row; });
-    vs.template load<false>(tid, a.E, a.wide_kv, [&](int i) { return vp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.vm.row; });
+    ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return kp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.km.row; });
+    vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return vp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.vm.row; });
   };
-  if (tiles > 0) fetch(0);
-  for (int t = 0; t < tiles; ++t) {
+  if (t_first < t_last) fetch(t_first);
+  for (int t = t_first; t < t_last; ++t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
     ks.write(kt, tid, [&](int i) { return kept(k0 + i); });
     vs.write(vt, tid, [&](int i) { return kept(k0 + i); });
     __syncthreads();
-    if (t + 1 < tiles) fetch(t + 1);
+    if (t + 1 < t_last) fetch(t + 1);
     const uint32_t bits = static_cast<uint32_t>(__ballot(kept(k0 + (lane & 31))));
     if (bits != 0) {
       const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
@@ -202,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void attn_dq_kernel(BwdP<T> a) {
     }
     __syncthreads();
   }
-  store_col<T, EP, false>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
+  store_col<T, EP, FULL>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -241,7 +239,7 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (p.Lk > 0) {
-    auto kern = attn_dkv_kernel<T, EP>;
+    auto kern = p.full ? attn_dkv_kernel<T, EP, true> : attn_dkv_kernel<T, EP, false>;
     constexpr int bytes = 2 * 32 * tile_pitch<T, EP>() + 64 * 4;
     if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
     tr->before(stream, "attn_dkv", p.B * p.Hkv);
@@ -259,7 +257,7 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
     }
   }
   if (p.rows > 0) {
-    auto kern = attn_dq_kernel<T, EP>;
+    auto kern = p.full ? attn_dq_kernel<T, EP, true> : attn_dq_kernel<T, EP, false>;
     constexpr int bytes = 2 * 32 * tile_pitch<T, EP>();
     if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
     tr->before(stream, "attn_dq", p.B * p.Hkv);
@@ -306,6 +304,8 @@ hipError_t bwd_dt(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws, h
   p.wide_g = whole && wide_ok(p.gy, 16, es, {p.gm.batch, p.gm.row, p.gm.head});
   p.wide_dq = eight && wide_ok(p.dq, 16, es, {});
   p.wide_dkv = eight && wide_ok(p.dk, 16, es, {}) && wide_ok(p.dv, 16, es, {});
+  // whole 16-byte pieces everywhere and no padding of the head
+  p.full = p.E == attn_ep(a.E) && p.wide_q && p.wide_kv && p.wide_g && p.wide_dq && p.wide_dkv;
   switch (attn_ep(a.E)) {
     case 32: return bwd_ep<T, 32>(p, stream, tr);
     case 64: return bwd_ep<T, 64>(p, stream, tr);

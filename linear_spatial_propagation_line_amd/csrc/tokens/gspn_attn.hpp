@@ -81,7 +81,9 @@ template <> struct Mma<float> {
 
 // LDS row pitch in bytes: 16 bytes of padding spread a column of 16-byte
 // pieces over the banks
-template <typename T, int EP> constexpr int tile_pitch() { return EP * static_cast<int>(sizeof(T)) + 16; }
+template <typename T, int EP> constexpr int tile_pitch() {
+  return EP * static_cast<int>(sizeof(T)) + (sizeof(T) == 2 ? 32 : 16);
+}
 
 // 16 bytes of row values e0 .. : whole when `wide`, else value by value with
 // the row's end honoured (a value past E is 0). FULL: the row holds all the

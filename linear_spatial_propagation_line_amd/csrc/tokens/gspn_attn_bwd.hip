@@ -110,8 +110,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int r = (i & 3) + 8 * (i >> 2) + 4 * hh;
-      p[i] = keep ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -st[r])) : 0.0f;
-      ds[i] = keep ? p[i] * (y[i] - st[TR + r]) : 0.0f;
+      // a dropped key's column is finite (its K and V are zeros) and not stored
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -st[r]));
+      ds[i] = p[i] * (y[i] - st[TR + r]);
     }
     tile_accum<EP>(gt, 0, p, dv, lane, T{});
     tile_accum<EP>(qt, 0, ds, dk, lane, T{});
@@ -189,13 +190,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
     if (bits != 0) {
       const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
       const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
-      const uint32_t mine = bits >> (4 * (lane >> 5));
       float ds[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -lse));
-        ds[i] = (mine >> ((i & 3) + 8 * (i >> 2))) & 1u ? p * (y[i] - delta) : 0.0f;
-      }
+      for (int i = 0; i < 16; ++i) ds[i] = x[i];
+      drop_keys(ds, bits, lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(ds[i], a.c, -lse)) * (y[i] - delta);
       tile_accum<EP>(kt, 0, ds, dq, lane, T{});
     }
     __syncthreads();

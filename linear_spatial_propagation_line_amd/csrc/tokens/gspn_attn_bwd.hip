@@ -48,6 +48,13 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 }
 
 // ---- dK, dV: 128 keys per workgroup, rows 32 at a time through LDS ----------
+// Results and fragments of K and V are 6 E registers; where that leaves no
+// room for two wavefronts per SIMD the fragments of V stay in LDS (with them
+// in registers the loop spilled: 433 us against 3xx at E = 128).
+template <typename T, int EP> constexpr bool dkv_v_in_lds() { return EP * sizeof(T) >= 256; }
+template <typename T, int EP> constexpr int dkv_lds() {
+  return (2 * 32 + (dkv_v_in_lds<T, EP>() ? 128 : 0)) * tile_pitch<T, EP>() + 64 * 4;
+}
 template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
@@ -55,6 +62,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
   char* qt = lds;
   char* gt = lds + TR * tile_pitch<T, EP>();
   float* st = reinterpret_cast<float*>(lds + 2 * TR * tile_pitch<T, EP>());   // lse, delta
+  char* vt = lds + 2 * TR * tile_pitch<T, EP>() + 64 * 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hh = lane >> 5;
   uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int kt = static_cast<int>(blk % a.key_tiles);
@@ -70,6 +78,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
   typename Mma<T>::Frag kf[EP / Mma<T>::kChunk], vf[EP / Mma<T>::kChunk];
   row_frags<T, EP, FULL>(a.k + b * a.km.batch + kc * a.km.row + hk * a.km.head, keep, a.E, a.wide_kv, kf);
   row_frags<T, EP, FULL>(a.v + b * a.vm.batch + kc * a.vm.row + hk * a.vm.head, keep, a.E, a.wide_kv, vf);
+  if constexpr (dkv_v_in_lds<T, EP>()) {
+#pragma unroll
+    for (int j = 0; j < EP / Mma<T>::kChunk; ++j)
+      *reinterpret_cast<typename Mma<T>::Frag*>(vt + (wave * 32 + (lane & 31)) * tile_pitch<T, EP>() + j * 32 + hh * 16) = vf[j];
+  }
 
   f32x16 dk[EP / 32] = {}, dv[EP / 32] = {};
   // nothing to add up where the workgroup's keys are all dropped
@@ -104,7 +117,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
     if (tid < 2 * TR) st[tid] = stat;
     __syncthreads();
     if (t + 1 < t_last) fetch(t + 1);
+    asm volatile("" : : : "memory");   // the fragments of V are read anew
     const f32x16 x = tile_dot<T, EP>(qt, 0, kf, lane);
+    if constexpr (dkv_v_in_lds<T, EP>()) {
+#pragma unroll
+      for (int j = 0; j < EP / Mma<T>::kChunk; ++j) vf[j] = tile_frag<T, EP>(vt, wave * 32, j, lane);
+    }
     const f32x16 y = tile_dot<T, EP>(gt, 0, vf, lane);
     float p[16], ds[16];
 #pragma unroll
@@ -241,7 +259,7 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
   }
   if (p.Lk > 0) {
     auto kern = p.full ? attn_dkv_kernel<T, EP, true> : attn_dkv_kernel<T, EP, false>;
-    constexpr int bytes = 2 * 32 * tile_pitch<T, EP>() + 64 * 4;
+    constexpr int bytes = dkv_lds<T, EP>();
     if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
     tr->before(stream, "attn_dkv", p.B * p.Hkv);
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * p.splits * p.key_tiles)),

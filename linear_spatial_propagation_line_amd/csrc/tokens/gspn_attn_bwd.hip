@@ -53,16 +53,16 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 // in registers the loop spilled: 433 us against 3xx at E = 128).
 template <typename T, int EP> constexpr bool dkv_v_in_lds() { return EP * sizeof(T) >= 256; }
 template <typename T, int EP> constexpr int dkv_lds() {
-  return (2 * 32 + (dkv_v_in_lds<T, EP>() ? 128 : 0)) * tile_pitch<T, EP>() + 64 * 4;
+  return (4 * 32 + (dkv_v_in_lds<T, EP>() ? 128 : 0)) * tile_pitch<T, EP>() + 2 * 64 * 4;
 }
 template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
   constexpr int TR = 32;
-  char* qt = lds;
-  char* gt = lds + TR * tile_pitch<T, EP>();
-  float* st = reinterpret_cast<float*>(lds + 2 * TR * tile_pitch<T, EP>());   // lse, delta
-  char* vt = lds + 2 * TR * tile_pitch<T, EP>() + 64 * 4;
+  // two tiles of rows (Q, grad_out, and their lse and delta), one being
+  // computed with while the next is written: one barrier per tile
+  constexpr int kTile = 2 * TR * tile_pitch<T, EP>() + 2 * TR * 4;
+  char* vt = lds + 2 * kTile;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hh = lane >> 5;
   uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int kt = static_cast<int>(blk % a.key_tiles);
@@ -109,21 +109,35 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
       stat = tid < TR ? (r < a.rows ? a.lse[at] * kLog2e : INFINITY) : (r < a.rows ? a.delta[at] : 0.0f);
     }
   };
-  if (t_first < t_last) fetch(t_first);
-  for (int t = t_first; t < t_last; ++t) {
+  auto put = [&](int t) {
+    char* to = lds + (t & 1) * kTile;
     const int64_t left = a.rows - static_cast<int64_t>(t) * TR;
-    qs.write(qt, tid, [&](int i) { return i < left; });
-    gs.write(gt, tid, [&](int i) { return i < left; });
-    if (tid < 2 * TR) st[tid] = stat;
-    __syncthreads();
+    qs.write(to, tid, [&](int i) { return i < left; });
+    gs.write(to + TR * tile_pitch<T, EP>(), tid, [&](int i) { return i < left; });
+    if (tid < 2 * TR) reinterpret_cast<float*>(to + 2 * TR * tile_pitch<T, EP>())[tid] = stat;
+  };
+  if (t_first < t_last) {
+    fetch(t_first);
+    put(t_first);
+  }
+  lds_barrier();
+  for (int t = t_first; t < t_last; ++t) {
+    const char* qt = lds + (t & 1) * kTile;
+    const char* gt = qt + TR * tile_pitch<T, EP>();
+    const float* st = reinterpret_cast<const float*>(gt + TR * tile_pitch<T, EP>());
     if (t + 1 < t_last) fetch(t + 1);
-    asm volatile("" : : : "memory");   // the fragments of V are read anew
     const f32x16 x = tile_dot<T, EP>(qt, 0, kf, lane);
+    f32x16 y;
     if constexpr (dkv_v_in_lds<T, EP>()) {
+      y = f32x16{};
 #pragma unroll
-      for (int j = 0; j < EP / Mma<T>::kChunk; ++j) vf[j] = tile_frag<T, EP>(vt, wave * 32, j, lane);
+      for (int j = 0; j < EP / Mma<T>::kChunk; ++j) {
+        y = Mma<T>::mma(tile_frag<T, EP>(gt, 0, j, lane), tile_frag<T, EP>(vt, wave * 32, j, lane), y);
+        if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // not all fragments at once
+      }
+    } else {
+      y = tile_dot<T, EP>(gt, 0, vf, lane);
     }
-    const f32x16 y = tile_dot<T, EP>(gt, 0, vf, lane);
     float p[16], ds[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -134,7 +148,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
     }
     tile_accum<EP>(gt, 0, p, dv, lane, T{});
     tile_accum<EP>(qt, 0, ds, dk, lane, T{});
-    __syncthreads();
+    if (t + 1 < t_last) put(t + 1);
+    lds_barrier();
   }
   const int64_t at = ((b * a.Lk + key) * a.Hkv + hk) * a.E;
   if (a.part) {
@@ -165,9 +180,7 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(BwdP<T> a) {
 template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
-  constexpr int TK = 32;
-  char* kt = lds;
-  char* vt = lds + TK * tile_pitch<T, EP>();
+  constexpr int TK = 32, kTile = 2 * TK * tile_pitch<T, EP>();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rts = static_cast<int>((a.rows + 127) / 128);
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
@@ -192,19 +205,30 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
   int64_t k_lo, k_hi;
   key_range(mp, a.Lk, tid, &k_lo, &k_hi);
   const int t_first = static_cast<int>(k_lo / TK), t_last = static_cast<int>((k_hi + TK - 1) / TK);
+  bool keep = false;         // of key lane % 32 of the tile on its way
+  uint32_t bits = 0, next = 0;
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
+    keep = kept(k0 + (lane & 31));
     ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return kp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.km.row; });
     vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return vp + (k0 + i < a.Lk ? k0 + i : a.Lk - 1) * a.vm.row; });
   };
-  if (t_first < t_last) fetch(t_first);
+  auto put = [&](int t) {
+    char* to = lds + (t & 1) * kTile;
+    next = static_cast<uint32_t>(__ballot(keep));
+    ks.write(to, tid, [&](int i) { return (next >> i) & 1u; });
+    vs.write(to + TK * tile_pitch<T, EP>(), tid, [&](int i) { return (next >> i) & 1u; });
+  };
+  if (t_first < t_last) {
+    fetch(t_first);
+    put(t_first);
+  }
+  lds_barrier();
   for (int t = t_first; t < t_last; ++t) {
-    const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.write(kt, tid, [&](int i) { return kept(k0 + i); });
-    vs.write(vt, tid, [&](int i) { return kept(k0 + i); });
-    __syncthreads();
+    const char* kt = lds + (t & 1) * kTile;
+    const char* vt = kt + TK * tile_pitch<T, EP>();
+    bits = next;
     if (t + 1 < t_last) fetch(t + 1);
-    const uint32_t bits = static_cast<uint32_t>(__ballot(kept(k0 + (lane & 31))));
     if (bits != 0) {
       const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
       const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
@@ -217,7 +241,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
         ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(ds[i], a.c, -lse)) * (y[i] - delta);
       tile_accum<EP>(kt, 0, ds, dq, lane, T{});
     }
-    __syncthreads();
+    if (t + 1 < t_last) put(t + 1);
+    lds_barrier();
   }
   store_col<T, EP, FULL>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
 }
@@ -277,7 +302,7 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
   }
   if (p.rows > 0) {
     auto kern = p.full ? attn_dq_kernel<T, EP, true> : attn_dq_kernel<T, EP, false>;
-    constexpr int bytes = 2 * 32 * tile_pitch<T, EP>();
+    constexpr int bytes = 4 * 32 * tile_pitch<T, EP>();
     if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
     tr->before(stream, "attn_dq", p.B * p.Hkv);
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * cdiv(p.rows, 128))),

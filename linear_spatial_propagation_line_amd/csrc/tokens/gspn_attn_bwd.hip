@@ -126,7 +126,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
     const char* gt = qt + TR * tile_pitch<T, EP>();
     const float* st = reinterpret_cast<const float*>(gt + TR * tile_pitch<T, EP>());
     if (t + 1 < t_last) fetch(t + 1);
+    // the softmax of the tile between the two products, so that lse and delta
+    // are not held at once
     const f32x16 x = tile_dot<T, EP>(qt, 0, kf, lane);
+    float p[16], ds[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)   // a dropped key's column is finite (zeros) and not stored
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -st[(i & 3) + 8 * (i >> 2) + 4 * hh]));
     f32x16 y;
     if constexpr (dkv_v_in_lds<T, EP>()) {
       y = f32x16{};
@@ -138,14 +144,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
     } else {
       y = tile_dot<T, EP>(gt, 0, vf, lane);
     }
-    float p[16], ds[16];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = (i & 3) + 8 * (i >> 2) + 4 * hh;
-      // a dropped key's column is finite (its K and V are zeros) and not stored
-      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.c, -st[r]));
-      ds[i] = p[i] * (y[i] - st[TR + r]);
-    }
+    for (int i = 0; i < 16; ++i) ds[i] = p[i] * (y[i] - st[TR + (i & 3) + 8 * (i >> 2) + 4 * hh]);
     tile_accum<EP>(gt, 0, p, dv, lane, T{});
     tile_accum<EP>(qt, 0, ds, dk, lane, T{});
     if (t + 1 < t_last) put(t + 1);

@@ -144,28 +144,32 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
 }
 
 // ---- long key axes, rows enough to fill the chip, bf16 ---------------------------
-// 64 rows per wavefront in two column tiles, so that every K or V fragment read
-// from LDS feeds two products: with one, the reads alone (1 KB per 32-cycle
-// product and SIMD) would take all of LDS's 128 bytes per cycle. One wavefront
-// per SIMD then holds everything (256 registers of results and queries at
-// E = 128), so products and exponentials have to overlap inside it: the
-// products of P and V lag one subtile of 32 keys behind, and those of K and Q
-// run one ahead, of the exponentials that stand between them.
+// The products of P and V lag one subtile of 32 keys behind, and those of K and
+// Q run one ahead, of the exponentials that stand between them, so that a
+// wavefront's own products and exponentials can overlap. Tiles of 64 keys in
+// two LDS buffers. A product of 32 x 32 x 16 takes 32 cycles and 1 KB from LDS
+// on each of the four SIMDs, just LDS's 128 bytes per cycle; up to E = 64 a
+// wavefront therefore takes 64 rows in two column tiles, which share what is
+// read. At larger heads two column tiles need more than 256 registers: the
+// second wavefront per SIMD is lost, and results that the vector ALU works on
+// land in accumulation registers (2x4096x2048, 16 heads of 128: 250 us, with
+// one column tile 1xx).
+constexpr int wide_tiles(int EP) { return EP <= 64 ? 2 : 1; }
 template <int EP>
-__global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a) {
+__global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a) {
   using T = bf16_t;
   extern __shared__ __align__(16) char lds[];
-  constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32;
+  constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32, QT = wide_tiles(EP);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int rt = static_cast<int>(blk % a.row_tiles);
   const int64_t bh = blk / a.row_tiles, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const Keys<T> keys(a, b, hk);
-  const uint32_t r0 = (static_cast<uint32_t>(rt) * 4 + wave) * 64 + (lane & 31);
-  Mma<T>::Frag qf[2][EP / 16];
+  const uint32_t r0 = (static_cast<uint32_t>(rt) * 4 + wave) * (32 * QT) + (lane & 31);
+  Mma<T>::Frag qf[QT][EP / 16];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < QT; ++u) {
     const QRow w = q_row(a, hk, r0 + 32 * u);
     row_frags<T, EP, true>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, EP, true, qf[u]);
   }
@@ -173,8 +177,13 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
   key_range(keys.mask, a.Lk, tid, &k_lo, &k_hi);
   const int t0 = static_cast<int>(k_lo / 64), t1 = static_cast<int>((k_hi + 63) / 64);
 
-  f32x16 o[2][kN] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  f32x16 o[QT][kN] = {};
+  float m[QT], l[QT];
+#pragma unroll
+  for (int u = 0; u < QT; ++u) {
+    m[u] = -INFINITY;
+    l[u] = 0.0f;
+  }
   Stage<T, EP, 64, kThreads> ks, vs;
   bool keep = false;
   auto fetch = [&](int t) {
@@ -190,17 +199,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
     ks.write(k, tid, [&](int i) { return (bits_next >> i) & 1u; });
     vs.write(k + kTile, tid, [&](int i) { return (bits_next >> i) & 1u; });
   };
-  f32x16 x[2];          // scores of the subtile at hand
-  uint32_t p[2][8];     // probabilities of the subtile before, as bf16 pairs
+  f32x16 x[QT];          // scores of the subtile at hand
+  uint32_t p[QT][8];     // probabilities of the subtile before, as bf16 pairs
   auto scores = [&](int t, int s) {
     const char* k = lds + (t & 1) * 2 * kTile;
-    x[0] = f32x16{};
-    x[1] = f32x16{};
+#pragma unroll
+    for (int u = 0; u < QT; ++u) x[u] = f32x16{};
 #pragma unroll
     for (int j = 0; j < EP / 16; ++j) {
       const Mma<T>::Frag f = tile_frag<T, EP>(k, s * 32, j, lane);
-      x[0] = Mma<T>::mma(f, qf[0][j], x[0]);
-      x[1] = Mma<T>::mma(f, qf[1][j], x[1]);
+#pragma unroll
+      for (int u = 0; u < QT; ++u) x[u] = Mma<T>::mma(f, qf[u][j], x[u]);
     }
   };
   auto values = [&](int t, int s) {   // o += V^T P of subtile s of tile t
@@ -210,15 +219,16 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const char* q = v + (s * 32 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
-      const bf16x8 p0 = __builtin_bit_cast(bf16x8, u32x4{p[0][4 * kb], p[0][4 * kb + 1], p[0][4 * kb + 2], p[0][4 * kb + 3]});
-      const bf16x8 p1 = __builtin_bit_cast(bf16x8, u32x4{p[1][4 * kb], p[1][4 * kb + 1], p[1][4 * kb + 2], p[1][4 * kb + 3]});
 #pragma unroll
       for (int et = 0; et < kN; ++et) {
         const v4i16 lo = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64));
         const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
         const bf16x8 f = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
-        o[0][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p0, o[0][et], 0, 0, 0);
-        o[1][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, p1, o[1][et], 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          const bf16x8 pu = __builtin_bit_cast(bf16x8, u32x4{p[u][4 * kb], p[u][4 * kb + 1], p[u][4 * kb + 2], p[u][4 * kb + 3]});
+          o[u][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pu, o[u][et], 0, 0, 0);
+        }
       }
     }
   };
@@ -233,9 +243,9 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
     bits = bits_next;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float w[2][16];
+      float w[QT][16];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < QT; ++u) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[u][i] = x[u][i];
         drop_keys(w[u], static_cast<uint32_t>(bits >> (32 * s)), lane);
@@ -243,13 +253,15 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
       // the subtile before: its values are in this tile's buffer or the other
       if (s == 1) values(t, 0);
       else if (t > t0) values(t - 1, 1);
-      float top[2];
+      float top[QT];
+      bool far = false;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < QT; ++u) {
         top[u] = w[u][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top[u] = fmaxf(top[u], w[u][i]);
         top[u] = column_max(top[u]) * a.c;
+        far = far || top[u] > m[u] + kLag;
       }
       if (s == 0) {
         // all wavefronts are through with the other buffer
@@ -259,9 +271,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
       } else {
         lds_barrier();   // and now it holds the next tile
       }
-      if (__any(top[0] > m[0] + kLag || top[1] > m[1] + kLag)) {
+      if (__any(far)) {
+        asm volatile("");   // a branch: these products are not to be done every time
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < QT; ++u) {
           const float mn = fmaxf(m[u], top[u]);
           const float f = __builtin_amdgcn_exp2f(m[u] - (mn == -INFINITY ? 0.0f : mn));
           m[u] = mn;
@@ -273,7 +286,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
       if (s == 0) scores(t, 1);
       else if (t + 1 < t1) scores(t + 1, 0);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < QT; ++u) {
         const float base = m[u] == -INFINITY ? 0.0f : m[u];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -287,7 +300,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_wide_kernel(AttnP<bf16_t> a)
   }
   if (t0 < t1) values(t1 - 1, 1);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < QT; ++u) {
     const uint32_t r = r0 + 32 * u;
     const bool row_ok = r < a.rows;
     const QRow w = q_row(a, hk, r);
@@ -658,9 +671,9 @@ hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Trac
   if (k.plan == AttnPlan::kFew)
     return run<T>(attn_few_kernel<T, EP, FULL>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
   if constexpr (FULL && sizeof(T) == 2) {
-    // a workgroup of the wide kernel takes 256 rows and a compute unit
-    if (heads * cdiv(p.rows, 256) >= 192) {
-      p.row_tiles = static_cast<int>(cdiv(p.rows, 256));
+    constexpr int rows_each = 128 * wide_tiles(EP);
+    if (heads * cdiv(p.rows, rows_each) >= 192) {
+      p.row_tiles = static_cast<int>(cdiv(p.rows, rows_each));
       return run<T>(attn_wide_kernel<EP>, "attn_wide", 128 * row, heads * p.row_tiles, p, stream, tr);
     }
   }

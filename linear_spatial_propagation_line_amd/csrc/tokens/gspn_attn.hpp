@@ -198,7 +198,10 @@ __device__ __forceinline__ void drop_keys(float (&w)[16], uint32_t bits, int lan
   if (bits != 0xffffffffu) {
     const uint32_t mine = bits >> (4 * (lane >> 5));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = (mine >> ((i & 3) + 8 * (i >> 2))) & 1u ? w[i] : -INFINITY;
+    for (int i = 0; i < 16; ++i) {   // all ones or zeros from the key's bit, then a bitwise select
+      const uint32_t m = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(mine), (i & 3) + 8 * (i >> 2), 1));
+      w[i] = __uint_as_float((__float_as_uint(w[i]) & m) | (0xff800000u & ~m));
+    }
   }
 }
 

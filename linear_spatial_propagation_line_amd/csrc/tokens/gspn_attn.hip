@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
 // read. At larger heads two column tiles need more than 256 registers: the
 // second wavefront per SIMD is lost, and results that the vector ALU works on
 // land in accumulation registers (2x4096x2048, 16 heads of 128: 250 us, with
-// one column tile 1xx).
+// one column tile 190).
 constexpr int wide_tiles(int EP) { return EP <= 64 ? 2 : 1; }
 template <int EP>
 __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a) {
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
   extern __shared__ __align__(16) char lds[];
   constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32, QT = wide_tiles(EP);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  uint32_t blk = blockIdx.x;
   const int rt = static_cast<int>(blk % a.row_tiles);
   const int64_t bh = blk / a.row_tiles, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);

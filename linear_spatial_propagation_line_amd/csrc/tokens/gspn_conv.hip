@@ -8,16 +8,16 @@
 // (forward), so the work is to move each row once in wide accesses. A lane
 // owns V adjacent channels (16 bytes) and walks a run of tokens with the last
 // K - 1 rows in registers, so each row is read once per run plus K - 1 rows
-// of the run before; rows are loaded kAhead at a time, which keeps that many
-// 16-byte loads in flight per lane.
+// of the run before (from L2); the run's rows are all loaded first, which keeps
+// that many 16-byte loads in flight per lane.
+#include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 
 namespace gspn {
 
 namespace {
 
-constexpr int kRun = 32;     // tokens one lane walks
-constexpr int kAhead = 8;    // rows loaded together
+constexpr int kRun = 16;     // tokens one lane walks, all loaded before the first is used
 
 template <typename T> struct ConvP {
   const T* x; int64_t xb, xr;
@@ -43,6 +43,46 @@ template <int V> __device__ __forceinline__ void ldv(const bf16_t* p, float* d) 
 template <int V, typename T> __device__ __forceinline__ void stv(T* p, const float* d) {
   if constexpr (V == 1) Store<T>::put(p, 0, d[0]);
   else run_st<V>(p, 0, d);
+}
+
+// V values as they lie in memory
+template <typename T, int V> struct Raw {
+  u32x4 q;
+  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void wide(float* d) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        d[k] = __uint_as_float(q[k]);
+      } else {
+        d[2 * k] = bf16_lo(q[k]);
+        d[2 * k + 1] = bf16_hi(q[k]);
+      }
+    }
+  }
+};
+template <typename T> struct Raw<T, 1> {
+  T q;
+  __device__ __forceinline__ void load(const T* p) { q = *p; }
+  __device__ __forceinline__ void wide(float* d) const { d[0] = to_f32(q); }
+};
+// rows t .. t + N - 1 of a [B, L, C] tensor's entry, clamped to the last of n
+template <int N, typename T, int V>
+__device__ __forceinline__ void load_run(const T* base, int64_t stride, int64_t t, int64_t n, Raw<T, V> (&r)[N]) {
+  const T* p = base + t * stride;
+  if (t + N <= n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(p);
+      p += stride;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(p);
+      p += t + k + 1 < n ? stride : 0;
+    }
+  }
 }
 
 // row t of xx without the K - 1 offset: x[t] for 0 <= t < n, the state for
@@ -74,6 +114,10 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
   const int64_t n = seq_len(a.lens, b, a.L);
   const int64_t t0 = run * kRun, t1 = t0 + kRun < a.L ? t0 + kRun : a.L;
 
+  // the run's rows first; a run of padding reads nothing
+  const int live = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kRun ? n - t0 : kRun));
+  Raw<T, V> raw[kRun];
+  if (live > 0) load_run(a.x + b * a.xb + c, a.xr, t0, n, raw);
   float w[K][V], bias[V], win[K - 1 > 0 ? K - 1 : 1][V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -93,33 +137,31 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
     for (int j = 0; j < K - 1; ++j) stv<V>(a.state_out + (b * (K - 1) + j) * a.C + c, last[j]);
   }
   T* o = a.out + (b * a.L + t0) * a.C + c;
-  for (int64_t t = t0; t < t1; t += kAhead) {
-    float r[kAhead][V];
+  const int rows = static_cast<int>(t1 - t0);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) row_at<K, V>(a, b, c, t + k, n, r[k]);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (t + k < t1) {
-        float y[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float s = bias[e];
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
-          s = __builtin_fmaf(w[K - 1][e], r[k][e], s);
-          if (a.silu) s *= sigmoid_f32(s);
-          y[e] = t + k < n ? s : 0.0f;
-        }
-        stv<V>(o, y);
-        o += a.C;
-      }
+  for (int k = 0; k < kRun; ++k) {
+    float y[V];
+    if (k < live) {
+      float r[V];
+      raw[k].wide(r);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
+        float s = bias[e];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
+        s = __builtin_fmaf(w[K - 1][e], r[e], s);
+        if (a.silu) s *= sigmoid_f32(s);
+        y[e] = s;
 #pragma unroll
         for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
-        if (K > 1) win[K > 1 ? K - 2 : 0][e] = r[k][e];
+        if (K > 1) win[K > 1 ? K - 2 : 0][e] = r[e];
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = 0.0f;
     }
+    if (k < rows) stv<V>(o, y);
+    o += a.C;
   }
 }
 
@@ -157,55 +199,59 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j + 1]);
-    const T* gp = a.gy + b * a.gb + c;
-    for (int64_t t = t0; t < t1 + K - 1; t += kAhead) {
-      float r[kAhead][V], gy[kAhead][V];
+    constexpr int kNeed = kRun + K - 1;
+    Raw<T, V> rx[kNeed], rg[kNeed];
+    const int tokens = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kNeed ? n - t0 : kNeed));   // others give dpre = 0
+    if (tokens > 0) {
+      load_run(a.x + b * a.xb + c, a.xr, t0, n, rx);
+      load_run(a.gy + b * a.gb + c, a.gr, t0, n, rg);
+    }
+    const int rows = static_cast<int>(t1 - t0);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const bool in = t + k < n;   // rows past the end give dpre = 0
-        row_at<K, V>(a, b, c, in ? t + k : n, n, r[k]);
-        if (in) ldv<V>(gp + (t + k) * a.gr, gy[k]);
-      }
+    for (int k = 0; k < kNeed; ++k) {
+      if (k < rows + K - 1) {
+        float o[V], r[V], gy[V];
+        if (k < tokens) {
+          rx[k].wide(r);
+          rg[k].wide(gy);
+        }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int64_t tt = t + k;
-        if (tt < t1 + K - 1) {
-          float o[V];
+        for (int e = 0; e < V; ++e) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) win[j][e] = win[j + 1][e];
-            win[K - 1][e] = r[k][e];
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) dp[j][e] = dp[j + 1][e];
+          for (int j = 0; j < K - 1; ++j) {
+            win[j][e] = win[j + 1][e];
+            dp[j][e] = dp[j + 1][e];
+          }
+          dp[K - 1][e] = 0.0f;
+          if (k < tokens) {
+            win[K - 1][e] = r[e];
             float s = bias[e];
 #pragma unroll
             for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
-            float d = 1.0f;
+            float d = gy[e];
             if (a.silu) {
               const float sg = sigmoid_f32(s);
-              d = sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
+              d *= sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
             }
-            d = tt < n ? d * gy[k][e] : 0.0f;
             dp[K - 1][e] = d;
-            if (tt < t1 && tt < n) {
+            if (k < rows) {
               db[e] += d;
 #pragma unroll
               for (int j = 0; j < K; ++j) dw[j][e] = __builtin_fmaf(d, win[j][e], dw[j][e]);
             }
-            // dxx of row s = tt - (K - 1): w[j] meets dpre[s + K - 1 - j]
-            o[e] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
           }
-          const int64_t s = tt - (K - 1);
-          if (s >= t0) {
+          // dxx of row s = t0 + k - (K - 1): w[j] meets dpre[s + K - 1 - j]
+          o[e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
-            stv<V>(a.dx + (b * a.L + s) * a.C + c, o);
-          } else if (run == 0 && a.dstate) {
-            stv<V>(a.dstate + (b * (K - 1) + s + K - 1) * a.C + c, o);
-          }
+          for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
+        }
+        const int64_t s = t0 + k - (K - 1);
+        if (s >= t0) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
+          stv<V>(a.dx + (b * a.L + s) * a.C + c, o);
+        } else if (run == 0 && a.dstate) {
+          stv<V>(a.dstate + (b * (K - 1) + s + K - 1) * a.C + c, o);
         }
       }
     }

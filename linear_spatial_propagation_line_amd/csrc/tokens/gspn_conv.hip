@@ -18,6 +18,15 @@ namespace gspn {
 namespace {
 
 constexpr int kRun = 16;     // tokens one lane walks, all loaded before the first is used
+constexpr int kStepBwd = 8;  // backward: tokens loaded together
+// Backward: tokens per run. Long runs leave few partial sums and re-read few
+// rows; shorter ones where the wavefronts would not fill the chip four times
+// (8x4096x2304 bf16: 64 tokens 238 us, 16 tokens 341; 3x1021x1153: 42, 32).
+int64_t bwd_run(int64_t B, int64_t L, int64_t C) {
+  for (int64_t run = 64; run > 16; run /= 2)
+    if (B * cdiv(L, run) * cdiv(C, 256) >= 4096) return run;
+  return 16;
+}
 
 template <typename T> struct ConvP {
   const T* x; int64_t xb, xr;
@@ -26,32 +35,38 @@ template <typename T> struct ConvP {
   T* out; T* state_out;
   T* dx; T* dstate; float* part;
   int64_t L, C;
-  int64_t runs;       // runs of kRun tokens per entry (at least 1)
+  int64_t run, runs;  // backward: tokens per run; runs per entry (at least 1)
   int64_t ctiles;     // tiles of 64 * V channels
   int silu;
 };
 
 // V values at p, widened
-template <int V> __device__ __forceinline__ void ldv(const float* p, float* d) {
-  if constexpr (V == 1) d[0] = p[0];
-  else run_ld<V>(p, 0, d);
-}
-template <int V> __device__ __forceinline__ void ldv(const bf16_t* p, float* d) {
-  if constexpr (V == 1) d[0] = to_f32(p[0]);
-  else run_ld<V>(p, 0, d);
+template <int V, typename T> __device__ __forceinline__ void ldv(const T* p, float* d) {
+  if constexpr (V == 1) {
+    d[0] = to_f32(p[0]);
+  } else if constexpr (V == 4) {
+    const auto q = V4<T>::load(p, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = V4<T>::get(q, e);
+  } else {
+    run_ld<V>(p, 0, d);
+  }
 }
 template <int V, typename T> __device__ __forceinline__ void stv(T* p, const float* d) {
   if constexpr (V == 1) Store<T>::put(p, 0, d[0]);
+  else if constexpr (V == 4) V4<T>::store(p, 0, d);
   else run_st<V>(p, 0, d);
 }
 
 // V values as they lie in memory
 template <typename T, int V> struct Raw {
-  u32x4 q;
-  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const u32x4*>(p); }
+  static constexpr int kWords = V * static_cast<int>(sizeof(T)) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  Words q;
+  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const Words*>(p); }
   __device__ __forceinline__ void wide(float* d) const {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kWords; ++k) {
       if constexpr (sizeof(T) == 4) {
         d[k] = __uint_as_float(q[k]);
       } else {
@@ -165,7 +180,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
   }
 }
 
-// A run of kRun tokens computes dpre for its own tokens and the K - 1 after
+// A run computes dpre for its own tokens and the K - 1 after
 // them (which its dx needs too); dw and db take its own tokens only. The
 // partial sums of the workgroup's four runs are joined in LDS, in run order,
 // into row (b, group of runs) of part: [K + 1][C], taps first, then the bias.
@@ -190,7 +205,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
   }
   if (live) {
     const int64_t n = seq_len(a.lens, b, a.L);
-    const int64_t t0 = run * kRun, t1 = t0 + kRun < a.L ? t0 + kRun : a.L;
+    const int64_t t0 = run * a.run, t1 = t0 + a.run < a.L ? t0 + a.run : a.L;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
 #pragma unroll
@@ -199,59 +214,62 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j + 1]);
-    constexpr int kNeed = kRun + K - 1;
-    Raw<T, V> rx[kNeed], rg[kNeed];
-    const int tokens = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kNeed ? n - t0 : kNeed));   // others give dpre = 0
-    if (tokens > 0) {
-      load_run(a.x + b * a.xb + c, a.xr, t0, n, rx);
-      load_run(a.gy + b * a.gb + c, a.gr, t0, n, rg);
-    }
-    const int rows = static_cast<int>(t1 - t0);
+    Raw<T, V> rx[kStepBwd], rg[kStepBwd];
+    for (int64_t t = t0; t < t1 + K - 1; t += kStepBwd) {
+      // tokens from here on that are no padding; others give dpre = 0
+      const int tokens = static_cast<int>(n - t < 0 ? 0 : (n - t < kStepBwd ? n - t : kStepBwd));
+      const int rows = static_cast<int>(t1 - t < kStepBwd ? t1 - t : kStepBwd);   // of this run (may be <= 0)
+      const int need = static_cast<int>(t1 + K - 1 - t < kStepBwd ? t1 + K - 1 - t : kStepBwd);
+      if (tokens > 0) {
+        load_run(a.x + b * a.xb + c, a.xr, t, n, rx);
+        load_run(a.gy + b * a.gb + c, a.gr, t, n, rg);
+      }
 #pragma unroll
-    for (int k = 0; k < kNeed; ++k) {
-      if (k < rows + K - 1) {
-        float o[V], r[V], gy[V];
-        if (k < tokens) {
-          rx[k].wide(r);
-          rg[k].wide(gy);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) {
-            win[j][e] = win[j + 1][e];
-            dp[j][e] = dp[j + 1][e];
-          }
-          dp[K - 1][e] = 0.0f;
+      for (int k = 0; k < kStepBwd; ++k) {
+        if (k < need) {
+          float o[V], r[V], gy[V];
           if (k < tokens) {
-            win[K - 1][e] = r[e];
-            float s = bias[e];
-#pragma unroll
-            for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
-            float d = gy[e];
-            if (a.silu) {
-              const float sg = sigmoid_f32(s);
-              d *= sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
-            }
-            dp[K - 1][e] = d;
-            if (k < rows) {
-              db[e] += d;
-#pragma unroll
-              for (int j = 0; j < K; ++j) dw[j][e] = __builtin_fmaf(d, win[j][e], dw[j][e]);
-            }
+            rx[k].wide(r);
+            rg[k].wide(gy);
           }
-          // dxx of row s = t0 + k - (K - 1): w[j] meets dpre[s + K - 1 - j]
-          o[e] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
-        }
-        const int64_t s = t0 + k - (K - 1);
-        if (s >= t0) {
+          for (int e = 0; e < V; ++e) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
-          stv<V>(a.dx + (b * a.L + s) * a.C + c, o);
-        } else if (run == 0 && a.dstate) {
-          stv<V>(a.dstate + (b * (K - 1) + s + K - 1) * a.C + c, o);
+            for (int j = 0; j < K - 1; ++j) {
+              win[j][e] = win[j + 1][e];
+              dp[j][e] = dp[j + 1][e];
+            }
+            dp[K - 1][e] = 0.0f;
+            if (k < tokens) {
+              win[K - 1][e] = r[e];
+              float s = bias[e];
+#pragma unroll
+              for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[j][e], win[j][e], s);
+              float d = gy[e];
+              if (a.silu) {
+                const float sg = sigmoid_f32(s);
+                d *= sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
+              }
+              dp[K - 1][e] = d;
+              if (k < rows) {
+                db[e] += d;
+#pragma unroll
+                for (int j = 0; j < K; ++j) dw[j][e] = __builtin_fmaf(d, win[j][e], dw[j][e]);
+              }
+            }
+            // dxx of row s = t + k - (K - 1): w[j] meets dpre[s + K - 1 - j]
+            o[e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
+          }
+          const int64_t s = t + k - (K - 1);
+          if (s >= t0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
+            stv<V>(a.dx + (b * a.L + s) * a.C + c, o);
+          } else if (run == 0 && a.dstate) {
+            stv<V>(a.dstate + (b * (K - 1) + s + K - 1) * a.C + c, o);
+          }
         }
       }
     }
@@ -344,7 +362,8 @@ template <typename T> ConvP<T> conv_params(const gspn_conv_args& a) {
 template <typename T, int K>
 hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, hipStream_t stream,
                    Tracer* tr) {
-  constexpr int V = 16 / sizeof(T);
+  // backward: four channels per lane, since their sums and windows fill registers
+  constexpr int V = 16 / sizeof(T), VB = 4;
   ConvP<T> p = conv_params<T>(a);
   const size_t es = sizeof(T);
   bool wide = a.C % V == 0 && wide_ok(a.x.p, 16, es, {a.x.batch, a.x.row}) &&
@@ -356,19 +375,21 @@ hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, 
     p.dx = static_cast<T*>(g->x);
     p.dstate = static_cast<T*>(g->state);
     p.part = static_cast<float*>(ws);
+    p.run = bwd_run(a.B, a.L, a.C);
+    p.runs = std::max<int64_t>(1, cdiv(a.L, p.run));
     wide = wide && wide_ok(p.gy, 16, es, {p.gb, p.gr}) && wide_ok(p.dx, 16, es, {}) &&
            (!p.dstate || wide_ok(p.dstate, 16, es, {}));
   } else {
     wide = wide && wide_ok(p.out, 16, es, {}) && (!p.state_out || wide_ok(p.state_out, 16, es, {}));
   }
-  p.ctiles = cdiv(a.C, 64 * (wide ? V : 1));
+  p.ctiles = cdiv(a.C, 64 * (wide ? (g ? VB : V) : 1));
   const int64_t rgroups = cdiv(p.runs, 4);
   const dim3 grid(static_cast<unsigned>(a.B * rgroups * p.ctiles));
   const char* name = g ? "conv_bwd" : "conv_fwd";
   tr->before(stream, name, a.B);
   if (a.B > 0) {
     if (g) {
-      if (wide) hipLaunchKernelGGL((conv_bwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
+      if (wide) hipLaunchKernelGGL((conv_bwd_kernel<T, K, VB>), grid, dim3(256), 0, stream, p);
       else hipLaunchKernelGGL((conv_bwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);
     } else {
       if (wide) hipLaunchKernelGGL((conv_fwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
@@ -412,7 +433,7 @@ hipError_t reduce_rows(const float* part, int64_t rows, int64_t cols, T* out, hi
 template hipError_t reduce_rows<float>(const float*, int64_t, int64_t, float*, hipStream_t, Tracer*);
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t K) {
-  const int64_t rgroups = cdiv(std::max<int64_t>(1, cdiv(L, kRun)), 4);
+  const int64_t rgroups = cdiv(std::max<int64_t>(1, cdiv(L, bwd_run(B, L, C))), 4);
   return static_cast<size_t>(B * rgroups * (K + 1) * C) * sizeof(float);
 }
 

@@ -100,6 +100,31 @@ __device__ __forceinline__ void load_run(const T* base, int64_t stride, int64_t 
   }
 }
 
+// taps and bias of V channels; V > 1: whole pieces, taps of a channel adjacent
+template <int K, int V, typename T>
+__device__ __forceinline__ void load_taps(const T* w, const T* bias, int64_t c, float (&tap)[K][V], float (&b)[V]) {
+  if constexpr (V > 1) {
+    Raw<T, V> raw[K + 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k) raw[k].load(w + c * K + k * V);
+    if (bias) raw[K].load(bias + c);
+    float flat[K * V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) raw[k].wide(flat + k * V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) tap[j][e] = flat[e * K + j];
+      b[e] = 0.0f;
+    }
+    if (bias) raw[K].wide(b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < K; ++j) tap[j][0] = ld1(w + c * K + j);
+    b[0] = bias ? ld1(bias + c) : 0.0f;
+  }
+}
+
 // row t of xx without the K - 1 offset: x[t] for 0 <= t < n, the state for
 // t < 0 (zeros without one); rows past n are not read
 template <int K, int V, typename T>
@@ -119,12 +144,12 @@ template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
   // four runs of one channel tile per workgroup, one per wavefront
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t rgroups = (a.runs + 3) / 4;
-  int64_t i = blockIdx.x;
-  const int64_t ct = i % a.ctiles;
-  i /= a.ctiles;
+  const uint32_t rgroups = static_cast<uint32_t>((a.runs + 3) / 4), ctiles = static_cast<uint32_t>(a.ctiles);
+  uint32_t i = blockIdx.x;
+  const uint32_t ct = i % ctiles;
+  i /= ctiles;
   const int64_t rg = i % rgroups, b = i / rgroups;
-  const int64_t run = rg * 4 + wave, c = (ct * 64 + lane) * V;
+  const int64_t run = rg * 4 + wave, c = (static_cast<int64_t>(ct) * 64 + lane) * V;
   if (run >= a.runs || c >= a.C) return;
   const int64_t n = seq_len(a.lens, b, a.L);
   const int64_t t0 = run * kRun, t1 = t0 + kRun < a.L ? t0 + kRun : a.L;
@@ -134,12 +159,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
   Raw<T, V> raw[kRun];
   if (live > 0) load_run(a.x + b * a.xb + c, a.xr, t0, n, raw);
   float w[K][V], bias[V], win[K - 1 > 0 ? K - 1 : 1][V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j][e] = ld1(a.w + (c + e) * K + j);
-    bias[e] = a.bias ? ld1(a.bias + c + e) : 0.0f;
-  }
+  load_taps<K, V>(a.w, a.bias, c, w, bias);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j]);
   // the run that reads the old state also writes the new one (they may be
@@ -188,12 +208,12 @@ template <typename T, int K, int V>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
   __shared__ float acc[3][(K + 1) * V][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t rgroups = (a.runs + 3) / 4;
-  int64_t i = blockIdx.x;
-  const int64_t ct = i % a.ctiles;
-  i /= a.ctiles;
+  const uint32_t rgroups = static_cast<uint32_t>((a.runs + 3) / 4), ctiles = static_cast<uint32_t>(a.ctiles);
+  uint32_t i = blockIdx.x;
+  const uint32_t ct = i % ctiles;
+  i /= ctiles;
   const int64_t rg = i % rgroups, b = i / rgroups;
-  const int64_t run = rg * 4 + wave, c = (ct * 64 + lane) * V;
+  const int64_t run = rg * 4 + wave, c = (static_cast<int64_t>(ct) * 64 + lane) * V;
   const bool live = run < a.runs && c < a.C;
 
   float w[K][V], bias[V], win[K][V], dp[K][V], dw[K][V], db[V];
@@ -206,12 +226,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
   if (live) {
     const int64_t n = seq_len(a.lens, b, a.L);
     const int64_t t0 = run * a.run, t1 = t0 + a.run < a.L ? t0 + a.run : a.L;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-#pragma unroll
-      for (int j = 0; j < K; ++j) w[j][e] = ld1(a.w + (c + e) * K + j);
-      bias[e] = a.bias ? ld1(a.bias + c + e) : 0.0f;
-    }
+    load_taps<K, V>(a.w, a.bias, c, w, bias);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) row_at<K, V>(a, b, c, t0 - (K - 1) + j, n, win[j + 1]);
     Raw<T, V> rx[kStepBwd], rg[kStepBwd];
@@ -323,21 +338,27 @@ __global__ __launch_bounds__(512) void conv_reduce_kernel(const float* part, int
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(512) void reduce_rows_kernel(const float* part, int64_t rows,
-                                                          int64_t cols, T* out) {
+__global__ __launch_bounds__(512) void reduce_rows_kernel(RowSums r) {
   __shared__ float acc[8][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i = blockIdx.x * int64_t(64) + lane;
+  int64_t blk = blockIdx.x;
+  int k = 0;   // the table this block works on
+  while (k < 2 && blk >= (r.cols[k] + 63) / 64) {
+    blk -= (r.cols[k] + 63) / 64;
+    ++k;
+  }
+  const float* part = k == 0 ? r.part[0] : (k == 1 ? r.part[1] : r.part[2]);
+  float* out = k == 0 ? r.out[0] : (k == 1 ? r.out[1] : r.out[2]);
+  const int64_t cols = k == 0 ? r.cols[0] : (k == 1 ? r.cols[1] : r.cols[2]), i = blk * 64 + lane;
   float s = 0.0f;
   if (i < cols)
-    for (int64_t r = wave; r < rows; r += 8) s += part[r * cols + i];
+    for (int64_t q = wave; q < r.rows; q += 8) s += part[q * cols + i];
   acc[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && i < cols) {
 #pragma unroll
     for (int q = 1; q < 8; ++q) s += acc[q][lane];
-    Store<T>::put(out, i, s);
+    out[i] = s;
   }
 }
 
@@ -367,6 +388,7 @@ hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, 
   ConvP<T> p = conv_params<T>(a);
   const size_t es = sizeof(T);
   bool wide = a.C % V == 0 && wide_ok(a.x.p, 16, es, {a.x.batch, a.x.row}) &&
+              wide_ok(a.weight, 16, es, {}) && (!a.bias || wide_ok(a.bias, 16, es, {})) &&
               (!a.state || wide_ok(a.state, 16, es, {}));
   if (g) {
     p.gy = static_cast<const T*>(g->grad_out.p);
@@ -421,16 +443,19 @@ hipError_t conv_k(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, h
 
 }  // namespace
 
-template <typename T>
-hipError_t reduce_rows(const float* part, int64_t rows, int64_t cols, T* out, hipStream_t stream,
-                       Tracer* tr) {
-  tr->before(stream, "reduce_rows", rows);
-  hipLaunchKernelGGL(reduce_rows_kernel<T>, dim3(static_cast<unsigned>(cdiv(cols, 64))), dim3(512),
-                     0, stream, part, rows, cols, out);
+hipError_t reduce_rows(const RowSums& s, hipStream_t stream, Tracer* tr) {
+  RowSums r = s;
+  int64_t grid = 0;
+  for (int k = 0; k < 3; ++k) {
+    if (!r.out[k]) r.cols[k] = 0;
+    grid += cdiv(r.cols[k], 64);
+  }
+  if (grid == 0) return hipSuccess;
+  tr->before(stream, "reduce_rows", r.rows);
+  hipLaunchKernelGGL(reduce_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(512), 0, stream, r);
   tr->after(stream);
   return hipGetLastError();
 }
-template hipError_t reduce_rows<float>(const float*, int64_t, int64_t, float*, hipStream_t, Tracer*);
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t K) {
   const int64_t rgroups = cdiv(std::max<int64_t>(1, cdiv(L, bwd_run(B, L, C))), 4);

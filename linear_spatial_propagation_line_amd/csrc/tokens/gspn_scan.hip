@@ -67,6 +67,7 @@ template <typename T> struct ScanP {
   float* dstate;
   int64_t B, L, Lp, C, G, Cg, chunks;   // Lp: L rounded up to whole chunks
   int N, tiles, segs, segChunks, softplus;
+  bool whole, whole_bc;   // single tokens: states, B and C in whole aligned pieces of four
 };
 
 // ---- B and C as fp32, zeros past N states and past the entry's tokens --------
@@ -419,30 +420,34 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
 // state's bytes, or by launch latency for small batches.
 template <typename T, int P>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanP<T> a) {
-  const int64_t per = 256 / P, ctiles = (a.C + per - 1) / per;
+  constexpr uint32_t per = 256 / P;
+  const uint32_t ctiles = (static_cast<uint32_t>(a.C) + per - 1) / per;
   const int64_t b = blockIdx.x / ctiles;
   const int q = threadIdx.x % P;
-  const int64_t c0 = (blockIdx.x % ctiles) * per + threadIdx.x / P;
+  const uint32_t c0 = (blockIdx.x % ctiles) * per + threadIdx.x / P;
   const bool live = c0 < a.C;
-  const int64_t c = live ? c0 : a.C - 1, g = c / a.Cg, n0 = 4 * q;
+  const int64_t c = live ? c0 : a.C - 1;
+  const int64_t g = static_cast<uint32_t>(c) / static_cast<uint32_t>(a.Cg), n0 = 4 * q;
   const int64_t len = seq_len(a.lens, b, a.L);
   const int64_t si = (b * a.C + c) * a.N + n0;
-  const bool vec = a.N % 4 == 0;   // then rows of four states are whole (and 16-byte aligned)
-  float A2[4], h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float A2[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool wide = a.whole;   // rows of four states are whole and aligned
+  if (wide) {
+    if (n0 < a.N) {
+      run_ld<4>(a.A, c * a.N + n0, A2);
+      if (a.state) run_ld<4>(a.state, si, h);
+    }
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    A2[k] = n0 + k < a.N ? a.A[c * a.N + n0 + k] * kLog2e : 0.0f;
-    if (a.state && !vec && n0 + k < a.N) h[k] = a.state[si + k];
-  }
-  const bool wide = vec && ((reinterpret_cast<uintptr_t>(a.state) | reinterpret_cast<uintptr_t>(a.state_out)) % 16 == 0);
-  if (a.state && vec && n0 < a.N) {
-    if (wide) {
-      run_ld<4>(a.state, si, h);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = a.state[si + k];
+    for (int k = 0; k < 4; ++k) {
+      if (n0 + k < a.N) {
+        A2[k] = a.A[c * a.N + n0 + k];
+        if (a.state) h[k] = a.state[si + k];
+      }
     }
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
   if (a.saved && live) {   // the state before token 0, padding states (zeros) included
 #pragma unroll
     for (int k = 0; k < 4; ++k) a.saved[(b * 4 * P + n0 + k) * a.C + c] = h[k];
@@ -456,12 +461,29 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanP<T> a) {
       const float dx = d * x;
       const T* Bt = a.Bm + b * a.bb + t * a.br + g * a.bh;
       const T* Ct = a.Cm + b * a.cb + t * a.cr + g * a.ch;
+      float Bv[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Cv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.whole_bc) {
+        if (n0 < a.N) {
+          const auto u = V4<T>::load(Bt, n0), v = V4<T>::load(Ct, n0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            Bv[k] = V4<T>::get(u, k);
+            Cv[k] = V4<T>::get(v, k);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (n0 + k < a.N) {
+            Bv[k] = ld1(Bt + n0 + k);
+            Cv[k] = ld1(Ct + n0 + k);
+          }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (n0 + k < a.N) {
-          h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[k]), h[k], dx * ld1(Bt + n0 + k));
-          y = __builtin_fmaf(ld1(Ct + n0 + k), h[k], y);
-        }
+        h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[k]), h[k], dx * Bv[k]);
+        y = __builtin_fmaf(Cv[k], h[k], y);
       }
 #pragma unroll
       for (int m = 1; m < P; m *= 2) y += __shfl_xor(y, m);
@@ -899,7 +921,12 @@ hipError_t scan_fwd_ns(const gspn_scan_args& a, void* ws, hipStream_t stream, Tr
 template <typename T>
 hipError_t scan_fwd_dt(const gspn_scan_args& a, void* ws, hipStream_t stream, Tracer* tr) {
   if (a.L <= kStepMax) {
-    const ScanP<T> p = scan_params<T>(a, false);
+    ScanP<T> p = scan_params<T>(a, false);
+    p.whole = a.N % 4 == 0 && wide_ok(a.A, 16, 4, {}) && (!a.state || wide_ok(a.state, 16, 4, {})) &&
+              (!a.state_out || wide_ok(a.state_out, 16, 4, {}));
+    p.whole_bc = a.N % 4 == 0 &&
+                 wide_ok(a.Bm.p, 4 * sizeof(T), sizeof(T), {a.Bm.batch, a.Bm.row, a.Bm.head}) &&
+                 wide_ok(a.Cm.p, 4 * sizeof(T), sizeof(T), {a.Cm.batch, a.Cm.row, a.Cm.head});
     const int lanes = scan_np(a.N) / 4;
     const int64_t grid = a.B * cdiv(a.C, 256 / lanes);
     switch (lanes) {
@@ -965,11 +992,8 @@ hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
                   static_cast<T*>(g.Cm));
   }
   const int64_t rows = p.B * p.segs;
-  e = reduce_rows<float>(p.partA, rows, p.C * p.N, g.A, stream, tr);
-  if (e == hipSuccess && g.D) e = reduce_rows<float>(p.partD, rows, p.C, g.D, stream, tr);
-  if (e == hipSuccess && g.dt_bias)
-    e = reduce_rows<float>(p.partD + rows * p.C, rows, p.C, g.dt_bias, stream, tr);
-  return e;
+  return reduce_rows(RowSums{{p.partA, p.partD, p.partD + rows * p.C}, {g.A, g.D, g.dt_bias},
+                             {p.C * p.N, p.C, p.C}, rows}, stream, tr);
 }
 
 template <typename T>

@@ -35,12 +35,17 @@ size_t attn_bwd_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, i
 hipError_t launch_attn_bwd(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws,
                            hipStream_t stream, Tracer* tr);
 
-// out[i] = sum over r < rows of part[r * cols + i], in row order within each
-// of eight interleaved row sets whose sums are then added in order; rows = 0
-// writes zeros (gspn_conv.hip)
-template <typename T>
-hipError_t reduce_rows(const float* part, int64_t rows, int64_t cols, T* out, hipStream_t stream,
-                       Tracer* tr);
+// Up to three tables of fp32 partial sums, [rows][cols] each, summed over
+// their rows into fp32 results, in row order within each of eight interleaved
+// row sets whose sums are then added in order; rows = 0 writes zeros, a table
+// without a result is left out (gspn_conv.hip)
+struct RowSums {
+  const float* part[3];
+  float* out[3];
+  int64_t cols[3];
+  int64_t rows;
+};
+hipError_t reduce_rows(const RowSums& s, hipStream_t stream, Tracer* tr);
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }

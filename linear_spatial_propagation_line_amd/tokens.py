@@ -9,7 +9,6 @@ on ``stream`` (default: torch's current stream of the inputs' device), and
 what a call allocates belongs to that stream."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import struct
 
@@ -26,6 +25,13 @@ _SCAN = struct.Struct("@5qii PqqPqqPqq P PqqqPqqq PPPP PPP".replace(" ", ""))
 _SCAN_GRADS = struct.Struct("@PqqPPPPPPPPPP")
 _ATTN = struct.Struct("@6qif PqqqPqqqPqqq Pq PP".replace(" ", ""))
 _ATTN_GRADS = struct.Struct("@PqqqPPP")
+
+_Tensor = torch.Tensor
+# the current stream's handle and the current device, without the objects
+# around them where torch offers that
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda i: torch.cuda.current_stream(i).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 _tok = None
 
@@ -65,8 +71,9 @@ class _Call:
         if first.dtype not in _CODE:
             raise TypeError(f"unsupported dtype {first.dtype} (float32 or bfloat16)")
         self.device, self.dtype, self.code = first.device, first.dtype, _CODE[first.dtype]
+        self.index = first.get_device()
         if stream is None:
-            self.ptr, self.own = torch.cuda.current_stream(first.device).cuda_stream, None
+            self.ptr, self.own = _stream_of(self.index), None
         elif hasattr(stream, "cuda_stream"):
             self.ptr, self.own = stream.cuda_stream, stream
         else:
@@ -75,9 +82,9 @@ class _Call:
 
     def tensor(self, t, shape, what, dtype=None, contiguous=False):
         """An input of the given shape, in the call's dtype (or ``dtype``)."""
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
             raise TypeError(f"{what} must be a torch tensor on {self.device}")
-        if t.dtype != (dtype or self.dtype):
+        if t.dtype is not (dtype or self.dtype):
             raise ValueError(f"{what} must be {dtype or self.dtype}, not {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -87,7 +94,9 @@ class _Call:
 
     def view(self, t, shape, what):
         """(address, strides) of an input whose last dimension is contiguous."""
-        self.tensor(t, shape, what)
+        if not (type(t) is _Tensor and t.get_device() == self.index and t.dtype is self.dtype
+                and t.shape == shape):
+            self.tensor(t, shape, what)
         s = t.stride()
         if s[-1] != 1 and shape[-1] > 1:
             raise ValueError(f"{what} must be contiguous in its last dimension")
@@ -97,10 +106,15 @@ class _Call:
         """Address of a contiguous input, 0 for None."""
         if t is None:
             return 0
-        return self.tensor(t, shape, what, dtype, True).data_ptr()
+        if not (type(t) is _Tensor and t.get_device() == self.index
+                and t.dtype is (dtype or self.dtype) and t.shape == shape and t.is_contiguous()):
+            self.tensor(t, shape, what, dtype, True)
+        return t.data_ptr()
 
     def empty(self, shape, dtype=None):
-        with torch.cuda.stream(self.own) if self.own is not None else contextlib.nullcontext():
+        if self.own is None:
+            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+        with torch.cuda.stream(self.own):
             return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
     def out(self, t, shape, what, dtype=None):
@@ -122,7 +136,7 @@ class _Call:
         return ws, ws.data_ptr(), ws.numel()
 
     def run(self, f, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if _device_now() == self.index:
             status = f(*args, self.ptr)
         else:
             with torch.cuda.device(self.device):

@@ -146,8 +146,9 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int row0,
 }
 
 // acc[et][32 e of slab et][lane column] += tile rows^T W, W[32 rows][lane
-// column] in the result layout above
-template <int EP>
+// column] in the result layout above. The bf16 form takes W in bf16; with
+// REST also what that rounding left, in bf16 (16 bits of mantissa together).
+template <int EP, bool REST = false>
 __device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
                                            f32x16 (&acc)[EP / 32], int lane, bf16_t) {
   const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
@@ -158,6 +159,15 @@ __device__ __forceinline__ void tile_accum(const char* tile, int row0, const flo
 #pragma unroll
     for (int k = 0; k < 4; ++k) p[k] = pack_bf16x2(w[8 * kb + 2 * k], w[8 * kb + 2 * k + 1]);
     const bf16x8 b = __builtin_bit_cast(bf16x8, p);
+    bf16x8 rest;
+    if constexpr (REST) {
+      u32x4 l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        l[k] = pack_bf16x2(w[8 * kb + 2 * k] - __uint_as_float(p[k] << 16),
+                           w[8 * kb + 2 * k + 1] - __uint_as_float(p[k] & 0xffff0000u));
+      rest = __builtin_bit_cast(bf16x8, l);
+    }
     const char* q = tile + (row0 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
 #pragma unroll
     for (int et = 0; et < EP / 32; ++et) {
@@ -165,10 +175,11 @@ __device__ __forceinline__ void tile_accum(const char* tile, int row0, const flo
       const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
       const bf16x8 a = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
       acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[et], 0, 0, 0);
+      if constexpr (REST) acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, rest, acc[et], 0, 0, 0);
     }
   }
 }
-template <int EP>
+template <int EP, bool REST = false>
 __device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
                                            f32x16 (&acc)[EP / 32], int lane, float) {
   constexpr int pitch = tile_pitch<float, EP>();

@@ -240,7 +240,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(ds[i], a.c, -lse)) * (y[i] - delta);
-      tile_accum<EP>(kt, 0, ds, dq, lane, T{});
+      // A row of dQ is one sum over its keys: dS in 8 bits of mantissa would be
+      // its largest error, so the rest of the rounding is multiplied as well.
+      tile_accum<EP, true>(kt, 0, ds, dq, lane, T{});
     }
     if (t + 1 < t_last) put(t + 1);
     lds_barrier();

@@ -574,12 +574,13 @@ __global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n,
 }
 
 // ---- host -------------------------------------------------------------------
-enum class AttnPlan { kShort, kFew, kRows };   // kRows: attn_wide or attn_fwd
+enum class AttnPlan { kShort, kFew, kRows, kWide };
 struct AttnCut {
   AttnPlan plan;
   int splits, parts, key_tiles, row_tiles, tiles_each;
 };
-AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, size_t es) {
+// `full`: whole 16-byte pieces everywhere and no padding of the head
+AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E, size_t es, bool full) {
   AttnCut k{};
   const int64_t rows = Lq * (Hq / Hkv), heads = std::max<int64_t>(1, B * Hkv);
   int64_t splits = 1;
@@ -602,6 +603,13 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, siz
     splits = std::max<int64_t>(1, std::min<int64_t>(64, std::min<int64_t>(cdiv(k.key_tiles, 8), cdiv(1024, heads))));
     k.tiles_each = static_cast<int>(cdiv(cdiv(k.key_tiles, splits), 4) * 4);
     k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
+  } else if (full && es == 2 && heads * cdiv(rows, 128 * wide_tiles(attn_ep(E))) >= 192) {
+    // Workgroups enough for three quarters of the compute units: no splits.
+    k.plan = AttnPlan::kWide;
+    k.key_tiles = static_cast<int>(cdiv(Lk, 64));
+    k.row_tiles = static_cast<int>(cdiv(rows, 128 * wide_tiles(attn_ep(E))));
+    k.tiles_each = k.key_tiles;
+    k.splits = 1;
   } else {
     // Few row tiles: the key axis is split until about two workgroups per
     // compute unit run.
@@ -617,7 +625,7 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, siz
   return k;
 }
 
-template <typename T> AttnP<T> attn_params(const gspn_attn_args& a, const AttnCut& k) {
+template <typename T> AttnP<T> attn_params(const gspn_attn_args& a) {
   AttnP<T> p{};
   p.q = static_cast<const T*>(a.q.p); p.qm = {a.q.batch, a.q.row, a.q.head};
   p.k = static_cast<const T*>(a.k.p); p.km = {a.k.batch, a.k.row, a.k.head};
@@ -630,8 +638,6 @@ template <typename T> AttnP<T> attn_params(const gspn_attn_args& a, const AttnCu
   p.share = p.Hq / p.Hkv;
   p.rows = a.Lq * p.share;
   p.E = static_cast<int>(a.E);
-  p.splits = k.splits; p.key_tiles = k.key_tiles; p.row_tiles = k.row_tiles;
-  p.tiles_each = k.tiles_each;
   p.c = a.scale * kLog2e;
   constexpr int per = 16 / sizeof(T);
   const bool whole = a.E % per == 0;
@@ -671,11 +677,8 @@ hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Trac
   if (k.plan == AttnPlan::kFew)
     return run<T>(attn_few_kernel<T, EP, FULL>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
   if constexpr (FULL && sizeof(T) == 2) {
-    constexpr int rows_each = 128 * wide_tiles(EP);
-    if (heads * cdiv(p.rows, rows_each) >= 192) {
-      p.row_tiles = static_cast<int>(cdiv(p.rows, rows_each));
+    if (k.plan == AttnPlan::kWide)
       return run<T>(attn_wide_kernel<EP>, "attn_wide", 128 * row, heads * p.row_tiles, p, stream, tr);
-    }
   }
   constexpr int TK = sizeof(T) == 2 ? 64 : 32;
   return run<T>(attn_fwd_kernel<T, EP, TK, FULL>, "attn_fwd", TK * row, heads * k.splits * k.row_tiles, p, stream, tr);
@@ -683,15 +686,16 @@ hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Trac
 
 template <typename T, int EP>
 hipError_t attn_ep_run(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr) {
-  const AttnCut k = cut_attn(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, sizeof(T));
-  AttnP<T> p = attn_params<T>(a, k);
+  AttnP<T> p = attn_params<T>(a);
+  const bool full = p.E == EP && p.wide_q && p.wide_kv && p.wide_o;
+  const AttnCut k = cut_attn(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, a.E, sizeof(T), full);
+  p.splits = k.splits; p.key_tiles = k.key_tiles; p.row_tiles = k.row_tiles;
+  p.tiles_each = k.tiles_each;
   const int64_t total = p.B * p.Hkv * p.rows;
   if (k.parts) {
     p.part = static_cast<float*>(ws);
     p.part_ml = p.part + k.parts * total * EP;
   }
-  // whole 16-byte pieces everywhere and no padding of the head
-  const bool full = p.E == EP && p.wide_q && p.wide_kv && p.wide_o;
   hipError_t e;
   if (full) e = attn_plan_run<T, EP, true>(p, k, stream, tr);
   else e = attn_plan_run<T, EP, false>(p, k, stream, tr);
@@ -721,8 +725,9 @@ template <typename T> hipError_t attn_dt(const gspn_attn_args& a, void* ws, hipS
 size_t attn_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E) {
   if (B == 0 || Lq == 0 || Lk == 0) return 0;
   size_t most = 0;
-  for (const size_t es : {size_t(2), size_t(4)}) {   // the larger of the two element types' needs
-    const AttnCut k = cut_attn(B, Lq, Lk, Hq, Hkv, es);
+  // the larger of the two element types' needs; whole pieces need no more
+  for (const size_t es : {size_t(2), size_t(4)}) {
+    const AttnCut k = cut_attn(B, Lq, Lk, Hq, Hkv, E, es, false);
     most = std::max(most, static_cast<size_t>(k.parts * B * Lq * Hq * (attn_ep(E) + 2)) * sizeof(float));
   }
   return most;

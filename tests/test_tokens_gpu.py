@@ -356,6 +356,87 @@ def test_attention(case, view):
         assert not got["k"][~d["mask"]].any() and not got["v"][~d["mask"]].any()
 
 
+# rows enough for the kernels that fill the chip (128 rows, up to E = 64 256 rows, per workgroup)
+MANY = [
+    # B, Lq, Lk, Hq, Hkv, E, dtype, mask
+    (2, 1570, 200, 16, 8, 128, BF16, "left"),
+    (2, 1600, 333, 8, 8, 96, BF16, "random"),
+    (2, 3200, 150, 8, 8, 64, BF16, "empty"),
+    (2, 3210, 129, 8, 8, 32, BF16, "one"),
+    (1, 3100, 257, 8, 8, 64, BF16, None),
+    (1, 2100, 33, 4, 2, 64, BF16, "random"),      # short key axis, several row tiles per wavefront
+    (1, 1300, 128, 8, 4, 72, BF16, "random"),
+    (1, 2050, 70, 3, 3, 64, F32, "random"),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_attention_many_rows(case):
+    inp, gy = attn_case(*case, seed=5)
+    B, Lq, Lk, Hq, Hkv, E, dtype, _ = case
+    d = dev(inp)
+    if d["mask"] is not None:
+        bad = ~d["mask"][:, :, None, None]
+        d["k"], d["v"] = d["k"].masked_fill(bad, float("nan")), d["v"].masked_fill(bad, float("inf"))
+    lse = torch.full((B, Hq, Lq), float("nan"), device=DEV)
+    out = g.cross_attention(d["q"], d["k"], d["v"], mask=d["mask"], lse=lse)
+    ref, ref_lse = plain.attention(**inp)
+    rtol = 1e-5 if dtype == F32 else 2e-2
+    close(out, ref, rtol, "out")
+    assert torch.equal(torch.isinf(lse.cpu()), torch.isinf(ref_lse))
+    got = g.cross_attention_backward(d["q"], d["k"], d["v"], out, lse, gy.to(DEV), mask=d["mask"])
+    rg = plain.gradients(plain.attention, inp, ["q", "k", "v"], gy)
+    close_all(got, rg, max(rtol, Lq * Hq * 2.0 ** -23), "attn")
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 600, 1, 1, 64), (1, 4, 100, 1, 1, 64), (1, 200, 300, 1, 1, 64),
+                                   (1, 3100, 300, 8, 8, 128)])
+@pytest.mark.parametrize("order", [1, -1])
+def test_attention_moving_maximum(shape, order):
+    """Scores that grow (or fall) by far along the key axis, in every kernel:
+    a result so far has to be rescaled, or later keys have to vanish."""
+    B, Lq, Lk, Hq, Hkv, E = shape
+    inp, _ = attn_case(B, Lq, Lk, Hq, Hkv, E, BF16, None, seed=6)
+    grow = torch.linspace(0, 40, Lk)
+    grow = grow if order > 0 else grow.flip(0)
+    inp["k"] = (inp["q"][:, :1, :1].float() * grow[None, :, None, None]).to(BF16).expand(-1, -1, Hkv, -1).contiguous()
+    d = dev(inp)
+    out = g.cross_attention(d["q"], d["k"], d["v"])
+    ref, _ = plain.attention(**inp)
+    close(out, ref, 2e-2, "out")
+
+
+def test_results_do_not_depend_on_the_neighbours():
+    """What a call chooses by its size (runs, segments) changes no token's
+    result beyond rounding: slices of a large call equal the calls on the
+    slices, convolution outputs bit for bit."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((16, 517, 4096), generator=gen, device=DEV).to(BF16)
+    gy = torch.randn((16, 517, 4096), generator=gen, device=DEV).to(BF16)
+    w, b = torch.randn((4096, 4), generator=gen, device=DEV).to(BF16), torch.randn(4096, generator=gen, device=DEV).to(BF16)
+    out = g.causal_conv(x, w, b)
+    big = g.causal_conv_backward(x, w, b, gy)
+    for sl in (slice(0, 128), slice(3000, 3128)):
+        part = g.causal_conv_backward(x[..., sl], w[sl].contiguous(), b[sl].contiguous(), gy[..., sl])
+        assert torch.equal(g.causal_conv(x[..., sl], w[sl].contiguous(), b[sl].contiguous()), out[..., sl])
+        assert torch.equal(part["x"], big["x"][..., sl])
+        # the same terms in another order, then one rounding to bf16
+        close(part["weight"], big["weight"][sl].cpu(), 2.0 ** -7, "dw")
+        close(part["bias"], big["bias"][sl].cpu(), 2.0 ** -7, "db")
+    inp, gy = scan_case(24, 300, 256, 16, 1, F32, tuple(range(300, 0, -13))[:24], True, True, True, True, True, seed=8)
+    d = dev(inp)
+    args, par = scan_args(d)
+    out = g.selective_scan(*args, **par)
+    big = g.selective_scan_backward(*args, gy.to(DEV), **par)
+    for e in (0, 7, 23):
+        one = {k: (v[e:e + 1] if isinstance(v, torch.Tensor) and v.shape[:1] == (24,) else v) for k, v in d.items()}
+        args, par = scan_args(one)
+        close(g.selective_scan(*args, **par), out[e:e + 1].cpu(), 300 * 2.0 ** -23, "out")
+        part = g.selective_scan_backward(*args, gy[e:e + 1].to(DEV), **par)
+        for k in ("x", "dt", "B", "C", "z", "state"):
+            close(part[k], big[k][e:e + 1].cpu(), 300 * 2.0 ** -23, k, 1e-3 * rms(big["x"]))
+
+
 def test_attention_scale_and_large_scores():
     """Scores far apart: the running maximum has to move, also late, and a
     row's probabilities underflow without harm."""

@@ -121,7 +121,9 @@ def attn(L, B=2, Lq=8, Lk=12, Hq=4, Hkv=2, E=16, dt=0, scale=0.25, q=at(0), k=at
     (dict(scale=float("inf")), "GSPN_E_SHAPE"), (dict(row=-64), "GSPN_E_SHAPE"), (dict(Lq=1 << 31), "GSPN_E_SHAPE"),
     (dict(q=at(0) + 2), "GSPN_E_ALIGN"), (dict(lse=at(5) + 2), "GSPN_E_ALIGN"),
     (dict(out=at(1)), "GSPN_E_ALIAS"), (dict(out=at(3)), "GSPN_E_ALIAS"), (dict(lse=at(4)), "GSPN_E_ALIAS"),
-    (dict(ws=None), "GSPN_E_WORKSPACE"), (dict(ws=at(6) + 128), "GSPN_E_ALIGN"), (dict(ws=at(2)), "GSPN_E_ALIAS"),
+    # few queries over a long key axis: partial results need scratch memory
+    (dict(Lq=1, Lk=8192, ws=None), "GSPN_E_WORKSPACE"), (dict(Lq=1, Lk=8192, ws=at(6) + 128), "GSPN_E_ALIGN"),
+    (dict(Lq=1, Lk=8192, ws=at(2)), "GSPN_E_ALIAS"),
 ])
 def test_attention_refusals(L, kw, status):
     assert attn(L, **kw) == g.STATUS[status]

@@ -73,12 +73,36 @@ __device__ __forceinline__ void softmax_step(float (&w)[16], float c, float& m, 
   }
 }
 
-// ---- long key axes, many rows -------------------------------------------------
-// Four wavefronts of 32 rows each; K and V pass through LDS 64 (fp32: 32)
-// keys at a time.
-template <typename T, int EP, int TK, bool FULL>
-__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
+// A row tile's result: into out and lse, or, where the keys are split, as it
+// stands into this split's partial results.
+template <typename T, int EP, bool FULL>
+__device__ __forceinline__ void finish_rows(const AttnP<T>& a, int split, int64_t bh, int64_t b, int hk, uint32_t r,
+                                            const f32x16 (&o)[EP / 32], float m, float l, int lane) {
+  const bool row_ok = r < a.rows;
+  const QRow w = q_row(a, hk, r);
+  l = column_sum(l);
+  if (a.splits > 1) {
+    const int64_t at = (split * a.B * a.Hkv + bh) * a.rows + r;
+    store_col<float, EP, true>(a.part + at * EP, row_ok, true, EP, true, o, 1.0f, lane);
+    if (row_ok && lane < 32) {
+      a.part_ml[at * 2] = m;
+      a.part_ml[at * 2 + 1] = l;
+    }
+  } else {
+    store_col<T, EP, FULL>(a.out + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_o, o,
+                           softmax_scale(l), lane);
+    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w.h) * a.Lq + w.q] = softmax_lse(m, l);
+  }
+}
+
+// ---- long key axes, many rows, fp32 --------------------------------------------
+// Four wavefronts of 32 rows each; K and V pass through LDS 32 keys at a time.
+// Bound by the fp32 products (an eighth of bf16's rate).
+template <int EP, bool FULL>
+__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<float> a) {
+  using T = float;
   extern __shared__ __align__(16) char lds[];
+  constexpr int TK = 32;
   char* kt = lds;
   char* vt = lds + TK * tile_pitch<T, EP>();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -89,11 +113,10 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   const int64_t bh = blk / a.splits, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const uint32_t r = (static_cast<uint32_t>(rt) * 4 + wave) * 32 + (lane & 31);
-  const bool row_ok = r < a.rows;
   const QRow w_ = q_row(a, hk, r);
   const Keys<T> keys(a, b, hk);
 
-  typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
+  Mma<T>::Frag qf[EP / Mma<T>::kChunk];
   row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w_.q * a.qm.row + w_.h * a.qm.head, true, a.E, a.wide_q, qf);
   f32x16 o[EP / 32] = {};
   float m = -INFINITY, l = 0.0f;
@@ -110,127 +133,80 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<T> a) {
   if (t_first < t_last) fetch(t_first);
   for (int t = t_first; t < t_last; ++t) {
     const int64_t k0 = static_cast<int64_t>(t) * TK;
-    ks.write(kt, tid, [&](int i) { return keys.kept(a, k0 + i); });
-    vs.write(vt, tid, [&](int i) { return keys.kept(a, k0 + i); });
+    ks.template write<FULL>(kt, tid, a.E, [&](int i) { return keys.kept(a, k0 + i); });
+    vs.template write<FULL>(vt, tid, a.E, [&](int i) { return keys.kept(a, k0 + i); });
     __syncthreads();
     if (t + 1 < t_last) fetch(t + 1);
-#pragma unroll
-    for (int s = 0; s < TK / 32; ++s) {
-      const uint32_t bits = static_cast<uint32_t>(__ballot(keys.kept(a, k0 + s * 32 + (lane & 31))));
-      if (bits == 0) continue;
-      const f32x16 x = tile_dot<T, EP>(kt, s * 32, qf, lane);
+    const uint32_t bits = static_cast<uint32_t>(__ballot(keys.kept(a, k0 + (lane & 31))));
+    if (bits != 0) {
+      const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
       float w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = x[i];
       drop_keys(w, bits, lane);
       softmax_step(w, a.c, m, l, o);
-      tile_accum<EP>(vt, s * 32, w, o, lane, T{});
+      tile_accum<EP>(vt, 0, w, o, lane, T{});
     }
     __syncthreads();
   }
-  l = column_sum(l);
-  if (a.splits > 1) {
-    const int64_t at = (split * a.B * a.Hkv + bh) * a.rows + r;
-    store_col<float, EP, true>(a.part + at * EP, row_ok, true, EP, true, o, 1.0f, lane);
-    if (row_ok && lane < 32) {
-      a.part_ml[at * 2] = m;
-      a.part_ml[at * 2 + 1] = l;
-    }
-  } else {
-    store_col<T, EP, FULL>(a.out + ((b * a.Lq + w_.q) * a.Hq + w_.h) * a.E, row_ok, true, a.E, a.wide_o, o,
-                     softmax_scale(l), lane);
-    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w_.h) * a.Lq + w_.q] = softmax_lse(m, l);
-  }
+  finish_rows<T, EP, FULL>(a, split, bh, b, hk, r, o, m, l, lane);
 }
 
-// ---- long key axes, rows enough to fill the chip, bf16 ---------------------------
-// The products of P and V lag one subtile of 32 keys behind, and those of K and
-// Q run one ahead, of the exponentials that stand between them, so that a
-// wavefront's own products and exponentials can overlap. Tiles of 64 keys in
-// two LDS buffers. A product of 32 x 32 x 16 takes 32 cycles and 1 KB from LDS
-// on each of the four SIMDs, just LDS's 128 bytes per cycle; up to E = 64 a
-// wavefront therefore takes 64 rows in two column tiles, which share what is
-// read. At larger heads two column tiles need more than 256 registers: the
-// second wavefront per SIMD is lost, and results that the vector ALU works on
-// land in accumulation registers (2x4096x2048, 16 heads of 128: 250 us, with
-// one column tile 190).
-constexpr int wide_tiles(int EP) { return EP <= 64 ? 2 : 1; }
-template <int EP>
+// ---- long key axes, many rows, bf16 ----------------------------------------------
+// Four wavefronts of 32 rows each. The products of P and V lag one subtile of
+// 32 keys behind, and those of K and Q run one ahead, of the exponentials that
+// stand between them, so that a wavefront's own products and exponentials can
+// overlap. Tiles of 64 keys in two LDS buffers. Two column tiles (64 rows) per
+// wavefront halve what is read from LDS per product, but cost the wavefronts
+// that fill each other's waits: 4x4096x2048 with ragged masks, 16 heads of 64,
+// 184 us with two, 130 with one (1056 TFLOP/s); 2x4096x2048, 16 heads of 128,
+// 250 with two (and accumulation registers), 190 with one.
+template <int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a) {
   using T = bf16_t;
   extern __shared__ __align__(16) char lds[];
-  constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32, QT = wide_tiles(EP);
+  constexpr int kTile = 64 * tile_pitch<T, EP>(), kN = EP / 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t blk = blockIdx.x;
   const int rt = static_cast<int>(blk % a.row_tiles);
-  const int64_t bh = blk / a.row_tiles, b = bh / a.Hkv;
+  blk /= a.row_tiles;
+  const int split = static_cast<int>(blk % a.splits);
+  const int64_t bh = blk / a.splits, b = bh / a.Hkv;
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const Keys<T> keys(a, b, hk);
-  const uint32_t r0 = (static_cast<uint32_t>(rt) * 4 + wave) * (32 * QT) + (lane & 31);
-  Mma<T>::Frag qf[QT][EP / 16];
-#pragma unroll
-  for (int u = 0; u < QT; ++u) {
-    const QRow w = q_row(a, hk, r0 + 32 * u);
-    row_frags<T, EP, true>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, EP, true, qf[u]);
+  const uint32_t r = (static_cast<uint32_t>(rt) * 4 + wave) * 32 + (lane & 31);
+  Mma<T>::Frag qf[EP / 16];
+  {
+    const QRow w = q_row(a, hk, r);
+    row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, a.E, a.wide_q, qf);
   }
   int64_t k_lo, k_hi;
   key_range(keys.mask, a.Lk, tid, &k_lo, &k_hi);
-  const int t0 = static_cast<int>(k_lo / 64), t1 = static_cast<int>((k_hi + 63) / 64);
+  const int t0 = max(split * a.tiles_each, static_cast<int>(k_lo / 64));
+  const int t1 = min((split + 1) * a.tiles_each, static_cast<int>((k_hi + 63) / 64));
 
-  f32x16 o[QT][kN] = {};
-  float m[QT], l[QT];
-#pragma unroll
-  for (int u = 0; u < QT; ++u) {
-    m[u] = -INFINITY;
-    l[u] = 0.0f;
-  }
+  f32x16 o[kN] = {};
+  float m = -INFINITY, l = 0.0f;
   Stage<T, EP, 64, kThreads> ks, vs;
   bool keep = false;
   auto fetch = [&](int t) {
     const int64_t k0 = static_cast<int64_t>(t) * 64;
     keep = keys.kept(a, k0 + lane);
-    ks.template load<true>(tid, EP, true, [&](int i) { return keys.k + keys.clamp(a, k0 + i) * a.km.row; });
-    vs.template load<true>(tid, EP, true, [&](int i) { return keys.v + keys.clamp(a, k0 + i) * a.vm.row; });
+    ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.k + keys.clamp(a, k0 + i) * a.km.row; });
+    vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, k0 + i) * a.vm.row; });
   };
   uint64_t bits = 0, bits_next = 0;   // kept keys of this tile and of the one in staging
   auto stage = [&](int t) {
     bits_next = __ballot(keep);
     char* k = lds + (t & 1) * 2 * kTile;
-    ks.write(k, tid, [&](int i) { return (bits_next >> i) & 1u; });
-    vs.write(k + kTile, tid, [&](int i) { return (bits_next >> i) & 1u; });
+    ks.template write<FULL>(k, tid, a.E, [&](int i) { return (bits_next >> i) & 1u; });
+    vs.template write<FULL>(k + kTile, tid, a.E, [&](int i) { return (bits_next >> i) & 1u; });
   };
-  f32x16 x[QT];          // scores of the subtile at hand
-  uint32_t p[QT][8];     // probabilities of the subtile before, as bf16 pairs
-  auto scores = [&](int t, int s) {
-    const char* k = lds + (t & 1) * 2 * kTile;
-#pragma unroll
-    for (int u = 0; u < QT; ++u) x[u] = f32x16{};
-#pragma unroll
-    for (int j = 0; j < EP / 16; ++j) {
-      const Mma<T>::Frag f = tile_frag<T, EP>(k, s * 32, j, lane);
-#pragma unroll
-      for (int u = 0; u < QT; ++u) x[u] = Mma<T>::mma(f, qf[u][j], x[u]);
-    }
-  };
+  f32x16 x;        // scores of the subtile at hand
+  uint32_t p[8];   // probabilities of the subtile before, as bf16 pairs
+  auto scores = [&](int t, int s) { x = tile_dot<T, EP>(lds + (t & 1) * 2 * kTile, s * 32, qf, lane); };
   auto values = [&](int t, int s) {   // o += V^T P of subtile s of tile t
-    const char* v = lds + (t & 1) * 2 * kTile + kTile;
-    const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
-    constexpr int pitch = tile_pitch<T, EP>();
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const char* q = v + (s * 32 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
-#pragma unroll
-      for (int et = 0; et < kN; ++et) {
-        const v4i16 lo = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64));
-        const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
-        const bf16x8 f = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
-#pragma unroll
-        for (int u = 0; u < QT; ++u) {
-          const bf16x8 pu = __builtin_bit_cast(bf16x8, u32x4{p[u][4 * kb], p[u][4 * kb + 1], p[u][4 * kb + 2], p[u][4 * kb + 3]});
-          o[u][et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pu, o[u][et], 0, 0, 0);
-        }
-      }
-    }
+    tile_accum_packed<EP>(lds + (t & 1) * 2 * kTile + kTile, s * 32, p, o, lane);
   };
   if (t0 < t1) {
     fetch(t0);
@@ -243,26 +219,17 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
     bits = bits_next;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float w[QT][16];
+      float w[16];
 #pragma unroll
-      for (int u = 0; u < QT; ++u) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[u][i] = x[u][i];
-        drop_keys(w[u], static_cast<uint32_t>(bits >> (32 * s)), lane);
-      }
+      for (int i = 0; i < 16; ++i) w[i] = x[i];
+      drop_keys(w, static_cast<uint32_t>(bits >> (32 * s)), lane);
       // the subtile before: its values are in this tile's buffer or the other
       if (s == 1) values(t, 0);
       else if (t > t0) values(t - 1, 1);
-      float top[QT];
-      bool far = false;
+      float top = w[0];
 #pragma unroll
-      for (int u = 0; u < QT; ++u) {
-        top[u] = w[u][0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top[u] = fmaxf(top[u], w[u][i]);
-        top[u] = column_max(top[u]) * a.c;
-        far = far || top[u] > m[u] + kLag;
-      }
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, w[i]);
+      top = column_max(top) * a.c;
       if (s == 0) {
         // all wavefronts are through with the other buffer
         lds_barrier();
@@ -271,44 +238,29 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
       } else {
         lds_barrier();   // and now it holds the next tile
       }
-      if (__any(far)) {
+      if (__any(top > m + kLag)) {
         asm volatile("");   // a branch: these products are not to be done every time
+        const float mn = fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+        m = mn;
+        l *= f;
 #pragma unroll
-        for (int u = 0; u < QT; ++u) {
-          const float mn = fmaxf(m[u], top[u]);
-          const float f = __builtin_amdgcn_exp2f(m[u] - (mn == -INFINITY ? 0.0f : mn));
-          m[u] = mn;
-          l[u] *= f;
-#pragma unroll
-          for (int et = 0; et < kN; ++et) o[u][et] *= f;
-        }
+        for (int et = 0; et < kN; ++et) o[et] *= f;
       }
       if (s == 0) scores(t, 1);
       else if (t + 1 < t1) scores(t + 1, 0);
+      const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int u = 0; u < QT; ++u) {
-        const float base = m[u] == -INFINITY ? 0.0f : m[u];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          w[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[u][i], a.c, -base));
-          l[u] += w[u][i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[u][i] = pack_bf16x2(w[u][2 * i], w[u][2 * i + 1]);
+      for (int i = 0; i < 16; ++i) {
+        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], a.c, -base));
+        l += w[i];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = pack_bf16x2(w[2 * i], w[2 * i + 1]);
     }
   }
   if (t0 < t1) values(t1 - 1, 1);
-#pragma unroll
-  for (int u = 0; u < QT; ++u) {
-    const uint32_t r = r0 + 32 * u;
-    const bool row_ok = r < a.rows;
-    const QRow w = q_row(a, hk, r);
-    const float sum = column_sum(l[u]);
-    store_col<T, EP, true>(a.out + ((b * a.Lq + w.q) * a.Hq + w.h) * EP, row_ok, true, EP, true, o[u],
-                           softmax_scale(sum), lane);
-    if (a.lse && row_ok && lane < 32) a.lse[(b * a.Hq + w.h) * a.Lq + w.q] = softmax_lse(m[u], sum);
-  }
+  finish_rows<T, EP, FULL>(a, split, bh, b, hk, r, o, m, l, lane);
 }
 
 // ---- at most 128 keys -----------------------------------------------------------
@@ -334,8 +286,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     Stage<T, EP, NT * 32, kThreads> vs;
     ks.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.k + keys.clamp(a, i) * a.km.row; });
     vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, i) * a.vm.row; });
-    ks.write(kt, tid, [&](int i) { return keys.kept(a, i); });
-    vs.write(vt, tid, [&](int i) { return keys.kept(a, i); });
+    ks.template write<FULL>(kt, tid, a.E, [&](int i) { return keys.kept(a, i); });
+    vs.template write<FULL>(vt, tid, a.E, [&](int i) { return keys.kept(a, i); });
     if (tid < NT * 32) bias[tid] = keys.kept(a, tid) ? 0.0f : -INFINITY;
   }
   __syncthreads();
@@ -363,7 +315,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     // rows' latency, so they are taken anew.
     asm volatile("" : "+s"(E) : : "memory");
     const RowTile rows(a, hk, static_cast<uint32_t>(t) * 32);
-    qs.write(mine, lane, [](int) { return true; });
+    qs.template write<FULL>(mine, lane, E, [](int) { return true; });
     lds_wave_sync();
     typename Mma<T>::Frag qf[EP / Mma<T>::kChunk];
 #pragma unroll
@@ -471,8 +423,8 @@ __global__ __launch_bounds__(kThreads) void attn_few_kernel(AttnP<T> a) {
   if (t < t_last) fetch(t);
   for (; t < t_last; t += 4) {
     const uint32_t bits = static_cast<uint32_t>(__ballot(keep));
-    ks.write(kt, lane, [&](int i) { return (bits >> i) & 1u; });
-    vs.write(vt, lane, [&](int i) { return (bits >> i) & 1u; });
+    ks.template write<FULL>(kt, lane, a.E, [&](int i) { return (bits >> i) & 1u; });
+    vs.template write<FULL>(vt, lane, a.E, [&](int i) { return (bits >> i) & 1u; });
     lds_wave_sync();
     if (t + 4 < t_last) fetch(t + 4);
     if (bits != 0) {
@@ -574,17 +526,27 @@ __global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n,
 }
 
 // ---- host -------------------------------------------------------------------
-enum class AttnPlan { kShort, kFew, kRows, kWide };
+enum class AttnPlan { kShort, kFew, kRows };
+// rows of K and V in LDS for attn_short: its keys, and 32 query rows (half as
+// many of both) for each of four wavefronts
+constexpr int short_rows(int nt) { return 32 * nt + 64; }
 struct AttnCut {
   AttnPlan plan;
   int splits, parts, key_tiles, row_tiles, tiles_each;
 };
-// `full`: whole 16-byte pieces everywhere and no padding of the head
 AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E, size_t es, bool full) {
   AttnCut k{};
   const int64_t rows = Lq * (Hq / Hkv), heads = std::max<int64_t>(1, B * Hkv);
   int64_t splits = 1;
-  if (Lk <= 128) {
+  // LDS bytes of a key's K and V, and of attn_short's workgroup
+  const int64_t row = 2 * (attn_ep(E) * static_cast<int64_t>(es) + (es == 2 ? 32 : 16));
+  const int64_t bytes = short_rows(static_cast<int>(cdiv(Lk, 32))) * row + 512;
+  if (Lk <= 128 && (bytes <= 81920 || (bytes <= 163840 && heads * cdiv(rows, 128) < 256))) {
+    // Taken where two workgroups fit a compute unit's LDS, or the chip would
+    // not be full anyway and splitting the keys would cost a second launch.
+    // us here and through the kernels below: 16384 rows, 16 heads of 64,
+    // 128 keys 23, 33; of 96, 96 keys 29, 33; of 128, 128 keys (one workgroup
+    // per compute unit) 53, 42; 512 rows, 16 heads of 128, 128 keys 11.5, 16.7.
     // Row tiles of 32; a workgroup's four wavefronts take up to 32 each, so
     // that staging the keys is a small part, but all compute units get some.
     k.plan = AttnPlan::kShort;
@@ -596,28 +558,29 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int
     return k;
   }
   if (rows <= 32) {
-    // Keys in tiles of 32, four at a time per workgroup; about four
-    // workgroups per compute unit keep enough loads in flight.
+    // (8 x 8192 keys, 8 key heads of 128, 4 rows each: 47 us here, 96 as row
+    // tiles of 128; 32 rows each: 70, 105.)
+    // Keys in tiles of 32, four at a time per workgroup. One workgroup per
+    // compute unit reads at the memory's rate (64 heads: 256 workgroups 47 us,
+    // 128 69, 512 52, 1024 59); a second, shorter round costs more than idle
+    // units do (160 heads: unsplit 125, split in two 148).
     k.plan = AttnPlan::kFew;
     k.key_tiles = static_cast<int>(cdiv(Lk, 32));
-    splits = std::max<int64_t>(1, std::min<int64_t>(64, std::min<int64_t>(cdiv(k.key_tiles, 8), cdiv(1024, heads))));
+    splits = std::max<int64_t>(1, std::min<int64_t>(64, std::min<int64_t>(cdiv(k.key_tiles, 8), 256 / heads)));
     k.tiles_each = static_cast<int>(cdiv(cdiv(k.key_tiles, splits), 4) * 4);
     k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
-  } else if (full && es == 2 && heads * cdiv(rows, 128 * wide_tiles(attn_ep(E))) >= 192) {
-    // Workgroups enough for three quarters of the compute units: no splits.
-    k.plan = AttnPlan::kWide;
-    k.key_tiles = static_cast<int>(cdiv(Lk, 64));
-    k.row_tiles = static_cast<int>(cdiv(rows, 128 * wide_tiles(attn_ep(E))));
-    k.tiles_each = k.key_tiles;
-    k.splits = 1;
   } else {
-    // Few row tiles: the key axis is split until about two workgroups per
-    // compute unit run.
+    // Row tiles of 128; where these are few the key axis is split, as often as
+    // two workgroups per compute unit allow. (2048 keys, 16 heads, us split and
+    // whole: bf16 of 128, 64 tiles 35, 59; 144 tiles, in three, 49, 59. fp32 of
+    // 72, 1024 keys, 128 tiles 84, 180; 240 tiles 151, 182.) In two it does not
+    // pay where aligned bf16 rows keep the loads short (of 64, 256 tiles 45, 41;
+    // of 72, padded, 74, 110 before pieces were loaded whole).
     k.plan = AttnPlan::kRows;
     k.key_tiles = static_cast<int>(cdiv(Lk, es == 2 ? 64 : 32));
     k.row_tiles = static_cast<int>(cdiv(rows, 128));
-    const int64_t groups = heads * k.row_tiles;
-    if (groups < 256) splits = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(k.key_tiles, 64), cdiv(512, groups)));
+    splits = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(k.key_tiles, 64), 512 / (heads * k.row_tiles)));
+    if (splits == 2 && full && es == 2) splits = 1;
     k.tiles_each = static_cast<int>(cdiv(k.key_tiles, splits));
     k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
   }
@@ -667,26 +630,22 @@ hipError_t attn_plan_run(AttnP<T>& p, const AttnCut& k, hipStream_t stream, Trac
   constexpr int row = 2 * tile_pitch<T, EP>();   // LDS bytes of a key's K and V
   const int64_t heads = p.B * p.Hkv;
   if (k.plan == AttnPlan::kShort) {
-    switch ((p.Lk + 31) / 32) {
-      case 1: return run<T>(attn_short_kernel<T, EP, 1, FULL>, "attn_short", 160 * row, heads * k.splits, p, stream, tr);
-      case 2: return run<T>(attn_short_kernel<T, EP, 2, FULL>, "attn_short", 192 * row, heads * k.splits, p, stream, tr);
-      case 3: return run<T>(attn_short_kernel<T, EP, 3, FULL>, "attn_short", 160 * row, heads * k.splits, p, stream, tr);
-      default: return run<T>(attn_short_kernel<T, EP, 4, FULL>, "attn_short", 192 * row, heads * k.splits, p, stream, tr);
-    }
+    const int nt = static_cast<int>(cdiv(p.Lk, 32)), bytes = short_rows(nt) * row;
+    auto kern = nt == 1 ? attn_short_kernel<T, EP, 1, FULL> : nt == 2 ? attn_short_kernel<T, EP, 2, FULL>
+              : nt == 3 ? attn_short_kernel<T, EP, 3, FULL> : attn_short_kernel<T, EP, 4, FULL>;
+    return run<T>(kern, "attn_short", bytes, heads * k.splits, p, stream, tr);
   }
   if (k.plan == AttnPlan::kFew)
     return run<T>(attn_few_kernel<T, EP, FULL>, "attn_few", 128 * row, heads * k.splits, p, stream, tr);
-  if constexpr (FULL && sizeof(T) == 2) {
-    if (k.plan == AttnPlan::kWide)
-      return run<T>(attn_wide_kernel<EP>, "attn_wide", 128 * row, heads * p.row_tiles, p, stream, tr);
-  }
-  constexpr int TK = sizeof(T) == 2 ? 64 : 32;
-  return run<T>(attn_fwd_kernel<T, EP, TK, FULL>, "attn_fwd", TK * row, heads * k.splits * k.row_tiles, p, stream, tr);
+  const int64_t grid = heads * k.splits * k.row_tiles;
+  if constexpr (sizeof(T) == 2) return run<T>(attn_wide_kernel<EP, FULL>, "attn_wide", 128 * row, grid, p, stream, tr);
+  else return run<T>(attn_fwd_kernel<EP, FULL>, "attn_fwd", 32 * row, grid, p, stream, tr);
 }
 
 template <typename T, int EP>
 hipError_t attn_ep_run(const gspn_attn_args& a, void* ws, hipStream_t stream, Tracer* tr) {
   AttnP<T> p = attn_params<T>(a);
+  // whole 16-byte pieces everywhere and no padding of the head
   const bool full = p.E == EP && p.wide_q && p.wide_kv && p.wide_o;
   const AttnCut k = cut_attn(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, a.E, sizeof(T), full);
   p.splits = k.splits; p.key_tiles = k.key_tiles; p.row_tiles = k.row_tiles;
@@ -725,7 +684,7 @@ template <typename T> hipError_t attn_dt(const gspn_attn_args& a, void* ws, hipS
 size_t attn_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E) {
   if (B == 0 || Lq == 0 || Lk == 0) return 0;
   size_t most = 0;
-  // the larger of the two element types' needs; whole pieces need no more
+  // the larger of the two element types' needs; a `full` call needs no more
   for (const size_t es : {size_t(2), size_t(4)}) {
     const AttnCut k = cut_attn(B, Lq, Lk, Hq, Hkv, E, es, false);
     most = std::max(most, static_cast<size_t>(k.parts * B * Lq * Hq * (attn_ep(E) + 2)) * sizeof(float));

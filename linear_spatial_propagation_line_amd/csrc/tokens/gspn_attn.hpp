@@ -146,28 +146,19 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int row0,
 }
 
 // acc[et][32 e of slab et][lane column] += tile rows^T W, W[32 rows][lane
-// column] in the result layout above. The bf16 form takes W in bf16; with
-// REST also what that rounding left, in bf16 (16 bits of mantissa together).
+// column] in the result layout above as bf16 pairs (and, with REST, `rest`,
+// what the rounding to bf16 left)
 template <int EP, bool REST = false>
-__device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
-                                           f32x16 (&acc)[EP / 32], int lane, bf16_t) {
+__device__ __forceinline__ void tile_accum_packed(const char* tile, int row0, const uint32_t (&p)[8],
+                                                  f32x16 (&acc)[EP / 32], int lane, const uint32_t* rest = nullptr) {
   const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
   constexpr int pitch = tile_pitch<bf16_t, EP>();
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
-    u32x4 p;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) p[k] = pack_bf16x2(w[8 * kb + 2 * k], w[8 * kb + 2 * k + 1]);
-    const bf16x8 b = __builtin_bit_cast(bf16x8, p);
-    bf16x8 rest;
-    if constexpr (REST) {
-      u32x4 l;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        l[k] = pack_bf16x2(w[8 * kb + 2 * k] - __uint_as_float(p[k] << 16),
-                           w[8 * kb + 2 * k + 1] - __uint_as_float(p[k] & 0xffff0000u));
-      rest = __builtin_bit_cast(bf16x8, l);
-    }
+    const bf16x8 b = __builtin_bit_cast(bf16x8, u32x4{p[4 * kb], p[4 * kb + 1], p[4 * kb + 2], p[4 * kb + 3]});
+    bf16x8 d;
+    if constexpr (REST)
+      d = __builtin_bit_cast(bf16x8, u32x4{rest[4 * kb], rest[4 * kb + 1], rest[4 * kb + 2], rest[4 * kb + 3]});
     const char* q = tile + (row0 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
 #pragma unroll
     for (int et = 0; et < EP / 32; ++et) {
@@ -175,9 +166,23 @@ __device__ __forceinline__ void tile_accum(const char* tile, int row0, const flo
       const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
       const bf16x8 a = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
       acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[et], 0, 0, 0);
-      if constexpr (REST) acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, rest, acc[et], 0, 0, 0);
+      if constexpr (REST) acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, d, acc[et], 0, 0, 0);
     }
   }
+}
+// The same from fp32 W. The bf16 form takes W in bf16; with REST also what that
+// rounding left, in bf16 (16 bits of mantissa together).
+template <int EP, bool REST = false>
+__device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
+                                           f32x16 (&acc)[EP / 32], int lane, bf16_t) {
+  uint32_t p[8], rest[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    p[k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+    if constexpr (REST)
+      rest[k] = pack_bf16x2(w[2 * k] - __uint_as_float(p[k] << 16), w[2 * k + 1] - __uint_as_float(p[k] & 0xffff0000u));
+  }
+  tile_accum_packed<EP, REST>(tile, row0, p, acc, lane, rest);
 }
 template <int EP, bool REST = false>
 __device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
@@ -253,8 +258,8 @@ __device__ __forceinline__ void key_range(const uint8_t* mask, int64_t Lk, int t
 // logical block of a launch of n blocks such that each XCD works on
 // neighbours, which read the same rows. (Where the work of an entry depends on
 // its mask, taking the blocks in turn balances the XCDs better than sharing
-// keys helps: 2x4096x2048 with ragged masks, 16 heads of 128, forward 204 us
-// against 188, dQ 242 against 228.)
+// keys helps: 2x4096x2048 with ragged masks, 16 heads of 128 on 4 key heads,
+// forward 204 us against 188, dQ 242 against 228.)
 __device__ __forceinline__ uint32_t xcd_block(uint32_t blk, uint32_t n) {
   const uint32_t each = n / 8, left = n % 8, x = blk % 8;
   return x * each + (x < left ? x : left) + blk / 8;
@@ -313,22 +318,34 @@ template <typename T, int EP, int ROWS, int THREADS> struct Stage {
   __device__ static __forceinline__ int e0(int tid, int i) {
     return (tid + i * THREADS) % kPieces * (16 / static_cast<int>(sizeof(T)));
   }
-  // at(r): the address of row r of the tile, which has to exist
+  // at(r): the address of row r of the tile, which has to exist. Whole pieces
+  // past the row's end are read from its start, and zeroed by write(): a
+  // branch per piece, or a look at what is still on its way, would end the
+  // loads in flight (8192 rows, 2048 keys, 16
+  // heads of 72, forward: 217 us with them, 150 without).
   template <bool FULL, typename F> __device__ __forceinline__ void load(int tid, int E, bool wide, F&& at) {
+    if (FULL || wide) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int r = row(tid, i);
-      v[i] = load16<T, FULL>(at(kExact || r < ROWS ? r : ROWS - 1), e0(tid, i), E, wide);
+      for (int i = 0; i < kEach; ++i) {
+        const int r = row(tid, i), e = e0(tid, i);
+        v[i] = load16<T, true>(at(kExact || r < ROWS ? r : ROWS - 1), FULL || e < E ? e : 0, E, true);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = row(tid, i);
+        v[i] = load16<T, false>(at(kExact || r < ROWS ? r : ROWS - 1), e0(tid, i), E, false);
+      }
     }
   }
   // keep(r): whether the row's values are kept (zeros otherwise)
-  template <typename F> __device__ __forceinline__ void write(char* tile, int tid, F&& keep) const {
+  template <bool FULL, typename F> __device__ __forceinline__ void write(char* tile, int tid, int E, F&& keep) const {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int r = row(tid, i);
+      const int r = row(tid, i), e = e0(tid, i);
       if (kExact || r < ROWS)
-        *reinterpret_cast<u32x4*>(tile + r * tile_pitch<T, EP>() + e0(tid, i) * static_cast<int>(sizeof(T))) =
-            keep(r) ? v[i] : u32x4{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4*>(tile + r * tile_pitch<T, EP>() + e * static_cast<int>(sizeof(T))) =
+            keep(r) && (FULL || e < E) ? v[i] : u32x4{0u, 0u, 0u, 0u};
     }
   }
 };

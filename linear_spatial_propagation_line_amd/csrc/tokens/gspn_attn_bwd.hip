@@ -112,8 +112,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dkv_ker
   auto put = [&](int t) {
     char* to = lds + (t & 1) * kTile;
     const int64_t left = a.rows - static_cast<int64_t>(t) * TR;
-    qs.write(to, tid, [&](int i) { return i < left; });
-    gs.write(to + TR * tile_pitch<T, EP>(), tid, [&](int i) { return i < left; });
+    qs.template write<FULL>(to, tid, a.E, [&](int i) { return i < left; });
+    gs.template write<FULL>(to + TR * tile_pitch<T, EP>(), tid, a.E, [&](int i) { return i < left; });
     if (tid < 2 * TR) reinterpret_cast<float*>(to + 2 * TR * tile_pitch<T, EP>())[tid] = stat;
   };
   if (t_first < t_last) {
@@ -217,8 +217,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
   auto put = [&](int t) {
     char* to = lds + (t & 1) * kTile;
     next = static_cast<uint32_t>(__ballot(keep));
-    ks.write(to, tid, [&](int i) { return (next >> i) & 1u; });
-    vs.write(to + TK * tile_pitch<T, EP>(), tid, [&](int i) { return (next >> i) & 1u; });
+    ks.template write<FULL>(to, tid, a.E, [&](int i) { return (next >> i) & 1u; });
+    vs.template write<FULL>(to + TK * tile_pitch<T, EP>(), tid, a.E, [&](int i) { return (next >> i) & 1u; });
   };
   if (t_first < t_last) {
     fetch(t_first);
@@ -254,15 +254,17 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
 struct BwdCut {
   int key_tiles, row_tiles, splits, tiles_each;
 };
-// the rows of the dK, dV pass are split until about 512 workgroups run
-BwdCut cut_bwd(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv) {
+// Row splits of the dK, dV pass: as many as the workgroups that run at once
+// allow, two per compute unit, one for fp32. (2048 rows, 16 heads of 128, bf16,
+// whole training step, us split and whole: 32 groups 77, 195; 128 groups 158,
+// 242; 240 groups in two 255, 299, in three 284. fp32, 1024 rows, 64 groups: in four
+// 278, in eight 293, whole 483.)
+BwdCut cut_bwd(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, size_t es) {
   BwdCut k;
   k.key_tiles = static_cast<int>(cdiv(Lk, 128));
   k.row_tiles = static_cast<int>(cdiv(Lq * (Hq / Hkv), 32));
   const int64_t groups = std::max<int64_t>(1, B * Hkv * k.key_tiles);
-  int64_t splits = 1;
-  if (groups < 256) splits = std::min<int64_t>(k.row_tiles, cdiv(512, groups));
-  splits = std::max<int64_t>(1, splits);
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(k.row_tiles, (es == 2 ? 512 : 256) / groups));
   k.tiles_each = static_cast<int>(cdiv(std::max(1, k.row_tiles), splits));
   k.splits = static_cast<int>(cdiv(std::max(1, k.row_tiles), k.tiles_each));
   return k;
@@ -320,7 +322,7 @@ template <typename T>
 hipError_t bwd_dt(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws, hipStream_t stream,
                   Tracer* tr) {
   BwdP<T> p{};
-  const BwdCut k = cut_bwd(a.B, a.Lq, a.Lk, a.Hq, a.Hkv);
+  const BwdCut k = cut_bwd(a.B, a.Lq, a.Lk, a.Hq, a.Hkv, sizeof(T));
   p.q = static_cast<const T*>(a.q.p); p.qm = {a.q.batch, a.q.row, a.q.head};
   p.k = static_cast<const T*>(a.k.p); p.km = {a.k.batch, a.k.row, a.k.head};
   p.v = static_cast<const T*>(a.v.p); p.vm = {a.v.batch, a.v.row, a.v.head};
@@ -365,7 +367,7 @@ hipError_t bwd_dt(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws, h
 
 size_t attn_bwd_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t E) {
   if (B == 0) return 0;
-  const BwdCut k = cut_bwd(B, Lq, Lk, Hq, Hkv);
+  const BwdCut k = cut_bwd(B, Lq, Lk, Hq, Hkv, 2);
   size_t n = up256(static_cast<size_t>(B * Hq * Lq) * sizeof(float));
   if (k.splits > 1) n += static_cast<size_t>(2 * k.splits * B * Lk * Hkv * E) * sizeof(float);
   return n;

@@ -21,7 +21,8 @@ constexpr int kRun = 16;     // tokens one lane walks, all loaded before the fir
 constexpr int kStepBwd = 8;  // backward: tokens loaded together
 // Backward: tokens per run. Long runs leave few partial sums and re-read few
 // rows; shorter ones where the wavefronts would not fill the chip four times
-// (8x4096x2304 bf16: 64 tokens 238 us, 16 tokens 341; 3x1021x1153: 42, 32).
+// (training step, bf16, 8x4096x2304: 64 tokens 187 us, 16 tokens 213;
+// 3x1021x1153: 35, 30).
 int64_t bwd_run(int64_t B, int64_t L, int64_t C) {
   for (int64_t run = 64; run > 16; run /= 2)
     if (B * cdiv(L, run) * cdiv(C, 256) >= 4096) return run;

@@ -367,6 +367,11 @@ MANY = [
     (1, 2100, 33, 4, 2, 64, BF16, "random"),      # short key axis, several row tiles per wavefront
     (1, 1300, 128, 8, 4, 72, BF16, "random"),
     (1, 2050, 70, 3, 3, 64, F32, "random"),
+    (1, 70, 128, 2, 2, 128, F32, "random"),       # keys that LDS does not hold as a whole
+    (1, 70, 97, 2, 1, 128, F32, None),
+    (1, 70, 65, 2, 2, 100, F32, "random"),
+    (1, 70, 100, 2, 1, 96, F32, "left"),
+    (16, 300, 128, 16, 16, 96, BF16, "random"),   # keys that LDS holds only once per compute unit
 ]
 
 

@@ -25,6 +25,8 @@
  * output is 0, it moves no state, and its gradients are 0. Lengths are taken
  * as clamped to 0 .. L.
  *
+ * gspn_trace_events() records the launches of these calls as well.
+ *
  * An output may overlap neither an input nor another output (GSPN_E_ALIAS),
  * except state_out, which may be the same memory as state (a step in place).
  */

@@ -48,6 +48,10 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 }
 
 // ---- dK, dV: 128 keys per workgroup, rows 32 at a time through LDS ----------
+// Four products per tile, S^T and dP^T from the keys' side, then dV and dK. A
+// tile's products wait for its exponentials and for LDS (57 % of the cycles are
+// waits, the matrix units work for a third). 2x4096x2048 with ragged masks, 16
+// heads of 128 on 4, bf16: 386 us.
 // Results and fragments of K and V are 6 E registers; where that leaves no
 // room for two wavefronts per SIMD the fragments of V stay in LDS (with them
 // in registers the loop spilled: 433 us against 382 at E = 128).
@@ -178,6 +182,8 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(BwdP<T> a) {
 }
 
 // ---- dQ: 128 rows per workgroup, keys 32 at a time through LDS --------------
+// Bound by the products (the matrix units work half of the time): 252 us at the
+// same size, of which the second product of dS takes 24.
 template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];

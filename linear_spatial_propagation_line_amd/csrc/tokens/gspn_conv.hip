@@ -9,7 +9,8 @@
 // owns V adjacent channels (16 bytes) and walks a run of tokens with the last
 // K - 1 rows in registers, so each row is read once per run plus K - 1 rows
 // of the run before (from L2); the run's rows are all loaded first, which keeps
-// that many 16-byte loads in flight per lane.
+// that many 16-byte loads in flight per lane. 8x4096x2304 bf16: 75 us, 4.0 TB/s
+// (a large copy reaches 4.9); a training step 187 to 239 us by box.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 

@@ -64,7 +64,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T> __device__ __forceinline__ float ld1(const T* p) { return to_f32(*p); }
-template <typename T> __device__ __forceinline__ void st1(T* p, float v) { Store<T>::put(p, 0, v); }
 
 // sigmoid(v); the exponent is capped so that the denominator stays finite (at
 // the cap the result is below 2^-125), NaN stays NaN through the callers'

@@ -185,7 +185,7 @@ size_t gspn_selective_scan_backward_workspace_bytes(int64_t B, int64_t L, int64_
  *   lse [B, Hq, Lq] fp32, or NULL
  *   E 1 .. 128; Hkv >= 1 dividing Hq; scale finite and > 0 (GSPN_E_SHAPE)
  * Products run on matrix cores with fp32 accumulation; with bf16 storage the
- * probabilities are rounded to bf16 as an operand of the second product.
+ * probabilities are an operand of the second product with 16 bits of mantissa.
  * Workspace: gspn_cross_attention_workspace_bytes() bytes, 256-byte aligned
  * (partial results where few queries read many keys; otherwise 0).
  */
@@ -210,7 +210,7 @@ size_t gspn_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, i
  * dtype) given grad_out = dL/dout. args->out and args->lse are read: they
  * hold the forward call's results. Sums over queries and over the heads that
  * share keys are in fp32, in a fixed order; with bf16 storage the
- * probabilities and the score gradients are rounded to bf16 as operands.
+ * probabilities and the score gradients are operands with 16 bits of mantissa.
  * Workspace: gspn_cross_attention_backward_workspace_bytes() bytes, 256-byte
  * aligned.
  */

@@ -203,10 +203,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
     vs.template write<FULL>(k + kTile, tid, a.E, [&](int i) { return (bits_next >> i) & 1u; });
   };
   f32x16 x;        // scores of the subtile at hand
-  uint32_t p[8];   // probabilities of the subtile before, as bf16 pairs
+  uint32_t p[8], rest[8];   // probabilities of the subtile before, in two bf16 parts
   auto scores = [&](int t, int s) { x = tile_dot<T, EP>(lds + (t & 1) * 2 * kTile, s * 32, qf, lane); };
   auto values = [&](int t, int s) {   // o += V^T P of subtile s of tile t
-    tile_accum_packed<EP>(lds + (t & 1) * 2 * kTile + kTile, s * 32, p, o, lane);
+    tile_accum_split<EP>(lds + (t & 1) * 2 * kTile + kTile, s * 32, p, rest, o, lane);
   };
   if (t0 < t1) {
     fetch(t0);
@@ -255,8 +255,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
         w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], a.c, -base));
         l += w[i];
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = pack_bf16x2(w[2 * i], w[2 * i + 1]);
+      split_bf16(w, p, rest);
     }
   }
   if (t0 < t1) values(t1 - 1, 1);

@@ -145,20 +145,32 @@ __device__ __forceinline__ f32x16 tile_dot(const char* tile, int row0,
   return x;
 }
 
+// Probabilities and score gradients are operands of the second products. In
+// bf16 alone (8 bits of mantissa) their rounding would be as large as the
+// result's own: outputs, dK and dV 0.00235 from 64 bits in the norm, where
+// rounding an exact result gives 0.00166. So they are taken as two bf16 parts,
+// the value rounded and what that left (16 bits together), at the price of one
+// more matrix product: 4x4096x2048 with ragged masks, 16 heads of 64, forward 153 us against
+// 126; 2x4096x2048, 16 heads of 128 on 4, training step 819 against 730;
+// 2097152 rows, 77 keys, 5 heads of 64, 626 against 553; few rows on long keys, none.
+__device__ __forceinline__ void split_bf16(const float (&w)[16], uint32_t (&p)[8], uint32_t (&rest)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    p[k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+    rest[k] = pack_bf16x2(w[2 * k] - __uint_as_float(p[k] << 16), w[2 * k + 1] - __uint_as_float(p[k] & 0xffff0000u));
+  }
+}
 // acc[et][32 e of slab et][lane column] += tile rows^T W, W[32 rows][lane
-// column] in the result layout above as bf16 pairs (and, with REST, `rest`,
-// what the rounding to bf16 left)
-template <int EP, bool REST = false>
-__device__ __forceinline__ void tile_accum_packed(const char* tile, int row0, const uint32_t (&p)[8],
-                                                  f32x16 (&acc)[EP / 32], int lane, const uint32_t* rest = nullptr) {
+// column] in the result layout above as bf16 pairs in two parts
+template <int EP>
+__device__ __forceinline__ void tile_accum_split(const char* tile, int row0, const uint32_t (&p)[8],
+                                                 const uint32_t (&rest)[8], f32x16 (&acc)[EP / 32], int lane) {
   const int hh = lane >> 5, g = (lane >> 4) & 1, c = lane & 15;
   constexpr int pitch = tile_pitch<bf16_t, EP>();
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     const bf16x8 b = __builtin_bit_cast(bf16x8, u32x4{p[4 * kb], p[4 * kb + 1], p[4 * kb + 2], p[4 * kb + 3]});
-    bf16x8 d;
-    if constexpr (REST)
-      d = __builtin_bit_cast(bf16x8, u32x4{rest[4 * kb], rest[4 * kb + 1], rest[4 * kb + 2], rest[4 * kb + 3]});
+    const bf16x8 d = __builtin_bit_cast(bf16x8, u32x4{rest[4 * kb], rest[4 * kb + 1], rest[4 * kb + 2], rest[4 * kb + 3]});
     const char* q = tile + (row0 + 16 * kb + 4 * hh + (c >> 2)) * pitch + (g * 16 + 4 * (c & 3)) * 2;
 #pragma unroll
     for (int et = 0; et < EP / 32; ++et) {
@@ -166,25 +178,19 @@ __device__ __forceinline__ void tile_accum_packed(const char* tile, int row0, co
       const v4i16 hi = lds_read_tr(reinterpret_cast<const uint16_t*>(q + et * 64 + 8 * pitch));
       const bf16x8 a = __builtin_bit_cast(bf16x8, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
       acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[et], 0, 0, 0);
-      if constexpr (REST) acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, d, acc[et], 0, 0, 0);
+      acc[et] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, d, acc[et], 0, 0, 0);
     }
   }
 }
-// The same from fp32 W. The bf16 form takes W in bf16; with REST also what that
-// rounding left, in bf16 (16 bits of mantissa together).
-template <int EP, bool REST = false>
+// the same from fp32 W
+template <int EP>
 __device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
                                            f32x16 (&acc)[EP / 32], int lane, bf16_t) {
   uint32_t p[8], rest[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    p[k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
-    if constexpr (REST)
-      rest[k] = pack_bf16x2(w[2 * k] - __uint_as_float(p[k] << 16), w[2 * k + 1] - __uint_as_float(p[k] & 0xffff0000u));
-  }
-  tile_accum_packed<EP, REST>(tile, row0, p, acc, lane, rest);
+  split_bf16(w, p, rest);
+  tile_accum_split<EP>(tile, row0, p, rest, acc, lane);
 }
-template <int EP, bool REST = false>
+template <int EP>
 __device__ __forceinline__ void tile_accum(const char* tile, int row0, const float (&w)[16],
                                            f32x16 (&acc)[EP / 32], int lane, float) {
   constexpr int pitch = tile_pitch<float, EP>();

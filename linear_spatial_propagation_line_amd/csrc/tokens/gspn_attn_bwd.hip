@@ -54,8 +54,9 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 // heads of 128 on 4, bf16: 386 us.
 // Results and fragments of K and V are 6 E registers; where that leaves no
 // room for two wavefronts per SIMD the fragments of V stay in LDS (with them
-// in registers the loop spilled: 433 us against 382 at E = 128).
-template <typename T, int EP> constexpr bool dkv_v_in_lds() { return EP * sizeof(T) >= 256; }
+// in registers the loop spills; training step, 4x2048x1024, 16 heads of 96:
+// 359 us against 347).
+template <typename T, int EP> constexpr bool dkv_v_in_lds() { return EP * sizeof(T) >= 192; }
 template <typename T, int EP> constexpr int dkv_lds() {
   return (4 * 32 + (dkv_v_in_lds<T, EP>() ? 128 : 0)) * tile_pitch<T, EP>() + 2 * 64 * 4;
 }
@@ -246,9 +247,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(ds[i], a.c, -lse)) * (y[i] - delta);
-      // A row of dQ is one sum over its keys: dS in 8 bits of mantissa would be
-      // its largest error, so the rest of the rounding is multiplied as well.
-      tile_accum<EP, true>(kt, 0, ds, dq, lane, T{});
+      tile_accum<EP>(kt, 0, ds, dq, lane, T{});
     }
     if (t + 1 < t_last) put(t + 1);
     lds_barrier();

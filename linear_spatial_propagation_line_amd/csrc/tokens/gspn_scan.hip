@@ -31,6 +31,8 @@
 // segments. A first pass finds each segment's state from zero and its sum of
 // d (the product of its decays is exp(A sum d): one exponential), and the full
 // pass folds the segments before its own into the state that it starts from.
+// The full pass reads the initial state from a copy that the first pass leaves:
+// its last segment may store the end state over it before others have begun.
 //
 // Measured, bf16, 16 states, 2304 channels: 8192 tokens 173 us (first pass 71,
 // full pass 112, of which the states' own operations need 48); 8 x 2048 training
@@ -65,7 +67,8 @@ template <typename T> struct ScanP {
   float* saved;        // [B][chunks][NP][C]
   float* pack;         // [B][G][kW][Lp][2][NS]
   float* sum_d;        // [B][segs][C]
-  float* carry;        // [B][segs][NP][C]: the segments' local results
+  float* carry;        // [B][segs][NP][C]: the segments' local results (forward: of the last
+                       // segment, which has none, a copy of the initial state)
   // backward
   T *dx, *ddt, *dz;
   float* partA;        // [B * segs][C][N]
@@ -193,16 +196,34 @@ __device__ __forceinline__ void load_A(const ScanP<T>& a, const Place<T>& p, flo
     A2[n] = p.w * NS + n < a.N ? a.A[p.c * a.N + p.w * NS + n] * kLog2e : 0.0f;
 }
 
-// What the segments before this one (after it: kReverse) hand to it, folded
-// in order from their local results and sums of d; `from` is the state
-// before all of them, or null.
-template <typename T, int NS, bool kReverse>
-__device__ __forceinline__ void carried_in(const ScanP<T>& a, const Place<T>& p, const float* from,
-                                           const float (&A2)[NS], float (&h)[NS]) {
+// this wavefront's states at the front or back end of the token axis, from
+// `from` [B][C][N] (zeros when null)
+template <typename T, int NS>
+__device__ __forceinline__ void load_state(const ScanP<T>& a, const Place<T>& p, const float* from, float (&h)[NS]) {
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
     const int k = p.w * NS + n;
     h[n] = from && k < a.N ? from[(p.b * a.C + p.c) * a.N + k] : 0.0f;
+  }
+}
+// this wavefront's first state of the lane's channel in a segment's part of carry
+template <typename T, int NS>
+__device__ __forceinline__ int64_t carry_at(const ScanP<T>& a, const Place<T>& p, int64_t seg) {
+  return ((p.b * a.segs + seg) * (kW * NS) + p.w * NS) * a.C + p.c;
+}
+
+// What the segments before this one (after it: kReverse) hand to it, folded
+// in order from their local results and sums of d; before all of them stands
+// the initial state, or (kReverse) grad_state.
+template <typename T, int NS, bool kReverse>
+__device__ __forceinline__ void carried_in(const ScanP<T>& a, const Place<T>& p, const float (&A2)[NS],
+                                           float (&h)[NS]) {
+  if (kReverse || a.segs == 1) {
+    load_state(a, p, kReverse ? a.gstate : a.state, h);
+  } else {
+    const int64_t at = carry_at<T, NS>(a, p, a.segs - 1);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = a.state ? a.carry[at + n * a.C] : 0.0f;
   }
   const int count = static_cast<int>(kReverse ? a.segs - 1 - p.seg : p.seg);
   constexpr int kAt = 8;   // segments loaded together
@@ -211,10 +232,10 @@ __device__ __forceinline__ void carried_in(const ScanP<T>& a, const Place<T>& p,
 #pragma unroll
     for (int j = 0; j < kAt; ++j) {
       const int q = i + j < count ? i + j : count - 1;
-      const int64_t s = p.b * a.segs + (kReverse ? a.segs - 1 - q : q);
-      sum[j] = a.sum_d[s * a.C + p.c];
+      const int64_t seg = kReverse ? a.segs - 1 - q : q, at = carry_at<T, NS>(a, p, seg);
+      sum[j] = a.sum_d[(p.b * a.segs + seg) * a.C + p.c];
 #pragma unroll
-      for (int n = 0; n < NS; ++n) local[j][n] = a.carry[(s * (kW * NS) + p.w * NS + n) * a.C + p.c];
+      for (int n = 0; n < NS; ++n) local[j][n] = a.carry[at + n * a.C];
     }
 #pragma unroll
     for (int j = 0; j < kAt; ++j) {
@@ -240,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanP<T> a) {
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
   float A2[NS], h[NS];
   load_A(a, p, A2);
-  carried_in<T, NS, false>(a, p, a.state, A2, h);
+  carried_in<T, NS, false>(a, p, A2, h);
   const bool zp = a.z != nullptr, keep = a.saved != nullptr;
   const float* pack = a.pack + ((p.b * a.G + p.g) * kW + w) * a.Lp * (2 * NS);
 
@@ -415,10 +436,17 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(ScanP<T> a) {
   sum[w][lane] = sum_d;
   __syncthreads();
   if (!p.live) return;
-  const int64_t s = p.b * a.segs + p.seg;
-  if (w == 0) a.sum_d[s * a.C + p.c] = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+  if (w == 0)
+    a.sum_d[(p.b * a.segs + p.seg) * a.C + p.c] = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+  const int64_t at = carry_at<T, NS>(a, p, p.seg);
 #pragma unroll
-  for (int n = 0; n < NS; ++n) a.carry[(s * (kW * NS) + w * NS + n) * a.C + p.c] = h[n];
+  for (int n = 0; n < NS; ++n) a.carry[at + n * a.C] = h[n];
+  if (!kReverse && p.seg == 0 && a.state) {   // the copy of the initial state
+    const int64_t to = carry_at<T, NS>(a, p, a.segs - 1);
+    load_state(a, p, a.state, h);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) a.carry[to + n * a.C] = h[n];
+  }
 }
 
 // ---- few tokens: the serving step -------------------------------------------
@@ -587,7 +615,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
   const float bias = a.bias ? a.bias[p.c] : 0.0f, Dc = a.D ? a.D[p.c] : 0.0f;
   float A2[NS], g[NS], dA[NS], dD = 0.0f, dbias = 0.0f;
   load_A(a, p, A2);
-  carried_in<T, NS, true>(a, p, a.gstate, A2, g);
+  carried_in<T, NS, true>(a, p, A2, g);
 #pragma unroll
   for (int n = 0; n < NS; ++n) dA[n] = 0.0f;
   const bool zp = a.z != nullptr;

@@ -80,10 +80,11 @@ typedef struct {
 gspn_status gspn_causal_conv(const gspn_conv_args* args, hipStream_t stream);
 
 /*
- * gspn_causal_conv_backward_ws -- gradients given grad_out = dL/dout: of x
- * [B, L, C], weight [C, K], bias [C] (or NULL) and state [B, K-1, C] (or
- * NULL), in dtype. args as for the forward call (out and state_out are not
- * read). Sums over tokens are in fp32, in a fixed order. Workspace:
+ * gspn_causal_conv_backward_ws -- gradients given grad_out = dL/dout and,
+ * unless NULL, grad_state = dL/dstate_out [B, K-1, C] (what the next chunk of a
+ * sequence hands back): of x [B, L, C], weight [C, K], bias [C] (or NULL) and
+ * state [B, K-1, C] (or NULL), all in dtype. args as for the forward call (out
+ * and state_out are not read). Sums over tokens are in fp32, in a fixed order. Workspace:
  * gspn_causal_conv_backward_workspace_bytes() bytes, 256-byte aligned.
  */
 typedef struct {
@@ -92,6 +93,7 @@ typedef struct {
   void* weight;
   void* bias;
   void* state;
+  const void* grad_state;
 } gspn_conv_grads;
 
 gspn_status gspn_causal_conv_backward_ws(const gspn_conv_args* args, const gspn_conv_grads* grads,

@@ -2,7 +2,8 @@
 //
 //   pre[t] = bias + sum_{j<K} w[j] xx[t + j],  xx = state ++ x,  out = silu(pre)
 //   dpre   = grad_out * silu'(pre)
-//   dxx[s] = sum_j w[j] dpre[s - j],  dw[j] = sum_t dpre[t] xx[t + j],  db = sum_t dpre[t]
+//   dxx[s] = sum_j w[j] dpre[s - j] (+ grad_state where state_out holds the row),
+//   dw[j] = sum_t dpre[t] xx[t + j],  db = sum_t dpre[t]
 //
 // Bound by memory: 2 K + 5 operations against 2 elements moved per value
 // (forward), so the work is to move each row once in wide accesses. A lane
@@ -35,7 +36,7 @@ template <typename T> struct ConvP {
   const T* gy; int64_t gb, gr;
   const T* w; const T* bias; const T* state; const int32_t* lens;
   T* out; T* state_out;
-  T* dx; T* dstate; float* part;
+  T* dx; T* dstate; const T* gstate; float* part;
   int64_t L, C;
   int64_t run, runs;  // backward: tokens per run; runs per entry (at least 1)
   int64_t ctiles;     // tiles of 64 * V channels
@@ -206,7 +207,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
 // them (which its dx needs too); dw and db take its own tokens only. The
 // partial sums of the workgroup's four runs are joined in LDS, in run order,
 // into row (b, group of runs) of part: [K + 1][C], taps first, then the bias.
-template <typename T, int K, int V>
+// HANDED: there is a grad_state (a look at every row whether it has one costs
+// the other calls 4 %: 8x4096x2304, bf16, training step 231 us, 240).
+template <typename T, int K, int V, bool HANDED>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
   __shared__ float acc[3][(K + 1) * V][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -280,6 +283,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
             for (int j = 0; j < K; ++j) o[e] = __builtin_fmaf(w[j][e], dp[K - 1 - j][e], o[e]);
           }
           const int64_t s = t + k - (K - 1);
+          if constexpr (HANDED) {
+            if (s >= n - (K - 1) && s < n) {   // one of state_out's rows
+              float gs[V];
+              ldv<V>(a.gstate + (b * (K - 1) + s - (n - (K - 1))) * a.C + c, gs);
+#pragma unroll
+              for (int e = 0; e < V; ++e) o[e] += gs[e];
+            }
+          }
           if (s >= t0) {
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] = s < n ? o[e] : 0.0f;
@@ -398,11 +409,12 @@ hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, 
     p.gr = g->grad_out.row;
     p.dx = static_cast<T*>(g->x);
     p.dstate = static_cast<T*>(g->state);
+    p.gstate = static_cast<const T*>(g->grad_state);
     p.part = static_cast<float*>(ws);
     p.run = bwd_run(a.B, a.L, a.C);
     p.runs = std::max<int64_t>(1, cdiv(a.L, p.run));
     wide = wide && wide_ok(p.gy, 16, es, {p.gb, p.gr}) && wide_ok(p.dx, 16, es, {}) &&
-           (!p.dstate || wide_ok(p.dstate, 16, es, {}));
+           (!p.dstate || wide_ok(p.dstate, 16, es, {})) && (!p.gstate || wide_ok(p.gstate, 16, es, {}));
   } else {
     wide = wide && wide_ok(p.out, 16, es, {}) && (!p.state_out || wide_ok(p.state_out, 16, es, {}));
   }
@@ -413,8 +425,10 @@ hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, 
   tr->before(stream, name, a.B);
   if (a.B > 0) {
     if (g) {
-      if (wide) hipLaunchKernelGGL((conv_bwd_kernel<T, K, VB>), grid, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((conv_bwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);
+      constexpr bool kState = K > 1;
+      auto kern = kState && p.gstate ? (wide ? conv_bwd_kernel<T, K, VB, kState> : conv_bwd_kernel<T, K, 1, kState>)
+                                     : (wide ? conv_bwd_kernel<T, K, VB, false> : conv_bwd_kernel<T, K, 1, false>);
+      hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, p);
     } else {
       if (wide) hipLaunchKernelGGL((conv_fwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
       else hipLaunchKernelGGL((conv_fwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);

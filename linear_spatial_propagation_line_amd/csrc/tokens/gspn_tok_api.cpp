@@ -275,6 +275,7 @@ gspn_status gspn_causal_conv_backward_ws(const gspn_conv_args* a, const gspn_con
     const size_t es = esize(a->dtype);
     conv_inputs(k, *a);
     k.view(g->grad_out.p, es, {a->B, a->L, a->C}, {g->grad_out.batch, g->grad_out.row});
+    k.input(g->grad_state, a->B * (a->K - 1) * a->C, es, false);
     k.output(g->x, a->B * a->L * a->C, es);
     k.output(g->weight, a->C * a->K, es);
     k.output(g->bias, a->C, es, false);

@@ -20,7 +20,7 @@ _CODE = {torch.float32: GSPN_F32, torch.bfloat16: GSPN_BF16}
 
 # the argument structs of gspn_tokens.h, in native layout
 _CONV = struct.Struct("@4qii PqqPPPPPP".replace(" ", ""))
-_CONV_GRADS = struct.Struct("@PqqPPPP")
+_CONV_GRADS = struct.Struct("@PqqPPPPP")
 _SCAN = struct.Struct("@5qii PqqPqqPqq P PqqqPqqq PPPP PPP".replace(" ", ""))
 _SCAN_GRADS = struct.Struct("@PqqPPPPPPPPPP")
 _ATTN = struct.Struct("@6qif PqqqPqqqPqqq Pq PP".replace(" ", ""))
@@ -186,11 +186,12 @@ def causal_conv(x, weight, bias=None, state=None, lens=None, silu: bool = True, 
 
 
 def causal_conv_backward(x, weight, bias, grad_out, state=None, lens=None, silu: bool = True,
-                         grads=None, workspace=None, stream=None) -> dict:
-    """Gradients of causal_conv() given ``grad_out`` = dL/dout [B, L, C]: a
-    dict with "x", "weight", "bias" (when there is one) and "state" (when
-    there is one), shaped and typed like the inputs (``grads`` may supply
-    them)."""
+                         grads=None, workspace=None, stream=None, grad_state=None) -> dict:
+    """Gradients of causal_conv() given ``grad_out`` = dL/dout [B, L, C] and
+    optionally ``grad_state`` = dL/dstate_out [B, K-1, C], which the next chunk
+    of a sequence hands back: a dict with "x", "weight", "bias" (when there is
+    one) and "state" (when there is one), shaped and typed like the inputs
+    (``grads`` may supply them)."""
     B, L, C = _shape3(x, "x")
     c = _Call(x, "x", stream)
     args, K = _conv_args(c, x, weight, bias, state, lens, silu, None, None)
@@ -202,7 +203,8 @@ def causal_conv_backward(x, weight, bias, grad_out, state=None, lens=None, silu:
     g = {k: c.out(None if grads is None else grads[k], s, f"grads[{k!r}]") for k, s in shapes.items()}
     packed = _CONV_GRADS.pack(*c.view(grad_out, (B, L, C), "grad_out"), g["x"].data_ptr(),
                               g["weight"].data_ptr(), *(g[k].data_ptr() if k in g else 0
-                                                        for k in ("bias", "state")))
+                                                        for k in ("bias", "state")),
+                              c.data(grad_state, (B, K - 1, C), "grad_state"))
     L_ = _lib()
     ws, wp, wn = c.workspace(workspace, L_.gspn_causal_conv_backward_workspace_bytes(B, L, C, K, c.code))
     c.run(L_.gspn_causal_conv_backward_ws, args, packed, wp, wn)

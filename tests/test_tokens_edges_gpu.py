@@ -9,7 +9,7 @@ import torch
 
 import linear_spatial_propagation_line_amd as g
 import plain_tokens as plain
-from test_tokens_gpu import BF16, DEV, F32, attn_case, close, conv_call, conv_case, dev, rms, scan_args, scan_case
+from test_tokens_gpu import BF16, CONV, DEV, F32, attn_case, close, close_all, conv_call, conv_case, dev, rms, scan_args, scan_case
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,60 @@ def test_conv_in_place_over_several_runs(dtype):
     end, st = torch.empty_like(d["state"]), d["state"].clone()
     out = conv_call(d, state_out=end)
     assert torch.equal(conv_call(dict(d, state=st), state_out=st), out) and torch.equal(st, end)
+
+
+# --------------------------------------------------------------------------
+# gradients handed from chunk to chunk
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("case", [c for c in CONV if c[3] > 1])
+def test_conv_gradient_of_the_state_handed_on(case):
+    """dL/dstate_out reaches x, and state where the entry is shorter than the
+    window (also with no tokens at all). One term more in the sums, so the
+    bounds of the plain gradients hold."""
+    inp, gy = conv_case(*case, seed=15)
+    B, L, C, K, dtype = case[:5]
+    gs = torch.randn((B, K - 1, C), generator=torch.Generator().manual_seed(16)).to(dtype)
+    d = dev(inp)
+    got = g.causal_conv_backward(d["x"], d["w"], d["bias"], gy.to(DEV), state=d["state"], lens=d["lens"],
+                                 silu=d["silu"], grad_state=gs.to(DEV))
+    got["w"] = got.pop("weight")
+    ref = plain.gradients(plain.conv, inp, list(got), torch.nan_to_num(gy), gs)
+    ref["x"] = torch.nan_to_num(ref["x"])
+    close_all(got, ref, max(1e-5, B * L * 2.0 ** -23) if dtype == F32 else 1e-2, "conv")
+
+
+def test_conv_gradients_in_chunks():
+    """A sequence trained in chunks, one shorter than the window, gives the
+    gradients of the whole."""
+    inp, gy = conv_case(2, 60, 70, 4, F32, None, True, True, True, seed=17)
+    d, gyd = dev(inp), gy.to(DEV)
+    whole = g.causal_conv_backward(d["x"], d["w"], d["bias"], gyd, state=d["state"])
+    cuts, states, t = [], [d["state"]], 0
+    for n in (1, 30, 2, 27):
+        cuts.append((t, t + n))
+        states.append(torch.empty_like(d["state"]))
+        conv_call(dict(d, x=d["x"][:, t:t + n], state=states[-2]), state_out=states[-1])
+        t += n
+    gs, parts = None, []
+    for (a, b), st in reversed(list(zip(cuts, states))):
+        parts.append(g.causal_conv_backward(d["x"][:, a:b], d["w"], d["bias"], gyd[:, a:b], state=st,
+                                            grad_state=gs))
+        gs = parts[-1]["state"]
+    # as many fp32 operations, in another order
+    close(torch.cat([p["x"] for p in reversed(parts)], 1), whole["x"].cpu(), 1e-5, "dx")
+    close(gs, whole["state"].cpu(), 1e-5, "dstate")
+    for n in ("weight", "bias"):
+        close(sum(p[n] for p in parts), whole[n].cpu(), 120 * 2.0 ** -23, n)
+
+
+def test_conv_grad_state_refusals():
+    x, w = torch.zeros(2, 6, 16, device=DEV), torch.zeros(16, 4, device=DEV)
+    for bad in (torch.zeros(2, 4, 16, device=DEV), torch.zeros(2, 3, 16, device=DEV, dtype=BF16),
+                torch.zeros(2, 3, 32, device=DEV)[..., ::2]):
+        with pytest.raises(ValueError):
+            g.causal_conv_backward(x, w, None, x.clone(), grad_state=bad)
+    gs = torch.zeros(2, 3, 16, device=DEV)
+    with pytest.raises(g.GspnError) as e:       # a gradient over an input
+        g.causal_conv_backward(x, w, None, x.clone(), state=torch.zeros_like(gs), grad_state=gs,
+                               grads=dict(x=None, weight=None, state=gs))
+    assert e.value.name == "GSPN_E_ALIAS"

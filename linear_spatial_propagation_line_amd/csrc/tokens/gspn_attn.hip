@@ -281,6 +281,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
   const int hk = static_cast<int>(bh - b * a.Hkv);
   const Keys<T> keys(a, b, hk);
   __shared__ __align__(16) float bias[NT * 32];   // 0 for a kept key, -inf for a dropped one
+  bool kept = false;
   {
     Stage<T, EP, NT * 32, kThreads> ks;
     Stage<T, EP, NT * 32, kThreads> vs;
@@ -288,9 +289,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
     vs.template load<FULL>(tid, a.E, a.wide_kv, [&](int i) { return keys.v + keys.clamp(a, i) * a.vm.row; });
     ks.template write<FULL>(kt, tid, a.E, [&](int i) { return keys.kept(a, i); });
     vs.template write<FULL>(vt, tid, a.E, [&](int i) { return keys.kept(a, i); });
-    if (tid < NT * 32) bias[tid] = keys.kept(a, tid) ? 0.0f : -INFINITY;
+    if (tid < NT * 32) {
+      kept = keys.kept(a, tid);
+      bias[tid] = kept ? 0.0f : -INFINITY;
+    }
   }
-  __syncthreads();
+  const bool any = __syncthreads_or(kept);   // a barrier too
   // Rows pass through LDS in both directions, so that every access to memory
   // is of whole 128-byte lines: fragments straight from memory take a line in
   // four 32-byte parts, and with the lines of all wavefronts in flight the
@@ -299,7 +303,35 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
   char* mine = lds + 2 * NT * 32 * kRow + wave * 32 * kRow;
   const int t_last = min((part + 1) * a.tiles_each, static_cast<uint32_t>(a.row_tiles));
   int E = a.E;
-  Stage<T, EP, 32, 64> qs;
+  using Rows = Stage<T, EP, 32, 64>;
+  // 16 bytes of a row of the result
+  auto put = [&](const RowTile& rows, int row, int e0, u32x4 v) {
+    if (rows.r0 + row >= a.rows) return;
+    const QRow u = rows.at(row);
+    T* out = a.out + ((b * a.Lq + u.q) * a.Hq + u.h) * E;
+    if (FULL || (a.wide_o && e0 < E)) {
+      *reinterpret_cast<u32x4*>(out + e0) = v;
+    } else {
+      const T* from = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int k = 0; k < 16 / static_cast<int>(sizeof(T)); ++k)
+        if (e0 + k < E) out[e0 + k] = from[k];
+    }
+  };
+  int t = part * a.tiles_each + wave;
+  if (!any) {   // no key kept: 0 whatever q holds (an infinity against the staged zeros would be NaN)
+    for (; t < t_last; t += 4) {
+      const RowTile rows(a, hk, static_cast<uint32_t>(t) * 32);
+#pragma unroll
+      for (int i = 0; i < Rows::kEach; ++i) put(rows, Rows::row(lane, i), Rows::e0(lane, i), u32x4{0u, 0u, 0u, 0u});
+      if (a.lse && lane < 32 && rows.r0 + lane < a.rows) {
+        const QRow u = rows.at(lane);
+        a.lse[(b * a.Hq + u.h) * a.Lq + u.q] = -INFINITY;
+      }
+    }
+    return;
+  }
+  Rows qs;
   auto fetch = [&](int t) {
     const RowTile rows(a, hk, static_cast<uint32_t>(t) * 32);
     qs.template load<FULL>(lane, E, a.wide_q, [&](int i) {
@@ -307,7 +339,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
       return a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head;
     });
   };
-  int t = part * a.tiles_each + wave;
   if (t < t_last) fetch(t);
   for (; t < t_last; t += 4) {
     // The keys' fragments and the comparisons with E are the same for every
@@ -325,7 +356,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
       const f32x16 x = tile_dot<T, EP>(kt, s * 32, qf, lane);
-      // dropped keys are zeros in LDS, so x is finite there
+      // dropped keys are zeros in LDS, so a finite row's x is 0 there (an
+      // infinity or a NaN in the row makes it NaN by its kept keys anyway)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x4 y = *reinterpret_cast<const f32x4*>(bias + s * 32 + 8 * j + 4 * (lane >> 5));
@@ -365,21 +397,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
       }
     }
     lds_wave_sync();
-    using St = Stage<T, EP, 32, 64>;
 #pragma unroll
-    for (int i = 0; i < St::kEach; ++i) {
-      const int row = St::row(lane, i), e0 = St::e0(lane, i);
-      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kRow + e0 * static_cast<int>(sizeof(T)));
-      if (rows.r0 + row >= a.rows) continue;
-      const QRow u = rows.at(row);
-      T* out = a.out + ((b * a.Lq + u.q) * a.Hq + u.h) * E;
-      if (FULL || (a.wide_o && e0 < E)) {
-        *reinterpret_cast<u32x4*>(out + e0) = v;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16 / static_cast<int>(sizeof(T)); ++k)
-          if (e0 + k < E) out[e0 + k] = reinterpret_cast<const T*>(mine + row * kRow)[e0 + k];
-      }
+    for (int i = 0; i < Rows::kEach; ++i) {
+      const int row = Rows::row(lane, i), e0 = Rows::e0(lane, i);
+      put(rows, row, e0, *reinterpret_cast<const u32x4*>(mine + row * kRow + e0 * static_cast<int>(sizeof(T))));
     }
     lds_wave_sync();   // before the next tile's queries go there
   }

@@ -52,6 +52,40 @@ def test_attention_operands_add_no_error_of_their_own(case):
 
 
 # --------------------------------------------------------------------------
+# attention: what dropped keys may not do
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(3, 70, 77, 4, 2, 64), (3, 2, 700, 4, 2, 64), (3, 300, 700, 4, 2, 64)])
+def test_attention_without_keys_whatever_the_query_holds(shape, dtype):
+    """An entry that keeps no key gives 0, lse = -inf and gradients of 0, also
+    for queries and gradients that hold infinities or NaN; and in entries that
+    keep some such a row spoils no other row."""
+    inp, gy = attn_case(*shape, dtype, "empty", seed=18)
+    B, Lq, Lk, Hq, Hkv, E = shape
+    bad = [float("nan"), float("inf"), -float("inf")]
+    q, gyb = inp["q"].clone(), gy.clone()
+    for t in (q, gyb):
+        t[:, 0, 0, :3] = torch.tensor(bad)
+        t[1] = torch.tensor(bad)[torch.arange(t[1].numel()) % 3].reshape(t[1].shape)
+    d = dev(inp)
+    lse = torch.full((B, Hq, Lq), 7.0, device=DEV)
+    out = g.cross_attention(q.to(DEV), d["k"], d["v"], mask=d["mask"], lse=lse)
+    assert not out[1].any() and bool((lse[1] == -float("inf")).all())
+    assert bool(out[0, 0, 0].isnan().all()) and bool(lse[0, 0, 0].isnan())
+    keep = torch.ones((B, Lq, Hq), dtype=torch.bool)
+    keep[:, 0, 0] = keep[1] = False
+    ref, ref_lse = plain.attention(**inp)
+    close(out.cpu()[keep], ref[keep], 1e-5 if dtype == F32 else 2e-2, "out")
+    alive = keep.transpose(1, 2)
+    assert float((lse.cpu().double() - ref_lse)[alive].abs().max()) <= 1e-5
+    got = g.cross_attention_backward(q.to(DEV), d["k"], d["v"], out, lse, gyb.to(DEV), mask=d["mask"])
+    for n in "qkv":
+        assert not got[n][1].any(), n
+    for n in "kv":      # dropped keys take no part in any entry
+        assert not got[n].cpu()[~inp["mask"]].any(), n
+
+
+# --------------------------------------------------------------------------
 # states moved on in place
 # --------------------------------------------------------------------------
 def launches(fn):

@@ -65,11 +65,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T> __device__ __forceinline__ float ld1(const T* p) { return to_f32(*p); }
 
-// sigmoid(v); the exponent is capped so that the denominator stays finite (at
-// the cap the result is below 2^-125), NaN stays NaN through the callers'
-// products with v
+// sigmoid(v) = (v < 0 ? e : 1) / (1 + e), e = exp(-|v|) in [0, 1]: nothing
+// overflows, and far below zero it is 0, so that v sigmoid(v) is 0 also at the
+// type's lowest value (a capped exponential left about 2^-125 there, and -8
+// as the product)
 __device__ __forceinline__ float sigmoid_f32(float v) {
-  return recip(1.0f + __builtin_amdgcn_exp2f(fminf(v * -kLog2e, 125.0f)));
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+  return (v < 0.0f ? e : 1.0f) * recip(1.0f + e);
 }
 
 // log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1]. The

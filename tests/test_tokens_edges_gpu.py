@@ -86,6 +86,37 @@ def test_attention_without_keys_whatever_the_query_holds(shape, dtype):
 
 
 # --------------------------------------------------------------------------
+# silu far below zero
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [1, 40])
+def test_silu_at_the_lowest_values(dtype, L):
+    """silu(v) and its slope vanish far below zero, down to the type's lowest
+    value, as a gate and as the convolution's activation. In 32 bits what is
+    left at v = -80 is below 1e-32."""
+    low = torch.finfo(dtype).min
+    vals = torch.tensor([low, low / 2, -1e30, -1e4, -200.0, -80.0, 0.0, 80.0]).to(dtype)
+    inp, gy = scan_case(1, L, 8, 4, 1, dtype, None, True, True, True, True, True, seed=19)
+    inp["z"] = vals.expand(1, L, 8).contiguous()
+    d = dev(inp)
+    args, par = scan_args(d)
+    out = g.selective_scan(*args, **par)
+    assert bool((out[..., :6].abs() <= 1e-30).all())
+    close(out[..., 6:], plain.scan(**inp)[0][..., 6:], 1e-5 if dtype == F32 else 1e-2, "out")
+    got = g.selective_scan_backward(*args, gy.to(DEV), **par)
+    assert all(bool(t.isfinite().all()) for t in got.values())
+    for n in ("x", "dt", "z"):
+        assert bool((got[n][..., :6].abs() <= 1e-30).all()), n
+    x = vals.expand(1, L, 8).contiguous().to(DEV)
+    w = torch.ones((8, 1), dtype=dtype, device=DEV)
+    out = g.causal_conv(x, w)
+    assert bool((out[..., :6].abs() <= 1e-30).all()) and torch.equal(out[..., 6:], x[..., 6:])
+    dx = g.causal_conv_backward(x, w, None, torch.ones_like(x))["x"]
+    want = torch.tensor([0, 0, 0, 0, 0, 0, 0.5, 1.0])
+    assert float((dx.float().cpu() - want).abs().max()) <= 1e-6
+
+
+# --------------------------------------------------------------------------
 # states moved on in place
 # --------------------------------------------------------------------------
 def launches(fn):

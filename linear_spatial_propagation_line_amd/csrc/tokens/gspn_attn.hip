@@ -542,8 +542,9 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnP<T> a) {
 
 // out = 0, lse = -inf when there is no key at all
 template <typename T>
-__global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n, float* lse, int64_t rows) {
-  const int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+__global__ __launch_bounds__(kThreads) void attn_empty_kernel(T* out, int64_t n, float* lse, int64_t rows,
+                                                              int64_t block0) {
+  const int64_t i = (block0 + blockIdx.x) * kThreads + threadIdx.x;
   if (i < n) Store<T>::put(out, i, 0.0f);
   if (lse && i < rows) lse[i] = -INFINITY;
 }
@@ -689,10 +690,12 @@ template <typename T> hipError_t attn_dt(const gspn_attn_args& a, void* ws, hipS
   if (a.Lk == 0) {
     const int64_t rows = a.B * a.Lq * a.Hq, n = rows * a.E;
     tr->before(stream, "attn_empty", a.B);
-    hipLaunchKernelGGL(attn_empty_kernel<T>, dim3(static_cast<unsigned>(cdiv(n, kThreads))),
-                       dim3(kThreads), 0, stream, static_cast<T*>(a.out), n, a.lse, rows);
+    const hipError_t e = in_parts(cdiv(n, kThreads), [&](int64_t first, unsigned count) {
+      hipLaunchKernelGGL(attn_empty_kernel<T>, dim3(count), dim3(kThreads), 0, stream, static_cast<T*>(a.out), n,
+                         a.lse, rows, first);
+    });
     tr->after(stream);
-    return hipGetLastError();
+    return e;
   }
   switch (attn_ep(a.E)) {
     case 32: return attn_ep_run<T, 32>(a, ws, stream, tr);

@@ -28,13 +28,14 @@ template <typename T> struct BwdP {
   int64_t B, Lq, Lk, rows;
   int Hq, Hkv, share, E, splits, key_tiles, row_tiles, tiles_each;
   float c, scale;      // scale * log2(e), scale
+  uint32_t block0;     // attn_delta: first workgroup of this launch
   bool wide_q, wide_kv, wide_g, wide_dq, wide_dkv, full;
 };
 
 // delta[b][h][q] = sum_e grad_out out: 16 lanes per row
 template <typename T>
 __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
-  const int64_t i = (blockIdx.x * int64_t(kThreads) + threadIdx.x) / 16;
+  const int64_t i = ((static_cast<int64_t>(a.block0) + blockIdx.x) * kThreads + threadIdx.x) / 16;
   const int64_t total = a.B * a.Hq * a.Lq;
   const int64_t ic = i < total ? i : total - 1;
   const int64_t q = ic % a.Lq, bh = ic / a.Lq, b = bh / a.Hq, h = bh - b * a.Hq;
@@ -286,11 +287,13 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
   hipError_t e;
   if (p.rows > 0) {
     tr->before(stream, "attn_delta", p.B);
-    hipLaunchKernelGGL(attn_delta_kernel<T>,
-                       dim3(static_cast<unsigned>(cdiv(p.B * p.Hq * p.Lq, kThreads / 16))),
-                       dim3(kThreads), 0, stream, p);
+    e = in_parts(cdiv(p.B * p.Hq * p.Lq, kThreads / 16), [&](int64_t first, unsigned count) {
+      BwdP<T> d = p;
+      d.block0 = static_cast<uint32_t>(first);
+      hipLaunchKernelGGL(attn_delta_kernel<T>, dim3(count), dim3(kThreads), 0, stream, d);
+    });
     tr->after(stream);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (e != hipSuccess) return e;
   }
   if (p.Lk > 0) {
     auto kern = p.full ? attn_dkv_kernel<T, EP, true> : attn_dkv_kernel<T, EP, false>;

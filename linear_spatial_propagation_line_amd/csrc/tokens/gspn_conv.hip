@@ -40,6 +40,7 @@ template <typename T> struct ConvP {
   int64_t L, C;
   int64_t run, runs;  // backward: tokens per run; runs per entry (at least 1)
   int64_t ctiles;     // tiles of 64 * V channels
+  uint32_t block0;    // first workgroup of this launch
   int silu;
 };
 
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
   // four runs of one channel tile per workgroup, one per wavefront
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t rgroups = static_cast<uint32_t>((a.runs + 3) / 4), ctiles = static_cast<uint32_t>(a.ctiles);
-  uint32_t i = blockIdx.x;
+  uint32_t i = blockIdx.x + a.block0;
   const uint32_t ct = i % ctiles;
   i /= ctiles;
   const int64_t rg = i % rgroups, b = i / rgroups;
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
   __shared__ float acc[3][(K + 1) * V][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t rgroups = static_cast<uint32_t>((a.runs + 3) / 4), ctiles = static_cast<uint32_t>(a.ctiles);
-  uint32_t i = blockIdx.x;
+  uint32_t i = blockIdx.x + a.block0;
   const uint32_t ct = i % ctiles;
   i /= ctiles;
   const int64_t rg = i % rgroups, b = i / rgroups;
@@ -332,11 +333,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvP<T> a) {
 // columns of part summed over its rows; the taps' sums go to dw [C][K] and
 // the last C columns to db
 template <typename T>
-__global__ __launch_bounds__(512) void conv_reduce_kernel(const float* part, int64_t rows, int64_t C,
-                                                          int K, T* dw, T* db) {
+__global__ __launch_bounds__(512) void conv_reduce_kernel(const float* part, int64_t rows, int64_t C, int K,
+                                                          int64_t block0, T* dw, T* db) {
   __shared__ float acc[8][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t cols = (K + 1) * C, i = blockIdx.x * int64_t(64) + lane;
+  const int64_t cols = (K + 1) * C, i = (blockIdx.x + block0) * 64 + lane;
   float s = 0.0f;
   if (i < cols)
     for (int64_t r = wave; r < rows; r += 8) s += part[r * cols + i];
@@ -354,7 +355,7 @@ __global__ __launch_bounds__(512) void conv_reduce_kernel(const float* part, int
 __global__ __launch_bounds__(512) void reduce_rows_kernel(RowSums r) {
   __shared__ float acc[8][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t blk = blockIdx.x;
+  int64_t blk = blockIdx.x + r.block0;
   int k = 0;   // the table this block works on
   while (k < 2 && blk >= (r.cols[k] + 63) / 64) {
     blk -= (r.cols[k] + 63) / 64;
@@ -420,30 +421,24 @@ hipError_t conv_dt(const gspn_conv_args& a, const gspn_conv_grads* g, void* ws, 
   }
   p.ctiles = cdiv(a.C, 64 * (wide ? (g ? VB : V) : 1));
   const int64_t rgroups = cdiv(p.runs, 4);
-  const dim3 grid(static_cast<unsigned>(a.B * rgroups * p.ctiles));
-  const char* name = g ? "conv_bwd" : "conv_fwd";
-  tr->before(stream, name, a.B);
-  if (a.B > 0) {
-    if (g) {
-      constexpr bool kState = K > 1;
-      auto kern = kState && p.gstate ? (wide ? conv_bwd_kernel<T, K, VB, kState> : conv_bwd_kernel<T, K, 1, kState>)
-                                     : (wide ? conv_bwd_kernel<T, K, VB, false> : conv_bwd_kernel<T, K, 1, false>);
-      hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, p);
-    } else {
-      if (wide) hipLaunchKernelGGL((conv_fwd_kernel<T, K, V>), grid, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((conv_fwd_kernel<T, K, 1>), grid, dim3(256), 0, stream, p);
-    }
-  }
+  constexpr bool kState = K > 1;
+  auto kern = !g ? (wide ? conv_fwd_kernel<T, K, V> : conv_fwd_kernel<T, K, 1>)
+              : kState && p.gstate ? (wide ? conv_bwd_kernel<T, K, VB, kState> : conv_bwd_kernel<T, K, 1, kState>)
+                                   : (wide ? conv_bwd_kernel<T, K, VB, false> : conv_bwd_kernel<T, K, 1, false>);
+  tr->before(stream, g ? "conv_bwd" : "conv_fwd", a.B);
+  hipError_t e = in_parts(a.B * rgroups * p.ctiles, [&](int64_t first, unsigned count) {
+    p.block0 = static_cast<uint32_t>(first);
+    hipLaunchKernelGGL(kern, dim3(count), dim3(256), 0, stream, p);
+  });
   tr->after(stream);
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || !g) return e;
-  const int64_t cols = (K + 1) * a.C;
   tr->before(stream, "conv_reduce", a.B);
-  hipLaunchKernelGGL(conv_reduce_kernel<T>, dim3(static_cast<unsigned>(cdiv(cols, 64))), dim3(512),
-                     0, stream, p.part, a.B * rgroups, a.C, K, static_cast<T*>(g->weight),
-                     static_cast<T*>(g->bias));
+  e = in_parts(cdiv((K + 1) * a.C, 64), [&](int64_t first, unsigned count) {
+    hipLaunchKernelGGL(conv_reduce_kernel<T>, dim3(count), dim3(512), 0, stream, p.part, a.B * rgroups, a.C, K, first,
+                       static_cast<T*>(g->weight), static_cast<T*>(g->bias));
+  });
   tr->after(stream);
-  return hipGetLastError();
+  return e;
 }
 
 template <typename T>
@@ -468,9 +463,12 @@ hipError_t reduce_rows(const RowSums& s, hipStream_t stream, Tracer* tr) {
   }
   if (grid == 0) return hipSuccess;
   tr->before(stream, "reduce_rows", r.rows);
-  hipLaunchKernelGGL(reduce_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(512), 0, stream, r);
+  const hipError_t e = in_parts(grid, [&](int64_t first, unsigned count) {
+    r.block0 = first;
+    hipLaunchKernelGGL(reduce_rows_kernel, dim3(count), dim3(512), 0, stream, r);
+  });
   tr->after(stream);
-  return hipGetLastError();
+  return e;
 }
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C, int64_t K) {

@@ -77,13 +77,14 @@ template <typename T> struct ScanP {
   float* dstate;
   int64_t B, L, Lp, C, G, Cg, chunks;   // Lp: L rounded up to whole chunks
   int N, tiles, segs, segChunks, softplus;
+  uint32_t block0;        // first workgroup of this launch
   bool whole, whole_bc;   // single tokens: states, B and C in whole aligned pieces of four
 };
 
 // ---- B and C as fp32, zeros past N states and past the entry's tokens --------
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void pack_kernel(ScanP<T> a) {
-  int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
+  int64_t i = (static_cast<int64_t>(a.block0) + blockIdx.x) * 256 + threadIdx.x;
   const int n = static_cast<int>(i % (2 * NS));
   i /= 2 * NS;
   const int w = static_cast<int>(i % kW);     // reads of a token's states stay adjacent
@@ -165,7 +166,7 @@ __device__ __forceinline__ Place<T> place(const ScanP<T>& a, int segs, int first
   Place<T> p;
   p.lane = threadIdx.x & 63;
   p.w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t i = blockIdx.x;
+  uint32_t i = blockIdx.x + a.block0;
   p.tile = static_cast<int>(i % a.tiles);
   i /= a.tiles;
   p.g = i % static_cast<uint32_t>(a.G);
@@ -457,9 +458,10 @@ template <typename T, int P>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanP<T> a) {
   constexpr uint32_t per = 256 / P;
   const uint32_t ctiles = (static_cast<uint32_t>(a.C) + per - 1) / per;
-  const int64_t b = blockIdx.x / ctiles;
+  const uint32_t blk = blockIdx.x + a.block0;
+  const int64_t b = blk / ctiles;
   const int q = threadIdx.x % P;
-  const uint32_t c0 = (blockIdx.x % ctiles) * per + threadIdx.x / P;
+  const uint32_t c0 = (blk % ctiles) * per + threadIdx.x / P;
   const bool live = c0 < a.C;
   const int64_t c = live ? c0 : a.C - 1;
   const int64_t g = static_cast<uint32_t>(c) / static_cast<uint32_t>(a.Cg), n0 = 4 * q;
@@ -798,7 +800,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanP<T> a) {
 // dB, dC: the channel tiles' sums added in tile order
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void reduce_bc_kernel(ScanP<T> a, T* dB, T* dC) {
-  int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
+  int64_t i = (static_cast<int64_t>(a.block0) + blockIdx.x) * 256 + threadIdx.x;
   const int n = static_cast<int>(i % (kW * 2 * NS));
   i /= kW * 2 * NS;
   const int64_t t = i % a.L;
@@ -916,31 +918,33 @@ template <typename T> ScanP<T> scan_params(const gspn_scan_args& a, bool bwd) {
 
 float* at_bytes(void* ws, size_t off) { return reinterpret_cast<float*>(static_cast<char*>(ws) + off); }
 
-#define GSPN_LAUNCH(name, units, kern, grid, block, ...)                                     \
-  do {                                                                                       \
-    tr->before(stream, name, units);                                                         \
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(block), 0, stream,      \
-                       __VA_ARGS__);                                                         \
-    tr->after(stream);                                                                       \
-    const hipError_t e_ = hipGetLastError();                                                 \
-    if (e_ != hipSuccess) return e_;                                                         \
-  } while (0)
+// one kernel of the scan over a grid of workgroups of 256, in order
+template <typename T, typename... A>
+hipError_t launch(const char* name, void (*kern)(ScanP<T>, A...), int64_t grid, ScanP<T> p, hipStream_t stream,
+                  Tracer* tr, A... more) {
+  tr->before(stream, name, p.B);
+  const hipError_t e = in_parts(grid, [&](int64_t first, unsigned count) {
+    p.block0 = static_cast<uint32_t>(first);
+    hipLaunchKernelGGL(kern, dim3(count), dim3(256), 0, stream, p, more...);
+  });
+  tr->after(stream);
+  return e;
+}
 
 // the forward passes over whole prompts; p.saved set: states are kept
 template <typename T, int NS>
 hipError_t scan_passes(const ScanP<T>& p, hipStream_t stream, Tracer* tr) {
   const int64_t grid = p.B * p.segs * p.G * p.tiles;
   if (p.segs > 1) {
-    GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, false>), grid / p.segs * (p.segs - 1),
-                kThreads, p);
+    const hipError_t e =
+        launch("scan_local", scan_local_kernel<T, NS, false>, grid / p.segs * (p.segs - 1), p, stream, tr);
+    if (e != hipSuccess) return e;
   }
-  GSPN_LAUNCH("scan_fwd", p.B, (scan_fwd_kernel<T, NS>), grid, kThreads, p);
-  return hipSuccess;
+  return launch("scan_fwd", scan_fwd_kernel<T, NS>, grid, p, stream, tr);
 }
 
 template <typename T, int NS> hipError_t run_pack(const ScanP<T>& p, hipStream_t stream, Tracer* tr) {
-  GSPN_LAUNCH("scan_pack", p.B, (pack_kernel<T, NS>), cdiv(p.B * p.G * p.Lp * kW * 2 * NS, 256), 256, p);
-  return hipSuccess;
+  return launch("scan_pack", pack_kernel<T, NS>, cdiv(p.B * p.G * p.Lp * kW * 2 * NS, 256), p, stream, tr);
 }
 
 template <typename T, int NS>
@@ -965,13 +969,9 @@ hipError_t scan_fwd_dt(const gspn_scan_args& a, void* ws, hipStream_t stream, Tr
                  wide_ok(a.Cm.p, 4 * sizeof(T), sizeof(T), {a.Cm.batch, a.Cm.row, a.Cm.head});
     const int lanes = scan_np(a.N) / 4;
     const int64_t grid = a.B * cdiv(a.C, 256 / lanes);
-    switch (lanes) {
-      case 1: GSPN_LAUNCH("scan_step", a.B, (scan_step_kernel<T, 1>), grid, 256, p); break;
-      case 2: GSPN_LAUNCH("scan_step", a.B, (scan_step_kernel<T, 2>), grid, 256, p); break;
-      case 4: GSPN_LAUNCH("scan_step", a.B, (scan_step_kernel<T, 4>), grid, 256, p); break;
-      default: GSPN_LAUNCH("scan_step", a.B, (scan_step_kernel<T, 8>), grid, 256, p); break;
-    }
-    return hipSuccess;
+    auto kern = lanes == 1 ? scan_step_kernel<T, 1> : lanes == 2 ? scan_step_kernel<T, 2>
+              : lanes == 4 ? scan_step_kernel<T, 4> : scan_step_kernel<T, 8>;
+    return launch("scan_step", kern, grid, p, stream, tr);
   }
   switch (scan_ns(a.N)) {
     case 1: return scan_fwd_ns<T, 1>(a, ws, stream, tr);
@@ -1017,15 +1017,16 @@ hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
         if ((e = scan_passes<T, NS>(f, stream, tr)) != hipSuccess) return e;
       }
       if (p.segs > 1) {
-        GSPN_LAUNCH("scan_local", p.B, (scan_local_kernel<T, NS, true>), grid / p.segs * (p.segs - 1),
-                    kThreads, p);
+        e = launch("scan_local", scan_local_kernel<T, NS, true>, grid / p.segs * (p.segs - 1), p, stream, tr);
+        if (e != hipSuccess) return e;
       }
     }
-    GSPN_LAUNCH("scan_bwd", p.B, (scan_bwd_kernel<T, NS>), grid, kThreads, p);
-    if (p.L > 0)
-      GSPN_LAUNCH("scan_reduce_bc", p.B, (reduce_bc_kernel<T, NS>),
-                  cdiv(p.B * p.G * p.L * kW * 2 * NS, 256), 256, p, static_cast<T*>(g.Bm),
-                  static_cast<T*>(g.Cm));
+    if ((e = launch("scan_bwd", scan_bwd_kernel<T, NS>, grid, p, stream, tr)) != hipSuccess) return e;
+    if (p.L > 0) {
+      e = launch("scan_reduce_bc", reduce_bc_kernel<T, NS>, cdiv(p.B * p.G * p.L * kW * 2 * NS, 256), p, stream, tr,
+                 static_cast<T*>(g.Bm), static_cast<T*>(g.Cm));
+      if (e != hipSuccess) return e;
+    }
   }
   const int64_t rows = p.B * p.segs;
   return reduce_rows(RowSums{{p.partA, p.partD, p.partD + rows * p.C}, {g.A, g.D, g.dt_bias},

@@ -187,7 +187,7 @@ void scan_shape(Check& k, int64_t B, int64_t L, int64_t C, int64_t N, int64_t G,
     k.bad(GSPN_E_SHAPE, "dimension too large");
   else if (k.product({B, L + 1, C + 64, 32}) >= (int64_t(1) << 52) ||
            k.product({B, L / 32 + 1, C / 64 + G}) >= k31 || k.product({B, N, C / 64 + 1}) >= k31 ||
-           k.product({B, G, L, 64}) / 256 >= k31)
+           k.product({B, G, L + 16, 64}) / 256 >= k31)
     k.bad(GSPN_E_SHAPE, "tensor too large for one launch");
 }
 void scan_inputs(Check& k, const gspn_scan_args& a) {
@@ -216,6 +216,7 @@ void attn_shape(Check& k, int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t
     k.bad(GSPN_E_SHAPE, "need B, Lq, Lk >= 0, Hkv >= 1 dividing Hq, 1 <= E <= 128");
   else if (B >= k31 || Lq >= k31 || Lk >= k31 - 256 || Hq >= k31 || k.product({Lq, Hq}) >= k31 - 256)
     k.bad(GSPN_E_SHAPE, "dimension too large (Lq * Hq and Lk must stay below 2^31)");
+  // the last two also keep every launch of tiles below 2^24 workgroups of 256
   else if (k.product({B, Lq + 1, Hq, 128, 4}) >= (int64_t(1) << 52) ||
            k.product({B, Lk + 1, Hkv, 128, 4}) >= (int64_t(1) << 52) ||
            k.product({B, Hkv, Lq * (Hq / Hkv) / 32 + 64}) >= k31 / 64 ||

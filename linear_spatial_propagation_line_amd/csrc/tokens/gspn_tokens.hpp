@@ -44,11 +44,26 @@ struct RowSums {
   float* out[3];
   int64_t cols[3];
   int64_t rows;
+  int64_t block0 = 0;   // set by reduce_rows
 };
 hipError_t reduce_rows(const RowSums& s, hipStream_t stream, Tracer* tr);
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A launch takes fewer than 2^32 threads; what is above is cut off without an
+// error. Where the host checks admit more workgroups than that, they go out in
+// parts of at most kMostBlocks (of up to 512 threads): part(first, count), in
+// order; the kernel adds `first`.
+constexpr int64_t kMostBlocks = int64_t(1) << 22;
+template <typename F> hipError_t in_parts(int64_t blocks, F&& part) {
+  for (int64_t first = 0; first < blocks; first += kMostBlocks) {
+    part(first, static_cast<unsigned>(std::min(kMostBlocks, blocks - first)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // a host-side check that a pointer and the strides used with it keep
 // `bytes`-wide accesses aligned

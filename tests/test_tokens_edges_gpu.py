@@ -234,3 +234,91 @@ def test_conv_grad_state_refusals():
         g.causal_conv_backward(x, w, None, x.clone(), state=torch.zeros_like(gs), grad_state=gs,
                                grads=dict(x=None, weight=None, state=gs))
     assert e.value.name == "GSPN_E_ALIAS"
+
+
+# --------------------------------------------------------------------------
+# more workgroups than one launch takes (2^32 threads)
+# --------------------------------------------------------------------------
+def big(gen, *shape, std=1.0, dtype=BF16):
+    return torch.empty(shape, dtype=dtype, device=DEV).normal_(0.0, std, generator=gen)
+
+
+def test_conv_of_many_sequences():
+    """One token each of 2^23 sequences, 65 channels: 2^24 workgroups."""
+    gen = torch.Generator(device=DEV).manual_seed(20)
+    B, C, K = (1 << 23) + 5, 65, 2
+    x, st, gy = big(gen, B, 1, C), big(gen, B, K - 1, C), big(gen, B, 1, C)
+    w, b = big(gen, C, K), big(gen, C)
+    out = g.causal_conv(x, w, b, state=st, state_out=st)
+    assert torch.equal(st, x)
+    got = g.causal_conv_backward(x, w, b, gy, state=st)
+    for e in (0, 1 << 22, B - 3):
+        sl = slice(e, e + 3)
+        old = st[sl].clone()
+        want = g.causal_conv_backward(x[sl], w, b, gy[sl], state=old)
+        assert torch.equal(got["x"][sl], want["x"]) and torch.equal(got["state"][sl], want["state"])
+    last = g.causal_conv(x[-3:], w, b, state=out.new_zeros(3, K - 1, C))
+    first = g.causal_conv(x[-3:], w, b, state=st[-3:])
+    assert not torch.equal(last, first)
+    assert all(bool(t.isfinite().all()) for t in got.values())
+
+
+def test_scan_of_many_tokens():
+    """2^26 tokens of 32 states: 2^32 values of B and C, read from one row."""
+    gen = torch.Generator(device=DEV).manual_seed(21)
+    B, L, N = (1 << 16) + 3, 1024, 32
+    x, dt, gy = (big(gen, B, L, 1) for _ in range(3))
+    Bm, Cm = (big(gen, 1, L, 1, N).expand(B, -1, -1, -1) for _ in range(2))
+    A = -torch.arange(1, N + 1, device=DEV, dtype=F32)[None]
+    out = g.selective_scan(x, dt, A, Bm, Cm)
+    got = g.selective_scan_backward(x, dt, A, Bm, Cm, gy)
+    for e in (0, 1 << 15, B - 2):
+        sl = slice(e, e + 2)
+        part = (x[sl], dt[sl], A, Bm[sl], Cm[sl])
+        close(out[sl], g.selective_scan(*part).cpu(), 1e-2, "out")
+        want = g.selective_scan_backward(*part, gy[sl])
+        for n in ("x", "dt", "B", "C"):
+            close(got[n][sl], want[n].cpu(), 1e-2, n)
+    assert bool(got["A"].isfinite().all())
+
+
+def test_scan_of_many_short_sequences():
+    """2^24 sequences of five tokens: as many workgroups."""
+    gen = torch.Generator(device=DEV).manual_seed(22)
+    B, L, N = (1 << 24) + 3, 5, 2
+    x, dt = big(gen, B, L, 1), big(gen, B, L, 1)
+    Bm, Cm = (big(gen, 1, L, 1, N).expand(B, -1, -1, -1) for _ in range(2))
+    A = -torch.arange(1, N + 1, device=DEV, dtype=F32)[None]
+    for t in (L, 1):
+        out = g.selective_scan(x[:, :t], dt[:, :t], A, Bm[:, :t], Cm[:, :t])
+        for e in (0, 1 << 23, B - 3):
+            sl = slice(e, e + 3)
+            close(out[sl], g.selective_scan(x[sl, :t], dt[sl, :t], A, Bm[sl, :t], Cm[sl, :t]).cpu(), 1e-2, "out")
+
+
+def test_attention_of_many_rows_backward():
+    """2^28 rows: sixteen lanes each for grad_out . out."""
+    gen = torch.Generator(device=DEV).manual_seed(23)
+    Lq, Lk = (1 << 28) + 100, 3
+    q, gy = big(gen, 1, Lq, 1, 1), big(gen, 1, Lq, 1, 1)
+    k, v = big(gen, 1, Lk, 1, 1), big(gen, 1, Lk, 1, 1)
+    lse = torch.empty((1, 1, Lq), device=DEV)
+    out = g.cross_attention(q, k, v, lse=lse)
+    got = g.cross_attention_backward(q, k, v, out, lse, gy)
+    for e in (0, 1 << 27, Lq - 64):
+        sl = slice(e, e + 64)
+        one = torch.empty((1, 1, 64), device=DEV)
+        o = g.cross_attention(q[:, sl], k, v, lse=one)
+        assert torch.equal(out[:, sl], o) and torch.equal(lse[..., sl], one)
+        want = g.cross_attention_backward(q[:, sl], k, v, o, one, gy[:, sl].contiguous())
+        assert torch.equal(got["q"][:, sl], want["q"])
+    assert bool(got["k"].isfinite().all()) and bool(got["v"].isfinite().all())
+
+
+def test_attention_without_keys_of_many_values():
+    Lq = (1 << 26) + 1
+    q = torch.ones((1, Lq, 1, 64), dtype=BF16, device=DEV)
+    none = q[:, :0]
+    out, lse = torch.ones_like(q), torch.zeros((1, 1, Lq), device=DEV)
+    g.cross_attention(q, none, none, out=out, lse=lse)
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())

@@ -242,8 +242,12 @@ __device__ __forceinline__ void carried_in(const ScanP<T>& a, const Place<T>& p,
     for (int j = 0; j < kAt; ++j) {
       if (i + j < count) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-          h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[n] * sum[j]), h[n], local[j][n]);
+        for (int n = 0; n < NS; ++n) {
+          // exp(A sum d) as the square of its root, below 2^128: where states
+          // grow (d A > 0) it would overflow over a state that is 0 or tiny
+          const float half = __builtin_amdgcn_exp2f(fminf(A2[n] * (0.5f * sum[j]), 127.0f));
+          h[n] = __builtin_fmaf(half * h[n], half, local[j][n]);
+        }
       }
     }
   }

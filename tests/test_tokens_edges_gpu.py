@@ -170,6 +170,47 @@ def test_scan_in_place_over_several_segments_is_right():
     close(st, ref_end, 300 * 2.0 ** -23, "state")
 
 
+def test_scan_states_that_grow_over_several_segments():
+    """Steps below zero (no softplus) make states grow, here by exp(96) and more
+    over 16 tokens. A channel without input before its last tokens stays at 0
+    until then, and its gradient at 0 behind the first ones; a tiny state that
+    grows and shrinks in turn is found again. 64-bit references; an exponent of
+    size s is off by s 2^-23, and every token adds two units of 2^-23."""
+    L, C, N = 512, 64, 2
+    gen = torch.Generator().manual_seed(24)
+    normal = lambda *s: torch.randn(s, generator=gen)    # noqa: E731
+    inp = dict(x=normal(1, L, C), dt=-torch.ones(1, L, C), A=torch.tensor([[-8.0, -6.0]]).repeat(C, 1),
+               Bm=normal(1, L, 1, N), Cm=normal(1, L, 1, N), D=normal(C), z=None, dt_bias=None, state=None,
+               lens=None, softplus=False)
+    inp["x"][:, :-8] = 0
+    gy = normal(1, L, C)
+    gy[:, 8:] = 0
+    d = dev(inp)
+    args, par = scan_args(d)
+    end = torch.empty((1, C, N), device=DEV)
+    out, names = launches(lambda: g.selective_scan(*args, **par, state_out=end))
+    assert "scan_local" in names, names
+    tol = 64 * 2.0 ** -23 + 16 * 2.0 ** -23
+    ref, ref_end = plain.scan(**inp)
+    close(out, ref, tol, "out")
+    close(end, ref_end, tol, "state")
+    got = g.selective_scan_backward(*args, gy.to(DEV), **par)
+    got["Bm"], got["Cm"] = got.pop("B"), got.pop("C")
+    rg = plain.gradients(plain.scan, inp, list(got), gy)
+    close_all(got, rg, 2 * tol, "scan")
+    inp["x"][:] = 0
+    inp["dt"] = inp["dt"].unflatten(1, (L // 32, 2, 16)) * torch.tensor([1.0, -1.0])[:, None, None]
+    inp["dt"] = inp["dt"].flatten(1, 3)
+    inp["state"] = torch.full((1, C, N), 1e-30)
+    d = dev(inp)
+    args, par = scan_args(d)
+    out = g.selective_scan(*args, **par, state_out=end)
+    ref, ref_end = plain.scan(**inp)
+    tol = L * 2.0 ** -22 + 128 * 2.0 ** -23
+    close(out, ref, tol, "out")
+    close(end, ref_end, tol, "state")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_conv_in_place_over_several_runs(dtype):
     inp, _ = conv_case(4, 300, 200, 4, dtype, (300, 0, 2, 129), True, True, True, seed=13)

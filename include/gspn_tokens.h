@@ -185,7 +185,7 @@ size_t gspn_selective_scan_backward_workspace_bytes(int64_t B, int64_t L, int64_
  * out = 0 and lse = -inf, and gradients of 0.
  *   q [B, Lq, Hq, E]; k, v [B, Lk, Hkv, E]; out [B, Lq, Hq, E]   in dtype
  *   lse [B, Hq, Lq] fp32, or NULL
- *   E 1 .. 128; Hkv >= 1 dividing Hq; scale finite and > 0 (GSPN_E_SHAPE)
+ *   E 1 .. 128; Hkv >= 1 dividing Hq; scale > 0 and below 2^127 (GSPN_E_SHAPE)
  * Products run on matrix cores with fp32 accumulation; with bf16 storage the
  * probabilities are an operand of the second product with 16 bits of mantissa.
  * Workspace: gspn_cross_attention_workspace_bytes() bytes, 256-byte aligned

@@ -225,8 +225,8 @@ void attn_shape(Check& k, int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t
 }
 void attn_inputs(Check& k, const gspn_attn_args& a) {
   const size_t es = esize(a.dtype);
-  if (k.ok() && !(std::isfinite(a.scale) && a.scale > 0.0f))
-    k.bad(GSPN_E_SHAPE, "scale must be finite and > 0");
+  if (k.ok() && !(a.scale > 0.0f && std::isfinite(a.scale * 2.0f)))   // the kernels take scale * log2(e)
+    k.bad(GSPN_E_SHAPE, "scale must be > 0 and at most half of the largest float");
   k.view(a.q.p, es, {a.B, a.Lq, a.Hq, a.E}, {a.q.batch, a.q.row, a.q.head});
   k.view(a.k.p, es, {a.B, a.Lk, a.Hkv, a.E}, {a.k.batch, a.k.row, a.k.head});
   k.view(a.v.p, es, {a.B, a.Lk, a.Hkv, a.E}, {a.v.batch, a.v.row, a.v.head});

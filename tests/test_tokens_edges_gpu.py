@@ -85,6 +85,17 @@ def test_attention_without_keys_whatever_the_query_holds(shape, dtype):
         assert not got[n].cpu()[~inp["mask"]].any(), n
 
 
+@pytest.mark.parametrize("scale", [3e38, 1e39, float("nan"), 1e-50])
+def test_attention_scales_that_no_float_holds(scale):
+    """The kernels take scale * log2(e): it has to be finite too (zeros times
+    an infinity would be NaN)."""
+    q = torch.zeros(1, 3, 2, 8, device=DEV)
+    with pytest.raises(g.GspnError) as e:
+        g.cross_attention(q, q, q, scale=scale)
+    assert e.value.name == "GSPN_E_SHAPE"
+    assert not g.cross_attention(q, q, q, scale=1e38).any()
+
+
 # --------------------------------------------------------------------------
 # silu far below zero
 # --------------------------------------------------------------------------

@@ -73,17 +73,17 @@ class Check {
     }
     add(p, top + 1, es, required, false);
   }
-  // an output that may be exactly the memory of one input
-  void update(void* p, const void* same, int64_t n, size_t es) {
-    if (p && p == same) {
-      if (n > 0) {
-        align(p, es);
-        outs_[nout_++] = span(p, n, es);
-        same_ = nout_;
-      }
-      return;
-    }
+  // an input, not required, that update() may name
+  void state(const void* p, int64_t n, size_t es) {
+    const int before = nin_;
+    add(p, n, es, false, false);
+    if (nin_ > before) state_in_ = before;
+  }
+  // an output that may be exactly the memory of the state
+  void update(void* p, int64_t n, size_t es) {
+    const int before = nout_;
     add(p, n, es, false, true);
+    if (nout_ > before) state_out_ = before;
   }
   void scratch(void* ws, size_t bytes, size_t need) {
     if (!ok() || need == 0) return;
@@ -101,13 +101,13 @@ class Check {
     for (int i = 0; i < nout_; ++i)
       if (meet(w, outs_[i])) bad(GSPN_E_ALIAS, "the workspace overlaps an output");
   }
-  // call after all tensors are named; state_in: the input an update may be
+  // call after all tensors are named
   void aliases() {
     if (!ok()) return;
     for (int i = 0; i < nout_; ++i) {
       for (int k = 0; k < nin_; ++k) {
         if (!meet(outs_[i], ins_[k])) continue;
-        if (same_ == i + 1 && ins_[k].lo == outs_[i].lo && ins_[k].hi == outs_[i].hi) continue;
+        if (i == state_out_ && k == state_in_ && ins_[k].lo == outs_[i].lo) continue;
         bad(GSPN_E_ALIAS, "an output overlaps an input");
       }
       for (int k = i + 1; k < nout_; ++k)
@@ -136,7 +136,7 @@ class Check {
     else ins_[nin_++] = span(p, n, es);
   }
   Span ins_[24], outs_[16];
-  int nin_ = 0, nout_ = 0, same_ = 0;
+  int nin_ = 0, nout_ = 0, state_in_ = -1, state_out_ = -1;
 };
 
 bool dtype_ok(gspn_dtype dt) { return dt == GSPN_F32 || dt == GSPN_BF16; }
@@ -174,7 +174,7 @@ void conv_inputs(Check& k, const gspn_conv_args& a) {
   k.view(a.x.p, es, {a.B, a.L, a.C}, {a.x.batch, a.x.row});
   k.input(a.weight, a.C * a.K, es);
   k.input(a.bias, a.C, es, false);
-  k.input(a.state, a.B * (a.K - 1) * a.C, es, false);
+  k.state(a.state, a.B * (a.K - 1) * a.C, es);
   k.input(a.lens, a.B, 4, false);
 }
 
@@ -200,7 +200,7 @@ void scan_inputs(Check& k, const gspn_scan_args& a) {
   k.view(a.Cm.p, es, {a.B, a.L, a.G, a.N}, {a.Cm.batch, a.Cm.row, a.Cm.head});
   k.input(a.D, a.C, 4, false);
   k.input(a.dt_bias, a.C, 4, false);
-  k.input(a.state, a.B * a.C * a.N, 4, false);
+  k.state(a.state, a.B * a.C * a.N, 4);
   k.input(a.lens, a.B, 4, false);
 }
 void check_saved(Check& k, const void* saved) {
@@ -246,7 +246,7 @@ gspn_status gspn_causal_conv(const gspn_conv_args* a, hipStream_t stream) {
     const size_t es = esize(a->dtype);
     conv_inputs(k, *a);
     k.output(a->out, a->B * a->L * a->C, es);
-    k.update(a->state_out, a->state, a->B * (a->K - 1) * a->C, es);
+    k.update(a->state_out, a->B * (a->K - 1) * a->C, es);
     k.aliases();
     if (!k.ok()) return k.status;
     if (a->B == 0 || a->C == 0) return GSPN_OK;
@@ -298,7 +298,7 @@ gspn_status gspn_selective_scan_ws(const gspn_scan_args* a, void* ws, size_t ws_
     if (!k.ok()) return k.status;
     scan_inputs(k, *a);
     k.output(a->out, a->B * a->L * a->C, esize(a->dtype));
-    k.update(a->state_out, a->state, a->B * a->C * a->N, 4);
+    k.update(a->state_out, a->B * a->C * a->N, 4);
     check_saved(k, a->saved);
     k.output(a->saved, static_cast<int64_t>(gspn::scan_saved_bytes(a->B, a->L, a->C, a->N)), 1, false);
     k.aliases();

@@ -1026,7 +1026,7 @@ hipError_t scan_bwd_ns(const gspn_scan_args& a, const gspn_scan_grads& g, void* 
       }
     }
     if ((e = launch("scan_bwd", scan_bwd_kernel<T, NS>, grid, p, stream, tr)) != hipSuccess) return e;
-    if (p.L > 0) {
+    if (p.L > 0) {   // zeros where there are no channels
       e = launch("scan_reduce_bc", reduce_bc_kernel<T, NS>, cdiv(p.B * p.G * p.L * kW * 2 * NS, 256), p, stream, tr,
                  static_cast<T*>(g.Bm), static_cast<T*>(g.Cm));
       if (e != hipSuccess) return e;

@@ -360,7 +360,6 @@ gspn_status gspn_selective_scan_backward_ws(const gspn_scan_args* a, const gspn_
     k.aliases();
     k.scratch(ws, ws_bytes, k.ok() ? gspn::scan_bwd_workspace_bytes(a->B, a->L, a->C, a->N, a->G) : 0);
     if (!k.ok()) return k.status;
-    if (a->C == 0) return GSPN_OK;
     return enqueue([&](gspn::Tracer* tr) { return gspn::launch_scan_bwd(*a, *g, ws, stream, tr); });
   });
 }

@@ -288,6 +288,22 @@ def test_conv_grad_state_refusals():
     assert e.value.name == "GSPN_E_ALIAS"
 
 
+@pytest.mark.parametrize("shape", [(2, 40, 0, 4, 2), (2, 3, 0, 9, 1), (0, 40, 6, 4, 2), (2, 0, 6, 4, 2)])
+def test_scan_gradients_of_nothing_are_zeros(shape):
+    """No channels, no entries, no tokens: sums of nothing are written too."""
+    B, L, C, N, G = shape
+    zeros = lambda *s: torch.zeros(s, device=DEV)    # noqa: E731
+    x, bc, state = zeros(B, L, C), zeros(B, L, G, N) + 1, zeros(B, C, N) + 1
+    like = dict(x=x, dt=x, A=zeros(C, N), B=bc, C=bc, D=zeros(C), dt_bias=zeros(C), state=state)
+    grads = {n: torch.full_like(t, float("nan")) for n, t in like.items()}
+    out = g.selective_scan(x, x, like["A"], bc, bc, D=like["D"], dt_bias=like["dt_bias"], state=state)
+    assert out.shape == x.shape
+    got = g.selective_scan_backward(x, x, like["A"], bc, bc, x, D=like["D"], dt_bias=like["dt_bias"], state=state,
+                                    grads=grads)
+    for n, t in got.items():
+        assert not t.any(), n
+
+
 # --------------------------------------------------------------------------
 # more workgroups than one launch takes (2^32 threads)
 # --------------------------------------------------------------------------

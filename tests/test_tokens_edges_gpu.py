@@ -9,7 +9,8 @@ import torch
 
 import linear_spatial_propagation_line_amd as g
 import plain_tokens as plain
-from test_tokens_gpu import BF16, CONV, DEV, F32, attn_case, close, close_all, conv_call, conv_case, dev, rms, scan_args, scan_case
+from test_tokens_gpu import (BF16, CONV, DEV, F32, MANY, attn_case, close, close_all, conv_call, conv_case, dev, rms,
+                             scan_args, scan_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +50,22 @@ def test_attention_operands_add_no_error_of_their_own(case):
         own = rms(ref[n].to(BF16).double() - ref[n])
         err = rms(got[n].cpu().double() - ref[n])
         assert err <= most * own, f"{n}: {err / own:.3f} of the result's own rounding"
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_attention_lse_of_many_rows(case):
+    """The values of lse, row by row, in the kernels that fill the chip. The
+    scores' rounding (fp32 sums of E products) is absolute, a few 2^-24 of a
+    score; scores stay below 8 here."""
+    inp, _ = attn_case(*case, seed=5)
+    B, Lq, Lk, Hq, Hkv, E, _, _ = case
+    d = dev(inp)
+    lse = torch.full((B, Hq, Lq), float("nan"), device=DEV)
+    g.cross_attention(d["q"], d["k"], d["v"], mask=d["mask"], lse=lse)
+    ref = plain.attention(**inp)[1]
+    dead = torch.isinf(ref)
+    assert torch.equal(lse.cpu() == -float("inf"), dead)
+    assert float((lse.cpu().double() - ref)[~dead].abs().max()) <= 1e-5
 
 
 # --------------------------------------------------------------------------

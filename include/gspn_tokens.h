@@ -213,6 +213,9 @@ size_t gspn_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, i
  * hold the forward call's results. Sums over queries and over the heads that
  * share keys are in fp32, in a fixed order; with bf16 storage the
  * probabilities and the score gradients are operands with 16 bits of mantissa.
+ * The sum over e of grad_out out, which every score gradient takes, is found
+ * from the probabilities where an entry's kept keys lie within 128 (fp32: 32)
+ * and from out as it is stored where they do not.
  * Workspace: gspn_cross_attention_backward_workspace_bytes() bytes, 256-byte
  * aligned.
  */

@@ -1,13 +1,13 @@
-// Cross attention, backward. With P from the forward pass's lse and
-// D[row] = sum_e grad_out out:
+// Cross attention, backward. With P from the forward pass's lse, dP = dO V^T and
+// D[row] = sum_e grad_out out (= sum over keys of P dP):
 //
-//   dV = P^T dO,   dS = P (dO V^T - D),   dQ = scale dS K,   dK = scale dS^T Q
+//   dV = P^T dO,   dS = P (dP - D),   dQ = scale dS K,   dK = scale dS^T Q
 //
-// Two passes recompute P: one owns keys (a wavefront 32 of them, their K and
-// V fragments and their dK, dV in registers) and walks the rows, one owns
-// rows and walks the keys. Each sum then has one owner, so nothing is added
-// atomically; where few keys leave the chip idle, the rows of the first pass
-// are split and the parts added in order.
+// Two passes recompute P: one owns rows and walks the keys, one owns keys (a
+// wavefront 32 of them, their K and V fragments and their dK, dV in registers)
+// and walks the rows. Each sum then has one owner, so nothing is added
+// atomically; where few keys leave the chip idle, the rows of the second
+// pass are split and the parts added in order.
 #include "gspn_attn.hpp"
 
 namespace gspn {
@@ -31,6 +31,17 @@ template <typename T> struct BwdP {
   uint32_t block0;     // attn_delta: first workgroup of this launch
   bool wide_q, wide_kv, wide_g, wide_dq, wide_dkv, full;
 };
+
+// D of a row is sum_e grad_out out = sum_j P dP. The first takes the rounding of
+// out with it, which is large against score gradients that are small differences
+// of few terms (bf16, rms of dQ's error in units of its own rounding: 2 keys 1.6,
+// 17 keys 1.4, 77 keys 1.06; 2048 keys 1.00). The second needs all of a row's
+// keys before the first score gradient. So attn_dq walks the kept keys twice
+// where they lie in at most this many tiles of 32, and leaves D for attn_dkv; the
+// launch that reads grad_out and out falls away where no entry can have more
+// (262144 rows, 77 keys, 5 heads of 64, training step 464 us, 550 by out; with
+// both 572). fp32 rounds out as finely as all else: one tile, which costs nothing.
+template <typename T> constexpr int exact_tiles() { return sizeof(T) == 2 ? 4 : 1; }
 
 // delta[b][h][q] = sum_e grad_out out: 16 lanes per row
 template <typename T>
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
   row_frags<T, EP, FULL>(a.q + b * a.qm.batch + w.q * a.qm.row + w.h * a.qm.head, true, a.E, a.wide_q, qf);
   row_frags<T, EP, FULL>(a.gy + b * a.gm.batch + w.q * a.gm.row + w.h * a.gm.head, true, a.E, a.wide_g, gf);
   const int64_t at = (b * a.Hq + w.h) * a.Lq + w.q;
-  const float lse = row_ok ? a.lse[at] * kLog2e : INFINITY, delta = row_ok ? a.delta[at] : 0.0f;
+  const float lse = row_ok ? a.lse[at] * kLog2e : INFINITY;
 
   const T* kp = a.k + b * a.km.batch + hk * a.km.head;
   const T* vp = a.v + b * a.vm.batch + hk * a.vm.head;
@@ -228,31 +239,53 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kern
     ks.template write<FULL>(to, tid, a.E, [&](int i) { return (next >> i) & 1u; });
     vs.template write<FULL>(to + TK * tile_pitch<T, EP>(), tid, a.E, [&](int i) { return (next >> i) & 1u; });
   };
-  if (t_first < t_last) {
-    fetch(t_first);
-    put(t_first);
-  }
-  lds_barrier();
-  for (int t = t_first; t < t_last; ++t) {
-    const char* kt = lds + (t & 1) * kTile;
-    const char* vt = kt + TK * tile_pitch<T, EP>();
-    bits = next;
-    if (t + 1 < t_last) fetch(t + 1);
-    if (bits != 0) {
-      const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
-      const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
-      float ds[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ds[i] = x[i];
-      drop_keys(ds, bits, lane);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(ds[i], a.c, -lse)) * (y[i] - delta);
-      tile_accum<EP>(kt, 0, ds, dq, lane, T{});
+  // use(K tile, V tile) for every tile that keeps a key
+  auto walk = [&](auto&& use) {
+    if (t_first < t_last) {
+      fetch(t_first);
+      put(t_first);
     }
-    if (t + 1 < t_last) put(t + 1);
     lds_barrier();
+    for (int t = t_first; t < t_last; ++t) {
+      const char* kt = lds + (t & 1) * kTile;
+      bits = next;
+      if (t + 1 < t_last) fetch(t + 1);
+      if (bits != 0) use(kt, kt + TK * tile_pitch<T, EP>());
+      if (t + 1 < t_last) put(t + 1);
+      lds_barrier();
+    }
+  };
+  auto probabilities = [&](const char* kt, float (&p)[16]) {
+    const f32x16 x = tile_dot<T, EP>(kt, 0, qf, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = x[i];
+    drop_keys(p, bits, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], a.c, -lse));
+  };
+  float delta;
+  if (t_last - t_first > exact_tiles<T>()) {
+    delta = row_ok ? a.delta[at] : 0.0f;
+  } else {
+    float sum = 0.0f;
+    walk([&](const char* kt, const char* vt) {
+      float p[16];
+      probabilities(kt, p);
+      const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(p[i], y[i], sum);
+    });
+    delta = column_sum(sum);
+    if (row_ok && lane < 32) a.delta[at] = delta;
   }
+  walk([&](const char* kt, const char* vt) {
+    float ds[16];
+    probabilities(kt, ds);
+    const f32x16 y = tile_dot<T, EP>(vt, 0, gf, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ds[i] *= y[i] - delta;
+    tile_accum<EP>(kt, 0, ds, dq, lane, T{});
+  });
   store_col<T, EP, FULL>(a.dq + ((b * a.Lq + w.q) * a.Hq + w.h) * a.E, row_ok, true, a.E, a.wide_dq, dq, a.scale, lane);
 }
 
@@ -285,7 +318,7 @@ template <typename K> hipError_t more_lds(K kern, int bytes) {
 template <typename T, int EP>
 hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
   hipError_t e;
-  if (p.rows > 0) {
+  if (p.rows > 0 && cdiv(p.Lk, 32) > exact_tiles<T>()) {   // some entry may keep keys in more tiles
     tr->before(stream, "attn_delta", p.B);
     e = in_parts(cdiv(p.B * p.Hq * p.Lq, kThreads / 16), [&](int64_t first, unsigned count) {
       BwdP<T> d = p;
@@ -294,6 +327,16 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
     });
     tr->after(stream);
     if (e != hipSuccess) return e;
+  }
+  if (p.rows > 0) {
+    auto kern = p.full ? attn_dq_kernel<T, EP, true> : attn_dq_kernel<T, EP, false>;
+    constexpr int bytes = 4 * 32 * tile_pitch<T, EP>();
+    if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
+    tr->before(stream, "attn_dq", p.B * p.Hkv);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * cdiv(p.rows, 128))),
+                       dim3(kThreads), bytes, stream, p);
+    tr->after(stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (p.Lk > 0) {
     auto kern = p.full ? attn_dkv_kernel<T, EP, true> : attn_dkv_kernel<T, EP, false>;
@@ -312,16 +355,6 @@ hipError_t bwd_ep(const BwdP<T>& p, hipStream_t stream, Tracer* tr) {
       tr->after(stream);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-  }
-  if (p.rows > 0) {
-    auto kern = p.full ? attn_dq_kernel<T, EP, true> : attn_dq_kernel<T, EP, false>;
-    constexpr int bytes = 4 * 32 * tile_pitch<T, EP>();
-    if ((e = more_lds(kern, bytes)) != hipSuccess) return e;
-    tr->before(stream, "attn_dq", p.B * p.Hkv);
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.B * p.Hkv * cdiv(p.rows, 128))),
-                       dim3(kThreads), bytes, stream, p);
-    tr->after(stream);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
 }

@@ -52,6 +52,37 @@ def test_attention_operands_add_no_error_of_their_own(case):
         assert err <= most * own, f"{n}: {err / own:.3f} of the result's own rounding"
 
 
+@pytest.mark.parametrize("case", [
+    (2, 300, 2, 4, 2, 64, None), (2, 70, 5, 4, 4, 128, "random"), (1, 700, 8, 6, 3, 32, None),
+    (2, 200, 32, 2, 2, 96, None), (2, 90, 900, 4, 2, 64, "few"), (2, 90, 900, 2, 2, 40, "across"),
+    (2, 300, 77, 5, 5, 64, "sharp"),
+])
+def test_attention_gradients_with_few_keys(case):
+    """Few kept keys: a row's probabilities are large and its score gradients
+    small differences, which the rounding of out (grad_out . out) would change
+    by more than their own rounding. Taken from the probabilities themselves
+    they leave the result's own rounding, as above: 1.1 of it."""
+    B, Lq, Lk, Hq, Hkv, E, kind = case
+    inp, gy = attn_case(B, Lq, Lk, Hq, Hkv, E, BF16, "random" if kind == "random" else None, seed=25)
+    key = torch.arange(Lk)[None]
+    if kind == "few":         # right padding down to 17 and 4 keys
+        inp["mask"] = key < torch.tensor([[17], [4]])
+    elif kind == "across":    # a few keys in two tiles
+        inp["mask"] = (key >= torch.tensor([[30], [445]])) & (key < torch.tensor([[34], [450]]))
+    elif kind == "random":
+        inp["mask"][:, 0] = True
+    scale = inp["scale"] = 1.0 if kind == "sharp" else E ** -0.5    # scores of 8: one key or two count
+    d = dev(inp)
+    lse = torch.empty((B, Hq, Lq), device=DEV)
+    out = g.cross_attention(d["q"], d["k"], d["v"], mask=d["mask"], scale=scale, lse=lse)
+    got = g.cross_attention_backward(d["q"], d["k"], d["v"], out, lse, gy.to(DEV), mask=d["mask"], scale=scale)
+    ref = plain.gradients(plain.attention, inp, ["q", "k", "v"], gy)
+    for n in "qkv":
+        own = rms(ref[n].to(BF16).double() - ref[n])
+        err = rms(got[n].cpu().double() - ref[n])
+        assert err <= 1.1 * own, f"{n}: {err / own:.3f} of the result's own rounding"
+
+
 @pytest.mark.parametrize("case", MANY)
 def test_attention_lse_of_many_rows(case):
     """The values of lse, row by row, in the kernels that fill the chip. The

@@ -596,15 +596,15 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int
   } else {
     // Row tiles of 128; where these are few the key axis is split, as often as
     // two workgroups per compute unit allow. (2048 keys, 16 heads, us split and
-    // whole: bf16 of 128, 64 tiles 35, 59; 144 tiles, in three, 49, 59. fp32 of
-    // 72, 1024 keys, 128 tiles 84, 180; 240 tiles 151, 182.) In two it does not
-    // pay where aligned bf16 rows keep the loads short (of 64, 256 tiles 45, 41;
-    // of 72, padded, 74, 110 before pieces were loaded whole).
+    // whole: bf16 of 128, 64 tiles 37, 68; 144 tiles, in three, 55, 69. fp32 of
+    // 72, 1024 keys, 128 tiles 81, 124; 144 tiles, in three, 104, 126.) In two it
+    // pays only where padded bf16 rows make the loads long (bf16 of 64, 256 tiles
+    // 51, 48; of 72 68, 79; fp32 of 72, 240 tiles 146, 127).
     k.plan = AttnPlan::kRows;
     k.key_tiles = static_cast<int>(cdiv(Lk, es == 2 ? 64 : 32));
     k.row_tiles = static_cast<int>(cdiv(rows, 128));
     splits = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(k.key_tiles, 64), 512 / (heads * k.row_tiles)));
-    if (splits == 2 && full && es == 2) splits = 1;
+    if (splits == 2 && (full || es == 4)) splits = 1;
     k.tiles_each = static_cast<int>(cdiv(k.key_tiles, splits));
     k.splits = static_cast<int>(cdiv(k.key_tiles, k.tiles_each));
   }

@@ -158,9 +158,12 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnP<float> a) {
 // stand between them, so that a wavefront's own products and exponentials can
 // overlap. Tiles of 64 keys in two LDS buffers. Two column tiles (64 rows) per
 // wavefront halve what is read from LDS per product, but cost the wavefronts
-// that fill each other's waits: 4x4096x2048 with ragged masks, 16 heads of 64,
-// 184 us with two, 130 with one (1056 TFLOP/s); 2x4096x2048, 16 heads of 128,
-// 250 with two (and accumulation registers), 190 with one.
+// that fill each other's waits (with P in bf16 alone, 4x4096x2048 with ragged
+// masks, 16 heads of 64: 184 us with two, 130 with one; 2x4096x2048, 16 heads of
+// 128: 250 with two and accumulation registers, 190 with one). Now 153 us and
+// 175: 500 and 550 TFLOP/s of the products with kept keys (0.55 and 0.70 of all),
+// P's second part not counted. The matrix units work for two fifths of the time;
+// a wavefront's exponentials and its products still wait for each other.
 template <int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a) {
   using T = bf16_t;
@@ -266,8 +269,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnP<bf16_t> a)
 // All keys of an (entry, key head) stay in LDS while each wavefront walks row
 // tiles of its own, with no barrier after the keys are staged: all scores of
 // a row are in registers, so its maximum is known before the first exponential.
-// Bound by the rows' bytes (q in, out back); the next tile's q is loaded ahead.
-// 2097152 rows, 77 keys, 5 heads of 64, bf16: 553 us, 4.86 TB/s, a copy's rate.
+// Bound by the rows' bytes (q in, out back), nearly matched by the products and
+// exponentials of a row; the next tile's q is loaded ahead. 2097152 rows, 77 keys,
+// 5 heads of 64, bf16: 625 to 645 us by box, 4.2 TB/s (a copy 4.86, and this
+// kernel 4.8 with P in bf16 alone).
 template <typename T, int EP, int NT, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_kernel(AttnP<T> a) {
   extern __shared__ __align__(16) char lds[];
@@ -408,8 +413,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_short_k
 
 // ---- at most 32 rows share a key head, more keys ---------------------------------
 // Bound by the bytes of K and V (8 x 8192 keys, 8 key heads of 128, 4 rows
-// each, bf16: 65 us from memory, 4.1 TB/s; 47 us where the last-level cache
-// holds them). Each wavefront walks 32 keys at a time of its
+// each, bf16: 62 to 66 us from memory by box, 4.1 TB/s; 47 us where the last-level
+// cache holds them). What the mask drops is loaded too: with padding to between
+// half and all of the keys and one empty entry, a third of these bytes. Each wavefront walks 32 keys at a time of its
 // own through its own part of LDS, without barriers, so that wavefronts drift
 // apart and loads stay in flight; the four are joined at the end, and the
 // workgroups of an (entry, key head) by attn_join_kernel.
@@ -568,9 +574,10 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int
   if (Lk <= 128 && (bytes <= 81920 || (bytes <= 163840 && heads * cdiv(rows, 128) < 256))) {
     // Taken where two workgroups fit a compute unit's LDS, or the chip would
     // not be full anyway and splitting the keys would cost a second launch.
-    // us here and through the kernels below: 16384 rows, 16 heads of 64,
-    // 128 keys 23, 33; of 96, 96 keys 29, 33; of 128, 128 keys (one workgroup
-    // per compute unit) 53, 42; 512 rows, 16 heads of 128, 128 keys 11.5, 16.7.
+    // us here and through the kernels below: 262144 rows, 5 heads of 64, 77 keys
+    // 92, 131; 131072 rows, 64 heads of 64, 128 keys 173, 186 (16384 rows 28, 27);
+    // of 96, 96 keys 34, 38; of 128, 64 keys 33, 34, 128 keys (one workgroup per
+    // compute unit) 59, 44; 512 rows, 16 heads of 128, 128 keys 11.7, 11.6.
     // Row tiles of 32; a workgroup's four wavefronts take up to 32 each, so
     // that staging the keys is a small part, but all compute units get some.
     k.plan = AttnPlan::kShort;
@@ -582,8 +589,8 @@ AttnCut cut_attn(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int
     return k;
   }
   if (rows <= 32) {
-    // (8 x 8192 keys, 8 key heads of 128, cached: 4 rows each 47 us here, 96 as
-    // row tiles of 128; 32 rows each 70, 105.)
+    // (8 x 8192 keys, 8 key heads of 128, cached: 4 rows each 48 us here, 62 as
+    // row tiles of 128; 32 rows each 52, 63.)
     // Keys in tiles of 32, four at a time per workgroup. One workgroup per
     // compute unit reads at the memory's rate (64 heads, from memory: 128
     // workgroups 91 us, 256 65, 512 65, 1024 71); a second, shorter round costs

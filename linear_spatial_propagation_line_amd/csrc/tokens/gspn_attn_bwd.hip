@@ -61,9 +61,9 @@ __global__ __launch_bounds__(kThreads) void attn_delta_kernel(BwdP<T> a) {
 
 // ---- dK, dV: 128 keys per workgroup, rows 32 at a time through LDS ----------
 // Four products per tile, S^T and dP^T from the keys' side, then dV and dK. A
-// tile's products wait for its exponentials and for LDS (57 % of the cycles are
-// waits, the matrix units work for a third). 2x4096x2048 with ragged masks, 16
-// heads of 128 on 4, bf16: 386 us.
+// tile's products wait for its exponentials and for LDS (47 % of the cycles are
+// waits, the matrix units work for 44 %). 2x4096x2048 with ragged masks, 16
+// heads of 128 on 4, bf16: 460 us.
 // Results and fragments of K and V are 6 E registers; where that leaves no
 // room for two wavefronts per SIMD the fragments of V stay in LDS (with them
 // in registers the loop spills; training step, 4x2048x1024, 16 heads of 96:
@@ -195,8 +195,8 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(BwdP<T> a) {
 }
 
 // ---- dQ: 128 rows per workgroup, keys 32 at a time through LDS --------------
-// Bound by the products (the matrix units work half of the time): 252 us at the
-// same size, of which the second product of dS takes 24.
+// Bound by the products (the matrix units work half of the time): 250 us at the
+// same size.
 template <typename T, int EP, bool FULL>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(BwdP<T> a) {
   extern __shared__ __align__(16) char lds[];
@@ -295,9 +295,9 @@ struct BwdCut {
 };
 // Row splits of the dK, dV pass: as many as the workgroups that run at once
 // allow, two per compute unit, one for fp32. (2048 rows, 16 heads of 128, bf16,
-// whole training step, us split and whole: 32 groups 77, 195; 128 groups 158,
-// 242; 240 groups in two 255, 299, in three 284. fp32, 1024 rows, 64 groups: in four
-// 278, in eight 293, whole 483.)
+// whole training step, us split and whole: 32 groups 81, 206; 128 groups 166,
+// 257; 240 groups in two 272, 315, in three 303. fp32 of 64, 1024 rows, 64 groups: in
+// four 160, in eight 158, whole 278.)
 BwdCut cut_bwd(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, size_t es) {
   BwdCut k;
   k.key_tiles = static_cast<int>(cdiv(Lk, 128));

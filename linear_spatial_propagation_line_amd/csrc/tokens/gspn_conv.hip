@@ -10,8 +10,9 @@
 // owns V adjacent channels (16 bytes) and walks a run of tokens with the last
 // K - 1 rows in registers, so each row is read once per run plus K - 1 rows
 // of the run before (from L2); the run's rows are all loaded first, which keeps
-// that many 16-byte loads in flight per lane. 8x4096x2304 bf16: 75 us, 4.0 TB/s
-// (a large copy reaches 4.9); a training step 187 to 239 us by box.
+// that many 16-byte loads in flight per lane. 8x4096x2304 bf16: 69 us, 4.4 TB/s
+// (a large copy reaches 4.9), fp32 119 us, 5.1 TB/s; a training step 187 to 239 us
+// by box, fp32 351, where its passes' bytes take 155 and 311 at the copy's rate.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 
@@ -205,7 +206,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvP<T> a) {
 }
 
 // A run computes dpre for its own tokens and the K - 1 after
-// them (which its dx needs too); dw and db take its own tokens only. The
+// them (which its dx needs too); dw and db take its own tokens only. Rows are
+// loaded eight at a time, for the K - 1 too: 24 rows for a run of 16, 72 for one
+// of 64 (3x1021x1153 fp32, runs of 16: 66 MB read where x and grad_out are 28). The
 // partial sums of the workgroup's four runs are joined in LDS, in run order,
 // into row (b, group of runs) of part: [K + 1][C], taps first, then the bias.
 // HANDED: there is a grad_state (a look at every row whether it has one costs

@@ -34,10 +34,12 @@
 // The full pass reads the initial state from a copy that the first pass leaves:
 // its last segment may store the end state over it before others have begun.
 //
-// Measured, bf16, 16 states, 2304 channels: 8192 tokens 173 us (first pass 71,
-// full pass 112, of which the states' own operations need 48); 8 x 2048 training
-// step 982 us (forward 115 + 186, adjoint first pass 125, backward 566, sums of
-// dB and dC 21). Waits for LDS and memory are a third of the wavefronts' cycles.
+// Measured, bf16, 16 states, 2304 channels, a call among calls: 8192 tokens 173
+// us, of which the states' own operations need 48; 8 x 2048 training step 985 us.
+// The profiler, whose launches do not overlap, gives the kernels 192 us together
+// (first pass 72, full pass 115, B and C 5) and 1055 (forward 118 + 190, adjoint
+// first pass 130, backward 582, sums of dB and dC 21, of the parameters 6, B and C
+// twice 5). Waits for LDS and memory are a third of the wavefronts' cycles.
 #include <cmath>
 
 #include "gspn_mfma.hpp"

@@ -8,6 +8,9 @@
  *                         2D one), for whole prompts and for single tokens,
  *   gspn_cross_attention  attention of image or text tokens to an encoder's
  *                         states of another length,
+ *   gspn_token_embedding  the lookup of token ids in a table,
+ *   gspn_gated_recurrence a linear recurrence whose decay and input are gated,
+ *                         one state per channel,
  *
  * each with its backward pass. Conventions are those of gspn.h: arguments are
  * validated on the host before anything is enqueued, work is asynchronous on
@@ -231,6 +234,107 @@ gspn_status gspn_cross_attention_backward_ws(const gspn_attn_args* args,
                                              size_t ws_bytes, hipStream_t stream);
 size_t gspn_cross_attention_backward_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
                                                      int64_t Hkv, int64_t E, gspn_dtype dtype);
+
+/*
+ * gspn_token_embedding -- rows of a table by token id:
+ *   out[b,l] = scale * weight[ids[b,l]].
+ * Ids outside 0 .. V-1 (a padding id, -1) give rows of zeros, as padding does.
+ *   ids                 [B, L], int64 with ids64, else int32; id l of entry b
+ *                       is ids[b * ids_batch + l]
+ *   weight [V, D], out [B, L, D]   in dtype; V, D >= 1; scale finite
+ *                       (GSPN_E_SHAPE)
+ */
+typedef struct {
+  int64_t B, L, V, D;
+  gspn_dtype dtype;
+  int32_t ids64;
+  float scale;
+  const void* ids;
+  int64_t ids_batch;
+  const int32_t* lens;
+  const void* weight;
+  void* out;
+} gspn_embed_args;
+
+gspn_status gspn_token_embedding(const gspn_embed_args* args, hipStream_t stream);
+
+/*
+ * gspn_token_embedding_backward_ws -- the table's gradient [V, D] in dtype,
+ *   weight[v] = scale * sum over the tokens with id v of grad_out,
+ * zeros for rows that no token names. args as for the forward call (weight and
+ * out are not read). Tokens are sorted by id; sums are in fp32, in token order.
+ * Workspace: gspn_token_embedding_backward_workspace_bytes() bytes, 256-byte
+ * aligned.
+ */
+typedef struct {
+  gspn_seq grad_out;
+  void* weight;
+} gspn_embed_grads;
+
+gspn_status gspn_token_embedding_backward_ws(const gspn_embed_args* args,
+                                             const gspn_embed_grads* grads, void* workspace,
+                                             size_t ws_bytes, hipStream_t stream);
+size_t gspn_token_embedding_backward_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                                     gspn_dtype dtype);
+
+/*
+ * gspn_gated_recurrence_ws -- a linear recurrence with gates, one state per
+ * channel. For every entry b and channel c:
+ *   a_t = exp(A[c] sigmoid(r_t)),   h_{-1} = state,
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   out_t = h_t
+ *   x, r, i             [B, L, C] in dtype
+ *   A [C], state and state_out [B, C]   fp32; A <= 0 (a_t is a decay; not
+ *                       checked); state and state_out may be NULL
+ *   out [B, L, C]       in dtype
+ *   saved               NULL, or gspn_gated_recurrence_saved_bytes() bytes,
+ *                       256-byte aligned: receives the states at every 64th
+ *                       token, which the backward pass of the same arguments
+ *                       then takes instead of finding them again
+ * A call with L = 1 and state_out = state is one step of a serving loop.
+ * Workspace: gspn_gated_recurrence_workspace_bytes() bytes, 256-byte aligned
+ * (0 for L <= 64).
+ */
+typedef struct {
+  int64_t B, L, C;
+  gspn_dtype dtype;
+  gspn_seq x, r, i;
+  const float* A;
+  const float* state;
+  const int32_t* lens;
+  void* out;
+  float* state_out;
+  void* saved;
+} gspn_gated_args;
+
+gspn_status gspn_gated_recurrence_ws(const gspn_gated_args* args, void* workspace,
+                                     size_t ws_bytes, hipStream_t stream);
+size_t gspn_gated_recurrence_workspace_bytes(int64_t B, int64_t L, int64_t C, gspn_dtype dtype);
+size_t gspn_gated_recurrence_saved_bytes(int64_t B, int64_t L, int64_t C);
+
+/*
+ * gspn_gated_recurrence_backward_ws -- gradients given grad_out = dL/dout and,
+ * unless NULL, grad_state = dL/dstate_out [B, C] (fp32): of x, r, i [B, L, C]
+ * in dtype, of A [C] and state [B, C] (or NULL) in fp32. Where a_t = 1 the
+ * input has no weight, and the weight's slope, which has no bound there, is
+ * taken as 0. args as for the forward call (out and state_out are not read;
+ * saved is read unless NULL). Sums are in fp32, in a fixed order. Workspace:
+ * gspn_gated_recurrence_backward_workspace_bytes() bytes, 256-byte aligned.
+ */
+typedef struct {
+  gspn_seq grad_out;
+  const float* grad_state;
+  void* x;
+  void* r;
+  void* i;
+  float* A;
+  float* state;
+} gspn_gated_grads;
+
+gspn_status gspn_gated_recurrence_backward_ws(const gspn_gated_args* args,
+                                              const gspn_gated_grads* grads, void* workspace,
+                                              size_t ws_bytes, hipStream_t stream);
+size_t gspn_gated_recurrence_backward_workspace_bytes(int64_t B, int64_t L, int64_t C,
+                                                      gspn_dtype dtype);
 
 #ifdef __cplusplus
 }

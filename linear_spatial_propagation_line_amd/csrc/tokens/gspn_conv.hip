@@ -45,66 +45,6 @@ template <typename T> struct ConvP {
   int silu;
 };
 
-// V values at p, widened
-template <int V, typename T> __device__ __forceinline__ void ldv(const T* p, float* d) {
-  if constexpr (V == 1) {
-    d[0] = to_f32(p[0]);
-  } else if constexpr (V == 4) {
-    const auto q = V4<T>::load(p, 0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) d[e] = V4<T>::get(q, e);
-  } else {
-    run_ld<V>(p, 0, d);
-  }
-}
-template <int V, typename T> __device__ __forceinline__ void stv(T* p, const float* d) {
-  if constexpr (V == 1) Store<T>::put(p, 0, d[0]);
-  else if constexpr (V == 4) V4<T>::store(p, 0, d);
-  else run_st<V>(p, 0, d);
-}
-
-// V values as they lie in memory
-template <typename T, int V> struct Raw {
-  static constexpr int kWords = V * static_cast<int>(sizeof(T)) / 4;
-  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
-  Words q;
-  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const Words*>(p); }
-  __device__ __forceinline__ void wide(float* d) const {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      if constexpr (sizeof(T) == 4) {
-        d[k] = __uint_as_float(q[k]);
-      } else {
-        d[2 * k] = bf16_lo(q[k]);
-        d[2 * k + 1] = bf16_hi(q[k]);
-      }
-    }
-  }
-};
-template <typename T> struct Raw<T, 1> {
-  T q;
-  __device__ __forceinline__ void load(const T* p) { q = *p; }
-  __device__ __forceinline__ void wide(float* d) const { d[0] = to_f32(q); }
-};
-// rows t .. t + N - 1 of a [B, L, C] tensor's entry, clamped to the last of n
-template <int N, typename T, int V>
-__device__ __forceinline__ void load_run(const T* base, int64_t stride, int64_t t, int64_t n, Raw<T, V> (&r)[N]) {
-  const T* p = base + t * stride;
-  if (t + N <= n) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      r[k].load(p);
-      p += stride;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      r[k].load(p);
-      p += t + k + 1 < n ? stride : 0;
-    }
-  }
-}
-
 // taps and bias of V channels; V > 1: whole pieces, taps of a channel adjacent
 template <int K, int V, typename T>
 __device__ __forceinline__ void load_taps(const T* w, const T* bias, int64_t c, float (&tap)[K][V], float (&b)[V]) {

@@ -233,6 +233,38 @@ void attn_inputs(Check& k, const gspn_attn_args& a) {
   k.view(a.mask, 1, {a.B, a.Lk}, {a.mask_batch}, false);
 }
 
+// ---- embedding --------------------------------------------------------------
+void embed_shape(Check& k, int64_t B, int64_t L, int64_t V, int64_t D, gspn_dtype dt) {
+  if (!dtype_ok(dt)) k.bad(GSPN_E_DTYPE, "dtype must be GSPN_F32 or GSPN_BF16");
+  else if (B < 0 || L < 0 || V < 1 || D < 1) k.bad(GSPN_E_SHAPE, "need B, L >= 0 and V, D >= 1");
+  else if (V >= k31 - 2048 || D >= k31 - 2048 || k.product({B, L}) >= k31 - 2048)
+    k.bad(GSPN_E_SHAPE, "dimension too large (V, D and B * L must stay below 2^31)");
+  else if (k.product({B, L, D}) >= (int64_t(1) << 52) || k.product({V, D}) >= (int64_t(1) << 52))
+    k.bad(GSPN_E_SHAPE, "tensor too large");
+}
+void embed_inputs(Check& k, const gspn_embed_args& a) {
+  if (k.ok() && !std::isfinite(a.scale)) k.bad(GSPN_E_SHAPE, "scale must be finite");
+  k.view(a.ids, a.ids64 ? 8 : 4, {a.B, a.L}, {a.ids_batch});
+  k.input(a.lens, a.B, 4, false);
+}
+
+// ---- gated recurrence -------------------------------------------------------
+void gated_shape(Check& k, int64_t B, int64_t L, int64_t C, gspn_dtype dt) {
+  if (!dtype_ok(dt)) k.bad(GSPN_E_DTYPE, "dtype must be GSPN_F32 or GSPN_BF16");
+  else if (B < 0 || L < 0 || C < 0) k.bad(GSPN_E_SHAPE, "need B, L, C >= 0");
+  else if (B >= k31 || L >= k31 || C >= k31 / 64) k.bad(GSPN_E_SHAPE, "dimension too large");
+  else if (k.product({B, L + 64, C + 128}) >= (int64_t(1) << 52)) k.bad(GSPN_E_SHAPE, "tensor too large");
+}
+void gated_inputs(Check& k, const gspn_gated_args& a) {
+  const size_t es = esize(a.dtype);
+  k.view(a.x.p, es, {a.B, a.L, a.C}, {a.x.batch, a.x.row});
+  k.view(a.r.p, es, {a.B, a.L, a.C}, {a.r.batch, a.r.row});
+  k.view(a.i.p, es, {a.B, a.L, a.C}, {a.i.batch, a.i.row});
+  k.input(a.A, a.C, 4);
+  k.state(a.state, a.B * a.C, 4);
+  k.input(a.lens, a.B, 4, false);
+}
+
 }  // namespace
 
 extern "C" {
@@ -440,6 +472,135 @@ size_t gspn_cross_attention_backward_workspace_bytes(int64_t B, int64_t Lq, int6
     Check k;
     attn_shape(k, B, Lq, Lk, Hq, Hkv, E, dtype);
     if (k.ok()) need = gspn::attn_bwd_workspace_bytes(B, Lq, Lk, Hq, Hkv, E);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+gspn_status gspn_token_embedding(const gspn_embed_args* a, hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a) return set_error(GSPN_E_NULL, "args must be non-null");
+    Check k;
+    embed_shape(k, a->B, a->L, a->V, a->D, a->dtype);
+    if (!k.ok()) return k.status;
+    const size_t es = esize(a->dtype);
+    const int64_t tokens = a->B * a->L;
+    embed_inputs(k, *a);
+    k.input(a->weight, a->V * a->D, es, tokens > 0);
+    k.output(a->out, tokens * a->D, es);
+    k.aliases();
+    if (!k.ok()) return k.status;
+    if (tokens == 0) return GSPN_OK;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_embed(*a, stream, tr); });
+  });
+}
+
+size_t gspn_token_embedding_backward_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                                     gspn_dtype dtype) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    embed_shape(k, B, L, V, D, dtype);
+    if (k.ok()) need = gspn::embed_bwd_workspace_bytes(B, L, V, D);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+gspn_status gspn_token_embedding_backward_ws(const gspn_embed_args* a, const gspn_embed_grads* g,
+                                             void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a || !g) return set_error(GSPN_E_NULL, "args and grads must be non-null");
+    Check k;
+    embed_shape(k, a->B, a->L, a->V, a->D, a->dtype);
+    if (!k.ok()) return k.status;
+    const size_t es = esize(a->dtype);
+    embed_inputs(k, *a);
+    k.view(g->grad_out.p, es, {a->B, a->L, a->D}, {g->grad_out.batch, g->grad_out.row});
+    k.output(g->weight, a->V * a->D, es);
+    k.aliases();
+    k.scratch(ws, ws_bytes, k.ok() ? gspn::embed_bwd_workspace_bytes(a->B, a->L, a->V, a->D) : 0);
+    if (!k.ok()) return k.status;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_embed_bwd(*a, *g, ws, stream, tr); });
+  });
+}
+
+gspn_status gspn_gated_recurrence_ws(const gspn_gated_args* a, void* ws, size_t ws_bytes,
+                                     hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a) return set_error(GSPN_E_NULL, "args must be non-null");
+    Check k;
+    gated_shape(k, a->B, a->L, a->C, a->dtype);
+    if (!k.ok()) return k.status;
+    gated_inputs(k, *a);
+    k.output(a->out, a->B * a->L * a->C, esize(a->dtype));
+    k.update(a->state_out, a->B * a->C, 4);
+    check_saved(k, a->saved);
+    k.output(a->saved, static_cast<int64_t>(gspn::gated_saved_bytes(a->B, a->L, a->C)), 1, false);
+    k.aliases();
+    k.scratch(ws, ws_bytes, k.ok() ? gspn::gated_workspace_bytes(a->B, a->L, a->C) : 0);
+    if (!k.ok()) return k.status;
+    if (a->B == 0 || a->C == 0) return GSPN_OK;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_gated(*a, ws, stream, tr); });
+  });
+}
+
+size_t gspn_gated_recurrence_workspace_bytes(int64_t B, int64_t L, int64_t C, gspn_dtype dtype) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    gated_shape(k, B, L, C, dtype);
+    if (k.ok()) need = gspn::gated_workspace_bytes(B, L, C);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+size_t gspn_gated_recurrence_saved_bytes(int64_t B, int64_t L, int64_t C) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    gated_shape(k, B, L, C, GSPN_F32);
+    if (k.ok()) need = gspn::gated_saved_bytes(B, L, C);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+gspn_status gspn_gated_recurrence_backward_ws(const gspn_gated_args* a, const gspn_gated_grads* g,
+                                              void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a || !g) return set_error(GSPN_E_NULL, "args and grads must be non-null");
+    Check k;
+    gated_shape(k, a->B, a->L, a->C, a->dtype);
+    if (!k.ok()) return k.status;
+    const size_t es = esize(a->dtype);
+    const int64_t rows = a->B * a->L * a->C;
+    gated_inputs(k, *a);
+    check_saved(k, a->saved);
+    k.input(a->saved, static_cast<int64_t>(gspn::gated_saved_bytes(a->B, a->L, a->C)), 1, false);
+    k.view(g->grad_out.p, es, {a->B, a->L, a->C}, {g->grad_out.batch, g->grad_out.row});
+    k.input(g->grad_state, a->B * a->C, 4, false);
+    k.output(g->x, rows, es);
+    k.output(g->r, rows, es);
+    k.output(g->i, rows, es);
+    k.output(g->A, a->C, 4);
+    k.output(g->state, a->B * a->C, 4, false);
+    k.aliases();
+    k.scratch(ws, ws_bytes, k.ok() ? gspn::gated_bwd_workspace_bytes(a->B, a->L, a->C) : 0);
+    if (!k.ok()) return k.status;
+    if (a->C == 0) return GSPN_OK;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_gated_bwd(*a, *g, ws, stream, tr); });
+  });
+}
+
+size_t gspn_gated_recurrence_backward_workspace_bytes(int64_t B, int64_t L, int64_t C,
+                                                      gspn_dtype dtype) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    gated_shape(k, B, L, C, dtype);
+    if (k.ok()) need = gspn::gated_bwd_workspace_bytes(B, L, C);
     return GSPN_OK;
   });
   return need;

@@ -35,6 +35,31 @@ size_t attn_bwd_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, i
 hipError_t launch_attn_bwd(const gspn_attn_args& a, const gspn_attn_grads& g, void* ws,
                            hipStream_t stream, Tracer* tr);
 
+size_t embed_bwd_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D);
+hipError_t launch_embed(const gspn_embed_args& a, hipStream_t stream, Tracer* tr);
+hipError_t launch_embed_bwd(const gspn_embed_args& a, const gspn_embed_grads& g, void* ws,
+                            hipStream_t stream, Tracer* tr);
+
+// Tokens sorted by their row of a table of V rows, in token order within a row:
+// row v owns places start[v] .. start[v + 1] - 1 (start [V + 1]); token and row
+// hold each place's token and its row. Padding and ids outside the table are
+// left out. ws: token_sort_bytes() bytes (gspn_embed.hip)
+struct TokenSort {
+  const int32_t* start;
+  const int32_t* token;
+  const int32_t* row;
+};
+size_t token_sort_bytes(int64_t tokens, int64_t V);
+hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int32_t* lens, int64_t B,
+                       int64_t L, int64_t V, void* ws, TokenSort* out, hipStream_t stream, Tracer* tr);
+
+size_t gated_saved_bytes(int64_t B, int64_t L, int64_t C);
+size_t gated_workspace_bytes(int64_t B, int64_t L, int64_t C);
+hipError_t launch_gated(const gspn_gated_args& a, void* ws, hipStream_t stream, Tracer* tr);
+size_t gated_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C);
+hipError_t launch_gated_bwd(const gspn_gated_args& a, const gspn_gated_grads& g, void* ws,
+                            hipStream_t stream, Tracer* tr);
+
 // Up to three tables of fp32 partial sums, [rows][cols] each, summed over
 // their rows into fp32 results, in row order within each of eight interleaved
 // row sets whose sums are then added in order; rows = 0 writes zeros, a table
@@ -49,7 +74,7 @@ struct RowSums {
 hipError_t reduce_rows(const RowSums& s, hipStream_t stream, Tracer* tr);
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // A launch takes fewer than 2^32 threads; what is above is cut off without an
 // error. Where the host checks admit more workgroups than that, they go out in
@@ -79,6 +104,83 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T> __device__ __forceinline__ float ld1(const T* p) { return to_f32(*p); }
+
+// V values at p, widened
+template <int V, typename T> __device__ __forceinline__ void ldv(const T* p, float* d) {
+  if constexpr (V == 1) {
+    d[0] = to_f32(p[0]);
+  } else if constexpr (V == 2) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t q = *reinterpret_cast<const uint32_t*>(p);
+      d[0] = bf16_lo(q);
+      d[1] = bf16_hi(q);
+    } else {
+      const float2 q = *reinterpret_cast<const float2*>(p);
+      d[0] = q.x;
+      d[1] = q.y;
+    }
+  } else if constexpr (V == 4) {
+    const auto q = V4<T>::load(p, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = V4<T>::get(q, e);
+  } else {
+    run_ld<V>(p, 0, d);
+  }
+}
+template <int V, typename T> __device__ __forceinline__ void stv(T* p, const float* d) {
+  if constexpr (V == 1) {
+    Store<T>::put(p, 0, d[0]);
+  } else if constexpr (V == 2) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(d[0], d[1]);
+    else *reinterpret_cast<float2*>(p) = make_float2(d[0], d[1]);
+  } else if constexpr (V == 4) {
+    V4<T>::store(p, 0, d);
+  } else {
+    run_st<V>(p, 0, d);
+  }
+}
+
+// V values as they lie in memory
+template <typename T, int V> struct Raw {
+  static constexpr int kWords = V * static_cast<int>(sizeof(T)) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  Words q;
+  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const Words*>(p); }
+  __device__ __forceinline__ void wide(float* d) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        d[k] = __uint_as_float(q[k]);
+      } else {
+        d[2 * k] = bf16_lo(q[k]);
+        d[2 * k + 1] = bf16_hi(q[k]);
+      }
+    }
+  }
+};
+template <typename T> struct Raw<T, 1> {
+  T q;
+  __device__ __forceinline__ void load(const T* p) { q = *p; }
+  __device__ __forceinline__ void wide(float* d) const { d[0] = to_f32(q); }
+};
+// rows t .. t + N - 1 of a [B, L, C] tensor's entry, clamped to the last of n
+template <int N, typename T, int V>
+__device__ __forceinline__ void load_run(const T* base, int64_t stride, int64_t t, int64_t n, Raw<T, V> (&r)[N]) {
+  const T* p = base + t * stride;
+  if (t + N <= n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(p);
+      p += stride;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(p);
+      p += t + k + 1 < n ? stride : 0;
+    }
+  }
+}
 
 // sigmoid(v) = (v < 0 ? e : 1) / (1 + e), e = exp(-|v|) in [0, 1]: nothing
 // overflows, and far below zero it is 0, so that v sigmoid(v) is 0 also at the

@@ -1,6 +1,7 @@
 """The token-sequence operators of ``libgspn.so`` (include/gspn_tokens.h):
 the short causal convolution and the selective scan of a state space block,
-and cross attention to an encoder's states, each with its gradients.
+cross attention to an encoder's states, the token embedding and the gated
+linear recurrence, each with its gradients.
 
 Like the rest of the binding this module only checks and marshals arguments.
 Tensors are token-major device tensors of float32 or bfloat16, the last
@@ -25,6 +26,11 @@ _SCAN = struct.Struct("@5qii PqqPqqPqq P PqqqPqqq PPPP PPP".replace(" ", ""))
 _SCAN_GRADS = struct.Struct("@PqqPPPPPPPPPP")
 _ATTN = struct.Struct("@6qif PqqqPqqqPqqq Pq PP".replace(" ", ""))
 _ATTN_GRADS = struct.Struct("@PqqqPPP")
+
+_EMBED = struct.Struct("@4qiifPqPPP")
+_EMBED_GRADS = struct.Struct("@PqqP")
+_GATED = struct.Struct("@3qi PqqPqqPqq PPPPPP".replace(" ", ""))
+_GATED_GRADS = struct.Struct("@PqqPPPPPP")
 
 _Tensor = torch.Tensor
 # the current stream's handle and the current device, without the objects
@@ -54,7 +60,15 @@ def _lib():
                 ("gspn_cross_attention_ws", [a, vp, sz, vp], ctypes.c_int),
                 ("gspn_cross_attention_workspace_bytes", [i64] * 6 + [ctypes.c_int], sz),
                 ("gspn_cross_attention_backward_ws", [a, a, vp, sz, vp], ctypes.c_int),
-                ("gspn_cross_attention_backward_workspace_bytes", [i64] * 6 + [ctypes.c_int], sz)):
+                ("gspn_cross_attention_backward_workspace_bytes", [i64] * 6 + [ctypes.c_int], sz),
+                ("gspn_token_embedding", [a, vp], ctypes.c_int),
+                ("gspn_token_embedding_backward_ws", [a, a, vp, sz, vp], ctypes.c_int),
+                ("gspn_token_embedding_backward_workspace_bytes", [i64] * 4 + [ctypes.c_int], sz),
+                ("gspn_gated_recurrence_ws", [a, vp, sz, vp], ctypes.c_int),
+                ("gspn_gated_recurrence_workspace_bytes", [i64] * 3 + [ctypes.c_int], sz),
+                ("gspn_gated_recurrence_saved_bytes", [i64] * 3, sz),
+                ("gspn_gated_recurrence_backward_ws", [a, a, vp, sz, vp], ctypes.c_int),
+                ("gspn_gated_recurrence_backward_workspace_bytes", [i64] * 3 + [ctypes.c_int], sz)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
         _tok = L
@@ -101,6 +115,18 @@ class _Call:
         if s[-1] != 1 and shape[-1] > 1:
             raise ValueError(f"{what} must be contiguous in its last dimension")
         return (t.data_ptr(),) + s[:-1]
+
+    def ids(self, t, shape, what):
+        """(address, entry stride, 1 for int64) of token ids."""
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
+            raise TypeError(f"{what} must be a torch tensor on {self.device}")
+        if t.dtype not in (torch.int64, torch.int32):
+            raise ValueError(f"{what} must be int64 or int32, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.stride(1) != 1 and shape[1] > 1:
+            raise ValueError(f"{what} must be contiguous in its last dimension")
+        return t.data_ptr(), t.stride(0), int(t.dtype is torch.int64)
 
     def data(self, t, shape, what, dtype=None):
         """Address of a contiguous input, 0 for None."""
@@ -368,4 +394,121 @@ def cross_attention_backward(q, k, v, out, lse, grad_out, mask=None, scale=None,
     L_ = _lib()
     ws, wp, wn = c.workspace(workspace, L_.gspn_cross_attention_backward_workspace_bytes(*sizes, c.code))
     c.run(L_.gspn_cross_attention_backward_ws, args, packed, wp, wn)
+    return g
+
+
+# --------------------------------------------------------------------------
+# token embedding
+# --------------------------------------------------------------------------
+def _shape2(ids, what):
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError(f"{what} must be a [B, L] tensor")
+    return tuple(ids.shape)
+
+
+def _embed_args(c, ids, B, L, V, D, scale, lens, weight, out):
+    ip, ib, wide = c.ids(ids, (B, L), "ids")
+    return _EMBED.pack(B, L, V, D, c.code, wide, float(scale), ip, ib,
+                       c.data(lens, (B,), "lens", torch.int32), weight, out)
+
+
+def token_embedding(ids, weight, scale: float = 1.0, lens=None, out=None, stream=None):
+    """out[b, l] = scale * weight[ids[b, l]]: [B, L, D] for ``ids`` [B, L]
+    (int64 or int32) and ``weight`` [V, D]. Ids outside 0 .. V - 1 give zeros,
+    as do tokens past an entry's length (``lens``, int32 [B])."""
+    B, L = _shape2(ids, "ids")
+    c = _Call(weight, "weight", stream)
+    if weight.dim() != 2:
+        raise ValueError("weight must be a [V, D] tensor")
+    V, D = weight.shape
+    out = c.out(out, (B, L, D), "out")
+    args = _embed_args(c, ids, B, L, V, D, scale, lens, c.data(weight, (V, D), "weight"), out.data_ptr())
+    c.run(_lib().gspn_token_embedding, args)
+    return out
+
+
+def token_embedding_backward(ids, grad_out, vocab: int, scale: float = 1.0, lens=None, grads=None,
+                             workspace=None, stream=None) -> dict:
+    """Gradient of token_embedding() given ``grad_out`` = dL/dout [B, L, D]: a
+    dict with "weight" [vocab, D] (``grads`` may supply it), zeros in rows that
+    no token names. Sums are in float32, in token order."""
+    B, L = _shape2(ids, "ids")
+    c = _Call(grad_out, "grad_out", stream)
+    D = _shape3(grad_out, "grad_out")[2]
+    V = int(vocab)
+    view = c.view(grad_out, (B, L, D), "grad_out")
+    args = _embed_args(c, ids, B, L, V, D, scale, lens, 0, 0)
+    L_ = _lib()
+    need = L_.gspn_token_embedding_backward_workspace_bytes(B, L, V, D, c.code)
+    g = {"weight": c.out(None if grads is None else grads["weight"], (max(V, 0), D), "grads['weight']")}
+    ws, wp, wn = c.workspace(workspace, need)
+    c.run(L_.gspn_token_embedding_backward_ws, args, _EMBED_GRADS.pack(*view, g["weight"].data_ptr()), wp, wn)
+    return g
+
+
+# --------------------------------------------------------------------------
+# gated recurrence
+# --------------------------------------------------------------------------
+def _gated_args(c, shape, x, r, i, A, state, lens, out, state_out, saved):
+    B, L, C = shape
+    f32 = torch.float32
+    if saved is not None:
+        need = _lib().gspn_gated_recurrence_saved_bytes(B, L, C)
+        c.tensor(saved, (need,), "saved", torch.uint8, True)
+    return _GATED.pack(B, L, C, c.code, *c.view(x, shape, "x"), *c.view(r, shape, "r"), *c.view(i, shape, "i"),
+                       c.data(A, (C,), "A", f32), c.data(state, (B, C), "state", f32),
+                       c.data(lens, (B,), "lens", torch.int32), 0 if out is None else out.data_ptr(),
+                       c.data(state_out, (B, C), "state_out", f32), 0 if saved is None else saved.data_ptr())
+
+
+def gated_recurrence_saved(x, stream=None):
+    """An uninitialised buffer for gated_recurrence()'s ``saved``."""
+    need = _lib().gspn_gated_recurrence_saved_bytes(*_shape3(x, "x"))
+    return _Call(x, "x", stream).empty((need,), torch.uint8)
+
+
+def gated_recurrence(x, r, i, A, state=None, lens=None, out=None, state_out=None, saved=None,
+                     workspace=None, stream=None):
+    """A linear recurrence with one state per channel, its decay and its input
+    gated:
+        a_t = exp(A sigmoid(r_t)),
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,  out_t = h_t.
+    ``x``, ``r``, ``i`` [B, L, C]; ``A`` [C] (<= 0), ``state`` and ``state_out``
+    [B, C] in float32. ``lens`` int32 [B]: tokens past an entry's length are
+    padding (out = 0, the state stays). ``state_out`` may be ``state`` itself:
+    with L = 1 that is one step of a serving loop. ``saved``
+    (gated_recurrence_saved()) keeps what the backward pass of the same
+    arguments needs."""
+    shape = _shape3(x, "x")
+    c = _Call(x, "x", stream)
+    out = c.out(out, shape, "out")
+    args = _gated_args(c, shape, x, r, i, A, state, lens, out, state_out, saved)
+    L_ = _lib()
+    ws, wp, wn = c.workspace(workspace, L_.gspn_gated_recurrence_workspace_bytes(*shape, c.code))
+    c.run(L_.gspn_gated_recurrence_ws, args, wp, wn)
+    return out
+
+
+def gated_recurrence_backward(x, r, i, A, grad_out, state=None, lens=None, grad_state=None, saved=None,
+                              grads=None, workspace=None, stream=None) -> dict:
+    """Gradients of gated_recurrence() given ``grad_out`` = dL/dout [B, L, C]
+    and optionally ``grad_state`` = dL/dstate_out: a dict with "x", "r", "i",
+    "A" and "state" (when there is one), shaped and typed like the inputs
+    (``grads`` may supply them). ``saved`` is what the forward call of the same
+    arguments kept; without it the states are found again."""
+    shape = _shape3(x, "x")
+    B, L, C = shape
+    c = _Call(x, "x", stream)
+    args = _gated_args(c, shape, x, r, i, A, state, lens, None, None, saved)
+    f32 = torch.float32
+    want = {"x": (shape, None), "r": (shape, None), "i": (shape, None), "A": ((C,), f32)}
+    if state is not None:
+        want["state"] = ((B, C), f32)
+    g = {k: c.out(None if grads is None else grads[k], s, f"grads[{k!r}]", d) for k, (s, d) in want.items()}
+    packed = _GATED_GRADS.pack(*c.view(grad_out, shape, "grad_out"),
+                               c.data(grad_state, (B, C), "grad_state", f32),
+                               *(g[k].data_ptr() if k in g else 0 for k in ("x", "r", "i", "A", "state")))
+    L_ = _lib()
+    ws, wp, wn = c.workspace(workspace, L_.gspn_gated_recurrence_backward_workspace_bytes(*shape, c.code))
+    c.run(L_.gspn_gated_recurrence_backward_ws, args, packed, wp, wn)
     return g

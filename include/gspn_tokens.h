@@ -11,6 +11,8 @@
  *   gspn_token_embedding  the lookup of token ids in a table,
  *   gspn_gated_recurrence a linear recurrence whose decay and input are gated,
  *                         one state per channel,
+ *   gspn_vocab_loss       softmax cross entropy over a vocabulary, from hidden
+ *                         states and the vocabulary's weights,
  *
  * each with its backward pass. Conventions are those of gspn.h: arguments are
  * validated on the host before anything is enqueued, work is asynchronous on
@@ -335,6 +337,61 @@ gspn_status gspn_gated_recurrence_backward_ws(const gspn_gated_args* args,
                                               size_t ws_bytes, hipStream_t stream);
 size_t gspn_gated_recurrence_backward_workspace_bytes(int64_t B, int64_t L, int64_t C,
                                                       gspn_dtype dtype);
+
+/*
+ * gspn_vocab_loss_ws -- softmax cross entropy of hidden states over a
+ * vocabulary, without the logits in memory. For every token, with
+ * z_v = x . weight[v]:
+ *   lse = log sum_v exp(z_v),   loss = lse - z_target
+ * A token whose target lies outside 0 .. V-1 (-100, say) has loss 0 and no
+ * gradient; padding has loss 0 and lse 0 as well.
+ *   x [B, L, D], weight [V, D]   in dtype; V, D >= 1. Where D values are whole
+ *                       pieces of 16 bytes, weight has to begin on one
+ *                       (GSPN_E_ALIGN)
+ *   targets [B, L], int64 with targets64, else int32; target l of entry b is
+ *                       targets[b * targets_batch + l]
+ *   loss, lse [B, L] fp32; lse may be NULL
+ * Products run on matrix cores with fp32 accumulation. Workspace:
+ * gspn_vocab_loss_workspace_bytes() bytes, 256-byte aligned.
+ */
+typedef struct {
+  int64_t B, L, V, D;
+  gspn_dtype dtype;
+  int32_t targets64;
+  gspn_seq x;
+  const void* weight;
+  const void* targets;
+  int64_t targets_batch;
+  const int32_t* lens;
+  float* loss;
+  float* lse;
+} gspn_loss_args;
+
+gspn_status gspn_vocab_loss_ws(const gspn_loss_args* args, void* workspace, size_t ws_bytes,
+                               hipStream_t stream);
+size_t gspn_vocab_loss_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                       gspn_dtype dtype);
+
+/*
+ * gspn_vocab_loss_backward_ws -- gradients of x [B, L, D] and weight [V, D]
+ * (in dtype) given grad_loss = dL/dloss [B, L] (fp32) and the forward call's
+ * lse. args as for the forward call (loss and lse of args are not touched).
+ * The logits are found again, in pieces of the vocabulary; with bf16 storage
+ * their gradients are operands in bf16, those at the targets in fp32. Sums are
+ * in fp32, in a fixed order. Workspace:
+ * gspn_vocab_loss_backward_workspace_bytes() bytes, 256-byte aligned.
+ */
+typedef struct {
+  const float* lse;
+  const float* grad_loss;
+  void* x;
+  void* weight;
+} gspn_loss_grads;
+
+gspn_status gspn_vocab_loss_backward_ws(const gspn_loss_args* args, const gspn_loss_grads* grads,
+                                        void* workspace, size_t ws_bytes, hipStream_t stream);
+size_t gspn_vocab_loss_backward_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                                gspn_dtype dtype);
 
 #ifdef __cplusplus
 }

@@ -545,7 +545,8 @@ def propagate_backward(x, logits, lam, u, grad_out, dirs: int = ALL, group_rows:
 _TOKENS = ("causal_conv", "causal_conv_backward", "selective_scan", "selective_scan_saved",
            "selective_scan_backward", "cross_attention", "cross_attention_backward",
            "token_embedding", "token_embedding_backward", "gated_recurrence",
-           "gated_recurrence_saved", "gated_recurrence_backward")
+           "gated_recurrence_saved", "gated_recurrence_backward", "vocab_loss",
+           "vocab_loss_backward")
 
 
 def __getattr__(name):

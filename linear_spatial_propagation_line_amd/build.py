@@ -23,7 +23,7 @@ SOURCES = ["gspn_api.cpp", "gspn_plane.hip", "gspn_stream.hip", "gspn_tpipe.hip"
            "gspn_calib.hip", "gspn_fused.hip", "gspn_strip.hip",
            "tokens/gspn_tok_api.cpp", "tokens/gspn_conv.hip", "tokens/gspn_scan.hip",
            "tokens/gspn_attn.hip", "tokens/gspn_attn_bwd.hip", "tokens/gspn_embed.hip",
-           "tokens/gspn_gated.hip"]
+           "tokens/gspn_gated.hip", "tokens/gspn_loss.hip"]
 ARCH = os.environ.get("GSPN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -57,18 +57,6 @@ template <typename T> struct GatedP {
   int64_t block0;
 };
 
-// exp(v) - 1: the series where it keeps more digits than the difference
-// (relative error 2e-9 at 1/4)
-__device__ __forceinline__ float expm1_f32(float v) {
-  float p = __builtin_fmaf(v, 1.0f / 5040.0f, 1.0f / 720.0f);
-  p = __builtin_fmaf(v, p, 1.0f / 120.0f);
-  p = __builtin_fmaf(v, p, 1.0f / 24.0f);
-  p = __builtin_fmaf(v, p, 1.0f / 6.0f);
-  p = __builtin_fmaf(v, p, 0.5f);
-  p = __builtin_fmaf(v, p, 1.0f) * v;
-  const float d = __builtin_amdgcn_exp2f(v * kLog2e) - 1.0f;
-  return fabsf(v) < 0.25f ? p : d;
-}
 // 1 / (1 + exp(-v)); the exponential may be infinite, the result is then 0
 __device__ __forceinline__ float gate_f32(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));

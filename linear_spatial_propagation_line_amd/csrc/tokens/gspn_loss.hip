@@ -1,0 +1,711 @@
+// Softmax cross entropy of hidden states over a vocabulary, and its gradients,
+// without the logits in memory.
+//
+//   z = x W^T,  lse = log sum_v exp(z_v),  loss = lse - z_target
+//   G = g (softmax(z) - onehot(target)),  dx = G W,  dW = G^T x
+//
+// Bound by matrix products: 2 T V D operations forward, 6 T V D backward (the
+// logits are found again). Forward: each tile of logits, 256 vocabulary rows by
+// 256 tokens, leaves its maximum and sum of every token, which a last kernel
+// joins. Backward, in pieces of the vocabulary: G of the piece goes to the
+// workspace, then one launch takes dW of the piece (complete) and the piece's
+// part of dx.
+//
+// Tokens that count are first packed into whole rows (padding, strides and
+// widths that are no multiple of a stage end there).
+//
+// G is an operand, in bf16 for bf16 storage. Its entries at the targets, g (p - 1),
+// are most of its norm, and their rounding would add to a gradient as much as
+// the result's own (0.0023 from 64 bits in the norm for 0.00166). So they are 0
+// in the operand; they are found apart, one fp32 value per token, and their
+// products with W's rows and x's are added to dx and dW in fp32. The other
+// entries' rounding is small beside that and independent.
+#include "gspn_loss_gemm.hpp"
+
+namespace gspn {
+
+namespace {
+
+constexpr int kTile = 256;       // tokens, vocabulary rows and columns of a tile
+constexpr int kFewTile = 64;     // tokens of a tile where there are few
+constexpr int kFewRows = 128;    // vocabulary rows of a tile then
+
+template <typename T> constexpr int k_step() { return 128 / static_cast<int>(sizeof(T)); }
+
+// Tokens that count, in order. pos >= count: target -1, g 0, lse 0
+struct TokenList {
+  int32_t* count;
+  int32_t* token;    // [Tp]
+  int32_t* target;   // [Tp]
+  float* g;          // [Tp] backward: the loss's gradient
+  float* lse;        // [Tp]
+  float* at;         // [Tp] forward: the target's logit; backward: G there
+  int32_t* pos;      // [T] backward: the token's place, -1 without
+};
+
+template <typename T> struct LossP {
+  TokenList list;
+  const T* x; int64_t xb, xr;
+  const T* weight;
+  const void* targets; int64_t targets_batch; int64_t targets64;
+  const int32_t* lens;
+  float* loss; float* lse;
+  const float* glse; const float* gloss;
+  T* packed;           // [Tp][Dp]
+  const T* w;          // the weight, or its packed copy
+  int64_t wld;
+  float2* part;        // [tiles of V][Tp]: maximum and sum
+  int64_t L, V, D, T_, Tp, Dp;
+  int64_t block0;
+};
+
+// ---- tokens -----------------------------------------------------------------
+// One workgroup: the tokens that count in their order. Forward all but the
+// padding (whose results are set to 0 here), backward those with a target.
+template <typename P, bool BACK>
+__global__ __launch_bounds__(1024) void loss_list_kernel(P a) {
+  __shared__ int32_t sums[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t done = 0;
+  for (int64_t t0 = 0; t0 < a.T_; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    bool keep = false;
+    int64_t target = -1;
+    if (t < a.T_) {
+      const int64_t b = t / a.L, l = t - b * a.L;
+      keep = l < seq_len(a.lens, b, a.L);
+      if (keep) {
+        const int64_t i = b * a.targets_batch + l;
+        target = a.targets64 ? static_cast<const int64_t*>(a.targets)[i] : static_cast<const int32_t*>(a.targets)[i];
+        if (target < 0 || target >= a.V) target = -1;
+        if (BACK) keep = target >= 0;
+      }
+    }
+    const uint64_t mask = __ballot(keep);
+    if (lane == 0) sums[wave] = __popcll(mask);
+    __syncthreads();
+    int32_t before = done, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? sums[w] : 0;
+      all += sums[w];
+    }
+    const int32_t at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
+    done += all;
+    if (keep) {
+      a.list.token[at] = static_cast<int32_t>(t);
+      a.list.target[at] = static_cast<int32_t>(target);
+      if constexpr (BACK) {
+        a.list.g[at] = a.gloss[t];
+        a.list.lse[at] = a.glse[t];
+      }
+    } else if (t < a.T_) {
+      if constexpr (!BACK) {
+        a.loss[t] = 0.0f;
+        if (a.lse) a.lse[t] = 0.0f;
+      }
+    }
+    if constexpr (BACK)
+      if (t < a.T_) a.list.pos[t] = keep ? at : -1;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *a.list.count = done;
+  for (int64_t p = done + threadIdx.x; p < a.Tp; p += 1024) {
+    a.list.token[p] = -1;
+    a.list.target[p] = -1;
+    if constexpr (BACK) {
+      a.list.g[p] = 0.0f;
+      a.list.lse[p] = 0.0f;
+      a.list.at[p] = 0.0f;
+    }
+  }
+}
+
+// Rows packed to Dp values, 16 bytes per lane, zeros past D and for places
+// without a token. `list` null: rows as they come (the weight).
+template <typename T>
+__global__ __launch_bounds__(256) void loss_pack_kernel(const T* x, int64_t xb, int64_t xr, int64_t L, int64_t D,
+                                                        int64_t Dp, int64_t rows, const int32_t* token,
+                                                        const int32_t* count, T* out, int wide, int64_t block0) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int64_t per = Dp / kPer, i = (block0 + blockIdx.x) * 256 + threadIdx.x;
+  const int64_t p = i / per, at = (i - p * per) * kPer;
+  if (p >= rows) return;
+  const T* src = x + p * xr;
+  bool some = true;
+  if (token) {
+    const int64_t all = *count;
+    if (p >= (all + kTile - 1) / kTile * kTile) return;
+    some = p < all;
+    const int64_t t = some ? token[p] : 0, b = some ? t / L : 0;
+    src = x + b * xb + (t - b * L) * xr;
+  }
+  *reinterpret_cast<u32x4*>(out + p * Dp + at) =
+      load16<T, false>(src, static_cast<int>(at), some ? static_cast<int>(D) : 0, wide);
+}
+
+// ---- forward ----------------------------------------------------------------
+// Tiles of vocabulary rows by tokens, dealt to the eight XCDs in contiguous
+// shares (each has its own L2), within a share 8 row tiles by as many token
+// tiles as run at once.
+struct TilePlace {
+  int64_t m, n;
+};
+__device__ __forceinline__ TilePlace tile_place(int64_t g, int64_t mt, int64_t nt) {
+  const int64_t all = mt * nt, per = (all + 7) / 8;
+  int64_t o = (g & 7) * per + (g >> 3);
+  if ((g >> 3) >= per || o >= all) return TilePlace{-1, 0};
+  const int64_t band = o / (8 * nt), in = o - band * 8 * nt;
+  const int64_t high = mt - band * 8 < 8 ? mt - band * 8 : 8;
+  return TilePlace{band * 8 + in % high, in / high};
+}
+int64_t tile_blocks(int64_t mt, int64_t nt) { return cdiv(mt * nt, 8) * 8; }
+
+template <typename T, int BM, int BN, int WM>
+__global__ __launch_bounds__(512) void loss_logits_kernel(LossP<T> a, int64_t mt, int64_t nt) {
+  using P = Product<T, true, true, BM, BN, WM>;
+  __shared__ __align__(16) char lds[P::kLds];
+  const TilePlace at = tile_place(a.block0 + blockIdx.x, mt, nt);
+  if (at.m < 0 || at.n * BN >= *a.list.count) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / P::WN);
+  const int64_t m0 = at.m * BM, n0 = at.n * BN;
+  f32x16 acc[P::MI][P::NI] = {};
+  P::run(Operand<T>{a.w, a.wld, a.V, a.Dp}, Operand<T>{a.packed, a.Dp, a.Tp, a.Dp}, m0, n0, 0, a.D, lds, acc);
+  // every token's maximum and sum over the tile's rows
+  float2* red = reinterpret_cast<float2*>(lds);   // [WM][BN]
+#pragma unroll
+  for (int j = 0; j < P::NI; ++j) {
+    const int col = wn + 32 * j + (lane & 31);
+    const int target = a.list.target[n0 + col];
+    const int64_t want = target - m0 - wm;   // the target's row in the wavefront's
+    if (__ballot(target >= 0 && want >= 0 && want < BM / WM)) {
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (target >= 0 && 32 * i + tile_row(r, lane) == want) a.list.at[n0 + col] = acc[i][j][r];
+    }
+    if (m0 + BM > a.V) {
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (m0 + wm + 32 * i + tile_row(r, lane) >= a.V) acc[i][j][r] = -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
+    sum += __shfl_xor(sum, 32, 64);
+    if (lane < 32) red[(wave % WM) * BN + col] = make_float2(top, sum);
+  }
+  lds_barrier();
+  for (int col = threadIdx.x; col < BN; col += 512) {
+    float2 s = red[col];
+#pragma unroll
+    for (int w = 1; w < WM; ++w) {
+      const float2 o = red[w * BN + col];
+      const float top = fmaxf(s.x, o.x), base = top == -INFINITY ? 0.0f : top;
+      s.y = s.y * __builtin_amdgcn_exp2f((s.x - base) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - base) * kLog2e);
+      s.x = top;
+    }
+    a.part[at.m * a.Tp + n0 + col] = s;
+  }
+}
+
+// lse and loss from the tiles' maxima and sums: 64 tokens by 8 wavefronts,
+// each an eighth of the tiles
+template <typename T>
+__global__ __launch_bounds__(512) void loss_join_kernel(LossP<T> a, int64_t mt) {
+  __shared__ float2 red[8][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t p = (a.block0 + blockIdx.x) * 64 + lane, all = *a.list.count;
+  if ((a.block0 + blockIdx.x) * 64 >= all) return;
+  const int64_t per = (mt + 7) / 8, m0 = wave * per, m1 = m0 + per < mt ? m0 + per : mt;
+  float top = -INFINITY, sum = 0.0f;
+  constexpr int kAhead = 8;
+  for (int64_t m = m0; m < m1; m += kAhead) {
+    float2 s[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) s[k] = a.part[(m + k < m1 ? m + k : m1 - 1) * a.Tp + p];
+    float t = top;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) t = fmaxf(t, s[k].x);
+    const float base = t == -INFINITY ? 0.0f : t;
+    sum *= __builtin_amdgcn_exp2f((top - base) * kLog2e);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      sum += m + k < m1 ? s[k].y * __builtin_amdgcn_exp2f((s[k].x - base) * kLog2e) : 0.0f;
+    top = t;
+  }
+  red[wave][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (wave != 0 || p >= all) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float2 o = red[w][lane];
+    const float t = fmaxf(top, o.x), base = t == -INFINITY ? 0.0f : t;
+    sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - base) * kLog2e);
+    top = t;
+  }
+  const float lse = top + __builtin_amdgcn_logf(sum) * kLn2;
+  const int64_t t = a.list.token[p];
+  a.loss[t] = a.list.target[p] >= 0 ? lse - a.list.at[p] : 0.0f;
+  if (a.lse) a.lse[t] = lse;
+}
+
+// ---- backward ---------------------------------------------------------------
+// The logits of a piece again, G to the workspace: [Tp][Vp], token rows, through
+// LDS so that memory sees whole lines.
+template <typename T>
+__global__ __launch_bounds__(512) void loss_g_kernel(LossP<T> a, T* G, int64_t v0, int64_t Vp, int64_t mt, int64_t nt) {
+  using P = Product<T, true, true, kTile, kTile, 2>;
+  constexpr int kHalves = sizeof(T) == 2 ? 1 : 2;             // fp32: a half of the rows at a time
+  constexpr int kRows = kTile / kHalves;
+  constexpr int kPitch = kRows * sizeof(T) + 16;
+  constexpr int kOut = kTile * kPitch;
+  __shared__ __align__(16) char lds[P::kLds > kOut ? P::kLds : kOut];
+  const TilePlace at = tile_place(a.block0 + blockIdx.x, mt, nt);
+  if (at.m < 0 || at.n * kTile >= *a.list.count) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave % 2) * (kTile / 2), wn = (wave / 2) * (kTile / 4);
+  const int64_t m0 = v0 + at.m * kTile, n0 = at.n * kTile;
+  f32x16 acc[P::MI][P::NI] = {};
+  P::run(Operand<T>{a.w, a.wld, a.V, a.Dp}, Operand<T>{a.packed, a.Dp, a.Tp, a.Dp}, m0, n0, 0, a.D, lds, acc);
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+    if (kHalves == 1 || wave % 2 == half) {
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) {
+        const int col = wn + 32 * j + (lane & 31);
+        const int target = a.list.target[n0 + col];
+        const float g = a.list.g[n0 + col], lse = a.list.lse[n0 + col];
+        const int64_t want = target >= 0 ? target - m0 - wm : -1;
+        char* row_out = lds + col * kPitch + (kHalves == 1 ? wm : 0) * sizeof(T);
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float y[4];
+            const int row = 32 * i + tile_row(4 * q, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float p = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - lse) * kLog2e);
+              if (m0 + kTile > a.V) p = m0 + wm + row + e < a.V ? p : 0.0f;
+              y[e] = g * p;
+            }
+            if constexpr (sizeof(T) == 2) {
+              *reinterpret_cast<uint2*>(row_out + row * 2) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            } else {
+              *reinterpret_cast<float4*>(row_out + row * 4) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        lds_wave_sync();
+        if (lane < 32 && want >= 0 && want < kTile / 2) Store<T>::put(reinterpret_cast<T*>(row_out), want, 0.0f);
+      }
+    }
+    lds_barrier();
+    constexpr int kPieces = kRows * sizeof(T) / 16;   // of a token's row
+    T* out = G + n0 * Vp + at.m * kTile + half * kRows;
+    for (int c = tid; c < kTile * kPieces; c += 512) {
+      const int t = c / kPieces, q = c % kPieces;
+      *reinterpret_cast<u32x4*>(out + t * Vp + q * (16 / sizeof(T))) =
+          *reinterpret_cast<const u32x4*>(lds + t * kPitch + q * 16);
+    }
+    lds_barrier();
+  }
+}
+
+struct GradPlan {
+  int64_t Vp, pieces, splits;   // vocabulary rows of a piece, pieces, parts of dx's contraction
+};
+
+// dW of a piece and the piece's part of dx in one launch: the tiles of dx first
+// (their contraction is a part of the piece), then those of dW (over all tokens).
+template <typename T>
+__global__ __launch_bounds__(512) void loss_grads_kernel(LossP<T> a, const T* G, int64_t v0, GradPlan plan, float* dx,
+                                                         T* dw, const int32_t* start, const float* rest,
+                                                         int64_t xblocks, int64_t ttiles, int64_t dtiles,
+                                                         int64_t vtiles) {
+  using PX = Product<T, true, false, kTile, kTile, 2>;
+  using PW = Product<T, false, false, kTile, kTile, 2>;
+  __shared__ __align__(16) char lds[PX::kLds];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave % 2) * (kTile / 2), wn = (wave / 2) * (kTile / 4);
+  const int64_t count = *a.list.count, Vp = plan.Vp;
+  int64_t g = a.block0 + blockIdx.x;
+  f32x16 acc[PX::MI][PX::NI] = {};
+  if (g < xblocks) {
+    const TilePlace at = tile_place(g, ttiles, dtiles * plan.splits);
+    if (at.m < 0 || at.m * kTile >= count) return;
+    const int64_t slot = at.n / dtiles, m0 = at.m * kTile, n0 = (at.n - slot * dtiles) * kTile;
+    const int64_t live = a.V - v0 < Vp ? a.V - v0 : Vp;      // the piece's rows
+    constexpr int64_t step = k_step<T>();
+    const int64_t per = ((live + plan.splits - 1) / plan.splits + step - 1) / step * step;
+    const int64_t k = slot * per, kend = k + per < live ? k + per : live;
+    PX::run(Operand<T>{G, Vp, a.Tp, Vp}, Operand<T>{a.w + v0 * a.wld, a.wld, live, a.wld}, m0, n0, k, kend, lds, acc);
+    float* out = dx + (slot * a.Tp + m0 + wm) * a.Dp;
+#pragma unroll
+    for (int j = 0; j < PX::NI; ++j) {
+      const int64_t col = n0 + wn + 32 * j + (lane & 31);
+      if (col >= a.Dp) continue;
+#pragma unroll
+      for (int i = 0; i < PX::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float* p = out + (32 * i + tile_row(r, lane)) * a.Dp + col;
+          *p = v0 == 0 ? acc[i][j][r] : *p + acc[i][j][r];
+        }
+    }
+    return;
+  }
+  const TilePlace at = tile_place(g - xblocks, vtiles, dtiles);
+  if (at.m < 0) return;
+  const int64_t m0 = at.m * kTile, n0 = at.n * kTile;
+  PW::run(Operand<T>{G, Vp, a.Tp, Vp}, Operand<T>{a.packed, a.Dp, a.Tp, a.Dp}, m0, n0, 0, count, lds, acc);
+#pragma unroll
+  for (int i = 0; i < PW::MI; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t v = v0 + m0 + wm + 32 * i + tile_row(r, lane);
+      if (v >= a.V) continue;
+      const int64_t s0 = start[v];
+      const bool some = start[v + 1] > s0;
+#pragma unroll
+      for (int j = 0; j < PW::NI; ++j) {
+        const int64_t col = n0 + wn + 32 * j + (lane & 31);
+        if (col >= a.D) continue;
+        const float y = some ? acc[i][j][r] + rest[s0 * a.Dp + col] : acc[i][j][r];
+        Store<T>::put(dw, v * a.D + col, y);
+      }
+    }
+}
+
+// G at the targets: g (exp(z - lse) - 1), one wavefront per token
+template <typename T>
+__global__ __launch_bounds__(256) void loss_target_kernel(LossP<T> a) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int lane = threadIdx.x & 63;
+  const int64_t p = (a.block0 + blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (p >= *a.list.count) return;
+  const T* x = a.packed + p * a.Dp;
+  const T* w = a.w + a.list.target[p] * a.wld;
+  float s = 0.0f;
+  for (int64_t at = lane * kPer; at < a.wld; at += 64 * kPer) {
+    Raw<T, kPer> rx, rw;
+    rx.load(x + at);
+    rw.load(w + at);
+    float dx[kPer], dw[kPer];
+    rx.wide(dx);
+    rw.wide(dw);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s = __builtin_fmaf(dx[e], dw[e], s);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) s += __shfl_xor(s, k, 64);
+  if (lane == 0) a.list.at[p] = a.list.g[p] * expm1_f32(s - a.list.lse[p]);
+}
+
+// G at the targets times the tokens' rows, summed for each target: row start[v]
+// of `rest`. Tokens come sorted by target; a workgroup
+// owns kRestChunk of them and 256 columns. A run that lies within the chunk
+// is finished here, one that goes past it leaves its part (begun before the chunk:
+// slot 0, in it: slot 1) for the join.
+constexpr int kRestChunk = 32;
+template <typename T>
+__global__ __launch_bounds__(256) void loss_rest_kernel(LossP<T> a, TokenSort s, float* rest, float* part, int64_t slices) {
+  const int64_t g = a.block0 + blockIdx.x, c = g / slices, col = (g - c * slices) * 256 + threadIdx.x;
+  const int64_t all = s.start[a.V], p0 = c * kRestChunk;
+  if (p0 >= all || col >= a.Dp) return;
+  const int64_t p1 = p0 + kRestChunk < all ? p0 + kRestChunk : all;
+  float sum = 0.0f;
+  constexpr int kAhead = 8;
+  for (int64_t p = p0; p < p1; p += kAhead) {
+    float d[kAhead], w[kAhead];
+    int32_t row[kAhead + 1];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t q = p + k < p1 ? p + k : p1 - 1;
+      const int64_t place = s.token[q];
+      row[k] = s.row[q];
+      w[k] = a.list.at[place];
+      d[k] = to_f32(a.packed[place * a.Dp + col]);
+    }
+    row[kAhead] = p + kAhead < p1 ? s.row[p + kAhead] : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (p + k >= p1) break;
+      sum = __builtin_fmaf(w[k], d[k], sum);
+      if (p + k + 1 < p1 && row[k + 1] == row[k]) continue;
+      // the run ends here or goes on after the chunk
+      const int64_t r0 = s.start[row[k]], r1 = s.start[row[k] + 1];
+      if (r0 >= p0 && r1 <= p1) rest[r0 * a.Dp + col] = sum;
+      else part[(c * 2 + (r0 >= p0 ? 1 : 0)) * a.Dp + col] = sum;
+      sum = 0.0f;
+    }
+  }
+}
+// joins the run that begins in chunk c and goes on after it
+template <typename T>
+__global__ __launch_bounds__(256) void loss_rest_join_kernel(LossP<T> a, TokenSort s, float* rest, const float* part,
+                                                             int64_t slices) {
+  const int64_t g = a.block0 + blockIdx.x, c = g / slices, col = (g - c * slices) * 256 + threadIdx.x;
+  const int64_t all = s.start[a.V], p0 = c * kRestChunk, p1 = p0 + kRestChunk;
+  if (p1 >= all || col >= a.Dp) return;
+  const int64_t v = s.row[p1 - 1], r0 = s.start[v], r1 = s.start[v + 1];
+  if (r0 < p0 || r1 <= p1) return;
+  const int64_t last = (r1 - 1) / kRestChunk;
+  float sum = part[(c * 2 + 1) * a.Dp + col];
+  constexpr int kAhead = 8;
+  for (int64_t q = c + 1; q <= last; q += kAhead) {
+    float d[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) d[k] = part[(q + k <= last ? q + k : last) * 2 * a.Dp + col];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) sum += q + k <= last ? d[k] : 0.0f;
+  }
+  rest[r0 * a.Dp + col] = sum;
+}
+
+// dx: the splits' sums and the target's part, rounded once; zeros for tokens
+// that do not count
+template <typename T>
+__global__ __launch_bounds__(256) void loss_dx_kernel(LossP<T> a, const float* parts, int64_t splits, T* dx) {
+  const int64_t i = (a.block0 + blockIdx.x) * 256 + threadIdx.x, t = i / a.D, col = i - t * a.D;
+  if (t >= a.T_) return;
+  const int64_t p = a.list.pos[t];
+  float s = 0.0f;
+  if (p >= 0) {
+    for (int64_t k = 0; k < splits; ++k) s += parts[(k * a.Tp + p) * a.Dp + col];
+    s = __builtin_fmaf(a.list.at[p], to_f32(a.w[a.list.target[p] * a.wld + col]), s);
+  }
+  Store<T>::put(dx, t * a.D + col, s);
+}
+
+// ---- host -------------------------------------------------------------------
+bool packs_weight(int64_t D, size_t es) { return D * es % 16 != 0; }
+int64_t padded(int64_t D, size_t es) { return cdiv(D, 128 / static_cast<int64_t>(es)) * (128 / static_cast<int64_t>(es)); }
+// at least one tile: without a token the weight's gradient is still written
+int64_t padded_tokens(int64_t T) { return std::max<int64_t>(1, cdiv(T, kTile)) * kTile; }
+
+// pieces of a workspace, in turn
+class Space {
+ public:
+  explicit Space(void* p) : p_(static_cast<char*>(p)) {}
+  template <typename E> E* take(int64_t n) {
+    E* r = reinterpret_cast<E*>(p_ + used_);
+    used_ += up256(static_cast<size_t>(n) * sizeof(E));
+    return r;
+  }
+  size_t used() const { return used_; }
+
+ private:
+  char* p_;
+  size_t used_ = 0;
+};
+
+template <typename T> void take_common(Space& s, LossP<T>& p) {
+  p.list.count = s.take<int32_t>(1);
+  p.list.token = s.take<int32_t>(p.Tp);
+  p.list.target = s.take<int32_t>(p.Tp);
+  p.list.at = s.take<float>(p.Tp);
+  p.packed = s.take<T>(p.Tp * p.Dp);
+  p.w = packs_weight(p.D, sizeof(T)) ? s.take<T>(p.V * p.Dp) : p.weight;
+  p.wld = packs_weight(p.D, sizeof(T)) ? p.Dp : p.D;
+}
+template <typename T> void take_forward(Space& s, LossP<T>& p) {
+  take_common(s, p);
+  p.part = s.take<float2>(cdiv(p.V, kFewRows) * p.Tp);
+}
+
+// G of a piece is at most half a GiB, and pieces are alike. dx's contraction is
+// cut where its tiles alone are fewer than the compute units.
+GradPlan grad_plan(int64_t T, int64_t V, int64_t D, size_t es) {
+  GradPlan g;
+  const int64_t Tp = padded_tokens(T), most = std::max<int64_t>(kTile, (int64_t(1) << 29) / (Tp * static_cast<int64_t>(es)));
+  g.pieces = cdiv(V, std::max<int64_t>(1, most / kTile) * kTile);
+  g.Vp = cdiv(cdiv(V, g.pieces), kTile) * kTile;
+  g.pieces = cdiv(V, g.Vp);
+  const int64_t tiles = (Tp / kTile) * cdiv(D, kTile);
+  g.splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, g.Vp / 512));
+  return g;
+}
+template <typename T> struct BackSpace {
+  T* G;
+  float* dx;
+  float* rest;
+  float* rest_part;
+  void* sort;
+};
+template <typename T> BackSpace<T> take_backward(Space& s, LossP<T>& p, const GradPlan& g) {
+  BackSpace<T> b{};
+  take_common(s, p);
+  p.list.g = s.take<float>(p.Tp);
+  p.list.lse = s.take<float>(p.Tp);
+  p.list.pos = s.take<int32_t>(p.T_);
+  b.G = s.take<T>(p.Tp * g.Vp);
+  b.dx = s.take<float>(g.splits * p.Tp * p.Dp);
+  b.rest = s.take<float>(p.Tp * p.Dp);
+  b.rest_part = s.take<float>(cdiv(p.Tp, kRestChunk) * 2 * p.Dp);
+  b.sort = s.take<char>(static_cast<int64_t>(token_sort_bytes(p.Tp, p.V)));
+  return b;
+}
+
+template <typename T> LossP<T> loss_sizes(int64_t tokens, int64_t L, int64_t V, int64_t D) {
+  LossP<T> p{};
+  p.L = L;
+  p.V = V;
+  p.D = D;
+  p.T_ = tokens;
+  p.Tp = padded_tokens(tokens);
+  p.Dp = padded(D, sizeof(T));
+  return p;
+}
+template <typename T> LossP<T> loss_params(const gspn_loss_args& a) {
+  LossP<T> p = loss_sizes<T>(a.B * a.L, a.L, a.V, a.D);
+  p.x = static_cast<const T*>(a.x.p);
+  p.xb = a.x.batch;
+  p.xr = a.x.row;
+  p.weight = static_cast<const T*>(a.weight);
+  p.targets = a.targets;
+  p.targets_batch = a.targets_batch;
+  p.targets64 = a.targets64;
+  p.lens = a.lens;
+  return p;
+}
+
+template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stream, Tracer* tr) {
+  tr->before(stream, "loss_list", p.T_);
+  hipLaunchKernelGGL((loss_list_kernel<LossP<T>, BACK>), dim3(1), dim3(1024), 0, stream, p);
+  hipError_t e = hipGetLastError();
+  tr->after(stream);
+  if (e != hipSuccess) return e;
+  auto pack = [&](const T* x, int64_t xb, int64_t xr, int64_t rows, const int32_t* token, T* out) {
+    const int wide = wide_ok(x, 16, sizeof(T), {xb, xr}) && p.D % (16 / static_cast<int64_t>(sizeof(T))) == 0;
+    tr->before(stream, "loss_pack", rows);
+    const hipError_t r = in_parts(cdiv(rows * (p.Dp * static_cast<int64_t>(sizeof(T)) / 16), 256), [&](int64_t first, unsigned count) {
+      hipLaunchKernelGGL((loss_pack_kernel<T>), dim3(count), dim3(256), 0, stream, x, xb, xr, p.L, p.D, p.Dp, rows, token,
+                         p.list.count, out, wide, first);
+    });
+    tr->after(stream);
+    return r;
+  };
+  if ((e = pack(p.x, p.xb, p.xr, p.Tp, p.list.token, p.packed)) != hipSuccess) return e;
+  if (p.w != p.weight) e = pack(p.weight, 0, p.D, p.V, nullptr, const_cast<T*>(p.w));
+  return e;
+}
+
+template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hipStream_t stream, Tracer* tr) {
+  LossP<T> p = loss_params<T>(a);
+  p.loss = a.loss;
+  p.lse = a.lse;
+  Space s(ws);
+  take_forward(s, p);
+  hipError_t e = gather<T, false>(p, stream, tr);
+  if (e != hipSuccess) return e;
+  const bool few = p.T_ <= kFewTile;
+  const int64_t mt = cdiv(p.V, few ? kFewRows : kTile), nt = few ? 1 : p.Tp / kTile;
+  tr->before(stream, "loss_logits", p.V);
+  e = in_parts(tile_blocks(mt, nt), [&](int64_t first, unsigned count) {
+    p.block0 = first;
+    if (few) hipLaunchKernelGGL((loss_logits_kernel<T, kFewRows, kFewTile, 4>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    else hipLaunchKernelGGL((loss_logits_kernel<T, kTile, kTile, 2>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+  });
+  tr->after(stream);
+  if (e != hipSuccess) return e;
+  tr->before(stream, "loss_join", p.T_);
+  e = in_parts(cdiv(p.T_, 64), [&](int64_t first, unsigned count) {
+    p.block0 = first;
+    hipLaunchKernelGGL((loss_join_kernel<T>), dim3(count), dim3(512), 0, stream, p, mt);
+  });
+  tr->after(stream);
+  return e;
+}
+
+template <typename T>
+hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws, hipStream_t stream, Tracer* tr) {
+  LossP<T> p = loss_params<T>(a);
+  p.glse = g.lse;
+  p.gloss = g.grad_loss;
+  const GradPlan plan = grad_plan(p.T_, p.V, p.D, sizeof(T));
+  Space s(ws);
+  const BackSpace<T> b = take_backward(s, p, plan);
+  hipError_t e = gather<T, true>(p, stream, tr);
+  if (e != hipSuccess) return e;
+  TokenSort sorted{};
+  e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
+  if (e != hipSuccess) return e;
+  const int64_t ttiles = p.Tp / kTile, dtiles = cdiv(p.D, kTile), slices = cdiv(p.Dp, 256);
+  auto launch = [&](const char* name, int64_t blocks, auto&& kernel) {
+    tr->before(stream, name, p.T_);
+    const hipError_t r = in_parts(blocks, [&](int64_t first, unsigned count) {
+      p.block0 = first;
+      kernel(dim3(count));
+    });
+    tr->after(stream);
+    return r;
+  };
+  e = launch("loss_target", cdiv(p.T_, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
+  if (e != hipSuccess) return e;
+  e = launch("loss_rest", cdiv(p.Tp, kRestChunk) * slices, [&](dim3 n) {
+    hipLaunchKernelGGL((loss_rest_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part, slices);
+  });
+  if (e != hipSuccess) return e;
+  e = launch("loss_rest_join", cdiv(p.Tp, kRestChunk) * slices, [&](dim3 n) {
+    hipLaunchKernelGGL((loss_rest_join_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part, slices);
+  });
+  if (e != hipSuccess) return e;
+  for (int64_t k = 0; k < plan.pieces; ++k) {
+    const int64_t v0 = k * plan.Vp, vtiles = cdiv(std::min(plan.Vp, p.V - v0), kTile);
+    e = launch("loss_g", tile_blocks(vtiles, ttiles), [&](dim3 n) {
+      hipLaunchKernelGGL((loss_g_kernel<T>), n, dim3(512), 0, stream, p, b.G, v0, plan.Vp, vtiles, ttiles);
+    });
+    if (e != hipSuccess) return e;
+    const int64_t xblocks = tile_blocks(ttiles, dtiles * plan.splits);
+    e = launch("loss_grads", xblocks + tile_blocks(vtiles, dtiles), [&](dim3 n) {
+      hipLaunchKernelGGL((loss_grads_kernel<T>), n, dim3(512), 0, stream, p, b.G, v0, plan, b.dx, static_cast<T*>(g.weight),
+                         sorted.start, b.rest, xblocks, ttiles, dtiles, vtiles);
+    });
+    if (e != hipSuccess) return e;
+  }
+  return launch("loss_dx", cdiv(p.T_ * p.D, 256), [&](dim3 n) {
+    hipLaunchKernelGGL((loss_dx_kernel<T>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
+  });
+}
+
+template <typename T> size_t loss_bytes(int64_t B, int64_t L, int64_t V, int64_t D, bool back) {
+  LossP<T> p = loss_sizes<T>(B * L, L, V, D);
+  if (p.T_ == 0 && !back) return 0;
+  Space s(nullptr);
+  if (back) take_backward(s, p, grad_plan(p.T_, V, D, sizeof(T)));
+  else take_forward(s, p);
+  return s.used();
+}
+
+}  // namespace
+
+size_t loss_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D, gspn_dtype dt) {
+  return dt == GSPN_F32 ? loss_bytes<float>(B, L, V, D, false) : loss_bytes<bf16_t>(B, L, V, D, false);
+}
+hipError_t launch_loss(const gspn_loss_args& a, void* ws, hipStream_t stream, Tracer* tr) {
+  if (a.dtype == GSPN_F32) return loss_fwd<float>(a, ws, stream, tr);
+  return loss_fwd<bf16_t>(a, ws, stream, tr);
+}
+size_t loss_bwd_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D, gspn_dtype dt) {
+  return dt == GSPN_F32 ? loss_bytes<float>(B, L, V, D, true) : loss_bytes<bf16_t>(B, L, V, D, true);
+}
+hipError_t launch_loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws, hipStream_t stream, Tracer* tr) {
+  if (a.dtype == GSPN_F32) return loss_bwd<float>(a, g, ws, stream, tr);
+  return loss_bwd<bf16_t>(a, g, ws, stream, tr);
+}
+
+}  // namespace gspn

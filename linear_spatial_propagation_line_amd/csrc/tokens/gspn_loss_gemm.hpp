@@ -1,0 +1,178 @@
+// The matrix products of the vocabulary loss: C = A B on matrix cores, with
+// either operand stored along the contraction or across it.
+//
+// A workgroup of eight wavefronts owns BM x BN of C. The contraction advances
+// 128 bytes of a row at a time (64 bf16 values, 32 fp32) through LDS in two
+// buffers: while one is multiplied, the next stage's 16-byte pieces are on their
+// way into registers and are written to the other buffer after it, so there
+// is one barrier per stage. An operand stored along the contraction lies in LDS
+// as [row][128 bytes], its 16-byte pieces swizzled by the row's last three
+// bits, so that a column of pieces meets every bank once; one stored across
+// it lies as it is in memory, [k][BM or BN values], and is read by the
+// transposing LDS read (bf16, the pieces of 64 bytes swizzled by the row's
+// last two bits) or value by value (fp32).
+//
+// Results are 32 x 32 tiles (v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32):
+// lane l holds column l % 32 and the rows (i % 4) + 8 (i / 4) + 4 (l / 32), i < 16.
+#pragma once
+
+#include "gspn_attn.hpp"
+
+namespace gspn {
+
+// An operand: rows of `ld` values. Along the contraction (kAlong): element
+// (m, k) is p[m * ld + k], m < outer, k < inner. Across it: element (m, k) is
+// p[k * ld + m], k < outer, m < inner. Rows begin on 16 bytes, and `inner` is a
+// multiple of 16 bytes. Pieces past the contraction's end are zeros, pieces past
+// the result's edge are some others of the same tensor.
+template <typename T> struct Operand {
+  const T* p;
+  int64_t ld;
+  int64_t outer, inner;
+};
+
+__device__ __forceinline__ int tile_row(int i, int lane) { return (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5); }
+
+template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct Product {
+  static constexpr int kWaves = 8;
+  static constexpr int kStep = 128 / sizeof(T);       // contraction of a stage
+  static constexpr int kPer = 16 / sizeof(T);         // values in 16 bytes
+  static constexpr int WN = kWaves / WM;              // wavefronts over M, over N
+  static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;   // a wavefront's tiles
+  static constexpr int kA = BM * 128, kStage = (BM + BN) * 128;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kPA = BM / 64, kPB = BN / 64;  // pieces per thread and stage
+  using Frag = typename Mma<T>::Frag;
+  static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0 && BM % 64 == 0 && BN % 64 == 0, "tiles");
+
+  // which piece of a stage this thread moves: row and first value of the n-th
+  template <bool ALONG, int W> __device__ static __forceinline__ void piece(int n, int tid, int& row, int& at) {
+    if constexpr (ALONG) {
+      const int o = n * 512 + tid;
+      row = o >> 3;
+      at = ((o & 7) ^ (row & 7)) * kPer;
+    } else {
+      constexpr int per = W * static_cast<int>(sizeof(T)) / 16;   // pieces of a row
+      const int o = n * 512 + tid;
+      row = o / per;
+      const int s = o % per;
+      at = (sizeof(T) == 2 ? s ^ ((row & 3) << 2) : s ^ (((row >> 2) & 1) << 3)) * kPer;
+    }
+  }
+
+  template <bool ALONG, int W, int N> struct Mover {
+    const char* base;      // the tile's first row at the stage's first contraction index
+    uint32_t off[N];       // the thread's pieces from there
+    int64_t step;          // bytes per stage
+    int k0[N];             // contraction index of each piece within a stage
+    int64_t left;          // contraction indexes left
+
+    __device__ __forceinline__ void set(const Operand<T>& o, int64_t first, int64_t k, int64_t kend, int tid) {
+      if constexpr (ALONG) base = reinterpret_cast<const char*>(o.p + first * o.ld + k);
+      else base = reinterpret_cast<const char*>(o.p + k * o.ld + first);
+      step = (ALONG ? kStep : kStep * o.ld) * static_cast<int64_t>(sizeof(T));
+      left = kend - k;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        int row, at;
+        piece<ALONG, W>(n, tid, row, at);
+        if constexpr (ALONG) {
+          k0[n] = at;
+          const int64_t r = first + row < o.outer ? row : o.outer - 1 - first;
+          off[n] = static_cast<uint32_t>((r * o.ld + at) * static_cast<int64_t>(sizeof(T)));
+        } else {
+          k0[n] = row;
+          const int64_t c = first + at < o.inner ? at : 0;
+          off[n] = static_cast<uint32_t>((row * o.ld + c) * static_cast<int64_t>(sizeof(T)));
+        }
+      }
+    }
+    __device__ __forceinline__ void load(u32x4 (&r)[N]) {
+      if (left >= kStep) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) r[n] = *reinterpret_cast<const u32x4*>(base + off[n]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          r[n] = u32x4{0u, 0u, 0u, 0u};
+          if (k0[n] < left) r[n] = *reinterpret_cast<const u32x4*>(base + off[n]);
+        }
+      }
+      base += step;
+      left -= kStep;
+    }
+    __device__ static __forceinline__ void store(char* lds, const u32x4 (&r)[N], int tid) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + (n * 512 + tid) * 16) = r[n];
+    }
+  };
+
+  // fragment kk (of four in a stage) of the 32 rows from r0
+  template <bool ALONG, int W> __device__ static __forceinline__ Frag frag(const char* lds, int r0, int kk, int lane) {
+    if constexpr (ALONG) {
+      const int row = r0 + (lane & 31);
+      return *reinterpret_cast<const Frag*>(lds + row * 128 + (((2 * kk + (lane >> 5)) ^ (lane & 7)) << 4));
+    } else if constexpr (sizeof(T) == 2) {
+      const int c = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
+      const int row = 16 * kk + 8 * h + (c >> 2), col = r0 + 16 * g + 4 * (c & 3);
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(
+          lds + row * (W * 2) + (((col >> 3) ^ ((c >> 2) << 2)) << 4) + (col & 7) * 2);
+      const v4i16 lo = lds_read_tr(q), hi = lds_read_tr(q + 4 * W);
+      return __builtin_bit_cast(Frag, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+    } else {
+      Frag f;
+      const int col = r0 + (lane & 31), h = lane >> 5;
+      const char* q = lds + (8 * kk + 4 * h) * (W * 4) + (((col >> 2) ^ (h << 3)) << 4) + (col & 3) * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float*>(q + j * W * 4);
+      return f;
+    }
+  }
+
+  // acc += A[m0 ..][k .. kend) B[k .. kend)[n0 ..]; all threads of the workgroup
+  __device__ static __forceinline__ void run(const Operand<T>& A, const Operand<T>& B, int64_t m0, int64_t n0,
+                                             int64_t k, int64_t kend, char* lds, f32x16 (&acc)[MI][NI]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+    Mover<A_ALONG, BM, kPA> ma;
+    Mover<B_ALONG, BN, kPB> mb;
+    ma.set(A, m0, k, kend, tid);
+    mb.set(B, n0, k, kend, tid);
+    const int stages = static_cast<int>((kend - k + kStep - 1) / kStep);
+    if (stages <= 0) return;
+    u32x4 ra[kPA], rb[kPB];
+    ma.load(ra);
+    mb.load(rb);
+    ma.store(lds, ra, tid);
+    mb.store(lds + kA, rb, tid);
+    lds_barrier();
+    for (int s = 0; s < stages; ++s) {
+      const char* cur = lds + (s & 1) * kStage;
+      char* next = lds + ((s + 1) & 1) * kStage;
+      const bool more = s + 1 < stages;
+      if (more) {
+        ma.load(ra);
+        mb.load(rb);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        Frag fa[MI], fb[NI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = frag<A_ALONG, BM>(cur, wm + 32 * i, kk, lane);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j] = frag<B_ALONG, BN>(cur + kA, wn + 32 * j, kk, lane);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
+      }
+      if (more) {
+        ma.store(next, ra, tid);
+        mb.store(next + kA, rb, tid);
+      }
+      lds_barrier();
+    }
+  }
+};
+
+}  // namespace gspn

@@ -265,6 +265,28 @@ void gated_inputs(Check& k, const gspn_gated_args& a) {
   k.input(a.lens, a.B, 4, false);
 }
 
+// ---- vocabulary loss --------------------------------------------------------
+void loss_shape(Check& k, int64_t B, int64_t L, int64_t V, int64_t D, gspn_dtype dt) {
+  if (!dtype_ok(dt)) k.bad(GSPN_E_DTYPE, "dtype must be GSPN_F32 or GSPN_BF16");
+  else if (B < 0 || L < 0 || V < 1 || D < 1) k.bad(GSPN_E_SHAPE, "need B, L >= 0 and V, D >= 1");
+  else if (V >= k31 - 2048 || D >= (int64_t(1) << 20) || k.product({B, L}) >= (int64_t(1) << 28))
+    k.bad(GSPN_E_SHAPE, "dimension too large (V < 2^31, D < 2^20, B * L < 2^28)");
+  else if (k.product({B * L + 256, D + 256, 256}) >= (int64_t(1) << 56) || k.product({V, D + 256}) >= (int64_t(1) << 46) ||
+           k.product({B * L + 256, V / 128 + 1}) >= (int64_t(1) << 46))
+    k.bad(GSPN_E_SHAPE, "tensor too large");
+}
+void loss_inputs(Check& k, const gspn_loss_args& a) {
+  const size_t es = esize(a.dtype);
+  k.view(a.x.p, es, {a.B, a.L, a.D}, {a.x.batch, a.x.row});
+  if (a.B * a.L > 0) {
+    k.input(a.weight, a.V * a.D, es);
+    if (k.ok() && a.D * static_cast<int64_t>(es) % 16 == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16)
+      k.bad(GSPN_E_ALIGN, "weight must be 16-byte aligned");
+  }
+  k.view(a.targets, a.targets64 ? 8 : 4, {a.B, a.L}, {a.targets_batch});
+  k.input(a.lens, a.B, 4, false);
+}
+
 }  // namespace
 
 extern "C" {
@@ -601,6 +623,69 @@ size_t gspn_gated_recurrence_backward_workspace_bytes(int64_t B, int64_t L, int6
     Check k;
     gated_shape(k, B, L, C, dtype);
     if (k.ok()) need = gspn::gated_bwd_workspace_bytes(B, L, C);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+gspn_status gspn_vocab_loss_ws(const gspn_loss_args* a, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a) return set_error(GSPN_E_NULL, "args must be non-null");
+    Check k;
+    loss_shape(k, a->B, a->L, a->V, a->D, a->dtype);
+    if (!k.ok()) return k.status;
+    loss_inputs(k, *a);
+    k.output(a->loss, a->B * a->L, 4);
+    k.output(a->lse, a->B * a->L, 4, false);
+    k.aliases();
+    k.scratch(ws, ws_bytes, k.ok() ? gspn::loss_workspace_bytes(a->B, a->L, a->V, a->D, a->dtype) : 0);
+    if (!k.ok()) return k.status;
+    if (a->B * a->L == 0) return GSPN_OK;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_loss(*a, ws, stream, tr); });
+  });
+}
+
+size_t gspn_vocab_loss_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                       gspn_dtype dtype) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    loss_shape(k, B, L, V, D, dtype);
+    if (k.ok()) need = gspn::loss_workspace_bytes(B, L, V, D, dtype);
+    return GSPN_OK;
+  });
+  return need;
+}
+
+gspn_status gspn_vocab_loss_backward_ws(const gspn_loss_args* a, const gspn_loss_grads* g, void* ws,
+                                        size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> gspn_status {
+    if (!a || !g) return set_error(GSPN_E_NULL, "args and grads must be non-null");
+    Check k;
+    loss_shape(k, a->B, a->L, a->V, a->D, a->dtype);
+    if (!k.ok()) return k.status;
+    const size_t es = esize(a->dtype);
+    const int64_t tokens = a->B * a->L;
+    loss_inputs(k, *a);
+    k.input(g->lse, tokens, 4);
+    k.input(g->grad_loss, tokens, 4);
+    k.output(g->x, tokens * a->D, es);
+    k.output(g->weight, a->V * a->D, es);
+    k.aliases();
+    k.scratch(ws, ws_bytes, k.ok() ? gspn::loss_bwd_workspace_bytes(a->B, a->L, a->V, a->D, a->dtype) : 0);
+    if (!k.ok()) return k.status;
+    return enqueue([&](gspn::Tracer* tr) { return gspn::launch_loss_bwd(*a, *g, ws, stream, tr); });
+  });
+}
+
+size_t gspn_vocab_loss_backward_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D,
+                                                gspn_dtype dtype) {
+  size_t need = 0;
+  guarded([&]() -> gspn_status {
+    Check k;
+    loss_shape(k, B, L, V, D, dtype);
+    if (k.ok()) need = gspn::loss_bwd_workspace_bytes(B, L, V, D, dtype);
     return GSPN_OK;
   });
   return need;

@@ -1,7 +1,7 @@
 """The token-sequence operators of ``libgspn.so`` (include/gspn_tokens.h):
 the short causal convolution and the selective scan of a state space block,
-cross attention to an encoder's states, the token embedding and the gated
-linear recurrence, each with its gradients.
+cross attention to an encoder's states, the token embedding, the gated linear
+recurrence and the vocabulary loss, each with its gradients.
 
 Like the rest of the binding this module only checks and marshals arguments.
 Tensors are token-major device tensors of float32 or bfloat16, the last
@@ -31,6 +31,8 @@ _EMBED = struct.Struct("@4qiifPqPPP")
 _EMBED_GRADS = struct.Struct("@PqqP")
 _GATED = struct.Struct("@3qi PqqPqqPqq PPPPPP".replace(" ", ""))
 _GATED_GRADS = struct.Struct("@PqqPPPPPP")
+_LOSS = struct.Struct("@4qii Pqq PPqP PP".replace(" ", ""))
+_LOSS_GRADS = struct.Struct("@4P")
 
 _Tensor = torch.Tensor
 # the current stream's handle and the current device, without the objects
@@ -68,7 +70,11 @@ def _lib():
                 ("gspn_gated_recurrence_workspace_bytes", [i64] * 3 + [ctypes.c_int], sz),
                 ("gspn_gated_recurrence_saved_bytes", [i64] * 3, sz),
                 ("gspn_gated_recurrence_backward_ws", [a, a, vp, sz, vp], ctypes.c_int),
-                ("gspn_gated_recurrence_backward_workspace_bytes", [i64] * 3 + [ctypes.c_int], sz)):
+                ("gspn_gated_recurrence_backward_workspace_bytes", [i64] * 3 + [ctypes.c_int], sz),
+                ("gspn_vocab_loss_ws", [a, vp, sz, vp], ctypes.c_int),
+                ("gspn_vocab_loss_workspace_bytes", [i64] * 4 + [ctypes.c_int], sz),
+                ("gspn_vocab_loss_backward_ws", [a, a, vp, sz, vp], ctypes.c_int),
+                ("gspn_vocab_loss_backward_workspace_bytes", [i64] * 4 + [ctypes.c_int], sz)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
         _tok = L
@@ -511,4 +517,58 @@ def gated_recurrence_backward(x, r, i, A, grad_out, state=None, lens=None, grad_
     L_ = _lib()
     ws, wp, wn = c.workspace(workspace, L_.gspn_gated_recurrence_backward_workspace_bytes(*shape, c.code))
     c.run(L_.gspn_gated_recurrence_backward_ws, args, packed, wp, wn)
+    return g
+
+
+# --------------------------------------------------------------------------
+# vocabulary loss
+# --------------------------------------------------------------------------
+def _loss_args(c, x, weight, targets, lens, loss, lse):
+    B, L, D = _shape3(x, "x")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [V, D] tensor")
+    V = weight.shape[0]
+    tp, tb, wide = c.ids(targets, (B, L), "targets")
+    return _LOSS.pack(B, L, V, D, c.code, wide, *c.view(x, (B, L, D), "x"), c.data(weight, (V, D), "weight"), tp, tb,
+                      c.data(lens, (B,), "lens", torch.int32), 0 if loss is None else loss.data_ptr(),
+                      0 if lse is None else lse.data_ptr()), (B, L, V, D)
+
+
+def vocab_loss(x, weight, targets, lens=None, out=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of ``x`` [B, L, D] over the rows of ``weight``
+    [V, D], without the logits in memory: out = lse - x . weight[target],
+    float32 [B, L], lse = log sum_v exp(x . weight[v]). ``targets`` [B, L]
+    (int64 or int32): a token whose target is outside 0 .. V - 1 has loss 0 and
+    no gradient. Tokens past an entry's length (``lens``, int32 [B]) have loss
+    and lse 0. ``lse`` (float32 [B, L]) receives the lse, which the backward
+    pass needs."""
+    shape = _shape3(x, "x")[:2]
+    c = _Call(x, "x", stream)
+    out = c.out(out, shape, "out", torch.float32)
+    if lse is not None:
+        c.tensor(lse, shape, "lse", torch.float32, True)
+    args, sizes = _loss_args(c, x, weight, targets, lens, out, lse)
+    L_ = _lib()
+    ws, wp, wn = c.workspace(workspace, L_.gspn_vocab_loss_workspace_bytes(*sizes, c.code))
+    c.run(L_.gspn_vocab_loss_ws, args, wp, wn)
+    return out
+
+
+def vocab_loss_backward(x, weight, targets, lse, grad_loss, lens=None, grads=None, workspace=None,
+                        stream=None) -> dict:
+    """Gradients of vocab_loss() given its ``lse`` and ``grad_loss`` = dL/dloss
+    (float32 [B, L]): a dict with "x" and "weight", contiguous, shaped and
+    typed like the inputs (``grads`` may supply them). The logits are found
+    again, in pieces of the vocabulary."""
+    shape = _shape3(x, "x")
+    c = _Call(x, "x", stream)
+    args, sizes = _loss_args(c, x, weight, targets, lens, None, None)
+    g = {n: c.out(None if grads is None else grads[n], tuple(t.shape), f"grads[{n!r}]")
+         for n, t in (("x", x), ("weight", weight))}
+    packed = _LOSS_GRADS.pack(c.data(lse, shape[:2], "lse", torch.float32),
+                              c.data(grad_loss, shape[:2], "grad_loss", torch.float32),
+                              g["x"].data_ptr(), g["weight"].data_ptr())
+    L_ = _lib()
+    ws, wp, wn = c.workspace(workspace, L_.gspn_vocab_loss_backward_workspace_bytes(*sizes, c.code))
+    c.run(L_.gspn_vocab_loss_backward_ws, args, packed, wp, wn)
     return g

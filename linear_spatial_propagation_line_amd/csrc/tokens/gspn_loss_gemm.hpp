@@ -60,43 +60,44 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct
     }
   }
 
+  // Moves an operand's stages from memory. Loads go through a buffer
+  // descriptor whose range check gives zeros for a lane that asks past the end,
+  // so the contraction's last stage needs no branch.
   template <bool ALONG, int W, int N> struct Mover {
+    static constexpr uint32_t kRange = 0xfffffff0u;
+    // rows of a stage between a thread's pieces (across: contraction indexes)
+    static constexpr int kApart = ALONG ? 64 : 512 / (W * static_cast<int>(sizeof(T)) / 16);
     const char* base;      // the tile's first row at the stage's first contraction index
     uint32_t off[N];       // the thread's pieces from there
     int64_t step;          // bytes per stage
-    int k0[N];             // contraction index of each piece within a stage
-    int64_t left;          // contraction indexes left
+    int k0;                // contraction index of the first piece within a stage
+    int left;              // contraction indexes left
 
     __device__ __forceinline__ void set(const Operand<T>& o, int64_t first, int64_t k, int64_t kend, int tid) {
       if constexpr (ALONG) base = reinterpret_cast<const char*>(o.p + first * o.ld + k);
       else base = reinterpret_cast<const char*>(o.p + k * o.ld + first);
       step = (ALONG ? kStep : kStep * o.ld) * static_cast<int64_t>(sizeof(T));
-      left = kend - k;
+      left = static_cast<int>(kend - k);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         int row, at;
         piece<ALONG, W>(n, tid, row, at);
+        if (n == 0) k0 = ALONG ? at : row;
         if constexpr (ALONG) {
-          k0[n] = at;
           const int64_t r = first + row < o.outer ? row : o.outer - 1 - first;
           off[n] = static_cast<uint32_t>((r * o.ld + at) * static_cast<int64_t>(sizeof(T)));
         } else {
-          k0[n] = row;
           const int64_t c = first + at < o.inner ? at : 0;
           off[n] = static_cast<uint32_t>((row * o.ld + c) * static_cast<int64_t>(sizeof(T)));
         }
       }
     }
     __device__ __forceinline__ void load(u32x4 (&r)[N]) {
-      if (left >= kStep) {
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, kRange, 0x00027000);
 #pragma unroll
-        for (int n = 0; n < N; ++n) r[n] = *reinterpret_cast<const u32x4*>(base + off[n]);
-      } else {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          r[n] = u32x4{0u, 0u, 0u, 0u};
-          if (k0[n] < left) r[n] = *reinterpret_cast<const u32x4*>(base + off[n]);
-        }
+      for (int n = 0; n < N; ++n) {
+        const uint32_t at = (ALONG ? k0 : k0 + n * kApart) < left ? off[n] : 0xffffffffu;
+        r[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
       }
       base += step;
       left -= kStep;
@@ -129,49 +130,57 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct
     }
   }
 
+  // the products of the stage in LDS, the fragments of the next quarter read
+  // ahead of the products of this one
+  __device__ static __forceinline__ void multiply(const char* lds, int wm, int wn, int lane, f32x16 (&acc)[MI][NI]) {
+    Frag fa[2][MI], fb[2][NI];
+    auto read = [&](int kk) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[kk & 1][i] = frag<A_ALONG, BM>(lds, wm + 32 * i, kk, lane);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[kk & 1][j] = frag<B_ALONG, BN>(lds + kA, wn + 32 * j, kk, lane);
+    };
+    read(0);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (kk < 3) read(kk + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
   // acc += A[m0 ..][k .. kend) B[k .. kend)[n0 ..]; all threads of the workgroup
   __device__ static __forceinline__ void run(const Operand<T>& A, const Operand<T>& B, int64_t m0, int64_t n0,
                                              int64_t k, int64_t kend, char* lds, f32x16 (&acc)[MI][NI]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+    if (kend <= k) return;
     Mover<A_ALONG, BM, kPA> ma;
     Mover<B_ALONG, BN, kPB> mb;
     ma.set(A, m0, k, kend, tid);
     mb.set(B, n0, k, kend, tid);
-    const int stages = static_cast<int>((kend - k + kStep - 1) / kStep);
-    if (stages <= 0) return;
     u32x4 ra[kPA], rb[kPB];
+    int cur = 0;   // the stage in use: LDS offset
     ma.load(ra);
     mb.load(rb);
     ma.store(lds, ra, tid);
     mb.store(lds + kA, rb, tid);
     lds_barrier();
-    for (int s = 0; s < stages; ++s) {
-      const char* cur = lds + (s & 1) * kStage;
-      char* next = lds + ((s + 1) & 1) * kStage;
-      const bool more = s + 1 < stages;
-      if (more) {
-        ma.load(ra);
-        mb.load(rb);
-      }
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        Frag fa[MI], fb[NI];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = frag<A_ALONG, BM>(cur, wm + 32 * i, kk, lane);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j] = frag<B_ALONG, BN>(cur + kA, wn + 32 * j, kk, lane);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
-      }
-      if (more) {
-        ma.store(next, ra, tid);
-        mb.store(next + kA, rb, tid);
-      }
+    while (ma.left > 0) {
+      ma.load(ra);
+      mb.load(rb);
+      multiply(lds + cur, wm, wn, lane, acc);
+      cur ^= kStage;
+      ma.store(lds + cur, ra, tid);
+      mb.store(lds + cur + kA, rb, tid);
       lds_barrier();
     }
+    multiply(lds + cur, wm, wn, lane, acc);
+    lds_barrier();
   }
 };
 

@@ -26,9 +26,12 @@ namespace gspn {
 
 namespace {
 
-constexpr int kTile = 256;       // tokens, vocabulary rows and columns of a tile
+constexpr int kTile = 256;       // the largest tile: tokens, vocabulary rows or columns
 constexpr int kFewTile = 64;     // tokens of a tile where there are few
 constexpr int kFewRows = 128;    // vocabulary rows of a tile then
+
+// wavefronts of a square tile
+constexpr int waves_of(int tile) { return tile == 64 ? 4 : 8; }
 
 template <typename T> constexpr int k_step() { return 128 / static_cast<int>(sizeof(T)); }
 
@@ -161,9 +164,9 @@ __device__ __forceinline__ TilePlace tile_place(int64_t g, int64_t mt, int64_t n
 }
 int64_t tile_blocks(int64_t mt, int64_t nt) { return cdiv(mt * nt, 8) * 8; }
 
-template <typename T, int BM, int BN, int WM>
-__global__ __launch_bounds__(512) void loss_logits_kernel(LossP<T> a, int64_t mt, int64_t nt) {
-  using P = Product<T, true, true, BM, BN, WM>;
+template <typename T, int BM, int BN, int WM, int NW>
+__global__ __launch_bounds__(64 * NW) void loss_logits_kernel(LossP<T> a, int64_t mt, int64_t nt) {
+  using P = Product<T, true, true, BM, BN, WM, NW>;
   __shared__ __align__(16) char lds[P::kLds];
   const TilePlace at = tile_place(a.block0 + blockIdx.x, mt, nt);
   if (at.m < 0 || at.n * BN >= *a.list.count) return;
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(512) void loss_logits_kernel(LossP<T> a, int64_t mt
     if (lane < 32) red[(wave % WM) * BN + col] = make_float2(top, sum);
   }
   lds_barrier();
-  for (int col = threadIdx.x; col < BN; col += 512) {
+  for (int col = threadIdx.x; col < BN; col += 64 * NW) {
     float2 s = red[col];
 #pragma unroll
     for (int w = 1; w < WM; ++w) {
@@ -266,19 +269,20 @@ __global__ __launch_bounds__(512) void loss_join_kernel(LossP<T> a, int64_t mt) 
 // ---- backward ---------------------------------------------------------------
 // The logits of a piece again, G to the workspace: [Tp][Vp], token rows, through
 // LDS so that memory sees whole lines.
-template <typename T>
-__global__ __launch_bounds__(512) void loss_g_kernel(LossP<T> a, T* G, int64_t v0, int64_t Vp, int64_t mt, int64_t nt) {
-  using P = Product<T, true, true, kTile, kTile, 2>;
-  constexpr int kHalves = sizeof(T) == 2 ? 1 : 2;             // fp32: a half of the rows at a time
-  constexpr int kRows = kTile / kHalves;
+template <typename T, int S>
+__global__ __launch_bounds__(64 * waves_of(S)) void loss_g_kernel(LossP<T> a, T* G, int64_t v0, int64_t Vp, int64_t mt,
+                                                                  int64_t nt) {
+  using P = Product<T, true, true, S, S, 2, waves_of(S)>;
+  constexpr int kHalves = S * sizeof(T) > 512 ? 2 : 1;        // rows of 1 KB: a half of them at a time
+  constexpr int kRows = S / kHalves;
   constexpr int kPitch = kRows * sizeof(T) + 16;
-  constexpr int kOut = kTile * kPitch;
+  constexpr int kOut = S * kPitch;
   __shared__ __align__(16) char lds[P::kLds > kOut ? P::kLds : kOut];
   const TilePlace at = tile_place(a.block0 + blockIdx.x, mt, nt);
-  if (at.m < 0 || at.n * kTile >= *a.list.count) return;
+  if (at.m < 0 || at.n * S >= *a.list.count) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wave % 2) * (kTile / 2), wn = (wave / 2) * (kTile / 4);
-  const int64_t m0 = v0 + at.m * kTile, n0 = at.n * kTile;
+  const int wm = (wave % 2) * (S / 2), wn = (wave / 2) * (S / P::WN);
+  const int64_t m0 = v0 + at.m * S, n0 = at.n * S;
   f32x16 acc[P::MI][P::NI] = {};
   P::run(Operand<T>{a.w, a.wld, a.V, a.Dp}, Operand<T>{a.packed, a.Dp, a.Tp, a.Dp}, m0, n0, 0, a.D, lds, acc);
 #pragma unroll
@@ -300,7 +304,7 @@ __global__ __launch_bounds__(512) void loss_g_kernel(LossP<T> a, T* G, int64_t v
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float p = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - lse) * kLog2e);
-              if (m0 + kTile > a.V) p = m0 + wm + row + e < a.V ? p : 0.0f;
+              if (m0 + S > a.V) p = m0 + wm + row + e < a.V ? p : 0.0f;
               y[e] = g * p;
             }
             if constexpr (sizeof(T) == 2) {
@@ -310,13 +314,13 @@ __global__ __launch_bounds__(512) void loss_g_kernel(LossP<T> a, T* G, int64_t v
             }
           }
         lds_wave_sync();
-        if (lane < 32 && want >= 0 && want < kTile / 2) Store<T>::put(reinterpret_cast<T*>(row_out), want, 0.0f);
+        if (lane < 32 && want >= 0 && want < S / 2) Store<T>::put(reinterpret_cast<T*>(row_out), want, 0.0f);
       }
     }
     lds_barrier();
     constexpr int kPieces = kRows * sizeof(T) / 16;   // of a token's row
-    T* out = G + n0 * Vp + at.m * kTile + half * kRows;
-    for (int c = tid; c < kTile * kPieces; c += 512) {
+    T* out = G + n0 * Vp + at.m * S + half * kRows;
+    for (int c = tid; c < S * kPieces; c += P::kThreads) {
       const int t = c / kPieces, q = c % kPieces;
       *reinterpret_cast<u32x4*>(out + t * Vp + q * (16 / sizeof(T))) =
           *reinterpret_cast<const u32x4*>(lds + t * kPitch + q * 16);
@@ -327,27 +331,28 @@ __global__ __launch_bounds__(512) void loss_g_kernel(LossP<T> a, T* G, int64_t v
 
 struct GradPlan {
   int64_t Vp, pieces, splits;   // vocabulary rows of a piece, pieces, parts of dx's contraction
+  int64_t tile, gtile;          // of the gradients, of G
 };
 
 // dW of a piece and the piece's part of dx in one launch: the tiles of dx first
 // (their contraction is a part of the piece), then those of dW (over all tokens).
-template <typename T>
-__global__ __launch_bounds__(512) void loss_grads_kernel(LossP<T> a, const T* G, int64_t v0, GradPlan plan, float* dx,
+template <typename T, int S>
+__global__ __launch_bounds__(64 * waves_of(S)) void loss_grads_kernel(LossP<T> a, const T* G, int64_t v0, GradPlan plan, float* dx,
                                                          T* dw, const int32_t* start, const float* rest,
                                                          int64_t xblocks, int64_t ttiles, int64_t dtiles,
                                                          int64_t vtiles) {
-  using PX = Product<T, true, false, kTile, kTile, 2>;
-  using PW = Product<T, false, false, kTile, kTile, 2>;
+  using PX = Product<T, true, false, S, S, 2, waves_of(S)>;
+  using PW = Product<T, false, false, S, S, 2, waves_of(S)>;
   __shared__ __align__(16) char lds[PX::kLds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = (wave % 2) * (kTile / 2), wn = (wave / 2) * (kTile / 4);
+  const int wm = (wave % 2) * (S / 2), wn = (wave / 2) * (S / PX::WN);
   const int64_t count = *a.list.count, Vp = plan.Vp;
   int64_t g = a.block0 + blockIdx.x;
   f32x16 acc[PX::MI][PX::NI] = {};
   if (g < xblocks) {
     const TilePlace at = tile_place(g, ttiles, dtiles * plan.splits);
-    if (at.m < 0 || at.m * kTile >= count) return;
-    const int64_t slot = at.n / dtiles, m0 = at.m * kTile, n0 = (at.n - slot * dtiles) * kTile;
+    if (at.m < 0 || at.m * S >= count) return;
+    const int64_t slot = at.n / dtiles, m0 = at.m * S, n0 = (at.n - slot * dtiles) * S;
     const int64_t live = a.V - v0 < Vp ? a.V - v0 : Vp;      // the piece's rows
     constexpr int64_t step = k_step<T>();
     const int64_t per = ((live + plan.splits - 1) / plan.splits + step - 1) / step * step;
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(512) void loss_grads_kernel(LossP<T> a, const T* G,
   }
   const TilePlace at = tile_place(g - xblocks, vtiles, dtiles);
   if (at.m < 0) return;
-  const int64_t m0 = at.m * kTile, n0 = at.n * kTile;
+  const int64_t m0 = at.m * S, n0 = at.n * S;
   PW::run(Operand<T>{G, Vp, a.Tp, Vp}, Operand<T>{a.packed, a.Dp, a.Tp, a.Dp}, m0, n0, 0, count, lds, acc);
 #pragma unroll
   for (int i = 0; i < PW::MI; ++i)
@@ -513,6 +518,14 @@ class Space {
   size_t used_ = 0;
 };
 
+// The largest square tile of which there are enough for the compute units;
+// large tiles read their operands less often.
+int64_t tile_for(int64_t m, int64_t n) {
+  for (const int64_t s : {256, 128})
+    if (cdiv(m, s) * cdiv(n, s) >= 192) return s;
+  return 64;
+}
+
 template <typename T> void take_common(Space& s, LossP<T>& p) {
   p.list.count = s.take<int32_t>(1);
   p.list.token = s.take<int32_t>(p.Tp);
@@ -524,7 +537,7 @@ template <typename T> void take_common(Space& s, LossP<T>& p) {
 }
 template <typename T> void take_forward(Space& s, LossP<T>& p) {
   take_common(s, p);
-  p.part = s.take<float2>(cdiv(p.V, kFewRows) * p.Tp);
+  p.part = s.take<float2>(cdiv(p.V, p.T_ <= kFewTile ? kFewRows : tile_for(p.V, p.T_)) * p.Tp);
 }
 
 // G of a piece is at most half a GiB, and pieces are alike. dx's contraction is
@@ -535,9 +548,21 @@ GradPlan grad_plan(int64_t T, int64_t V, int64_t D, size_t es) {
   g.pieces = cdiv(V, std::max<int64_t>(1, most / kTile) * kTile);
   g.Vp = cdiv(cdiv(V, g.pieces), kTile) * kTile;
   g.pieces = cdiv(V, g.Vp);
-  const int64_t tiles = (Tp / kTile) * cdiv(D, kTile);
+  const int64_t rows = std::min(g.Vp, V), tokens = std::max<int64_t>(1, T);
+  g.gtile = tile_for(rows, tokens);
+  g.tile = tile_for(rows, D);
+  const int64_t tiles = cdiv(tokens, g.tile) * cdiv(D, g.tile);
   g.splits = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, g.Vp / 512));
   return g;
+}
+// calls f with the tile as a constant
+template <int S> struct TileOf {
+  static constexpr int value = S;
+};
+template <typename F> void by_tile(int64_t tile, F&& f) {
+  if (tile == 256) f(TileOf<256>{});
+  else if (tile == 128) f(TileOf<128>{});
+  else f(TileOf<64>{});
 }
 template <typename T> struct BackSpace {
   T* G;
@@ -613,12 +638,15 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   hipError_t e = gather<T, false>(p, stream, tr);
   if (e != hipSuccess) return e;
   const bool few = p.T_ <= kFewTile;
-  const int64_t mt = cdiv(p.V, few ? kFewRows : kTile), nt = few ? 1 : p.Tp / kTile;
+  const int64_t tile = tile_for(p.V, p.T_);
+  const int64_t mt = cdiv(p.V, few ? kFewRows : tile), nt = few ? 1 : cdiv(p.T_, tile);
   tr->before(stream, "loss_logits", p.V);
   e = in_parts(tile_blocks(mt, nt), [&](int64_t first, unsigned count) {
     p.block0 = first;
-    if (few) hipLaunchKernelGGL((loss_logits_kernel<T, kFewRows, kFewTile, 4>), dim3(count), dim3(512), 0, stream, p, mt, nt);
-    else hipLaunchKernelGGL((loss_logits_kernel<T, kTile, kTile, 2>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    if (few) hipLaunchKernelGGL((loss_logits_kernel<T, kFewRows, kFewTile, 4, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    else if (tile == 256) hipLaunchKernelGGL((loss_logits_kernel<T, 256, 256, 2, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    else if (tile == 128) hipLaunchKernelGGL((loss_logits_kernel<T, 128, 128, 2, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    else hipLaunchKernelGGL((loss_logits_kernel<T, 64, 64, 2, 4>), dim3(count), dim3(256), 0, stream, p, mt, nt);
   });
   tr->after(stream);
   if (e != hipSuccess) return e;
@@ -644,7 +672,8 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   TokenSort sorted{};
   e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
   if (e != hipSuccess) return e;
-  const int64_t ttiles = p.Tp / kTile, dtiles = cdiv(p.D, kTile), slices = cdiv(p.Dp, 256);
+  const int64_t ttiles = cdiv(p.T_, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.T_, plan.gtile),
+                slices = cdiv(p.Dp, 256);
   auto launch = [&](const char* name, int64_t blocks, auto&& kernel) {
     tr->before(stream, name, p.T_);
     const hipError_t r = in_parts(blocks, [&](int64_t first, unsigned count) {
@@ -665,15 +694,24 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   });
   if (e != hipSuccess) return e;
   for (int64_t k = 0; k < plan.pieces; ++k) {
-    const int64_t v0 = k * plan.Vp, vtiles = cdiv(std::min(plan.Vp, p.V - v0), kTile);
-    e = launch("loss_g", tile_blocks(vtiles, ttiles), [&](dim3 n) {
-      hipLaunchKernelGGL((loss_g_kernel<T>), n, dim3(512), 0, stream, p, b.G, v0, plan.Vp, vtiles, ttiles);
+    const int64_t v0 = k * plan.Vp, rows = std::min(plan.Vp, p.V - v0);
+    const int64_t mtiles = cdiv(rows, plan.gtile), vtiles = cdiv(rows, plan.tile);
+    e = launch("loss_g", tile_blocks(mtiles, gtiles), [&](dim3 n) {
+      auto go = [&](auto s) {
+        constexpr int S = decltype(s)::value;
+        hipLaunchKernelGGL((loss_g_kernel<T, S>), n, dim3(64 * waves_of(S)), 0, stream, p, b.G, v0, plan.Vp, mtiles, gtiles);
+      };
+      by_tile(plan.gtile, go);
     });
     if (e != hipSuccess) return e;
     const int64_t xblocks = tile_blocks(ttiles, dtiles * plan.splits);
     e = launch("loss_grads", xblocks + tile_blocks(vtiles, dtiles), [&](dim3 n) {
-      hipLaunchKernelGGL((loss_grads_kernel<T>), n, dim3(512), 0, stream, p, b.G, v0, plan, b.dx, static_cast<T*>(g.weight),
-                         sorted.start, b.rest, xblocks, ttiles, dtiles, vtiles);
+      auto go = [&](auto s) {
+        constexpr int S = decltype(s)::value;
+        hipLaunchKernelGGL((loss_grads_kernel<T, S>), n, dim3(64 * waves_of(S)), 0, stream, p, b.G, v0, plan, b.dx,
+                           static_cast<T*>(g.weight), sorted.start, b.rest, xblocks, ttiles, dtiles, vtiles);
+      };
+      by_tile(plan.tile, go);
     });
     if (e != hipSuccess) return e;
   }

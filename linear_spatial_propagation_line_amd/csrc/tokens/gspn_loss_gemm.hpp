@@ -1,7 +1,7 @@
 // The matrix products of the vocabulary loss: C = A B on matrix cores, with
 // either operand stored along the contraction or across it.
 //
-// A workgroup of eight wavefronts owns BM x BN of C. The contraction advances
+// A workgroup of eight wavefronts (four for tiles of 64 x 64) owns BM x BN of C. The contraction advances
 // 128 bytes of a row at a time (64 bf16 values, 32 fp32) through LDS in two
 // buffers: while one is multiplied, the next stage's 16-byte pieces are on their
 // way into registers and are written to the other buffer after it, so there
@@ -9,8 +9,7 @@
 // as [row][128 bytes], its 16-byte pieces swizzled by the row's last three
 // bits, so that a column of pieces meets every bank once; one stored across
 // it lies as it is in memory, [k][BM or BN values], and is read by the
-// transposing LDS read (bf16, the pieces of 64 bytes swizzled by the row's
-// last two bits) or value by value (fp32).
+// transposing LDS read (bf16, runs of 64 bytes swizzled by the row) or value by value (fp32).
 //
 // Results are 32 x 32 tiles (v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32):
 // lane l holds column l % 32 and the rows (i % 4) + 8 (i / 4) + 4 (l / 32), i < 16.
@@ -33,30 +32,37 @@ template <typename T> struct Operand {
 
 __device__ __forceinline__ int tile_row(int i, int lane) { return (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5); }
 
-template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct Product {
-  static constexpr int kWaves = 8;
+template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kWaves = 8> struct Product {
+  static constexpr int kThreads = 64 * kWaves;
   static constexpr int kStep = 128 / sizeof(T);       // contraction of a stage
   static constexpr int kPer = 16 / sizeof(T);         // values in 16 bytes
   static constexpr int WN = kWaves / WM;              // wavefronts over M, over N
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;   // a wavefront's tiles
   static constexpr int kA = BM * 128, kStage = (BM + BN) * 128;
   static constexpr int kLds = 2 * kStage;
-  static constexpr int kPA = BM / 64, kPB = BN / 64;  // pieces per thread and stage
+  static constexpr int kPA = BM * 8 / kThreads, kPB = BN * 8 / kThreads;   // pieces per thread and stage
   using Frag = typename Mma<T>::Frag;
-  static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0 && BM % 64 == 0 && BN % 64 == 0, "tiles");
+  static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0 && BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "tiles");
+
+  // what a row's pieces are swizzled by in LDS, of an operand across the contraction
+  template <int W> __device__ static __forceinline__ int swizzle(int row) {
+    if constexpr (sizeof(T) == 4) return ((row >> 2) & 1) << 3;
+    else if constexpr (W == 64) return ((row >> 1) & 1) << 2;
+    else return (row & 3) << 2;
+  }
 
   // which piece of a stage this thread moves: row and first value of the n-th
   template <bool ALONG, int W> __device__ static __forceinline__ void piece(int n, int tid, int& row, int& at) {
     if constexpr (ALONG) {
-      const int o = n * 512 + tid;
+      const int o = n * kThreads + tid;
       row = o >> 3;
       at = ((o & 7) ^ (row & 7)) * kPer;
     } else {
       constexpr int per = W * static_cast<int>(sizeof(T)) / 16;   // pieces of a row
-      const int o = n * 512 + tid;
+      const int o = n * kThreads + tid;
       row = o / per;
       const int s = o % per;
-      at = (sizeof(T) == 2 ? s ^ ((row & 3) << 2) : s ^ (((row >> 2) & 1) << 3)) * kPer;
+      at = (s ^ swizzle<W>(row)) * kPer;
     }
   }
 
@@ -66,7 +72,7 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct
   template <bool ALONG, int W, int N> struct Mover {
     static constexpr uint32_t kRange = 0xfffffff0u;
     // rows of a stage between a thread's pieces (across: contraction indexes)
-    static constexpr int kApart = ALONG ? 64 : 512 / (W * static_cast<int>(sizeof(T)) / 16);
+    static constexpr int kApart = ALONG ? kThreads / 8 : kThreads / (W * static_cast<int>(sizeof(T)) / 16);
     const char* base;      // the tile's first row at the stage's first contraction index
     uint32_t off[N];       // the thread's pieces from there
     int64_t step;          // bytes per stage
@@ -104,7 +110,7 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct
     }
     __device__ static __forceinline__ void store(char* lds, const u32x4 (&r)[N], int tid) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + (n * 512 + tid) * 16) = r[n];
+      for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + (n * kThreads + tid) * 16) = r[n];
     }
   };
 
@@ -117,13 +123,13 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM> struct
       const int c = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
       const int row = 16 * kk + 8 * h + (c >> 2), col = r0 + 16 * g + 4 * (c & 3);
       const uint16_t* q = reinterpret_cast<const uint16_t*>(
-          lds + row * (W * 2) + (((col >> 3) ^ ((c >> 2) << 2)) << 4) + (col & 7) * 2);
+          lds + row * (W * 2) + (((col >> 3) ^ swizzle<W>(row)) << 4) + (col & 7) * 2);
       const v4i16 lo = lds_read_tr(q), hi = lds_read_tr(q + 4 * W);
       return __builtin_bit_cast(Frag, v8i16{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
     } else {
       Frag f;
       const int col = r0 + (lane & 31), h = lane >> 5;
-      const char* q = lds + (8 * kk + 4 * h) * (W * 4) + (((col >> 2) ^ (h << 3)) << 4) + (col & 3) * 4;
+      const char* q = lds + (8 * kk + 4 * h) * (W * 4) + (((col >> 2) ^ swizzle<W>(4 * h)) << 4) + (col & 3) * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float*>(q + j * W * 4);
       return f;

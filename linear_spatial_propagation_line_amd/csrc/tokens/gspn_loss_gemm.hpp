@@ -6,8 +6,8 @@
 // buffers: while one is multiplied, the next stage's 16-byte pieces are on their
 // way into registers and are written to the other buffer after it, so there
 // is one barrier per stage. An operand stored along the contraction lies in LDS
-// as [row][128 bytes], its 16-byte pieces swizzled by the row's last three
-// bits, so that a column of pieces meets every bank once; one stored across
+// as [row][128 bytes], its 16-byte pieces swizzled by bits 1 to 3 of the
+// row, so that 16 rows' pieces of a column meet every bank once; one stored across
 // it lies as it is in memory, [k][BM or BN values], and is read by the
 // transposing LDS read (bf16, runs of 64 bytes swizzled by the row) or value by value (fp32).
 //
@@ -56,7 +56,7 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
     if constexpr (ALONG) {
       const int o = n * kThreads + tid;
       row = o >> 3;
-      at = ((o & 7) ^ (row & 7)) * kPer;
+      at = ((o & 7) ^ ((row >> 1) & 7)) * kPer;
     } else {
       constexpr int per = W * static_cast<int>(sizeof(T)) / 16;   // pieces of a row
       const int o = n * kThreads + tid;
@@ -118,7 +118,7 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
   template <bool ALONG, int W> __device__ static __forceinline__ Frag frag(const char* lds, int r0, int kk, int lane) {
     if constexpr (ALONG) {
       const int row = r0 + (lane & 31);
-      return *reinterpret_cast<const Frag*>(lds + row * 128 + (((2 * kk + (lane >> 5)) ^ (lane & 7)) << 4));
+      return *reinterpret_cast<const Frag*>(lds + row * 128 + (((2 * kk + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4));
     } else if constexpr (sizeof(T) == 2) {
       const int c = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
       const int row = 16 * kk + 8 * h + (c >> 2), col = r0 + 16 * g + 4 * (c & 3);
@@ -136,30 +136,29 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
     }
   }
 
-  // the products of the stage in LDS, the fragments of the next quarter read
-  // ahead of the products of this one
-  __device__ static __forceinline__ void multiply(const char* lds, int wm, int wn, int lane, f32x16 (&acc)[MI][NI]) {
-    Frag fa[2][MI], fb[2][NI];
-    auto read = [&](int kk) {
+  struct Frags {
+    Frag a[2][MI], b[2][NI];
+  };
+  // fragments of quarter kk of a stage
+  __device__ static __forceinline__ void read(const char* lds, int kk, int wm, int wn, int lane, Frags& f) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[kk & 1][i] = frag<A_ALONG, BM>(lds, wm + 32 * i, kk, lane);
+    for (int i = 0; i < MI; ++i) f.a[kk & 1][i] = frag<A_ALONG, BM>(lds, wm + 32 * i, kk, lane);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) fb[kk & 1][j] = frag<B_ALONG, BN>(lds + kA, wn + 32 * j, kk, lane);
-    };
-    read(0);
+    for (int j = 0; j < NI; ++j) f.b[kk & 1][j] = frag<B_ALONG, BN>(lds + kA, wn + 32 * j, kk, lane);
+  }
+  __device__ static __forceinline__ void multiply(int kk, const Frags& f, f32x16 (&acc)[MI][NI]) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) read(kk + 1);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+      for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(f.a[kk & 1][i], f.b[kk & 1][j], acc[i][j]);
   }
 
-  // acc += A[m0 ..][k .. kend) B[k .. kend)[n0 ..]; all threads of the workgroup
+  // acc += A[m0 ..][k .. kend) B[k .. kend)[n0 ..]; all threads of the workgroup.
+  // A stage in four quarters, the fragments of the next one read before the
+  // products of each. In the third the next stage, loaded a whole stage ago, goes
+  // to the other buffer and the one after it is asked for; the barrier comes
+  // before the last quarter's products, whose fragments are in registers by
+  // then, and they cover the first reads of the next stage.
   __device__ static __forceinline__ void run(const Operand<T>& A, const Operand<T>& B, int64_t m0, int64_t n0,
                                              int64_t k, int64_t kend, char* lds, f32x16 (&acc)[MI][NI]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -169,23 +168,51 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
     Mover<B_ALONG, BN, kPB> mb;
     ma.set(A, m0, k, kend, tid);
     mb.set(B, n0, k, kend, tid);
+    const int stages = static_cast<int>((kend - k + kStep - 1) / kStep);
     u32x4 ra[kPA], rb[kPB];
+    Frags f;
     int cur = 0;   // the stage in use: LDS offset
     ma.load(ra);
     mb.load(rb);
     ma.store(lds, ra, tid);
     mb.store(lds + kA, rb, tid);
+    ma.load(ra);   // past the end: zeros
+    mb.load(rb);
     lds_barrier();
-    while (ma.left > 0) {
-      ma.load(ra);
-      mb.load(rb);
-      multiply(lds + cur, wm, wn, lane, acc);
+    read(lds, 0, wm, wn, lane, f);
+    // the compiler is kept from moving the reads behind the products
+    auto fence = []() { __builtin_amdgcn_sched_barrier(0); };
+    for (int s = 1; s < stages; ++s) {
+      read(lds + cur, 1, wm, wn, lane, f);
+      fence();
+      multiply(0, f, acc);
+      fence();
+      read(lds + cur, 2, wm, wn, lane, f);
+      fence();
+      multiply(1, f, acc);
+      fence();
+      read(lds + cur, 3, wm, wn, lane, f);
       cur ^= kStage;
       ma.store(lds + cur, ra, tid);
       mb.store(lds + cur + kA, rb, tid);
+      ma.load(ra);
+      mb.load(rb);
+      fence();
+      multiply(2, f, acc);
+      fence();
       lds_barrier();
+      read(lds + cur, 0, wm, wn, lane, f);
+      fence();
+      multiply(3, f, acc);
+      fence();
     }
-    multiply(lds + cur, wm, wn, lane, acc);
+    read(lds + cur, 1, wm, wn, lane, f);
+    multiply(0, f, acc);
+    read(lds + cur, 2, wm, wn, lane, f);
+    multiply(1, f, acc);
+    read(lds + cur, 3, wm, wn, lane, f);
+    multiply(2, f, acc);
+    multiply(3, f, acc);
     lds_barrier();
   }
 };

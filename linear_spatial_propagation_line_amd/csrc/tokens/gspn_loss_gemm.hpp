@@ -98,19 +98,18 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
         }
       }
     }
-    __device__ __forceinline__ void load(u32x4 (&r)[N]) {
+    // piece n of the stage from memory, of the last stage to LDS
+    __device__ __forceinline__ u32x4 load(int n) const {
       const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, kRange, 0x00027000);
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const uint32_t at = (ALONG ? k0 : k0 + n * kApart) < left ? off[n] : 0xffffffffu;
-        r[n] = __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
-      }
+      const uint32_t at = (ALONG ? k0 : k0 + n * kApart) < left ? off[n] : 0xffffffffu;
+      return __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, 0);
+    }
+    __device__ __forceinline__ void advance() {
       base += step;
       left -= kStep;
     }
-    __device__ static __forceinline__ void store(char* lds, const u32x4 (&r)[N], int tid) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(lds + (n * kThreads + tid) * 16) = r[n];
+    __device__ static __forceinline__ void store(char* lds, int n, const u32x4& r, int tid) {
+      *reinterpret_cast<u32x4*>(lds + (n * kThreads + tid) * 16) = r;
     }
   };
 
@@ -153,11 +152,29 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
       for (int j = 0; j < NI; ++j) acc[i][j] = Mma<T>::mma(f.a[kk & 1][i], f.b[kk & 1][j], acc[i][j]);
   }
 
+  // The order of a quarter's instructions: its reads go out among the first
+  // products, two before each, the stage's pieces (one write to LDS, one load)
+  // among the others, so that none of them holds the matrix unit up.
+  static constexpr int kReads = (MI * (A_ALONG ? 1 : (sizeof(T) == 2 ? 2 : 4)) + NI * (B_ALONG ? 1 : (sizeof(T) == 2 ? 2 : 4)));
+  static constexpr int kProducts = MI * NI * (sizeof(T) == 2 ? 1 : 4);
+  static constexpr int kEach = 2 * kReads > kProducts ? (2 * kReads + kProducts - 1) / kProducts : 1;
+  template <int READS, int PIECES, int PRODUCTS> __device__ static __forceinline__ void weave() {
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS < kEach ? READS : kEach, 0);
+    if constexpr (PRODUCTS > 0) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr bool move = PIECES > 0 && (PRODUCTS <= PIECES || READS <= kEach);
+    if constexpr (move) {
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+    if constexpr (READS > 0 || PIECES > 0 || PRODUCTS > 0)
+      weave<(READS > kEach ? READS - kEach : 0), (move ? PIECES - 1 : PIECES), (PRODUCTS > 0 ? PRODUCTS - 1 : 0)>();
+  }
+
   // acc += A[m0 ..][k .. kend) B[k .. kend)[n0 ..]; all threads of the workgroup.
   // A stage in four quarters, the fragments of the next one read before the
-  // products of each. In the third the next stage, loaded a whole stage ago, goes
-  // to the other buffer and the one after it is asked for; the barrier comes
-  // before the last quarter's products, whose fragments are in registers by
+  // products of each. In the first three the next stage, loaded a whole stage
+  // ago, goes to the other buffer and the one after it is asked for; the barrier
+  // comes before the last quarter's products, whose fragments are in registers by
   // then, and they cover the first reads of the next stage.
   __device__ static __forceinline__ void run(const Operand<T>& A, const Operand<T>& B, int64_t m0, int64_t n0,
                                              int64_t k, int64_t kend, char* lds, f32x16 (&acc)[MI][NI]) {
@@ -169,41 +186,54 @@ template <typename T, bool A_ALONG, bool B_ALONG, int BM, int BN, int WM, int kW
     ma.set(A, m0, k, kend, tid);
     mb.set(B, n0, k, kend, tid);
     const int stages = static_cast<int>((kend - k + kStep - 1) / kStep);
-    u32x4 ra[kPA], rb[kPB];
+    constexpr int kPieces = kPA + kPB;
+    u32x4 r[kPieces];
+    auto load = [&](int n) { r[n] = n < kPA ? ma.load(n < kPA ? n : 0) : mb.load(n < kPA ? 0 : n - kPA); };
+    auto store = [&](char* to, int n) {
+      if (n < kPA) ma.store(to, n, r[n], tid);
+      else mb.store(to + kA, n - kPA, r[n], tid);
+    };
+    auto fence = []() { __builtin_amdgcn_sched_barrier(0); };
     Frags f;
     int cur = 0;   // the stage in use: LDS offset
-    ma.load(ra);
-    mb.load(rb);
-    ma.store(lds, ra, tid);
-    mb.store(lds + kA, rb, tid);
-    ma.load(ra);   // past the end: zeros
-    mb.load(rb);
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) load(n);
+    ma.advance();
+    mb.advance();
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) store(lds, n);
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) load(n);   // past the end: zeros
+    ma.advance();
+    mb.advance();
     lds_barrier();
     read(lds, 0, wm, wn, lane, f);
-    // the compiler is kept from moving the reads behind the products
-    auto fence = []() { __builtin_amdgcn_sched_barrier(0); };
+    fence();
+    constexpr int kThird = (kPieces + 2) / 3, kLast = kPieces - 2 * kThird;
+    static_assert(kLast >= 0, "pieces over three quarters");
     for (int s = 1; s < stages; ++s) {
-      read(lds + cur, 1, wm, wn, lane, f);
-      fence();
-      multiply(0, f, acc);
-      fence();
-      read(lds + cur, 2, wm, wn, lane, f);
-      fence();
-      multiply(1, f, acc);
-      fence();
-      read(lds + cur, 3, wm, wn, lane, f);
+      const char* now = lds + cur;
       cur ^= kStage;
-      ma.store(lds + cur, ra, tid);
-      mb.store(lds + cur + kA, rb, tid);
-      ma.load(ra);
-      mb.load(rb);
-      fence();
-      multiply(2, f, acc);
-      fence();
+      char* next = lds + cur;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        read(now, q + 1, wm, wn, lane, f);
+#pragma unroll
+        for (int n = q * kThird; n < (q + 1) * kThird && n < kPieces; ++n) {
+          store(next, n);
+          load(n);
+        }
+        multiply(q, f, acc);
+        if (q < 2) weave<kReads, kThird, kProducts>();
+        else weave<kReads, kLast, kProducts>();
+        fence();
+      }
+      ma.advance();
+      mb.advance();
       lds_barrier();
-      read(lds + cur, 0, wm, wn, lane, f);
-      fence();
+      read(next, 0, wm, wn, lane, f);
       multiply(3, f, acc);
+      weave<kReads, 0, kProducts>();
       fence();
     }
     read(lds + cur, 1, wm, wn, lane, f);

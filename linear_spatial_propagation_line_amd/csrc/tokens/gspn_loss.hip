@@ -57,59 +57,78 @@ template <typename T> struct LossP {
   T* packed;           // [Tp][Dp]
   const T* w;          // the weight, or its packed copy
   int64_t wld;
-  float2* part;        // [tiles of V][Tp]: maximum and sum
+  float2* part;        // maximum and sum of tile m of V and place p: [m * part_m + p * part_p]
+  int64_t part_m, part_p;
   int64_t L, V, D, T_, Tp, Dp;
   int64_t block0;
 };
 
 // ---- tokens -----------------------------------------------------------------
 // One workgroup: the tokens that count in their order. Forward all but the
-// padding (whose results are set to 0 here), backward those with a target.
+// padding (whose results are set to 0 here), backward those with a target. Eight
+// tokens per lane and turn, all loaded before the first is used (8192 tokens: 5 us,
+// one at a time 14).
+template <typename P> __device__ __forceinline__ bool token_counts(const P& a, int64_t t, bool back, int32_t& target) {
+  const int64_t b = t / a.L, l = t - b * a.L;
+  if (l >= seq_len(a.lens, b, a.L)) return false;
+  const int64_t i = b * a.targets_batch + l;
+  const int64_t v = a.targets64 ? static_cast<const int64_t*>(a.targets)[i] : static_cast<const int32_t*>(a.targets)[i];
+  target = v >= 0 && v < a.V ? static_cast<int32_t>(v) : -1;
+  return !back || target >= 0;
+}
 template <typename P, bool BACK>
 __global__ __launch_bounds__(1024) void loss_list_kernel(P a) {
-  __shared__ int32_t sums[16];
+  constexpr int kRows = 8;
+  __shared__ int32_t sums[kRows][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int32_t done = 0;
-  for (int64_t t0 = 0; t0 < a.T_; t0 += 1024) {
-    const int64_t t = t0 + threadIdx.x;
-    bool keep = false;
-    int64_t target = -1;
-    if (t < a.T_) {
-      const int64_t b = t / a.L, l = t - b * a.L;
-      keep = l < seq_len(a.lens, b, a.L);
-      if (keep) {
-        const int64_t i = b * a.targets_batch + l;
-        target = a.targets64 ? static_cast<const int64_t*>(a.targets)[i] : static_cast<const int32_t*>(a.targets)[i];
-        if (target < 0 || target >= a.V) target = -1;
-        if (BACK) keep = target >= 0;
-      }
-    }
-    const uint64_t mask = __ballot(keep);
-    if (lane == 0) sums[wave] = __popcll(mask);
-    __syncthreads();
-    int32_t before = done, all = 0;
+  for (int64_t t0 = 0; t0 < a.T_; t0 += kRows * 1024) {
+    bool keep[kRows];
+    int32_t target[kRows];
+    float g[kRows], lse[kRows];
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? sums[w] : 0;
-      all += sums[w];
-    }
-    const int32_t at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
-    done += all;
-    if (keep) {
-      a.list.token[at] = static_cast<int32_t>(t);
-      a.list.target[at] = static_cast<int32_t>(target);
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t t = t0 + k * 1024 + threadIdx.x;
+      target[k] = -1;
+      keep[k] = t < a.T_ && token_counts(a, t, BACK, target[k]);
       if constexpr (BACK) {
-        a.list.g[at] = a.gloss[t];
-        a.list.lse[at] = a.glse[t];
-      }
-    } else if (t < a.T_) {
-      if constexpr (!BACK) {
-        a.loss[t] = 0.0f;
-        if (a.lse) a.lse[t] = 0.0f;
+        const int64_t c = t < a.T_ ? t : a.T_ - 1;
+        g[k] = a.gloss[c];
+        lse[k] = a.glse[c];
       }
     }
-    if constexpr (BACK)
-      if (t < a.T_) a.list.pos[t] = keep ? at : -1;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const uint64_t mask = __ballot(keep[k]);
+      if (lane == 0) sums[k][wave] = __popcll(mask);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t t = t0 + k * 1024 + threadIdx.x;
+      const uint64_t mask = __ballot(keep[k]);
+      int32_t at = done + __popcll(mask & ((uint64_t(1) << lane) - 1));
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        at += w < wave ? sums[k][w] : 0;
+        done += sums[k][w];
+      }
+      if (keep[k]) {
+        a.list.token[at] = static_cast<int32_t>(t);
+        a.list.target[at] = target[k];
+        if constexpr (BACK) {
+          a.list.g[at] = g[k];
+          a.list.lse[at] = lse[k];
+        }
+      } else if (t < a.T_) {
+        if constexpr (!BACK) {
+          a.loss[t] = 0.0f;
+          if (a.lse) a.lse[t] = 0.0f;
+        }
+      }
+      if constexpr (BACK)
+        if (t < a.T_) a.list.pos[t] = keep[k] ? at : -1;
+    }
     __syncthreads();
   }
   if (threadIdx.x == 0) *a.list.count = done;
@@ -122,6 +141,38 @@ __global__ __launch_bounds__(1024) void loss_list_kernel(P a) {
       a.list.at[p] = 0.0f;
     }
   }
+}
+
+// Few tokens: list and rows in one launch. Workgroup p finds the tokens that count
+// among the first 64 by itself and packs the p-th's row; the first writes the list.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_few_kernel(LossP<T> a, int wide) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int lane = threadIdx.x & 63, p = blockIdx.x;
+  int32_t target = -1;
+  const bool keep = lane < a.T_ && token_counts(a, lane, false, target);
+  const uint64_t mask = __ballot(keep);
+  const int count = __popcll(mask);
+  if (p == 0 && threadIdx.x < 64) {
+    if (lane == 0) *a.list.count = count;
+    if (keep) {
+      const int at = __popcll(mask & ((uint64_t(1) << lane) - 1));
+      a.list.token[at] = lane;
+      a.list.target[at] = target;
+    } else if (lane < a.T_) {
+      a.loss[lane] = 0.0f;
+      if (a.lse) a.lse[lane] = 0.0f;
+    }
+    if (lane >= count) a.list.target[lane] = -1;
+  }
+  uint64_t rest = mask;
+  for (int k = 0; k < p; ++k) rest &= rest - 1;
+  const bool some = p < count;
+  const int64_t t = some ? __builtin_ctzll(rest) : 0, b = t / a.L;
+  const T* src = a.x + b * a.xb + (t - b * a.L) * a.xr;
+  for (int64_t at = threadIdx.x * kPer; at < a.Dp; at += 256 * kPer)
+    *reinterpret_cast<u32x4*>(a.packed + p * a.Dp + at) =
+        load16<T, false>(src, static_cast<int>(at), some ? static_cast<int>(a.D) : 0, wide);
 }
 
 // Rows packed to Dp values, 16 bytes per lane, zeros past D and for places
@@ -163,6 +214,13 @@ __device__ __forceinline__ TilePlace tile_place(int64_t g, int64_t mt, int64_t n
   return TilePlace{band * 8 + in % high, in / high};
 }
 int64_t tile_blocks(int64_t mt, int64_t nt) { return cdiv(mt * nt, 8) * 8; }
+
+// (top, sum) of exponentials joined with another pair of them
+__device__ __forceinline__ void join_sums(float& top, float& sum, float t, float u) {
+  const float high = fmaxf(top, t), base = high == -INFINITY ? 0.0f : high;
+  sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + u * __builtin_amdgcn_exp2f((t - base) * kLog2e);
+  top = high;
+}
 
 template <typename T, int BM, int BN, int WM, int NW>
 __global__ __launch_bounds__(64 * NW) void loss_logits_kernel(LossP<T> a, int64_t mt, int64_t nt) {
@@ -215,14 +273,16 @@ __global__ __launch_bounds__(64 * NW) void loss_logits_kernel(LossP<T> a, int64_
   for (int col = threadIdx.x; col < BN; col += 64 * NW) {
     float2 s = red[col];
 #pragma unroll
-    for (int w = 1; w < WM; ++w) {
-      const float2 o = red[w * BN + col];
-      const float top = fmaxf(s.x, o.x), base = top == -INFINITY ? 0.0f : top;
-      s.y = s.y * __builtin_amdgcn_exp2f((s.x - base) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - base) * kLog2e);
-      s.x = top;
-    }
-    a.part[at.m * a.Tp + n0 + col] = s;
+    for (int w = 1; w < WM; ++w) join_sums(s.x, s.y, red[w * BN + col].x, red[w * BN + col].y);
+    a.part[at.m * a.part_m + (n0 + col) * a.part_p] = s;
   }
+}
+
+template <typename P> __device__ __forceinline__ void write_loss(const P& a, int64_t p, float top, float sum) {
+  const float lse = top + __builtin_amdgcn_logf(sum) * kLn2;
+  const int64_t t = a.list.token[p];
+  a.loss[t] = a.list.target[p] >= 0 ? lse - a.list.at[p] : 0.0f;
+  if (a.lse) a.lse[t] = lse;
 }
 
 // lse and loss from the tiles' maxima and sums: 64 tokens by 8 wavefronts,
@@ -239,7 +299,7 @@ __global__ __launch_bounds__(512) void loss_join_kernel(LossP<T> a, int64_t mt) 
   for (int64_t m = m0; m < m1; m += kAhead) {
     float2 s[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) s[k] = a.part[(m + k < m1 ? m + k : m1 - 1) * a.Tp + p];
+    for (int k = 0; k < kAhead; ++k) s[k] = a.part[(m + k < m1 ? m + k : m1 - 1) * a.part_m + p];
     float t = top;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) t = fmaxf(t, s[k].x);
@@ -255,15 +315,40 @@ __global__ __launch_bounds__(512) void loss_join_kernel(LossP<T> a, int64_t mt) 
   if (wave != 0 || p >= all) return;
 #pragma unroll
   for (int w = 1; w < 8; ++w) {
-    const float2 o = red[w][lane];
-    const float t = fmaxf(top, o.x), base = t == -INFINITY ? 0.0f : t;
-    sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - base) * kLog2e);
-    top = t;
+    join_sums(top, sum, red[w][lane].x, red[w][lane].y);
   }
-  const float lse = top + __builtin_amdgcn_logf(sum) * kLn2;
-  const int64_t t = a.list.token[p];
-  a.loss[t] = a.list.target[p] >= 0 ? lse - a.list.at[p] : 0.0f;
-  if (a.lse) a.lse[t] = lse;
+  write_loss(a, p, top, sum);
+}
+
+// The same for few tokens, a workgroup for each: its tiles' values lie side by side
+template <typename T>
+__global__ __launch_bounds__(256) void loss_join_few_kernel(LossP<T> a, int64_t mt) {
+  __shared__ float2 red[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t p = blockIdx.x;
+  if (p >= *a.list.count) return;
+  float top = -INFINITY, sum = 0.0f;
+  for (int64_t m0 = 0; m0 < mt; m0 += 4 * 256) {
+    float2 s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t m = m0 + k * 256 + threadIdx.x;
+      s[k] = m < mt ? a.part[p * a.part_p + m] : make_float2(-INFINITY, 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) join_sums(top, sum, s[k].x, s[k].y);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const float t = __shfl_xor(top, k, 64), u = __shfl_xor(sum, k, 64);
+    join_sums(top, sum, t, u);
+  }
+  if (lane == 0) red[wave] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) join_sums(top, sum, red[w].x, red[w].y);
+  write_loss(a, p, top, sum);
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -421,41 +506,49 @@ __global__ __launch_bounds__(256) void loss_target_kernel(LossP<T> a) {
 }
 
 // G at the targets times the tokens' rows, summed for each target: row start[v]
-// of `rest`. Tokens come sorted by target; a workgroup
-// owns kRestChunk of them and 256 columns. A run that lies within the chunk
+// of `rest`. Tokens come sorted by target; a wavefront owns kRestChunk of them and
+// 64 kRestWide columns. A run that lies within the chunk
 // is finished here, one that goes past it leaves its part (begun before the chunk:
 // slot 0, in it: slot 1) for the join.
-constexpr int kRestChunk = 32;
+constexpr int kRestChunk = 16;
+constexpr int kRestWide = 4;   // columns per lane (Dp is a multiple of 32)
 template <typename T>
-__global__ __launch_bounds__(256) void loss_rest_kernel(LossP<T> a, TokenSort s, float* rest, float* part, int64_t slices) {
-  const int64_t g = a.block0 + blockIdx.x, c = g / slices, col = (g - c * slices) * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void loss_rest_kernel(LossP<T> a, TokenSort s, float* rest, float* part) {
+  // four chunks of 64 lanes' columns per workgroup
+  const int64_t slices = (a.Dp + 64 * kRestWide - 1) / (64 * kRestWide), chunks = (a.Tp + kRestChunk - 1) / kRestChunk;
+  const int64_t g = (a.block0 + blockIdx.x) * 4 + (threadIdx.x >> 6), slice = g / chunks, c = g - slice * chunks;
+  const int64_t col = (slice * 64 + (threadIdx.x & 63)) * kRestWide;
   const int64_t all = s.start[a.V], p0 = c * kRestChunk;
-  if (p0 >= all || col >= a.Dp) return;
+  if (slice >= slices || p0 >= all || col >= a.Dp) return;
   const int64_t p1 = p0 + kRestChunk < all ? p0 + kRestChunk : all;
-  float sum = 0.0f;
+  float sum[kRestWide] = {};
   constexpr int kAhead = 8;
-  for (int64_t p = p0; p < p1; p += kAhead) {
-    float d[kAhead], w[kAhead];
-    int32_t row[kAhead + 1];
+#pragma unroll
+  for (int k0 = 0; k0 < kRestChunk; k0 += kAhead) {
+    const int64_t p = p0 + k0;
+    if (p >= p1) break;
+    float d[kAhead][kRestWide], w[kAhead];
+    int32_t r0[kAhead], r1[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int64_t q = p + k < p1 ? p + k : p1 - 1;
-      const int64_t place = s.token[q];
-      row[k] = s.row[q];
+      const int64_t place = s.token[q], row = s.row[q];
+      r0[k] = s.start[row];
+      r1[k] = s.start[row + 1];
       w[k] = a.list.at[place];
-      d[k] = to_f32(a.packed[place * a.Dp + col]);
+      ldv<kRestWide>(a.packed + place * a.Dp + col, d[k]);
     }
-    row[kAhead] = p + kAhead < p1 ? s.row[p + kAhead] : -1;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (p + k >= p1) break;
-      sum = __builtin_fmaf(w[k], d[k], sum);
-      if (p + k + 1 < p1 && row[k + 1] == row[k]) continue;
+#pragma unroll
+      for (int e = 0; e < kRestWide; ++e) sum[e] = __builtin_fmaf(w[k], d[k][e], sum[e]);
+      if (p + k + 1 < p1 && p + k + 1 < r1[k]) continue;
       // the run ends here or goes on after the chunk
-      const int64_t r0 = s.start[row[k]], r1 = s.start[row[k] + 1];
-      if (r0 >= p0 && r1 <= p1) rest[r0 * a.Dp + col] = sum;
-      else part[(c * 2 + (r0 >= p0 ? 1 : 0)) * a.Dp + col] = sum;
-      sum = 0.0f;
+      if (r0[k] >= p0 && r1[k] <= p1) stv<kRestWide>(rest + r0[k] * a.Dp + col, sum);
+      else stv<kRestWide>(part + (c * 2 + (r0[k] >= p0 ? 1 : 0)) * a.Dp + col, sum);
+#pragma unroll
+      for (int e = 0; e < kRestWide; ++e) sum[e] = 0.0f;
     }
   }
 }
@@ -482,18 +575,29 @@ __global__ __launch_bounds__(256) void loss_rest_join_kernel(LossP<T> a, TokenSo
 }
 
 // dx: the splits' sums and the target's part, rounded once; zeros for tokens
-// that do not count
-template <typename T>
+// that do not count. V adjacent values per lane.
+template <typename T, int V>
 __global__ __launch_bounds__(256) void loss_dx_kernel(LossP<T> a, const float* parts, int64_t splits, T* dx) {
-  const int64_t i = (a.block0 + blockIdx.x) * 256 + threadIdx.x, t = i / a.D, col = i - t * a.D;
+  const int64_t per = a.D / V, first = (a.block0 + blockIdx.x) * 256, t0 = first / per;
+  const uint32_t i = static_cast<uint32_t>(first - t0 * per) + threadIdx.x;
+  const uint32_t up = i / static_cast<uint32_t>(per);
+  const int64_t t = t0 + up, col = static_cast<int64_t>(i - up * static_cast<uint32_t>(per)) * V;
   if (t >= a.T_) return;
   const int64_t p = a.list.pos[t];
-  float s = 0.0f;
+  float s[V] = {};
   if (p >= 0) {
-    for (int64_t k = 0; k < splits; ++k) s += parts[(k * a.Tp + p) * a.Dp + col];
-    s = __builtin_fmaf(a.list.at[p], to_f32(a.w[a.list.target[p] * a.wld + col]), s);
+    float w[V];
+    ldv<V>(a.w + a.list.target[p] * a.wld + col, w);
+    for (int64_t k = 0; k < splits; ++k) {
+      float y[V];
+      ldv<V>(parts + (k * a.Tp + p) * a.Dp + col, y);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] += y[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(a.list.at[p], w[e], s[e]);
   }
-  Store<T>::put(dx, t * a.D + col, s);
+  stv<V>(dx + t * a.D + col, s);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -609,8 +713,11 @@ template <typename T> LossP<T> loss_params(const gspn_loss_args& a) {
 }
 
 template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stream, Tracer* tr) {
-  tr->before(stream, "loss_list", p.T_);
-  hipLaunchKernelGGL((loss_list_kernel<LossP<T>, BACK>), dim3(1), dim3(1024), 0, stream, p);
+  const bool few = !BACK && p.T_ <= kFewTile;
+  const int wide_x = wide_ok(p.x, 16, sizeof(T), {p.xb, p.xr}) && p.D % (16 / static_cast<int64_t>(sizeof(T))) == 0;
+  tr->before(stream, few ? "loss_few" : "loss_list", p.T_);
+  if (few) hipLaunchKernelGGL((loss_few_kernel<T>), dim3(kFewTile), dim3(256), 0, stream, p, wide_x);
+  else hipLaunchKernelGGL((loss_list_kernel<LossP<T>, BACK>), dim3(1), dim3(1024), 0, stream, p);
   hipError_t e = hipGetLastError();
   tr->after(stream);
   if (e != hipSuccess) return e;
@@ -624,7 +731,7 @@ template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stre
     tr->after(stream);
     return r;
   };
-  if ((e = pack(p.x, p.xb, p.xr, p.Tp, p.list.token, p.packed)) != hipSuccess) return e;
+  if (!few && (e = pack(p.x, p.xb, p.xr, p.Tp, p.list.token, p.packed)) != hipSuccess) return e;
   if (p.w != p.weight) e = pack(p.weight, 0, p.D, p.V, nullptr, const_cast<T*>(p.w));
   return e;
 }
@@ -640,6 +747,8 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   const bool few = p.T_ <= kFewTile;
   const int64_t tile = tile_for(p.V, p.T_);
   const int64_t mt = cdiv(p.V, few ? kFewRows : tile), nt = few ? 1 : cdiv(p.T_, tile);
+  p.part_m = few ? 1 : p.Tp;
+  p.part_p = few ? mt : 1;
   tr->before(stream, "loss_logits", p.V);
   e = in_parts(tile_blocks(mt, nt), [&](int64_t first, unsigned count) {
     p.block0 = first;
@@ -650,6 +759,13 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   });
   tr->after(stream);
   if (e != hipSuccess) return e;
+  if (few) {
+    tr->before(stream, "loss_join_few", p.T_);
+    hipLaunchKernelGGL((loss_join_few_kernel<T>), dim3(static_cast<unsigned>(p.T_)), dim3(256), 0, stream, p, mt);
+    e = hipGetLastError();
+    tr->after(stream);
+    return e;
+  }
   tr->before(stream, "loss_join", p.T_);
   e = in_parts(cdiv(p.T_, 64), [&](int64_t first, unsigned count) {
     p.block0 = first;
@@ -685,8 +801,8 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   };
   e = launch("loss_target", cdiv(p.T_, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
   if (e != hipSuccess) return e;
-  e = launch("loss_rest", cdiv(p.Tp, kRestChunk) * slices, [&](dim3 n) {
-    hipLaunchKernelGGL((loss_rest_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part, slices);
+  e = launch("loss_rest", cdiv(cdiv(p.Tp, kRestChunk) * cdiv(p.Dp, 64 * kRestWide), 4), [&](dim3 n) {
+    hipLaunchKernelGGL((loss_rest_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part);
   });
   if (e != hipSuccess) return e;
   e = launch("loss_rest_join", cdiv(p.Tp, kRestChunk) * slices, [&](dim3 n) {
@@ -715,8 +831,12 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
     });
     if (e != hipSuccess) return e;
   }
-  return launch("loss_dx", cdiv(p.T_ * p.D, 256), [&](dim3 n) {
-    hipLaunchKernelGGL((loss_dx_kernel<T>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
+  // whole pieces of x's gradient where its rows allow them
+  constexpr int kPer = 16 / sizeof(T);
+  const bool wide = p.D % kPer == 0 && wide_ok(g.x, 16, sizeof(T), {});
+  return launch("loss_dx", cdiv(p.T_ * (wide ? p.D / kPer : p.D), 256), [&](dim3 n) {
+    if (wide) hipLaunchKernelGGL((loss_dx_kernel<T, kPer>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
+    else hipLaunchKernelGGL((loss_dx_kernel<T, 1>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
   });
 }
 

@@ -61,27 +61,46 @@ template <typename T> struct GatedP {
 __device__ __forceinline__ float gate_f32(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
 }
-// A gate kept as exp(-|v|) with v's sign: sigmoid(v) and 1 - sigmoid(v), each
-// to its own digits, are 1 and x over 1 + x, in an order that the sign gives.
-__device__ __forceinline__ float gate_keep(float v) {
-  return __builtin_copysignf(__builtin_amdgcn_exp2f(fabsf(v) * -kLog2e), v);
+// The same and 1 - it, each to its own digits; the exponential is kept finite, so
+// far below zero the gate is 2^-126.
+__device__ __forceinline__ void gate_both(float v, float& open, float& shut) {
+  const float t = __builtin_amdgcn_exp2f(fminf(v * -kLog2e, 126.0f));
+  open = __builtin_amdgcn_rcpf(1.0f + t);
+  shut = t * open;
 }
-__device__ __forceinline__ void gate_open(float x, float& open, float& shut) {
-  const float q = __builtin_amdgcn_rcpf(1.0f + fabsf(x)), xq = fabsf(x) * q;
-  const bool below = __float_as_int(x) < 0;
-  open = below ? xq : q;
-  shut = below ? q : xq;
-}
-// sqrt(1 - a^2) from e = a - 1; 0 where a = 1 to within the smallest normal number
+// 1 - a^2 from e = a - 1 <= 0
 __device__ __forceinline__ float left_f32(float e) { return -e * (2.0f + e); }
-__device__ __forceinline__ float beta_f32(float e) {
-  const float q = left_f32(e);
-  return q > 1.17549435e-38f ? __builtin_amdgcn_sqrtf(q) : 0.0f;
+
+// N rows of a [L, C] tensor's tile from row t on, clamped to the last of n > 0:
+// the row's address is uniform, the lane's place in it `off` bytes
+template <int N, typename T, int V>
+__device__ __forceinline__ void load_rows(const T* tile, int64_t stride, int64_t t, int64_t n, uint32_t off,
+                                          Raw<T, V> (&r)[N]) {
+  const char* p = reinterpret_cast<const char*>(tile + t * stride);
+  const int64_t step = stride * static_cast<int64_t>(sizeof(T));
+  if (t + N <= n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(reinterpret_cast<const T*>(p + off));
+      p += step;
+    }
+  } else {
+    const int some = static_cast<int>(n - t);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      r[k].load(reinterpret_cast<const T*>(p + off));
+      if (k + 1 < some) p += step;
+    }
+  }
 }
+template <int V, typename T> __device__ __forceinline__ void put_row(T* row, uint32_t off, const float (&y)[V]) {
+  stv<V>(reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off), y);
+}
+
 // zeros in `rows` rows of V values
-template <int V, typename T> __device__ __forceinline__ void zero_rows(T* p, int64_t stride, int rows) {
+template <int V, typename T> __device__ __forceinline__ void zero_rows(T* p, int64_t stride, int rows, uint32_t off) {
   const float zero[V] = {};
-  for (int k = 0; k < rows; ++k) stv<V>(p + k * stride, zero);
+  for (int k = 0; k < rows; ++k) put_row<V>(p + k * stride, off, zero);
 }
 
 // the published forms
@@ -147,22 +166,22 @@ template <typename P> __device__ __forceinline__ Place take_place(const P& a, ui
 }
 
 template <typename T, int V>
-__global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
+__global__ __launch_bounds__(64 * kChunk / kRunF) void gated_kernel(GatedP<T> a) {
   constexpr int kWaves = kChunk / kRunF;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], before[64 * V];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = take_place(a, &slot);
   const int64_t n = seq_len(a.lens, at.b, a.L), t0 = at.q * kChunk + wave * kRunF;
-  const int64_t c = (at.ct * 64 + lane) * V;
+  const int64_t c0 = at.ct * 64 * V, c = c0 + lane * V;
   const bool mine = c < a.C;
-  const int64_t cc = mine ? c : 0;
+  const uint32_t place = mine ? lane * V : 0, off = place * sizeof(T);   // lanes past the channels read the first
   const int rows = static_cast<int>(a.L - t0 < 0 ? 0 : (a.L - t0 < kRunF ? a.L - t0 : kRunF));
   const int live = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kRunF ? n - t0 : kRunF));
-  T* o = a.out + (at.b * a.L + t0) * a.C + cc;
+  T* o = a.out + (at.b * a.L + t0) * a.C + c0;
   // a chunk of padding has nothing to hand on: those behind it are padding too
   if (at.q * kChunk >= n && at.q > 0) {
-    if (a.out && mine) zero_rows<V>(o, a.C, rows);
+    if (a.out && mine) zero_rows<V>(o, a.C, rows, off);
     return;
   }
   float decay[kRunF][V], bu[kRunF][V], P[V], H[V];
@@ -173,12 +192,12 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
   }
   if (live > 0) {
     Raw<T, V> x[kRunF], r[kRunF], i[kRunF];
-    load_run(a.r + at.b * a.rb + cc, a.rr, t0, n, r);
-    load_run(a.i + at.b * a.ib + cc, a.ir, t0, n, i);
-    load_run(a.x + at.b * a.xb + cc, a.xr, t0, n, x);
+    load_rows(a.r + at.b * a.rb + c0, a.rr, t0, n, off, r);
+    load_rows(a.i + at.b * a.ib + c0, a.ir, t0, n, off, i);
+    load_rows(a.x + at.b * a.xb + c0, a.xr, t0, n, off, x);
     float A[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = a.A[cc + v];
+    for (int v = 0; v < V; ++v) A[v] = a.A[c0 + place + v];
 #pragma unroll
     for (int k = 0; k < kRunF; ++k) {
       float xv[V], rv[V], iv[V];
@@ -187,14 +206,27 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
       i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float ev = expm1_f32(A[v] * gate_f32(rv[v]));
-        const float bv = beta_f32(ev) * gate_f32(iv[v]) * xv[v];
-        decay[k][v] = k < live ? 1.0f + ev : 1.0f;
-        bu[k][v] = k < live ? bv : 0.0f;
+        const float e = expm1_f32(A[v] * gate_f32(rv[v]));
+        decay[k][v] = 1.0f + e;
+        bu[k][v] = __builtin_amdgcn_sqrtf(left_f32(e)) * gate_f32(iv[v]) * xv[v];
+      }
+    }
+    if (live < kRunF) {   // padding leaves the state
+#pragma unroll
+      for (int k = 0; k < kRunF; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          decay[k][v] = k < live ? decay[k][v] : 1.0f;
+          bu[k][v] = k < live ? bu[k][v] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRunF; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         H[v] = __builtin_fmaf(decay[k][v], H[v], bu[k][v]);
         P[v] *= decay[k][v];
       }
-    }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -206,7 +238,7 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
   if (threadIdx.x < 64 * V) {
     // one channel per lane
     const int j = threadIdx.x;
-    const int64_t ch = at.ct * 64 * V + j, base = at.chain * a.chunks * stride + j;
+    const int64_t ch = c0 + j, base = at.chain * a.chunks * stride + j;
     float p = 1.0f, h = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -237,7 +269,7 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
     for (int w = 0; w < wave; ++w) h[v] = __builtin_fmaf(sp[w][lane * V + v], h[v], sh[w][lane * V + v]);
   }
   if (live == 0) {
-    zero_rows<V>(o, a.C, rows);
+    zero_rows<V>(o, a.C, rows, off);
     return;
   }
 #pragma unroll
@@ -248,7 +280,7 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedP<T> a) {
       h[v] = __builtin_fmaf(decay[k][v], h[v], bu[k][v]);
       y[v] = k < live ? h[v] : 0.0f;
     }
-    if (k < rows) stv<V>(o, y);
+    if (k < rows) put_row<V>(o, off, y);
     o += a.C;
   }
 }
@@ -282,7 +314,7 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float e = expm1_f32(A[v] * gate_f32(rv[v]));
-        h[v] = __builtin_fmaf(1.0f + e, h[v], beta_f32(e) * gate_f32(iv[v]) * xv[v]);
+        h[v] = __builtin_fmaf(1.0f + e, h[v], __builtin_amdgcn_sqrtf(left_f32(e)) * gate_f32(iv[v]) * xv[v]);
         y[v] = h[v];
       }
     }
@@ -296,29 +328,29 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
 // Backward: chunks from the last; what is handed on is a_t g_t, by the same
 // rule. The states within the chunk are found again from the one before it.
 template <typename T, int V>
-__global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
+__global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T> a) {
   constexpr int kWaves = kChunk / kRunB;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], sg[kWaves][64 * V], after[64 * V];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = take_place(a, &slot);
   const int64_t q = a.chunks - 1 - at.q;
   const int64_t n = seq_len(a.lens, at.b, a.L), t0 = q * kChunk + wave * kRunB;
-  const int64_t c = (at.ct * 64 + lane) * V;
+  const int64_t c0 = at.ct * 64 * V, c = c0 + lane * V;
   const bool mine = c < a.C;
-  const int64_t cc = mine ? c : 0;
+  const uint32_t place = mine ? lane * V : 0, off = place * sizeof(T);
   const int rows = static_cast<int>(a.L - t0 < 0 ? 0 : (a.L - t0 < kRunB ? a.L - t0 : kRunB));
   const int live = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kRunB ? n - t0 : kRunB));
-  const int64_t to = (at.b * a.L + t0) * a.C + cc;
+  const int64_t to = (at.b * a.L + t0) * a.C + c0;
   const int64_t row = (at.b * a.chunks + q) * a.C;
   if (q * kChunk >= n) {   // padding, nothing is handed on
     if (mine) {
-      zero_rows<V>(a.dx + to, a.C, rows);
-      zero_rows<V>(a.dr + to, a.C, rows);
-      zero_rows<V>(a.di + to, a.C, rows);
+      zero_rows<V>(a.dx + to, a.C, rows, off);
+      zero_rows<V>(a.dr + to, a.C, rows, off);
+      zero_rows<V>(a.di + to, a.C, rows, off);
     }
     if (threadIdx.x < 64 * V) {
-      const int64_t ch = at.ct * 64 * V + threadIdx.x;
+      const int64_t ch = c0 + threadIdx.x;
       if (ch < a.C) {
         a.part[row + ch] = 0.0f;
         if (n == 0 && q == 0 && a.dstate) a.dstate[at.b * a.C + ch] = a.gstate ? a.gstate[at.b * a.C + ch] : 0.0f;
@@ -326,38 +358,53 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
     }
     return;
   }
-  float e[kRunB][V], s[kRunB][V], w[kRunB][V], P[V], H[V], G[V], A[V];
+  // kept of every token: e = a - 1, beta sigmoid(i), 1 - sigmoid(i), s, 1 - s, and x and grad_out as stored
+  float e[kRunB][V], bw[kRunB][V], wshut[kRunB][V], s[kRunB][V], sshut[kRunB][V], P[V], H[V], G[V], A[V];
   Raw<T, V> x[kRunB], gy[kRunB];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     P[v] = 1.0f;
     H[v] = G[v] = 0.0f;
-    A[v] = a.A[cc + v];
+    A[v] = a.A[c0 + place + v];
   }
   if (live > 0) {
     Raw<T, V> r[kRunB], i[kRunB];
-    load_run(a.r + at.b * a.rb + cc, a.rr, t0, n, r);
-    load_run(a.i + at.b * a.ib + cc, a.ir, t0, n, i);
-    load_run(a.x + at.b * a.xb + cc, a.xr, t0, n, x);
-    load_run(a.gy + at.b * a.gb + cc, a.gr, t0, n, gy);
+    load_rows(a.r + at.b * a.rb + c0, a.rr, t0, n, off, r);
+    load_rows(a.i + at.b * a.ib + c0, a.ir, t0, n, off, i);
+    load_rows(a.x + at.b * a.xb + c0, a.xr, t0, n, off, x);
+    load_rows(a.gy + at.b * a.gb + c0, a.gr, t0, n, off, gy);
 #pragma unroll
     for (int k = 0; k < kRunB; ++k) {
-      float xv[V], rv[V], iv[V];
-      x[k].wide(xv);
+      float rv[V], iv[V];
       r[k].wide(rv);
       i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s[k][v] = gate_keep(rv[v]);
-        w[k][v] = gate_keep(iv[v]);
-        float sv, wv, shut;
-        gate_open(s[k][v], sv, shut);
-        gate_open(w[k][v], wv, shut);
-        const float ev = expm1_f32(A[v] * sv);
-        const float bv = beta_f32(ev) * wv * xv[v];
-        e[k][v] = k < live ? ev : 0.0f;
+        float w;
+        gate_both(rv[v], s[k][v], sshut[k][v]);
+        gate_both(iv[v], w, wshut[k][v]);
+        e[k][v] = expm1_f32(A[v] * s[k][v]);
+        bw[k][v] = __builtin_amdgcn_sqrtf(left_f32(e[k][v])) * w;
+      }
+    }
+    if (live < kRunB) {
+      // padding: no decay, no input, no gradient; its x and grad_out are the last token's
+#pragma unroll
+      for (int k = 0; k < kRunB; ++k)
+        if (k >= live) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) e[k][v] = bw[k][v] = 0.0f;
+          gy[k] = Raw<T, V>{};
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRunB; ++k) {
+      float xv[V];
+      x[k].wide(xv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         const float av = 1.0f + e[k][v];
-        H[v] = __builtin_fmaf(av, H[v], k < live ? bv : 0.0f);
+        H[v] = __builtin_fmaf(av, H[v], bw[k][v] * xv[v]);
         P[v] *= av;
       }
     }
@@ -366,10 +413,7 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
       float gv[V];
       gy[k].wide(gv);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = k < live ? G[v] + gv[v] : G[v];
-        G[v] = (1.0f + e[k][v]) * g;
-      }
+      for (int v = 0; v < V; ++v) G[v] = (1.0f + e[k][v]) * (G[v] + gv[v]);
     }
   }
 #pragma unroll
@@ -382,7 +426,7 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
   const int64_t stride = 64 * V;
   if (threadIdx.x < 64 * V) {
     const int j = threadIdx.x;
-    const int64_t ch = at.ct * 64 * V + j, base = at.chain * a.chunks * stride + j;
+    const int64_t ch = c0 + j, base = at.chain * a.chunks * stride + j;
     float p = 1.0f, g = 0.0f;
 #pragma unroll
     for (int k = kWaves - 1; k >= 0; --k) {
@@ -408,7 +452,7 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int j = lane * V + v;
-    h[v] = mine ? a.saved[row + cc + v] : 0.0f;
+    h[v] = a.saved[row + c0 + place + v];
     for (int k = 0; k < wave; ++k) h[v] = __builtin_fmaf(sp[k][j], h[v], sh[k][j]);
     g[v] = after[j];
     for (int k = kWaves - 1; k > wave; --k) g[v] = __builtin_fmaf(sp[k][j], g[v], sg[k][j]);
@@ -422,10 +466,8 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
       x[k].wide(xv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float wv, shut;
-        gate_open(w[k][v], wv, shut);
         hp[k][v] = h[v];
-        h[v] = __builtin_fmaf(1.0f + e[k][v], h[v], k < live ? beta_f32(e[k][v]) * wv * xv[v] : 0.0f);
+        h[v] = __builtin_fmaf(1.0f + e[k][v], h[v], bw[k][v] * xv[v]);
       }
     }
     int64_t o = to + (kRunB - 1) * a.C;
@@ -436,44 +478,37 @@ __global__ __launch_bounds__(512) void gated_bwd_kernel(GatedP<T> a) {
       gy[k].wide(gv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float ev = e[k][v], av = 1.0f + ev, left = left_f32(ev);
-        float wv, sv, wshut, sshut;
-        gate_open(w[k][v], wv, wshut);
-        gate_open(s[k][v], sv, sshut);
-        const bool some = left > 1.17549435e-38f;
-        const float inv = some ? __builtin_amdgcn_rsqf(left) : 0.0f, beta = some ? left * inv : 0.0f;
+        // (a^2 / beta) u = a^2 (beta u) / (1 - a^2); 0 where a is 1 to within the smallest normal number
+        const float av = 1.0f + e[k][v], left = left_f32(e[k][v]);
+        const float inv = left > 1.17549435e-38f ? __builtin_amdgcn_rcpf(left) : 0.0f;
         const float gt = g[v] + gv[v];
-        const float kk = gt * av * __builtin_fmaf(-av * inv, wv * xv[v], hp[k][v]);
-        const float du = gt * beta;
-        const float ks = kk * sv;
-        dx[v] = du * wv;
-        di[v] = dx[v] * xv[v] * wshut;
-        dr[v] = ks * A[v] * sshut;
-        if (k < live) {
-          dA[v] += ks;
-          g[v] = gt * av;
-        } else {
-          dx[v] = di[v] = dr[v] = 0.0f;
-        }
+        const float ga = gt * av;
+        const float ks = ga * __builtin_fmaf(-av * inv, bw[k][v] * xv[v], hp[k][v]) * s[k][v];
+        dx[v] = gt * bw[k][v];
+        di[v] = dx[v] * xv[v] * wshut[k][v];
+        dr[v] = ks * A[v] * sshut[k][v];
+        if (k < live) dA[v] += ks;   // padding leaves g and has dx = di = 0 already
+        else dr[v] = 0.0f;
+        g[v] = ga;
       }
       if (k < rows && mine) {
-        stv<V>(a.dx + o, dx);
-        stv<V>(a.dr + o, dr);
-        stv<V>(a.di + o, di);
+        put_row<V>(a.dx + o, off, dx);
+        put_row<V>(a.dr + o, off, dr);
+        put_row<V>(a.di + o, off, di);
       }
       o -= a.C;
     }
   } else if (mine) {
-    zero_rows<V>(a.dx + to, a.C, rows);
-    zero_rows<V>(a.dr + to, a.C, rows);
-    zero_rows<V>(a.di + to, a.C, rows);
+    zero_rows<V>(a.dx + to, a.C, rows, off);
+    zero_rows<V>(a.dr + to, a.C, rows, off);
+    zero_rows<V>(a.di + to, a.C, rows, off);
   }
   lds_barrier();
 #pragma unroll
   for (int v = 0; v < V; ++v) sp[wave][lane * V + v] = dA[v];
   lds_barrier();
   if (threadIdx.x < 64 * V) {
-    const int64_t ch = at.ct * 64 * V + threadIdx.x;
+    const int64_t ch = c0 + threadIdx.x;
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) sum += sp[k][threadIdx.x];
@@ -564,7 +599,7 @@ hipError_t gated_fwd(GatedP<T> p, void* ws, hipStream_t stream, Tracer* tr) {
   tr->before(stream, "gated", p.B);
   e = in_parts(p.B * p.ctiles * p.chunks, [&](int64_t first, unsigned count) {
     p.block0 = first;
-    hipLaunchKernelGGL((gated_kernel<T, V>), dim3(count), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((gated_kernel<T, V>), dim3(count), dim3(64 * kChunk / kRunF), 0, stream, p);
   });
   tr->after(stream);
   return e;
@@ -589,7 +624,7 @@ hipError_t gated_bwd(GatedP<T> p, const gspn_gated_grads& g, void* ws, hipStream
     tr->before(stream, "gated_bwd", p.B);
     e = in_parts(p.B * p.ctiles * p.chunks, [&](int64_t first, unsigned count) {
       p.block0 = first;
-      hipLaunchKernelGGL((gated_bwd_kernel<T, V>), dim3(count), dim3(512), 0, stream, p);
+      hipLaunchKernelGGL((gated_bwd_kernel<T, V>), dim3(count), dim3(64 * kChunk / kRunB), 0, stream, p);
     });
     tr->after(stream);
     if (e != hipSuccess) return e;

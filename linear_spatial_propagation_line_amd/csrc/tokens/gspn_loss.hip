@@ -69,7 +69,7 @@ template <typename T> struct LossP {
 // tokens per lane and turn, all loaded before the first is used (8192 tokens: 5 us,
 // one at a time 14).
 template <typename P> __device__ __forceinline__ bool token_counts(const P& a, int64_t t, bool back, int32_t& target) {
-  const int64_t b = t / a.L, l = t - b * a.L;
+  const int64_t b = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L), l = t - b * a.L;   // fewer than 2^28 tokens
   if (l >= seq_len(a.lens, b, a.L)) return false;
   const int64_t i = b * a.targets_batch + l;
   const int64_t v = a.targets64 ? static_cast<const int64_t*>(a.targets)[i] : static_cast<const int32_t*>(a.targets)[i];

@@ -166,7 +166,7 @@ template <typename P> __device__ __forceinline__ Place take_place(const P& a, ui
 }
 
 template <typename T, int V>
-__global__ __launch_bounds__(64 * kChunk / kRunF) void gated_kernel(GatedP<T> a) {
+__global__ __launch_bounds__(64 * kChunk / kRunF, 4) void gated_kernel(GatedP<T> a) {
   constexpr int kWaves = kChunk / kRunF;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], before[64 * V];
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
 // Backward: chunks from the last; what is handed on is a_t g_t, by the same
 // rule. The states within the chunk are found again from the one before it.
 template <typename T, int V>
-__global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T> a) {
+__global__ __launch_bounds__(64 * kChunk / kRunB, sizeof(T) == 2 || V == 1 ? 4 : 2) void gated_bwd_kernel(GatedP<T> a) {
   constexpr int kWaves = kChunk / kRunB;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], sg[kWaves][64 * V], after[64 * V];
@@ -358,9 +358,10 @@ __global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T
     }
     return;
   }
-  // kept of every token: e = a - 1, beta sigmoid(i), 1 - sigmoid(i), s, 1 - s, and x and grad_out as stored
-  float e[kRunB][V], bw[kRunB][V], wshut[kRunB][V], s[kRunB][V], sshut[kRunB][V], P[V], H[V], G[V], A[V];
-  Raw<T, V> x[kRunB], gy[kRunB];
+  // kept of every token: e = a - 1, beta sigmoid(i), and the inputs as stored, whose gates are opened
+  // again at the end (kept open they would take registers that a second workgroup lives from)
+  float e[kRunB][V], bw[kRunB][V], P[V], H[V], G[V], A[V];
+  Raw<T, V> x[kRunB], gy[kRunB], r[kRunB], i[kRunB];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     P[v] = 1.0f;
@@ -368,7 +369,6 @@ __global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T
     A[v] = a.A[c0 + place + v];
   }
   if (live > 0) {
-    Raw<T, V> r[kRunB], i[kRunB];
     load_rows(a.r + at.b * a.rb + c0, a.rr, t0, n, off, r);
     load_rows(a.i + at.b * a.ib + c0, a.ir, t0, n, off, i);
     load_rows(a.x + at.b * a.xb + c0, a.xr, t0, n, off, x);
@@ -380,11 +380,8 @@ __global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T
       i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float w;
-        gate_both(rv[v], s[k][v], sshut[k][v]);
-        gate_both(iv[v], w, wshut[k][v]);
-        e[k][v] = expm1_f32(A[v] * s[k][v]);
-        bw[k][v] = __builtin_amdgcn_sqrtf(left_f32(e[k][v])) * w;
+        e[k][v] = expm1_f32(A[v] * gate_f32(rv[v]));
+        bw[k][v] = __builtin_amdgcn_sqrtf(left_f32(e[k][v])) * gate_f32(iv[v]);
       }
     }
     if (live < kRunB) {
@@ -473,20 +470,25 @@ __global__ __launch_bounds__(64 * kChunk / kRunB) void gated_bwd_kernel(GatedP<T
     int64_t o = to + (kRunB - 1) * a.C;
 #pragma unroll
     for (int k = kRunB - 1; k >= 0; --k) {
-      float xv[V], gv[V], dx[V], dr[V], di[V];
+      float xv[V], gv[V], rv[V], iv[V], dx[V], dr[V], di[V];
       x[k].wide(xv);
       gy[k].wide(gv);
+      r[k].wide(rv);
+      i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         // (a^2 / beta) u = a^2 (beta u) / (1 - a^2); 0 where a is 1 to within the smallest normal number
         const float av = 1.0f + e[k][v], left = left_f32(e[k][v]);
         const float inv = left > 1.17549435e-38f ? __builtin_amdgcn_rcpf(left) : 0.0f;
+        float s, sshut, w, wshut;
+        gate_both(rv[v], s, sshut);
+        gate_both(iv[v], w, wshut);
         const float gt = g[v] + gv[v];
         const float ga = gt * av;
-        const float ks = ga * __builtin_fmaf(-av * inv, bw[k][v] * xv[v], hp[k][v]) * s[k][v];
+        const float ks = ga * __builtin_fmaf(-av * inv, bw[k][v] * xv[v], hp[k][v]) * s;
         dx[v] = gt * bw[k][v];
-        di[v] = dx[v] * xv[v] * wshut[k][v];
-        dr[v] = ks * A[v] * sshut[k][v];
+        di[v] = dx[v] * xv[v] * wshut;
+        dr[v] = ks * A[v] * sshut;
         if (k < live) dA[v] += ks;   // padding leaves g and has dx = di = 0 already
         else dr[v] = 0.0f;
         g[v] = ga;

@@ -53,9 +53,13 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int ids64, int64_t i) 
   return ids64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
 }
 
+// entry of token t (fewer than 2^31 tokens)
+template <typename P> __device__ __forceinline__ int64_t entry_of(const P& a, int64_t t) {
+  return static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L);
+}
 // the table row of token t, -1 for padding and for ids outside the table
 template <typename P> __device__ __forceinline__ int64_t row_of(const P& a, int64_t t) {
-  const int64_t b = t / a.L, l = t - b * a.L;
+  const int64_t b = entry_of(a, t), l = t - b * a.L;
   if (l >= seq_len(a.lens, b, a.L)) return -1;
   const int64_t id = id_at(a.ids, a.ids64, b * a.ids_batch + l);
   return id >= 0 && id < a.V ? id : -1;
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
   __syncthreads();
   const int64_t share = cdiv(cdiv(tokens, kSortWaves), 64) * 64;
   const int64_t t0 = wave * share, t1 = t0 + share < tokens ? t0 + share : tokens;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   int32_t lower = 0;
   for (int64_t t = t0 + lane; t < t1; t += 64 * kAhead) {
     int32_t r[kAhead];
@@ -204,7 +208,7 @@ __device__ __forceinline__ void sum_tokens(const EmbedP<T>& a, int64_t p0, int64
     float d[kAhead][V];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int64_t t = a.token[p + k < p1 ? p + k : p1 - 1], b = t / a.L;
+      const int64_t t = a.token[p + k < p1 ? p + k : p1 - 1], b = entry_of(a, t);
       ldv<V>(a.gy + b * a.gb + (t - b * a.L) * a.gr + at, d[k]);
     }
 #pragma unroll
@@ -217,7 +221,8 @@ __device__ __forceinline__ void sum_tokens(const EmbedP<T>& a, int64_t p0, int64
 // Workgroups 0 .. long_blocks - 1: the parts of long runs, 256 pieces of one
 // chunk of sorted tokens. A chunk meets at most two long runs: one that its
 // first token continues or begins, one that begins later and reaches its end.
-// The other workgroups: 256 pieces of the gradient, each with its row's run.
+// The other workgroups: kPut * 256 pieces of the gradient, each with its row's run.
+constexpr int kPut = 4;
 template <typename T, int V>
 __global__ __launch_bounds__(kBlock) void embed_grad_kernel(EmbedP<T> a) {
   int64_t g = a.block0 + blockIdx.x;
@@ -242,28 +247,43 @@ __global__ __launch_bounds__(kBlock) void embed_grad_kernel(EmbedP<T> a) {
     return;
   }
   g -= a.long_blocks;
-  const int64_t first = g * kBlock, v0 = first / a.pieces;
-  const int64_t i = first - v0 * a.pieces + threadIdx.x;
-  const uint32_t up = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.pieces);
-  const int64_t v = v0 + up, at = (i - static_cast<int64_t>(up) * a.pieces) * V;
-  if (v >= a.V) return;
-  const int64_t p0 = a.start[v], p1 = a.start[v + 1];
-  if (p1 - p0 > kChunk) return;   // joined from its parts
-  sum_tokens<T, V>(a, p0, p1, at, s);
+  const int64_t first = g * (kBlock * kPut), v0 = first / a.pieces;
+  const uint32_t left = static_cast<uint32_t>(first - v0 * a.pieces), pieces = static_cast<uint32_t>(a.pieces);
+  int32_t p0[kPut], p1[kPut];
+  int64_t to[kPut];
+  uint32_t at[kPut];
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] *= a.scale;
-  stv<V>(a.dw + v * a.D + at, s);
+  for (int k = 0; k < kPut; ++k) {
+    const uint32_t i = left + k * kBlock + threadIdx.x, up = i / pieces;
+    const int64_t v = v0 + up;
+    at[k] = (i - up * pieces) * V;
+    to[k] = v * a.D + at[k];
+    p0[k] = 0;
+    p1[k] = kChunk + 1;   // past the table: not written
+    if (v < a.V) {
+      p0[k] = a.start[v];
+      p1[k] = a.start[v + 1];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPut; ++k) {
+    if (p1[k] - p0[k] > kChunk) continue;   // joined from its parts
+    sum_tokens<T, V>(a, p0[k], p1[k], at[k], s);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] *= a.scale;
+    stv<V>(a.dw + to[k], s);
+  }
 }
 
 // Joins the long run that begins in chunk c (one at most: it reaches the
-// chunk's end) from its parts, one value per lane; wavefront w sums the w-th
+// chunk's end) from its parts, V values per lane; wavefront w sums the w-th
 // quarter of them, in order.
-template <typename T>
+template <typename T, int V>
 __global__ __launch_bounds__(kBlock) void embed_join_kernel(EmbedP<T> a) {
-  __shared__ float acc[4][64];
+  __shared__ float acc[4][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t g = a.block0 + blockIdx.x, slices = cdiv(a.D, 64);
-  const int64_t c = g / slices, at = (g - c * slices) * 64 + lane;
+  const int64_t g = a.block0 + blockIdx.x, slices = cdiv(a.D, 64 * V);
+  const int64_t c = g / slices, at = ((g - c * slices) * 64 + lane) * V;
   const int64_t all = a.start[a.V], p0 = c * kChunk;
   if (p0 >= all) return;
   const int64_t p1 = p0 + kChunk < all ? p0 + kChunk : all;
@@ -271,25 +291,30 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(EmbedP<T> a) {
   if (r0 < p0 || r1 - r0 <= kChunk) return;
   const int64_t n = (r1 - 1) / kChunk - c + 1;   // chunks that hold it
   const int64_t per = cdiv(n, 4), k0 = wave * per, k1 = k0 + per < n ? k0 + per : n;
-  float s = 0.0f;
+  float s[V] = {};
   if (at < a.D) {
     constexpr int kAhead = 8;
     for (int64_t k = k0; k < k1; k += kAhead) {
-      float d[kAhead];
+      float d[kAhead][V];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int64_t q = k + j < k1 ? k + j : k1 - 1;
-        d[j] = a.part[((c + q) * 2 + (q == 0 ? 1 : 0)) * a.D + at];
+        ldv<V>(a.part + ((c + q) * 2 + (q == 0 ? 1 : 0)) * a.D + at, d[j]);
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) s += k + j < k1 ? d[j] : 0.0f;
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] += k + j < k1 ? d[j][e] : 0.0f;
     }
   }
-  acc[wave][lane] = s;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[wave][lane * V + e] = s[e];
   __syncthreads();
   if (wave == 0 && at < a.D) {
-    s = ((acc[0][lane] + acc[1][lane]) + acc[2][lane]) + acc[3][lane];
-    Store<T>::put(a.dw, v * a.D + at, s * a.scale);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      s[e] = (((acc[0][lane * V + e] + acc[1][lane * V + e]) + acc[2][lane * V + e]) + acc[3][lane * V + e]) * a.scale;
+    stv<V>(a.dw + v * a.D + at, s);
   }
 }
 
@@ -332,16 +357,17 @@ template <typename T, int V> hipError_t embed_grad_run(EmbedP<T> p, hipStream_t 
   const int64_t chunks = cdiv(p.tokens, kChunk);
   p.long_blocks = chunks * cdiv(p.pieces, kBlock);
   tr->before(stream, "embed_grad", p.V);
-  hipError_t e = in_parts(p.long_blocks + cdiv(p.V * p.pieces, kBlock), [&](int64_t first, unsigned count) {
+  hipError_t e = in_parts(p.long_blocks + cdiv(p.V * p.pieces, kBlock * kPut), [&](int64_t first, unsigned count) {
     p.block0 = first;
     hipLaunchKernelGGL((embed_grad_kernel<T, V>), dim3(count), dim3(kBlock), 0, stream, p);
   });
   tr->after(stream);
   if (e != hipSuccess || p.tokens <= kChunk) return e;   // no run is longer than the tokens
   tr->before(stream, "embed_join", chunks);
-  e = in_parts(chunks * cdiv(p.D, 64), [&](int64_t first, unsigned count) {
+  constexpr int J = V == 1 ? 1 : 4;
+  e = in_parts(chunks * cdiv(p.D, 64 * J), [&](int64_t first, unsigned count) {
     p.block0 = first;
-    hipLaunchKernelGGL((embed_join_kernel<T>), dim3(count), dim3(kBlock), 0, stream, p);
+    hipLaunchKernelGGL((embed_join_kernel<T, J>), dim3(count), dim3(kBlock), 0, stream, p);
   });
   tr->after(stream);
   return e;

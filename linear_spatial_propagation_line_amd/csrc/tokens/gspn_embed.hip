@@ -5,9 +5,10 @@
 // Both are bound by memory: a multiplication for two values moved. The lookup
 // takes 16 bytes per lane. The gradient sums in fp32 and in token order
 // without atomics on values: tokens are sorted by id (a stable counting sort),
-// a row of the table then owns a run of them. Most rows have few or no tokens,
-// a few rows have thousands, so runs of more than kChunk tokens are summed in
-// parts by workgroups that own kChunk sorted tokens each, and joined in order.
+// a row of the table then owns a run of them. Most rows have no token, a few have
+// thousands, so the work is dealt out by sorted tokens: a wavefront owns kChunk
+// of them, finishes the runs that lie within, and leaves a part of those that do
+// not, which are joined in order. Rows without a token are filled with zeros.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 
@@ -15,10 +16,16 @@ namespace gspn {
 
 namespace {
 
-constexpr int kChunk = 32;        // sorted tokens per part of a long run
+constexpr int kChunk = 16;        // sorted tokens that a wavefront sums
 constexpr int kSortWaves = 16;
-constexpr int kMaxRange = 1024;   // table rows that one sorting workgroup owns, at most
+constexpr int kRangeBits = 10;
+constexpr int kMaxRange = 1 << kRangeBits;   // table rows that one sorting workgroup owns, at most
 constexpr int kBlock = 256;
+
+// Tokens of a sorting wavefront, in whole turns of kTurn * 64: the rows are
+// padded to kSortWaves of these with -1, so that no load asks where the end is.
+constexpr int kTurn = 8;
+int64_t sort_share(int64_t tokens) { return cdiv(tokens, kSortWaves * kTurn * 64) * (kTurn * 64); }
 
 // Rows per sorting workgroup: about one workgroup per compute unit, each of
 // which reads all ids, at least a wavefront's worth of rows.
@@ -34,17 +41,9 @@ template <typename T> struct EmbedP {
   const int32_t* lens;
   const T* weight;
   T* out;
-  const T* gy;
-  int64_t gb, gr;
-  T* dw;
-  const int32_t* start;   // [V + 1]: row v owns sorted tokens start[v] .. start[v + 1] - 1
-  const int32_t* token;   // [tokens]: sorted tokens
-  const int32_t* row;     // [tokens]: their rows
-  float* part;            // [chunks][2][D]: sums of long runs, begun before the chunk or in it
   int64_t L, V, D, tokens;
   int64_t pieces;         // pieces of a row
   int64_t block0;         // first workgroup of this launch
-  int64_t long_blocks;    // workgroups of long runs' parts, before those of rows
   float scale;
   int ids64;
 };
@@ -65,44 +64,68 @@ template <typename P> __device__ __forceinline__ int64_t row_of(const P& a, int6
   return id >= 0 && id < a.V ? id : -1;
 }
 
-// A workgroup copies kCopies * 256 pieces of the output, whole rows or not
-constexpr int kCopies = 4;
+// How rows are dealt to wavefronts: `per` rows to one, a row's pieces in
+// `slices` shares where there are few rows. Row, id and run are the same for the
+// whole wavefront, so that a piece costs little more than its load and store
+// (a piece per lane with its own row: gradient of 65536 rows of 2304 107 us, 82).
+struct Deal {
+  int64_t rows;
+  int32_t slices, per;
+};
+constexpr int kAtOnce = 4;   // pieces that a lane has in flight
+Deal deal(int64_t rows, int64_t pieces) {
+  Deal d{rows, 1, 1};
+  const int64_t turns = cdiv(pieces, 64);
+  while (rows * d.slices < 8192 && d.slices < turns) ++d.slices;
+  while (d.per < 4 && rows / d.per > 16384) d.per *= 2;
+  return d;
+}
+int64_t deal_blocks(const Deal& d) { return cdiv(cdiv(d.rows, d.per) * d.slices, kBlock / 64); }
+// this wavefront's first row and its lane's first piece
+struct Share {
+  int64_t row;
+  int64_t piece;
+};
+__device__ __forceinline__ Share share_of(const Deal& d, int64_t block) {
+  const int64_t g = block * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t r = g / d.slices;
+  return Share{r * d.per, (g - r * d.slices) * 64 + (threadIdx.x & 63)};
+}
+
 template <typename T, int V>
-__global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a) {
-  const int64_t first = (a.block0 + blockIdx.x) * (kBlock * kCopies);
-  const int64_t t0 = first / a.pieces;
-  const int64_t left = first - t0 * a.pieces;
-  float d[kCopies][V];
-  int64_t to[kCopies];
+__global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a, Deal deal) {
+  const Share w = share_of(deal, a.block0 + blockIdx.x);
+  const int64_t step = deal.slices * int64_t(64);
+  for (int k = 0; k < deal.per; ++k) {
+    const int64_t t = w.row + k;
+    if (t >= a.tokens) return;
+    const int64_t row = row_of(a, t);
+    const T* src = a.weight + (row < 0 ? 0 : row) * a.D;
+    T* dst = a.out + t * a.D;
+    for (int64_t p = w.piece; p < a.pieces; p += step * kAtOnce) {
+      float d[kAtOnce][V];
 #pragma unroll
-  for (int k = 0; k < kCopies; ++k) {
-    const int64_t i = left + k * kBlock + threadIdx.x;
-    // a row of fewer than 2^31 pieces: the quotient fits 32 bits
-    const uint32_t up = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.pieces);
-    const int64_t t = t0 + up, at = (i - static_cast<int64_t>(up) * a.pieces) * V;
-    to[k] = -1;
+      for (int q = 0; q < kAtOnce; ++q) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) d[k][e] = 0.0f;
-    if (t < a.tokens) {
-      const int64_t row = row_of(a, t);
-      to[k] = t * a.D + at;
-      if (row >= 0) ldv<V>(a.weight + row * a.D + at, d[k]);
+        for (int e = 0; e < V; ++e) d[q][e] = 0.0f;
+        if (row >= 0 && p + q * step < a.pieces) ldv<V>(src + (p + q * step) * V, d[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        if (p + q * step >= a.pieces) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[q][e] *= a.scale;
+        stv<V>(dst + (p + q * step) * V, d[q]);
+      }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < kCopies; ++k) {
-    if (to[k] < 0) continue;
-#pragma unroll
-    for (int e = 0; e < V; ++e) d[k][e] *= a.scale;
-    stv<V>(a.out + to[k], d[k]);
   }
 }
 
-// rows of all tokens as 32-bit numbers, -1 for those without
+// rows of all tokens as 32-bit numbers, -1 for those without and for the padding
 template <typename P>
-__global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows) {
+__global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, int64_t padded) {
   const int64_t t = (a.block0 + blockIdx.x) * kBlock + threadIdx.x;
-  if (t < a.tokens) rows[t] = static_cast<int32_t>(row_of(a, t));
+  if (t < padded) rows[t] = t < a.tokens ? static_cast<int32_t>(row_of(a, t)) : -1;
 }
 
 // Stable counting sort. Workgroup g owns table rows v0 = g * range .. and
@@ -114,27 +137,25 @@ __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows) 
 // numbers, so that a lane's place is its wavefront's next one plus the lanes
 // of the same row before it.
 __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
-    const int32_t* rows, int64_t tokens, int64_t V, int range, int32_t* start, int32_t* token, int32_t* row) {
+    const int32_t* rows, int64_t share, int64_t V, int range, int32_t* start, int2* place_of) {
   __shared__ int32_t counts[kSortWaves * kMaxRange];   // [wavefront][row]
   __shared__ int32_t sums[kSortWaves], below[kSortWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int32_t* mine_next = counts + wave * range;
   const int32_t v0 = static_cast<int32_t>(blockIdx.x) * range;
   for (int i = threadIdx.x; i < kSortWaves * range; i += kSortWaves * 64) counts[i] = 0;
   __syncthreads();
-  const int64_t share = cdiv(cdiv(tokens, kSortWaves), 64) * 64;
-  const int64_t t0 = wave * share, t1 = t0 + share < tokens ? t0 + share : tokens;
-  constexpr int kAhead = 16;
+  const int32_t* own = rows + wave * share;
   int32_t lower = 0;
-  for (int64_t t = t0 + lane; t < t1; t += 64 * kAhead) {
-    int32_t r[kAhead];
+  for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
+    uint32_t r[kTurn];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) r[k] = t + 64 * k < t1 ? rows[t + 64 * k] : -1;
+    for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      lower += r[k] >= 0 && r[k] < v0 ? 1 : 0;
-      const int32_t i = r[k] - v0;
-      if (r[k] >= 0 && i >= 0 && i < range) atomicAdd(&mine_next[i], 1);
+    for (int k = 0; k < kTurn; ++k) {
+      lower += r[k] < static_cast<uint32_t>(v0) ? 1 : 0;   // -1 is the largest
+      const uint32_t i = r[k] - v0;
+      if (i < static_cast<uint32_t>(range)) atomicAdd(&mine_next[i], 1);
     }
   }
 #pragma unroll
@@ -169,126 +190,135 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
     }
   }
   __syncthreads();
-  const int bits = 31 - __builtin_clz(range);
-  for (int64_t t = t0; t < t1; t += 64 * kAhead) {
-    int32_t r[kAhead];
+  for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
+    uint32_t r[kTurn], lo[kTurn], hi[kTurn];   // rows; lanes whose row numbers agree in every bit
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) r[k] = t + 64 * k + lane < t1 ? rows[t + 64 * k + lane] : -1;
+    for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int32_t i = r[k] - v0;
-      const bool mine = r[k] >= 0 && i >= 0 && i < range;
-      uint64_t same = __ballot(mine);
-      if (same == 0) continue;
-      for (int b = 0; b < bits; ++b) {
-        const bool set = (i >> b) & 1;
-        const uint64_t have = __ballot(set);
-        same &= set ? have : ~have;
+    for (int k = 0; k < kTurn; ++k) {
+      const uint32_t i = r[k] - v0;
+      const uint64_t in = __ballot(i < static_cast<uint32_t>(range));
+      lo[k] = static_cast<uint32_t>(in);
+      hi[k] = static_cast<uint32_t>(in >> 32);
+      if (in == 0) continue;
+#pragma unroll
+      for (int b = 0; b < kRangeBits; ++b) {
+        const int32_t set = __builtin_amdgcn_sbfe(i, b, 1);   // 0 or -1
+        const uint64_t have = __ballot(set != 0);
+        lo[k] &= ~(static_cast<uint32_t>(have) ^ set);
+        hi[k] &= ~(static_cast<uint32_t>(have >> 32) ^ set);
       }
-      if (mine) {
-        const int32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-        const int32_t place = mine_next[i] + rank;
-        token[place] = static_cast<int32_t>(t + 64 * k + lane);
-        row[place] = r[k];
+    }
+    // a wavefront's LDS accesses take effect in their order, so a row's last lane
+    // moves its place on without a wait
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k) {
+      const uint32_t i = r[k] - v0;
+      if (i < static_cast<uint32_t>(range)) {
+        const uint64_t same = static_cast<uint64_t>(hi[k]) << 32 | lo[k];
+        const int32_t first = mine_next[i], place = first + __popcll(same & ((uint64_t(1) << lane) - 1));
+        __builtin_amdgcn_wave_barrier();
+        if ((same >> lane) == 1) mine_next[i] = place + 1;
+        place_of[place] = make_int2(static_cast<int32_t>(wave * share + turn + 64 * k + lane), r[k]);
       }
-      lds_wave_sync();
-      if (mine && (same >> lane) == 1) mine_next[i] += __popcll(same);   // the row's last lane
-      lds_wave_sync();
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
 
-// sum of grad_out over sorted tokens p0 .. p1 - 1 at values `at` ..
-template <typename T, int V>
-__device__ __forceinline__ void sum_tokens(const EmbedP<T>& a, int64_t p0, int64_t p1, int64_t at, float (&s)[V]) {
+// ---- sums of runs -----------------------------------------------------------
+template <typename T, typename O> struct RunP {
+  const int32_t* start;
+  const int2* place;
+  const T* x;
+  int64_t batch, stride, L;
+  const float* weight;   // of every token, or null
+  float scale;
+  O* out;
+  int by_place;          // a run's sum goes to row `start` of out, not to its table row
+  float* part;           // [chunks][2][D]: parts of a run begun before the chunk, begun in it
+  int64_t V, D, pieces, chunks;
+  int64_t block0, chunk_blocks;
+};
+
+template <int V, typename T, typename O>
+__device__ __forceinline__ void finish_run(const RunP<T, O>& a, int64_t v, int64_t r0, int64_t at, float (&s)[V]) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = 0.0f;
-  constexpr int kAhead = V > 4 ? 4 : 8;
-  for (int64_t p = p0; p < p1; p += kAhead) {
-    float d[kAhead][V];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t t = a.token[p + k < p1 ? p + k : p1 - 1], b = entry_of(a, t);
-      ldv<V>(a.gy + b * a.gb + (t - b * a.L) * a.gr + at, d[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[e] += p + k < p1 ? d[k][e] : 0.0f;
-  }
+  for (int e = 0; e < V; ++e) s[e] *= a.scale;
+  stv<V>(a.out + (a.by_place ? r0 : v) * a.D + at, s);
 }
 
-// Workgroups 0 .. long_blocks - 1: the parts of long runs, 256 pieces of one
-// chunk of sorted tokens. A chunk meets at most two long runs: one that its
-// first token continues or begins, one that begins later and reaches its end.
-// The other workgroups: kPut * 256 pieces of the gradient, each with its row's run.
-constexpr int kPut = 4;
-template <typename T, int V>
-__global__ __launch_bounds__(kBlock) void embed_grad_kernel(EmbedP<T> a) {
-  int64_t g = a.block0 + blockIdx.x;
-  float s[V];
-  if (g < a.long_blocks) {
-    const int64_t slices = cdiv(a.pieces, kBlock);
-    const int64_t c = g / slices, piece = (g - c * slices) * kBlock + threadIdx.x;
-    const int64_t all = a.start[a.V], p0 = c * kChunk;
-    if (p0 >= all) return;
-    const int64_t p1 = p0 + kChunk < all ? p0 + kChunk : all;
-    const int64_t va = a.row[p0], vb = a.row[p1 - 1];
-    const int64_t a0 = a.start[va], a1 = a.start[va + 1], b0 = a.start[vb], b1 = a.start[vb + 1];
-    if (piece >= a.pieces) return;
-    if (a1 - a0 > kChunk) {
-      sum_tokens<T, V>(a, p0, a1 < p1 ? a1 : p1, piece * V, s);
-      stv<V>(a.part + (c * 2 + (a0 < p0 ? 0 : 1)) * a.D + piece * V, s);
-    }
-    if (vb != va && b1 - b0 > kChunk) {
-      sum_tokens<T, V>(a, b0, p1, piece * V, s);
-      stv<V>(a.part + (c * 2 + 1) * a.D + piece * V, s);
+// Workgroups 0 .. chunk_blocks - 1: a chunk's tokens, 64 pieces of their rows
+// per wavefront, eight tokens loaded ahead. The others fill rows that no token
+// names.
+template <typename T, typename O, int V>
+__global__ __launch_bounds__(kBlock) void run_sums_kernel(RunP<T, O> a, Deal deal) {
+  const int64_t g = a.block0 + blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  if (g >= a.chunk_blocks) {
+    const Share w = share_of(deal, g - a.chunk_blocks);
+    const int64_t step = deal.slices * int64_t(64);
+    const float zero[V] = {};
+    for (int k = 0; k < deal.per; ++k) {
+      const int64_t v = w.row + k;
+      if (v >= a.V) return;
+      if (a.start[v + 1] != a.start[v]) continue;
+      for (int64_t p = w.piece; p < a.pieces; p += step) stv<V>(a.out + v * a.D + p * V, zero);
     }
     return;
   }
-  g -= a.long_blocks;
-  const int64_t first = g * (kBlock * kPut), v0 = first / a.pieces;
-  const uint32_t left = static_cast<uint32_t>(first - v0 * a.pieces), pieces = static_cast<uint32_t>(a.pieces);
-  int32_t p0[kPut], p1[kPut];
-  int64_t to[kPut];
-  uint32_t at[kPut];
+  const int64_t w = g * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slice = w / a.chunks, c = w - slice * a.chunks;
+  const int64_t piece = slice * 64 + lane, at = piece * V;
+  const int64_t all = a.start[a.V], p0 = c * kChunk;
+  if (p0 >= all || piece >= a.pieces) return;
+  const int64_t p1 = p0 + kChunk < all ? p0 + kChunk : all;
+  float s[V] = {};
+  constexpr int kAhead = 8;
 #pragma unroll
-  for (int k = 0; k < kPut; ++k) {
-    const uint32_t i = left + k * kBlock + threadIdx.x, up = i / pieces;
-    const int64_t v = v0 + up;
-    at[k] = (i - up * pieces) * V;
-    to[k] = v * a.D + at[k];
-    p0[k] = 0;
-    p1[k] = kChunk + 1;   // past the table: not written
-    if (v < a.V) {
-      p0[k] = a.start[v];
-      p1[k] = a.start[v + 1];
+  for (int k0 = 0; k0 < kChunk; k0 += kAhead) {
+    const int64_t p = p0 + k0;
+    if (p >= p1) break;
+    float d[kAhead][V], f[kAhead];
+    int32_t v[kAhead], r0[kAhead], r1[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t q = p + k < p1 ? p + k : p1 - 1;
+      const int2 tr = a.place[q];
+      const int64_t t = tr.x, b = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L);
+      v[k] = tr.y;
+      r0[k] = a.start[v[k]];
+      r1[k] = a.start[v[k] + 1];
+      f[k] = a.weight ? a.weight[t] : 1.0f;
+      ldv<V>(a.x + b * a.batch + (t - b * a.L) * a.stride + at, d[k]);
     }
-  }
 #pragma unroll
-  for (int k = 0; k < kPut; ++k) {
-    if (p1[k] - p0[k] > kChunk) continue;   // joined from its parts
-    sum_tokens<T, V>(a, p0[k], p1[k], at[k], s);
+    for (int k = 0; k < kAhead; ++k) {
+      if (p + k >= p1) break;
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] *= a.scale;
-    stv<V>(a.dw + to[k], s);
+      for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(f[k], d[k][e], s[e]);
+      if (p + k + 1 < p1 && p + k + 1 < r1[k]) continue;
+      // the run ends here, or goes on after the chunk
+      if (r0[k] >= p0 && r1[k] <= p1) finish_run<V>(a, v[k], r0[k], at, s);
+      else stv<V>(a.part + (c * 2 + (r0[k] >= p0 ? 1 : 0)) * a.D + at, s);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] = 0.0f;
+    }
   }
 }
 
-// Joins the long run that begins in chunk c (one at most: it reaches the
-// chunk's end) from its parts, V values per lane; wavefront w sums the w-th
-// quarter of them, in order.
-template <typename T, int V>
-__global__ __launch_bounds__(kBlock) void embed_join_kernel(EmbedP<T> a) {
+// Joins the run that begins in chunk c and goes on after it (one at most) from
+// its parts, V values per lane; wavefront w sums the w-th quarter of them, in order.
+template <typename T, typename O, int V>
+__global__ __launch_bounds__(kBlock) void run_join_kernel(RunP<T, O> a) {
   __shared__ float acc[4][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t g = a.block0 + blockIdx.x, slices = cdiv(a.D, 64 * V);
   const int64_t c = g / slices, at = ((g - c * slices) * 64 + lane) * V;
-  const int64_t all = a.start[a.V], p0 = c * kChunk;
-  if (p0 >= all) return;
-  const int64_t p1 = p0 + kChunk < all ? p0 + kChunk : all;
-  const int64_t v = a.row[p1 - 1], r0 = a.start[v], r1 = a.start[v + 1];
-  if (r0 < p0 || r1 - r0 <= kChunk) return;
+  const int64_t all = a.start[a.V], p0 = c * kChunk, p1 = p0 + kChunk;
+  if (p1 >= all) return;
+  const int64_t v = a.place[p1 - 1].y, r0 = a.start[v], r1 = a.start[v + 1];
+  if (r0 < p0 || r1 <= p1) return;
   const int64_t n = (r1 - 1) / kChunk - c + 1;   // chunks that hold it
   const int64_t per = cdiv(n, 4), k0 = wave * per, k1 = k0 + per < n ? k0 + per : n;
   float s[V] = {};
@@ -313,9 +343,52 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(EmbedP<T> a) {
   if (wave == 0 && at < a.D) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      s[e] = (((acc[0][lane * V + e] + acc[1][lane * V + e]) + acc[2][lane * V + e]) + acc[3][lane * V + e]) * a.scale;
-    stv<V>(a.dw + v * a.D + at, s);
+      s[e] = ((acc[0][lane * V + e] + acc[1][lane * V + e]) + acc[2][lane * V + e]) + acc[3][lane * V + e];
+    finish_run<V>(a, v, r0, at, s);
   }
+}
+
+template <typename T, typename O, int V>
+hipError_t run_sums_of(const RunSum& r, hipStream_t stream, Tracer* tr) {
+  RunP<T, O> p{};
+  p.start = r.sort.start;
+  p.place = r.sort.place;
+  p.x = static_cast<const T*>(r.x);
+  p.batch = r.batch;
+  p.stride = r.row;
+  p.L = r.L;
+  p.weight = r.weight;
+  p.scale = r.scale;
+  p.out = static_cast<O*>(r.out);
+  p.by_place = r.by_place;
+  p.part = r.part;
+  p.V = r.V;
+  p.D = r.D;
+  p.pieces = r.D / V;
+  p.chunks = cdiv(r.tokens, kChunk);
+  p.chunk_blocks = cdiv(p.chunks * cdiv(p.pieces, 64), kBlock / 64);
+  const Deal d = deal(r.V, p.pieces);
+  tr->before(stream, "run_sums", r.V);
+  hipError_t e = in_parts(p.chunk_blocks + (r.by_place ? 0 : deal_blocks(d)), [&](int64_t first, unsigned count) {
+    p.block0 = first;
+    hipLaunchKernelGGL((run_sums_kernel<T, O, V>), dim3(count), dim3(kBlock), 0, stream, p, d);
+  });
+  tr->after(stream);
+  if (e != hipSuccess || r.tokens <= kChunk) return e;   // no run goes past a chunk
+  tr->before(stream, "run_join", p.chunks);
+  e = in_parts(p.chunks * cdiv(p.D, 64 * V), [&](int64_t first, unsigned count) {
+    p.block0 = first;
+    hipLaunchKernelGGL((run_join_kernel<T, O, V>), dim3(count), dim3(kBlock), 0, stream, p);
+  });
+  tr->after(stream);
+  return e;
+}
+template <typename T, typename O> hipError_t run_sums_dt(const RunSum& r, hipStream_t stream, Tracer* tr) {
+  constexpr int V = 16 / sizeof(T);
+  if (r.D % V == 0 && wide_ok(r.out, 16, sizeof(O), {}) &&
+      (r.tokens == 0 || wide_ok(r.x, 16, sizeof(T), {r.batch, r.row})))
+    return run_sums_of<T, O, V>(r, stream, tr);
+  return run_sums_of<T, O, 1>(r, stream, tr);
 }
 
 template <typename T> EmbedP<T> embed_params(const gspn_embed_args& a) {
@@ -336,10 +409,11 @@ template <typename T> EmbedP<T> embed_params(const gspn_embed_args& a) {
 
 template <typename T, int V> hipError_t embed_run(EmbedP<T> p, hipStream_t stream, Tracer* tr) {
   p.pieces = p.D / V;
+  const Deal d = deal(p.tokens, p.pieces);
   tr->before(stream, "embed", p.tokens);
-  const hipError_t e = in_parts(cdiv(p.tokens * p.pieces, kBlock * kCopies), [&](int64_t first, unsigned count) {
+  const hipError_t e = in_parts(deal_blocks(d), [&](int64_t first, unsigned count) {
     p.block0 = first;
-    hipLaunchKernelGGL((embed_kernel<T, V>), dim3(count), dim3(kBlock), 0, stream, p);
+    hipLaunchKernelGGL((embed_kernel<T, V>), dim3(count), dim3(kBlock), 0, stream, p, d);
   });
   tr->after(stream);
   return e;
@@ -352,62 +426,22 @@ template <typename T> hipError_t embed_dt(const gspn_embed_args& a, hipStream_t 
   return embed_run<T, 1>(p, stream, tr);
 }
 
-template <typename T, int V> hipError_t embed_grad_run(EmbedP<T> p, hipStream_t stream, Tracer* tr) {
-  p.pieces = p.D / V;
-  const int64_t chunks = cdiv(p.tokens, kChunk);
-  p.long_blocks = chunks * cdiv(p.pieces, kBlock);
-  tr->before(stream, "embed_grad", p.V);
-  hipError_t e = in_parts(p.long_blocks + cdiv(p.V * p.pieces, kBlock * kPut), [&](int64_t first, unsigned count) {
-    p.block0 = first;
-    hipLaunchKernelGGL((embed_grad_kernel<T, V>), dim3(count), dim3(kBlock), 0, stream, p);
-  });
-  tr->after(stream);
-  if (e != hipSuccess || p.tokens <= kChunk) return e;   // no run is longer than the tokens
-  tr->before(stream, "embed_join", chunks);
-  constexpr int J = V == 1 ? 1 : 4;
-  e = in_parts(chunks * cdiv(p.D, 64 * J), [&](int64_t first, unsigned count) {
-    p.block0 = first;
-    hipLaunchKernelGGL((embed_join_kernel<T, J>), dim3(count), dim3(kBlock), 0, stream, p);
-  });
-  tr->after(stream);
-  return e;
-}
-template <typename T>
-hipError_t embed_grad_dt(const gspn_embed_args& a, const gspn_embed_grads& g, void* ws, hipStream_t stream, Tracer* tr) {
-  constexpr int V = 16 / sizeof(T);
-  EmbedP<T> p = embed_params<T>(a);
-  p.gy = static_cast<const T*>(g.grad_out.p);
-  p.gb = g.grad_out.batch;
-  p.gr = g.grad_out.row;
-  p.dw = static_cast<T*>(g.weight);
-  TokenSort s;
-  const hipError_t e = sort_tokens(a.ids, a.ids64, a.ids_batch, a.lens, a.B, a.L, a.V, ws, &s, stream, tr);
-  if (e != hipSuccess) return e;
-  p.start = s.start;
-  p.token = s.token;
-  p.row = s.row;
-  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + token_sort_bytes(p.tokens, a.V));
-  if (a.D % V == 0 && wide_ok(p.dw, 16, sizeof(T), {}) && (p.tokens == 0 || wide_ok(p.gy, 16, sizeof(T), {p.gb, p.gr})))
-    return embed_grad_run<T, V>(p, stream, tr);
-  return embed_grad_run<T, 1>(p, stream, tr);
-}
-
 }  // namespace
 
 size_t token_sort_bytes(int64_t tokens, int64_t V) {
-  return 3 * up256(static_cast<size_t>(tokens) * 4) + up256(static_cast<size_t>(V + 1) * 4);
+  return up256(static_cast<size_t>(sort_share(tokens)) * kSortWaves * 4) + up256(static_cast<size_t>(tokens) * 8) +
+         up256(static_cast<size_t>(V + 1) * 4);
 }
 
 hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int32_t* lens, int64_t B, int64_t L,
                        int64_t V, void* ws, TokenSort* out, hipStream_t stream, Tracer* tr) {
-  const int64_t tokens = B * L;
-  const size_t each = up256(static_cast<size_t>(tokens) * 4);
+  const int64_t tokens = B * L, share = sort_share(tokens), padded = share * kSortWaves;
+  const size_t each = up256(static_cast<size_t>(padded) * 4);
   char* w = static_cast<char*>(ws);
   int32_t* rows = reinterpret_cast<int32_t*>(w);
-  int32_t* token = reinterpret_cast<int32_t*>(w + each);
-  int32_t* row = reinterpret_cast<int32_t*>(w + 2 * each);
-  int32_t* start = reinterpret_cast<int32_t*>(w + 3 * each);
-  *out = TokenSort{start, token, row};
+  int2* place = reinterpret_cast<int2*>(w + each);
+  int32_t* start = reinterpret_cast<int32_t*>(w + each + up256(static_cast<size_t>(tokens) * 8));
+  *out = TokenSort{start, place};
   EmbedP<bf16_t> p{};
   p.ids = ids;
   p.ids_batch = ids_batch;
@@ -419,9 +453,9 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
   hipError_t e = hipSuccess;
   if (tokens > 0) {
     tr->before(stream, "embed_rows", tokens);
-    e = in_parts(cdiv(tokens, kBlock), [&](int64_t first, unsigned count) {
+    e = in_parts(cdiv(padded, kBlock), [&](int64_t first, unsigned count) {
       p.block0 = first;
-      hipLaunchKernelGGL((embed_rows_kernel<EmbedP<bf16_t>>), dim3(count), dim3(kBlock), 0, stream, p, rows);
+      hipLaunchKernelGGL((embed_rows_kernel<EmbedP<bf16_t>>), dim3(count), dim3(kBlock), 0, stream, p, rows, padded);
     });
     tr->after(stream);
     if (e != hipSuccess) return e;
@@ -429,7 +463,7 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
   const int range = sort_range(V);
   tr->before(stream, "embed_sort", tokens);
   hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(cdiv(V, range))), dim3(kSortWaves * 64), 0, stream,
-                     rows, tokens, V, range, start, token, row);
+                     rows, share, V, range, start, place);
   e = hipGetLastError();
   tr->after(stream);
   return e;
@@ -440,13 +474,34 @@ hipError_t launch_embed(const gspn_embed_args& a, hipStream_t stream, Tracer* tr
   return embed_dt<bf16_t>(a, stream, tr);
 }
 
-size_t embed_bwd_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D) {
-  return token_sort_bytes(B * L, V) + static_cast<size_t>(cdiv(B * L, kChunk)) * 2 * static_cast<size_t>(D) * 4;
+size_t run_part_bytes(int64_t tokens, int64_t D) {
+  return up256(static_cast<size_t>(cdiv(tokens, kChunk)) * 2 * static_cast<size_t>(D) * 4);
+}
+hipError_t run_sums(const RunSum& r, hipStream_t stream, Tracer* tr) {
+  if (r.dtype == GSPN_F32) return run_sums_dt<float, float>(r, stream, tr);
+  if (r.by_place) return run_sums_dt<bf16_t, float>(r, stream, tr);
+  return run_sums_dt<bf16_t, bf16_t>(r, stream, tr);
 }
 
+size_t embed_bwd_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t D) {
+  return token_sort_bytes(B * L, V) + run_part_bytes(B * L, D);
+}
 hipError_t launch_embed_bwd(const gspn_embed_args& a, const gspn_embed_grads& g, void* ws, hipStream_t stream, Tracer* tr) {
-  if (a.dtype == GSPN_F32) return embed_grad_dt<float>(a, g, ws, stream, tr);
-  return embed_grad_dt<bf16_t>(a, g, ws, stream, tr);
+  RunSum r{};
+  const hipError_t e = sort_tokens(a.ids, a.ids64, a.ids_batch, a.lens, a.B, a.L, a.V, ws, &r.sort, stream, tr);
+  if (e != hipSuccess) return e;
+  r.dtype = a.dtype;
+  r.x = g.grad_out.p;
+  r.batch = g.grad_out.batch;
+  r.row = g.grad_out.row;
+  r.L = a.L;
+  r.tokens = a.B * a.L;
+  r.scale = a.scale;
+  r.out = g.weight;
+  r.part = reinterpret_cast<float*>(static_cast<char*>(ws) + token_sort_bytes(r.tokens, a.V));
+  r.V = a.V;
+  r.D = a.D;
+  return run_sums(r, stream, tr);
 }
 
 }  // namespace gspn

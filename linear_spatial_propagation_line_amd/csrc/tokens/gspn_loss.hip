@@ -505,75 +505,6 @@ __global__ __launch_bounds__(256) void loss_target_kernel(LossP<T> a) {
   if (lane == 0) a.list.at[p] = a.list.g[p] * expm1_f32(s - a.list.lse[p]);
 }
 
-// G at the targets times the tokens' rows, summed for each target: row start[v]
-// of `rest`. Tokens come sorted by target; a wavefront owns kRestChunk of them and
-// 64 kRestWide columns. A run that lies within the chunk
-// is finished here, one that goes past it leaves its part (begun before the chunk:
-// slot 0, in it: slot 1) for the join.
-constexpr int kRestChunk = 16;
-constexpr int kRestWide = 4;   // columns per lane (Dp is a multiple of 32)
-template <typename T>
-__global__ __launch_bounds__(256) void loss_rest_kernel(LossP<T> a, TokenSort s, float* rest, float* part) {
-  // four chunks of 64 lanes' columns per workgroup
-  const int64_t slices = (a.Dp + 64 * kRestWide - 1) / (64 * kRestWide), chunks = (a.Tp + kRestChunk - 1) / kRestChunk;
-  const int64_t g = (a.block0 + blockIdx.x) * 4 + (threadIdx.x >> 6), slice = g / chunks, c = g - slice * chunks;
-  const int64_t col = (slice * 64 + (threadIdx.x & 63)) * kRestWide;
-  const int64_t all = s.start[a.V], p0 = c * kRestChunk;
-  if (slice >= slices || p0 >= all || col >= a.Dp) return;
-  const int64_t p1 = p0 + kRestChunk < all ? p0 + kRestChunk : all;
-  float sum[kRestWide] = {};
-  constexpr int kAhead = 8;
-#pragma unroll
-  for (int k0 = 0; k0 < kRestChunk; k0 += kAhead) {
-    const int64_t p = p0 + k0;
-    if (p >= p1) break;
-    float d[kAhead][kRestWide], w[kAhead];
-    int32_t r0[kAhead], r1[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t q = p + k < p1 ? p + k : p1 - 1;
-      const int64_t place = s.token[q], row = s.row[q];
-      r0[k] = s.start[row];
-      r1[k] = s.start[row + 1];
-      w[k] = a.list.at[place];
-      ldv<kRestWide>(a.packed + place * a.Dp + col, d[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (p + k >= p1) break;
-#pragma unroll
-      for (int e = 0; e < kRestWide; ++e) sum[e] = __builtin_fmaf(w[k], d[k][e], sum[e]);
-      if (p + k + 1 < p1 && p + k + 1 < r1[k]) continue;
-      // the run ends here or goes on after the chunk
-      if (r0[k] >= p0 && r1[k] <= p1) stv<kRestWide>(rest + r0[k] * a.Dp + col, sum);
-      else stv<kRestWide>(part + (c * 2 + (r0[k] >= p0 ? 1 : 0)) * a.Dp + col, sum);
-#pragma unroll
-      for (int e = 0; e < kRestWide; ++e) sum[e] = 0.0f;
-    }
-  }
-}
-// joins the run that begins in chunk c and goes on after it
-template <typename T>
-__global__ __launch_bounds__(256) void loss_rest_join_kernel(LossP<T> a, TokenSort s, float* rest, const float* part,
-                                                             int64_t slices) {
-  const int64_t g = a.block0 + blockIdx.x, c = g / slices, col = (g - c * slices) * 256 + threadIdx.x;
-  const int64_t all = s.start[a.V], p0 = c * kRestChunk, p1 = p0 + kRestChunk;
-  if (p1 >= all || col >= a.Dp) return;
-  const int64_t v = s.row[p1 - 1], r0 = s.start[v], r1 = s.start[v + 1];
-  if (r0 < p0 || r1 <= p1) return;
-  const int64_t last = (r1 - 1) / kRestChunk;
-  float sum = part[(c * 2 + 1) * a.Dp + col];
-  constexpr int kAhead = 8;
-  for (int64_t q = c + 1; q <= last; q += kAhead) {
-    float d[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) d[k] = part[(q + k <= last ? q + k : last) * 2 * a.Dp + col];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) sum += q + k <= last ? d[k] : 0.0f;
-  }
-  rest[r0 * a.Dp + col] = sum;
-}
-
 // dx: the splits' sums and the target's part, rounded once; zeros for tokens
 // that do not count. V adjacent values per lane.
 template <typename T, int V>
@@ -684,7 +615,7 @@ template <typename T> BackSpace<T> take_backward(Space& s, LossP<T>& p, const Gr
   b.G = s.take<T>(p.Tp * g.Vp);
   b.dx = s.take<float>(g.splits * p.Tp * p.Dp);
   b.rest = s.take<float>(p.Tp * p.Dp);
-  b.rest_part = s.take<float>(cdiv(p.Tp, kRestChunk) * 2 * p.Dp);
+  b.rest_part = reinterpret_cast<float*>(s.take<char>(static_cast<int64_t>(run_part_bytes(p.Tp, p.Dp))));
   b.sort = s.take<char>(static_cast<int64_t>(token_sort_bytes(p.Tp, p.V)));
   return b;
 }
@@ -788,8 +719,7 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   TokenSort sorted{};
   e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
   if (e != hipSuccess) return e;
-  const int64_t ttiles = cdiv(p.T_, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.T_, plan.gtile),
-                slices = cdiv(p.Dp, 256);
+  const int64_t ttiles = cdiv(p.T_, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.T_, plan.gtile);
   auto launch = [&](const char* name, int64_t blocks, auto&& kernel) {
     tr->before(stream, name, p.T_);
     const hipError_t r = in_parts(blocks, [&](int64_t first, unsigned count) {
@@ -801,14 +731,21 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   };
   e = launch("loss_target", cdiv(p.T_, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
   if (e != hipSuccess) return e;
-  e = launch("loss_rest", cdiv(cdiv(p.Tp, kRestChunk) * cdiv(p.Dp, 64 * kRestWide), 4), [&](dim3 n) {
-    hipLaunchKernelGGL((loss_rest_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part);
-  });
-  if (e != hipSuccess) return e;
-  e = launch("loss_rest_join", cdiv(p.Tp, kRestChunk) * slices, [&](dim3 n) {
-    hipLaunchKernelGGL((loss_rest_join_kernel<T>), n, dim3(256), 0, stream, p, sorted, b.rest, b.rest_part, slices);
-  });
-  if (e != hipSuccess) return e;
+  // G at the targets times the tokens' rows, summed for each target
+  RunSum sum{};
+  sum.sort = sorted;
+  sum.dtype = a.dtype;
+  sum.x = p.packed;
+  sum.row = p.Dp;
+  sum.L = sum.tokens = p.Tp;
+  sum.weight = p.list.at;
+  sum.scale = 1.0f;
+  sum.out = b.rest;
+  sum.by_place = 1;
+  sum.part = b.rest_part;
+  sum.V = p.V;
+  sum.D = p.Dp;
+  if ((e = run_sums(sum, stream, tr)) != hipSuccess) return e;
   for (int64_t k = 0; k < plan.pieces; ++k) {
     const int64_t v0 = k * plan.Vp, rows = std::min(plan.Vp, p.V - v0);
     const int64_t mtiles = cdiv(rows, plan.gtile), vtiles = cdiv(rows, plan.tile);

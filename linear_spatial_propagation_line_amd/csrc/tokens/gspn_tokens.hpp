@@ -41,17 +41,34 @@ hipError_t launch_embed_bwd(const gspn_embed_args& a, const gspn_embed_grads& g,
                             hipStream_t stream, Tracer* tr);
 
 // Tokens sorted by their row of a table of V rows, in token order within a row:
-// row v owns places start[v] .. start[v + 1] - 1 (start [V + 1]); token and row
-// hold each place's token and its row. Padding and ids outside the table are
-// left out. ws: token_sort_bytes() bytes (gspn_embed.hip)
+// row v owns places start[v] .. start[v + 1] - 1 (start [V + 1]); place holds each
+// place's token (x) and its row (y). Padding and ids outside the table are left out. ws: token_sort_bytes() bytes (gspn_embed.hip)
 struct TokenSort {
   const int32_t* start;
-  const int32_t* token;
-  const int32_t* row;
+  const int2* place;
 };
 size_t token_sort_bytes(int64_t tokens, int64_t V);
 hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int32_t* lens, int64_t B,
                        int64_t L, int64_t V, void* ws, TokenSort* out, hipStream_t stream, Tracer* tr);
+
+// Sums of the rows of sorted tokens, in fp32 and token order, a run's into its row of
+// the table ([V, D] in dtype, zeros in rows without a token) or, by_place, into row
+// `start` of an fp32 table. weight: a factor of every token, or null. part:
+// run_part_bytes() bytes (gspn_embed.hip)
+struct RunSum {
+  TokenSort sort;
+  gspn_dtype dtype;
+  const void* x;
+  int64_t batch, row, L, tokens;   // token t is row t % L of entry t / L
+  const float* weight;
+  float scale;
+  void* out;
+  int by_place;
+  float* part;
+  int64_t V, D;
+};
+size_t run_part_bytes(int64_t tokens, int64_t D);
+hipError_t run_sums(const RunSum& r, hipStream_t stream, Tracer* tr);
 
 size_t gated_saved_bytes(int64_t B, int64_t L, int64_t C);
 size_t gated_workspace_bytes(int64_t B, int64_t L, int64_t C);

@@ -12,7 +12,7 @@
 //
 // Bound by memory, with five or six transcendentals a value close behind
 // (four values moved forward, eight backward): so each value is read once and
-// its gates are computed once. A workgroup owns a chunk of kChunk tokens of
+// its gates are computed once. A workgroup owns a chunk of tokens of
 // 64 V channels and keeps it in registers; its wavefronts own runs of tokens.
 // A chunk's effect on the state is h -> P h + H. Chunks of a chain (the chunks
 // of one entry's channels) hand the state on through memory: each publishes
@@ -34,7 +34,8 @@ namespace gspn {
 
 namespace {
 
-constexpr int kChunk = 64;     // tokens of a chunk
+constexpr int kChunkF = 128;   // tokens of a chunk, forward
+constexpr int kChunkB = 64;    // backward: also what the saved states are apart
 constexpr int kWindow = 4;    // chunks that one looks back
 constexpr int kRunF = 16;      // tokens of a wavefront's run, forward
 constexpr int kRunB = 8;       // backward, which keeps twice the values of a token
@@ -54,6 +55,7 @@ template <typename T> struct GatedP {
   uint32_t* counter;   // [chains], 16 words apart
   int64_t L, C, B;
   int64_t chunks, ctiles;
+  int64_t saves;   // saved states of an entry
   int64_t block0;
 };
 
@@ -171,13 +173,13 @@ template <typename P> __device__ __forceinline__ Place take_place(const P& a, ui
 }
 
 template <typename T, int V>
-__global__ __launch_bounds__(64 * kChunk / kRunF, 4) void gated_kernel(GatedP<T> a) {
-  constexpr int kWaves = kChunk / kRunF;
+__global__ __launch_bounds__(64 * kChunkF / kRunF, 4) void gated_kernel(GatedP<T> a) {
+  constexpr int kWaves = kChunkF / kRunF;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], before[64 * V];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = take_place(a, &slot);
-  const int64_t n = seq_len(a.lens, at.b, a.L), t0 = at.q * kChunk + wave * kRunF;
+  const int64_t n = seq_len(a.lens, at.b, a.L), t0 = at.q * kChunkF + wave * kRunF;
   const int64_t c0 = at.ct * 64 * V, c = c0 + lane * V;
   const bool mine = c < a.C;
   const uint32_t place = mine ? lane * V : 0, off = place * sizeof(T);   // lanes past the channels read the first
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(64 * kChunk / kRunF, 4) void gated_kernel(GatedP<T>
   const int live = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kRunF ? n - t0 : kRunF));
   T* o = a.out + (at.b * a.L + t0) * a.C + c0;
   // a chunk of padding has nothing to hand on: those behind it are padding too
-  if (at.q * kChunk >= n && at.q > 0) {
+  if (at.q * kChunkF >= n && at.q > 0) {
     if (a.out && mine) zero_rows<V>(o, a.C, rows, off);
     return;
   }
@@ -261,8 +263,17 @@ __global__ __launch_bounds__(64 * kChunk / kRunF, 4) void gated_kernel(GatedP<T>
     if (a.chunks > 1) publish_state(a.behind + base + at.q * stride, last);
     before[j] = first;
     if (ch < a.C) {
-      if (a.saved) a.saved[(at.b * a.chunks + at.q) * a.C + ch] = first;
-      if (a.state_out && n <= (at.q + 1) * kChunk) a.state_out[at.b * a.C + ch] = n == 0 ? first : last;
+      if (a.saved) {
+        // the states that the backward pass begins its chunks with
+        float* to = a.saved + (at.b * a.saves + at.q * (kChunkF / kChunkB)) * a.C + ch;
+        float hs = first;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          if (w % (kChunkB / kRunF) == 0 && at.q * kChunkF + w * kRunF < n) to[w / (kChunkB / kRunF) * a.C] = hs;
+          hs = __builtin_fmaf(sp[w][j], hs, sh[w][j]);
+        }
+      }
+      if (a.state_out && n <= (at.q + 1) * kChunkF) a.state_out[at.b * a.C + ch] = n == 0 ? first : last;
     }
   }
   lds_barrier();
@@ -333,14 +344,14 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
 // Backward: chunks from the last; what is handed on is a_t g_t, by the same
 // rule. The states within the chunk are found again from the one before it.
 template <typename T, int V>
-__global__ __launch_bounds__(64 * kChunk / kRunB, sizeof(T) == 2 || V == 1 ? 4 : 2) void gated_bwd_kernel(GatedP<T> a) {
-  constexpr int kWaves = kChunk / kRunB;
+__global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 : 2) void gated_bwd_kernel(GatedP<T> a) {
+  constexpr int kWaves = kChunkB / kRunB;
   __shared__ uint32_t slot;
   __shared__ float sp[kWaves][64 * V], sh[kWaves][64 * V], sg[kWaves][64 * V], after[64 * V];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place at = take_place(a, &slot);
   const int64_t q = a.chunks - 1 - at.q;
-  const int64_t n = seq_len(a.lens, at.b, a.L), t0 = q * kChunk + wave * kRunB;
+  const int64_t n = seq_len(a.lens, at.b, a.L), t0 = q * kChunkB + wave * kRunB;
   const int64_t c0 = at.ct * 64 * V, c = c0 + lane * V;
   const bool mine = c < a.C;
   const uint32_t place = mine ? lane * V : 0, off = place * sizeof(T);
@@ -348,7 +359,7 @@ __global__ __launch_bounds__(64 * kChunk / kRunB, sizeof(T) == 2 || V == 1 ? 4 :
   const int live = static_cast<int>(n - t0 < 0 ? 0 : (n - t0 < kRunB ? n - t0 : kRunB));
   const int64_t to = (at.b * a.L + t0) * a.C + c0;
   const int64_t row = (at.b * a.chunks + q) * a.C;
-  if (q * kChunk >= n) {   // padding, nothing is handed on
+  if (q * kChunkB >= n) {   // padding, nothing is handed on
     if (mine) {
       zero_rows<V>(a.dx + to, a.C, rows, off);
       zero_rows<V>(a.dr + to, a.C, rows, off);
@@ -436,7 +447,7 @@ __global__ __launch_bounds__(64 * kChunk / kRunB, sizeof(T) == 2 || V == 1 ? 4 :
       p *= sp[k][j];
     }
     // chunks of padding come first in the chain and hand nothing on
-    const int64_t dead = a.chunks - (n + kChunk - 1) / kChunk;
+    const int64_t dead = a.chunks - (n + kChunkB - 1) / kChunkB;
     float first;
     if (at.q == dead) {
       first = a.gstate && ch < a.C ? a.gstate[at.b * a.C + ch] : 0.0f;
@@ -536,8 +547,8 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(u32x4* marks, int64_t 
 struct ChainSpace {
   size_t total, behind, counter, bytes;
 };
-ChainSpace chain_space(int64_t B, int64_t L, int64_t C) {
-  const int64_t chunks = cdiv(L, kChunk), wide = cdiv(C, 128) * 128, narrow = cdiv(C, 64) * 64;
+ChainSpace chain_space(int64_t B, int64_t L, int64_t C, int chunk) {
+  const int64_t chunks = cdiv(L, chunk), wide = cdiv(C, 128) * 128, narrow = cdiv(C, 64) * 64;
   ChainSpace s{};
   if (chunks <= 1) return s;
   const size_t n = static_cast<size_t>(B * chunks * std::max(wide, narrow));
@@ -568,15 +579,16 @@ template <typename T> GatedP<T> gated_params(const gspn_gated_args& a) {
   p.L = a.L;
   p.C = a.C;
   p.B = a.B;
-  p.chunks = std::max<int64_t>(1, cdiv(a.L, kChunk));
+  p.saves = std::max<int64_t>(1, cdiv(a.L, kChunkB));
   return p;
 }
 
 template <typename T, int V>
-hipError_t clear_chain(GatedP<T>& p, void* ws, hipStream_t stream, Tracer* tr) {
+hipError_t clear_chain(GatedP<T>& p, int chunk, void* ws, hipStream_t stream, Tracer* tr) {
   p.ctiles = cdiv(p.C, 64 * V);
+  p.chunks = std::max<int64_t>(1, cdiv(p.L, chunk));
   if (p.chunks <= 1) return hipSuccess;
-  const ChainSpace s = chain_space(p.B, p.L, p.C);
+  const ChainSpace s = chain_space(p.B, p.L, p.C, chunk);
   char* w = static_cast<char*>(ws);
   p.total = reinterpret_cast<uint64_t*>(w + s.total);
   p.behind = reinterpret_cast<uint32_t*>(w + s.behind);
@@ -601,12 +613,12 @@ hipError_t gated_fwd(GatedP<T> p, void* ws, hipStream_t stream, Tracer* tr) {
     tr->after(stream);
     return e;
   }
-  hipError_t e = clear_chain<T, V>(p, ws, stream, tr);
+  hipError_t e = clear_chain<T, V>(p, kChunkF, ws, stream, tr);
   if (e != hipSuccess) return e;
   tr->before(stream, "gated", p.B);
   e = in_parts(p.B * p.ctiles * p.chunks, [&](int64_t first, unsigned count) {
     p.block0 = first;
-    hipLaunchKernelGGL((gated_kernel<T, V>), dim3(count), dim3(64 * kChunk / kRunF), 0, stream, p);
+    hipLaunchKernelGGL((gated_kernel<T, V>), dim3(count), dim3(64 * kChunkF / kRunF), 0, stream, p);
   });
   tr->after(stream);
   return e;
@@ -614,7 +626,7 @@ hipError_t gated_fwd(GatedP<T> p, void* ws, hipStream_t stream, Tracer* tr) {
 
 template <typename T, int V>
 hipError_t gated_bwd(GatedP<T> p, const gspn_gated_grads& g, void* ws, hipStream_t stream, Tracer* tr) {
-  const ChainSpace s = chain_space(p.B, p.L, p.C);
+  const ChainSpace s = chain_space(p.B, p.L, p.C, kChunkB);   // the larger one
   char* w = static_cast<char*>(ws) + s.bytes;
   hipError_t e = hipSuccess;
   if (p.B > 0) {
@@ -627,11 +639,11 @@ hipError_t gated_bwd(GatedP<T> p, const gspn_gated_grads& g, void* ws, hipStream
       if ((e = gated_fwd<T, V>(f, ws, stream, tr)) != hipSuccess) return e;
     }
     p.part = reinterpret_cast<float*>(w);
-    if ((e = clear_chain<T, V>(p, ws, stream, tr)) != hipSuccess) return e;
+    if ((e = clear_chain<T, V>(p, kChunkB, ws, stream, tr)) != hipSuccess) return e;
     tr->before(stream, "gated_bwd", p.B);
     e = in_parts(p.B * p.ctiles * p.chunks, [&](int64_t first, unsigned count) {
       p.block0 = first;
-      hipLaunchKernelGGL((gated_bwd_kernel<T, V>), dim3(count), dim3(64 * kChunk / kRunB), 0, stream, p);
+      hipLaunchKernelGGL((gated_bwd_kernel<T, V>), dim3(count), dim3(64 * kChunkB / kRunB), 0, stream, p);
     });
     tr->after(stream);
     if (e != hipSuccess) return e;
@@ -640,7 +652,7 @@ hipError_t gated_bwd(GatedP<T> p, const gspn_gated_grads& g, void* ws, hipStream
   sums.part[0] = p.part;
   sums.out[0] = g.A;
   sums.cols[0] = p.C;
-  sums.rows = p.B * p.chunks;
+  sums.rows = p.B * p.saves;
   return reduce_rows(sums, stream, tr);
 }
 
@@ -672,11 +684,13 @@ hipError_t gated_dt(const gspn_gated_args& a, const gspn_gated_grads* g, void* w
 }  // namespace
 
 size_t gated_saved_bytes(int64_t B, int64_t L, int64_t C) {
-  return static_cast<size_t>(B * std::max<int64_t>(1, cdiv(L, kChunk)) * C) * 4;
+  return static_cast<size_t>(B * std::max<int64_t>(1, cdiv(L, kChunkB)) * C) * 4;
 }
-size_t gated_workspace_bytes(int64_t B, int64_t L, int64_t C) { return L <= kShort ? 0 : chain_space(B, L, C).bytes; }
+size_t gated_workspace_bytes(int64_t B, int64_t L, int64_t C) {
+  return L <= kShort ? 0 : chain_space(B, L, C, kChunkB).bytes;   // as the backward pass's chunks need it
+}
 size_t gated_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C) {
-  return chain_space(B, L, C).bytes + 2 * up256(gated_saved_bytes(B, L, C));
+  return chain_space(B, L, C, kChunkB).bytes + 2 * up256(gated_saved_bytes(B, L, C));
 }
 
 hipError_t launch_gated(const gspn_gated_args& a, void* ws, hipStream_t stream, Tracer* tr) {

@@ -273,34 +273,39 @@ __global__ __launch_bounds__(kBlock) void run_sums_kernel(RunP<T, O> a, Deal dea
   const int64_t all = a.start[a.V], p0 = c * kChunk;
   if (p0 >= all || piece >= a.pieces) return;
   const int64_t p1 = p0 + kChunk < all ? p0 + kChunk : all;
-  float s[V] = {};
+  float s[V] = {}, f[kChunk];
+  int64_t from[kChunk];
+  int32_t v[kChunk], r0[kChunk], r1[kChunk];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    const int2 tr = a.place[p0 + k < p1 ? p0 + k : p1 - 1];
+    const int64_t t = tr.x, b = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L);
+    from[k] = b * a.batch + (t - b * a.L) * a.stride;
+    v[k] = tr.y;
+    f[k] = a.weight ? a.weight[t] : 1.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    r0[k] = a.start[v[k]];
+    r1[k] = a.start[v[k] + 1];
+  }
   constexpr int kAhead = 8;
 #pragma unroll
   for (int k0 = 0; k0 < kChunk; k0 += kAhead) {
-    const int64_t p = p0 + k0;
-    if (p >= p1) break;
-    float d[kAhead][V], f[kAhead];
-    int32_t v[kAhead], r0[kAhead], r1[kAhead];
+    if (p0 + k0 >= p1) break;
+    float d[kAhead][V];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ldv<V>(a.x + from[k0 + k] + at, d[k]);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int64_t q = p + k < p1 ? p + k : p1 - 1;
-      const int2 tr = a.place[q];
-      const int64_t t = tr.x, b = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L);
-      v[k] = tr.y;
-      r0[k] = a.start[v[k]];
-      r1[k] = a.start[v[k] + 1];
-      f[k] = a.weight ? a.weight[t] : 1.0f;
-      ldv<V>(a.x + b * a.batch + (t - b * a.L) * a.stride + at, d[k]);
-    }
+      const int n = k0 + k;
+      if (p0 + n >= p1) break;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (p + k >= p1) break;
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(f[k], d[k][e], s[e]);
-      if (p + k + 1 < p1 && p + k + 1 < r1[k]) continue;
+      for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(f[n], d[k][e], s[e]);
+      if (p0 + n + 1 < p1 && p0 + n + 1 < r1[n]) continue;
       // the run ends here, or goes on after the chunk
-      if (r0[k] >= p0 && r1[k] <= p1) finish_run<V>(a, v[k], r0[k], at, s);
-      else stv<V>(a.part + (c * 2 + (r0[k] >= p0 ? 1 : 0)) * a.D + at, s);
+      if (r0[n] >= p0 && r1[n] <= p1) finish_run<V>(a, v[n], r0[n], at, s);
+      else stv<V>(a.part + (c * 2 + (r0[n] >= p0 ? 1 : 0)) * a.D + at, s);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] = 0.0f;
     }

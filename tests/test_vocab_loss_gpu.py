@@ -271,3 +271,47 @@ def test_binding_refuses():
         with pytest.raises(g.GspnError) as e:
             bad()
         assert e.value.name == name
+
+
+@pytest.mark.parametrize("T,V,D,dtype,ragged", [
+    (300, 13_000, 1032, BF16, False),      # whole tiles of 256 in the gradients, none whole at the edges
+    (300, 13_001, 1031, F32, True),        # the same in fp32, rows of no whole pieces
+    (1000, 5000, 520, BF16, True),         # tiles of 128
+    (999, 3001, 517, F32, False),
+    (4097, 700, 200, BF16, True),          # many tokens, few rows
+    (65, 9000, 264, BF16, False),          # one token past the kernel for few
+])
+def test_tiles_of_every_size(T, V, D, dtype, ragged):
+    """Tiles that run off every edge, against 64 bits on the GPU, in the norm: the
+    rounding of results and operands (see above) for bf16; for fp32 a sum of n
+    products has at most n roundings of 2^-24 of its size, their root as they fall."""
+    gen = torch.Generator(device=DEV).manual_seed(T + V)
+    B = 2
+    L = (T + 1) // 2
+    x = torch.randn(B, L, D, generator=gen, device=DEV).to(dtype)
+    w = (torch.randn(V, D, generator=gen, device=DEV) * 2 * D ** -0.5).to(dtype)
+    t = torch.randint(-1, V, (B, L), generator=gen, device=DEV)
+    gl = torch.rand(B, L, generator=gen, device=DEV) + 0.5
+    lens = torch.tensor([L, L // 3], dtype=torch.int32, device=DEV) if ragged else None
+    live = torch.ones(B, L, dtype=torch.bool, device=DEV)
+    if ragged:
+        live = torch.arange(L, device=DEV)[None] < lens[:, None]
+        x = x.masked_fill(~live[..., None], NAN)
+    lse = torch.empty(B, L, device=DEV)
+    loss = g.vocab_loss(x, w, t, lens=lens, lse=lse)
+    got = g.vocab_loss_backward(x, w, t, lse, gl, lens=lens)
+    on = live & (t >= 0)
+    xs = x.double().nan_to_num().masked_fill(~live[..., None], 0.0).requires_grad_()
+    ws = w.double().requires_grad_()
+    z = xs @ ws.T
+    ref_lse = torch.logsumexp(z, -1)
+    ref = (ref_lse - z.gather(2, t.clamp(min=0)[..., None])[..., 0]) * on
+    dx, dw = torch.autograd.grad((ref * gl.double()).sum(), (xs, ws))
+    for name, a, b in (("lse", lse, (ref_lse * live).detach()), ("loss", loss, ref.detach())):
+        assert float((a.double() - b).norm() / b.norm()) <= 2 * (D ** 0.5 + 30) * S, name
+    for name, a, b, n in (("x", got["x"], dx, V), ("weight", got["weight"], dw, T)):
+        own = float((b.to(dtype).double() - b).norm() / b.norm())
+        bound = 1.2 * own if dtype == BF16 else own + (n ** 0.5 + 2 * D ** 0.5 + 60) * S
+        assert float((a.double() - b).norm() / b.norm()) <= bound, name
+        assert torch.isfinite(a).all()
+    assert not got["x"][~on].any()

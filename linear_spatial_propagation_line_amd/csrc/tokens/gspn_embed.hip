@@ -22,10 +22,14 @@ constexpr int kRangeBits = 10;
 constexpr int kMaxRange = 1 << kRangeBits;   // table rows that one sorting workgroup owns, at most
 constexpr int kBlock = 256;
 
-// Tokens of a sorting wavefront, in whole turns of kTurn * 64: the rows are
-// padded to kSortWaves of these with -1, so that no load asks where the end is.
+// Tokens of a sorting wavefront: up to a turn of kTurn * 64 in steps of 64, from
+// there on whole turns, to which the rows are padded with -1, so that no load asks
+// where the end is.
 constexpr int kTurn = 8;
-int64_t sort_share(int64_t tokens) { return cdiv(tokens, kSortWaves * kTurn * 64) * (kTurn * 64); }
+int64_t sort_share(int64_t tokens) {
+  const int64_t share = cdiv(tokens, kSortWaves * 64) * 64;
+  return share <= kTurn * 64 ? share : cdiv(share, kTurn * 64) * (kTurn * 64);
+}
 
 // Rows per sorting workgroup: about one workgroup per compute unit, each of
 // which reads all ids, at least a wavefront's worth of rows.
@@ -48,20 +52,31 @@ template <typename T> struct EmbedP {
   int ids64;
 };
 
-__device__ __forceinline__ int64_t id_at(const void* ids, int ids64, int64_t i) {
-  return ids64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
-}
-
-// entry of token t (fewer than 2^31 tokens)
-template <typename P> __device__ __forceinline__ int64_t entry_of(const P& a, int64_t t) {
-  return static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L);
-}
-// the table row of token t, -1 for padding and for ids outside the table
-template <typename P> __device__ __forceinline__ int64_t row_of(const P& a, int64_t t) {
-  const int64_t b = entry_of(a, t), l = t - b * a.L;
-  if (l >= seq_len(a.lens, b, a.L)) return -1;
-  const int64_t id = id_at(a.ids, a.ids64, b * a.ids_batch + l);
-  return id >= 0 && id < a.V ? id : -1;
+// The table rows of N tokens t, t + apart, ...: -1 for padding, for ids outside
+// the table and past the last token. All ids are loaded, whatever they are for,
+// so that no load waits for another.
+template <int N, typename P>
+__device__ __forceinline__ void rows_of(const P& a, int64_t t, int64_t apart, int32_t (&row)[N]) {
+  int64_t at[N], id[N];
+  bool live[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t u = t + k * apart;
+    const uint32_t c = static_cast<uint32_t>(u < a.tokens ? u : a.tokens - 1), b = c / static_cast<uint32_t>(a.L);
+    const uint32_t l = c - b * static_cast<uint32_t>(a.L);
+    at[k] = b * a.ids_batch + l;
+    live[k] = u < a.tokens;
+    if (a.lens) live[k] = live[k] && static_cast<int32_t>(l) < a.lens[b];
+  }
+  if (a.ids64) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) id[k] = static_cast<const int64_t*>(a.ids)[at[k]];
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) id[k] = static_cast<const int32_t*>(a.ids)[at[k]];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) row[k] = live[k] && id[k] >= 0 && id[k] < a.V ? static_cast<int32_t>(id[k]) : -1;
 }
 
 // How rows are dealt to wavefronts: `per` rows to one, a row's pieces in
@@ -99,7 +114,9 @@ __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a, Deal deal) {
   for (int k = 0; k < deal.per; ++k) {
     const int64_t t = w.row + k;
     if (t >= a.tokens) return;
-    const int64_t row = row_of(a, t);
+    int32_t one[1];
+    rows_of<1>(a, t, 0, one);
+    const int64_t row = one[0];
     const T* src = a.weight + (row < 0 ? 0 : row) * a.D;
     T* dst = a.out + t * a.D;
     for (int64_t p = w.piece; p < a.pieces; p += step * kAtOnce) {
@@ -125,7 +142,9 @@ __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a, Deal deal) {
 template <typename P>
 __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, int64_t padded) {
   const int64_t t = (a.block0 + blockIdx.x) * kBlock + threadIdx.x;
-  if (t < padded) rows[t] = t < a.tokens ? static_cast<int32_t>(row_of(a, t)) : -1;
+  int32_t row[1];
+  rows_of<1>(a, t, 0, row);
+  if (t < padded) rows[t] = row[0];
 }
 
 // Stable counting sort. Workgroup g owns table rows v0 = g * range .. and
@@ -135,9 +154,12 @@ __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, 
 // then, with every row's and wavefront's first place known, it places them.
 // Equal rows among 64 tokens are found by comparing the bits of the row
 // numbers, so that a lane's place is its wavefront's next one plus the lanes
-// of the same row before it.
+// of the same row before it. DIRECT: one turn per wavefront, whose rows every
+// workgroup finds from the ids itself; more tokens come as rows that another
+// kernel has found once (a launch more, which few tokens would wait for).
+template <bool DIRECT, typename P>
 __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
-    const int32_t* rows, int64_t share, int64_t V, int range, int32_t* start, int2* place_of) {
+    P a, const int32_t* rows, int64_t share, int64_t V, int range, int32_t* start, int2* place_of) {
   __shared__ int32_t counts[kSortWaves * kMaxRange];   // [wavefront][row]
   __shared__ int32_t sums[kSortWaves], below[kSortWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -147,10 +169,18 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
   __syncthreads();
   const int32_t* own = rows + wave * share;
   int32_t lower = 0;
-  for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
-    uint32_t r[kTurn];
+  uint32_t r[kTurn];
+  if constexpr (DIRECT) {
+    int32_t own_rows[kTurn] = {};
+    if (share > 0) rows_of<kTurn>(a, wave * share + lane, 64, own_rows);
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
+    for (int k = 0; k < kTurn; ++k) r[k] = 64 * k < share ? own_rows[k] : -1;
+  }
+  for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
+    }
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) {
       lower += r[k] < static_cast<uint32_t>(v0) ? 1 : 0;   // -1 is the largest
@@ -191,9 +221,11 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
   }
   __syncthreads();
   for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
-    uint32_t r[kTurn], lo[kTurn], hi[kTurn];   // rows; lanes whose row numbers agree in every bit
+    uint32_t lo[kTurn], hi[kTurn];   // lanes whose row numbers agree in every bit
+    if constexpr (!DIRECT) {
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
+      for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
+    }
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) {
       const uint32_t i = r[k] - v0;
@@ -393,6 +425,11 @@ template <typename T, typename O> hipError_t run_sums_dt(const RunSum& r, hipStr
   if (r.D % V == 0 && wide_ok(r.out, 16, sizeof(O), {}) &&
       (r.tokens == 0 || wide_ok(r.x, 16, sizeof(T), {r.batch, r.row})))
     return run_sums_of<T, O, V>(r, stream, tr);
+  // rows of no whole 16 bytes: bf16 in pairs, if that
+  if constexpr (sizeof(T) == 2)
+    if (r.D % 2 == 0 && wide_ok(r.out, 2 * sizeof(O), sizeof(O), {}) &&
+        (r.tokens == 0 || wide_ok(r.x, 4, sizeof(T), {r.batch, r.row})))
+      return run_sums_of<T, O, 2>(r, stream, tr);
   return run_sums_of<T, O, 1>(r, stream, tr);
 }
 
@@ -428,6 +465,9 @@ template <typename T> hipError_t embed_dt(const gspn_embed_args& a, hipStream_t 
   const EmbedP<T> p = embed_params<T>(a);
   if (a.D % V == 0 && wide_ok(a.weight, 16, sizeof(T), {}) && wide_ok(a.out, 16, sizeof(T), {}))
     return embed_run<T, V>(p, stream, tr);
+  if constexpr (sizeof(T) == 2)
+    if (a.D % 2 == 0 && wide_ok(a.weight, 4, sizeof(T), {}) && wide_ok(a.out, 4, sizeof(T), {}))
+      return embed_run<T, 2>(p, stream, tr);
   return embed_run<T, 1>(p, stream, tr);
 }
 
@@ -455,8 +495,11 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
   p.V = V;
   p.tokens = tokens;
   p.ids64 = ids64;
+  const int range = sort_range(V);
+  const dim3 grid(static_cast<unsigned>(cdiv(V, range))), block(kSortWaves * 64);
+  const bool direct = share <= kTurn * 64;
   hipError_t e = hipSuccess;
-  if (tokens > 0) {
+  if (!direct) {
     tr->before(stream, "embed_rows", tokens);
     e = in_parts(cdiv(padded, kBlock), [&](int64_t first, unsigned count) {
       p.block0 = first;
@@ -465,10 +508,9 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
     tr->after(stream);
     if (e != hipSuccess) return e;
   }
-  const int range = sort_range(V);
   tr->before(stream, "embed_sort", tokens);
-  hipLaunchKernelGGL(embed_sort_kernel, dim3(static_cast<unsigned>(cdiv(V, range))), dim3(kSortWaves * 64), 0, stream,
-                     rows, share, V, range, start, place);
+  if (direct) hipLaunchKernelGGL((embed_sort_kernel<true, EmbedP<bf16_t>>), grid, block, 0, stream, p, rows, share, V, range, start, place);
+  else hipLaunchKernelGGL((embed_sort_kernel<false, EmbedP<bf16_t>>), grid, block, 0, stream, p, rows, share, V, range, start, place);
   e = hipGetLastError();
   tr->after(stream);
   return e;

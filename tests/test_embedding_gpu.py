@@ -37,6 +37,8 @@ CASES = [
     (5, 0, 20, 12, F32, torch.int64, None, 1.0),               # no tokens
     (0, 4, 20, 12, BF16, torch.int64, None, 1.0),
     (2, 9, 40, 520, BF16, torch.int64, (-3, 99), 1.0),         # lengths are clamped
+    (2, 50, 60, 70, BF16, torch.int64, (50, 44), 3.0),         # rows of whole pairs
+    (1, 40, 7, 131, BF16, torch.int32, None, 1.0),             # of none
 ]
 
 

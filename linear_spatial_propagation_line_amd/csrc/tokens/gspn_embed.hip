@@ -52,33 +52,6 @@ template <typename T> struct EmbedP {
   int ids64;
 };
 
-// The table rows of N tokens t, t + apart, ...: -1 for padding, for ids outside
-// the table and past the last token. All ids are loaded, whatever they are for,
-// so that no load waits for another.
-template <int N, typename P>
-__device__ __forceinline__ void rows_of(const P& a, int64_t t, int64_t apart, int32_t (&row)[N]) {
-  int64_t at[N], id[N];
-  bool live[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int64_t u = t + k * apart;
-    const uint32_t c = static_cast<uint32_t>(u < a.tokens ? u : a.tokens - 1), b = c / static_cast<uint32_t>(a.L);
-    const uint32_t l = c - b * static_cast<uint32_t>(a.L);
-    at[k] = b * a.ids_batch + l;
-    live[k] = u < a.tokens;
-    if (a.lens) live[k] = live[k] && static_cast<int32_t>(l) < a.lens[b];
-  }
-  if (a.ids64) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) id[k] = static_cast<const int64_t*>(a.ids)[at[k]];
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) id[k] = static_cast<const int32_t*>(a.ids)[at[k]];
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) row[k] = live[k] && id[k] >= 0 && id[k] < a.V ? static_cast<int32_t>(id[k]) : -1;
-}
-
 // How rows are dealt to wavefronts: `per` rows to one, a row's pieces in
 // `slices` shares where there are few rows. Row, id and run are the same for the
 // whole wavefront, so that a piece costs little more than its load and store
@@ -114,8 +87,9 @@ __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a, Deal deal) {
   for (int k = 0; k < deal.per; ++k) {
     const int64_t t = w.row + k;
     if (t >= a.tokens) return;
+    bool live[1];
     int32_t one[1];
-    rows_of<1>(a, t, 0, one);
+    ids_of<1>(a, t, 0, live, one);
     const int64_t row = one[0];
     const T* src = a.weight + (row < 0 ? 0 : row) * a.D;
     T* dst = a.out + t * a.D;
@@ -142,8 +116,9 @@ __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedP<T> a, Deal deal) {
 template <typename P>
 __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, int64_t padded) {
   const int64_t t = (a.block0 + blockIdx.x) * kBlock + threadIdx.x;
+  bool live[1];
   int32_t row[1];
-  rows_of<1>(a, t, 0, row);
+  ids_of<1>(a, t, 0, live, row);
   if (t < padded) rows[t] = row[0];
 }
 
@@ -171,8 +146,9 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
   int32_t lower = 0;
   uint32_t r[kTurn];
   if constexpr (DIRECT) {
+    bool live[kTurn];
     int32_t own_rows[kTurn] = {};
-    if (share > 0) rows_of<kTurn>(a, wave * share + lane, 64, own_rows);
+    if (share > 0) ids_of<kTurn>(a, wave * share + lane, 64, live, own_rows);
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) r[k] = 64 * k < share ? own_rows[k] : -1;
   }

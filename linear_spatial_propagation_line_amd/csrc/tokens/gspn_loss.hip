@@ -50,7 +50,7 @@ template <typename T> struct LossP {
   TokenList list;
   const T* x; int64_t xb, xr;
   const T* weight;
-  const void* targets; int64_t targets_batch; int64_t targets64;
+  const void* ids; int64_t ids_batch; int64_t ids64;   // the targets
   const int32_t* lens;
   float* loss; float* lse;
   const float* glse; const float* gloss;
@@ -59,7 +59,7 @@ template <typename T> struct LossP {
   int64_t wld;
   float2* part;        // maximum and sum of tile m of V and place p: [m * part_m + p * part_p]
   int64_t part_m, part_p;
-  int64_t L, V, D, T_, Tp, Dp;
+  int64_t L, V, D, tokens, Tp, Dp;
   int64_t block0;
 };
 
@@ -68,31 +68,22 @@ template <typename T> struct LossP {
 // padding (whose results are set to 0 here), backward those with a target. Eight
 // tokens per lane and turn, all loaded before the first is used (8192 tokens: 5 us,
 // one at a time 14).
-template <typename P> __device__ __forceinline__ bool token_counts(const P& a, int64_t t, bool back, int32_t& target) {
-  const int64_t b = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.L), l = t - b * a.L;   // fewer than 2^28 tokens
-  if (l >= seq_len(a.lens, b, a.L)) return false;
-  const int64_t i = b * a.targets_batch + l;
-  const int64_t v = a.targets64 ? static_cast<const int64_t*>(a.targets)[i] : static_cast<const int32_t*>(a.targets)[i];
-  target = v >= 0 && v < a.V ? static_cast<int32_t>(v) : -1;
-  return !back || target >= 0;
-}
 template <typename P, bool BACK>
 __global__ __launch_bounds__(1024) void loss_list_kernel(P a) {
   constexpr int kRows = 8;
   __shared__ int32_t sums[kRows][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int32_t done = 0;
-  for (int64_t t0 = 0; t0 < a.T_; t0 += kRows * 1024) {
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kRows * 1024) {
     bool keep[kRows];
     int32_t target[kRows];
     float g[kRows], lse[kRows];
+    ids_of<kRows>(a, t0 + threadIdx.x, 1024, keep, target);
+    if constexpr (BACK) {
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int64_t t = t0 + k * 1024 + threadIdx.x;
-      target[k] = -1;
-      keep[k] = t < a.T_ && token_counts(a, t, BACK, target[k]);
-      if constexpr (BACK) {
-        const int64_t c = t < a.T_ ? t : a.T_ - 1;
+      for (int k = 0; k < kRows; ++k) {
+        const int64_t t = t0 + k * 1024 + threadIdx.x, c = t < a.tokens ? t : a.tokens - 1;
+        keep[k] = target[k] >= 0;
         g[k] = a.gloss[c];
         lse[k] = a.glse[c];
       }
@@ -120,14 +111,14 @@ __global__ __launch_bounds__(1024) void loss_list_kernel(P a) {
           a.list.g[at] = g[k];
           a.list.lse[at] = lse[k];
         }
-      } else if (t < a.T_) {
+      } else if (t < a.tokens) {
         if constexpr (!BACK) {
           a.loss[t] = 0.0f;
           if (a.lse) a.lse[t] = 0.0f;
         }
       }
       if constexpr (BACK)
-        if (t < a.T_) a.list.pos[t] = keep[k] ? at : -1;
+        if (t < a.tokens) a.list.pos[t] = keep[k] ? at : -1;
     }
     __syncthreads();
   }
@@ -149,8 +140,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void loss_few_kernel(LossP<T> a, int wide) {
   constexpr int kPer = 16 / sizeof(T);
   const int lane = threadIdx.x & 63, p = blockIdx.x;
-  int32_t target = -1;
-  const bool keep = lane < a.T_ && token_counts(a, lane, false, target);
+  bool live[1];
+  int32_t id[1];
+  ids_of<1>(a, lane, 0, live, id);
+  const bool keep = live[0];
+  const int32_t target = id[0];
   const uint64_t mask = __ballot(keep);
   const int count = __popcll(mask);
   if (p == 0 && threadIdx.x < 64) {
@@ -159,7 +153,7 @@ __global__ __launch_bounds__(256) void loss_few_kernel(LossP<T> a, int wide) {
       const int at = __popcll(mask & ((uint64_t(1) << lane) - 1));
       a.list.token[at] = lane;
       a.list.target[at] = target;
-    } else if (lane < a.T_) {
+    } else if (lane < a.tokens) {
       a.loss[lane] = 0.0f;
       if (a.lse) a.lse[lane] = 0.0f;
     }
@@ -513,7 +507,7 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(LossP<T> a, const float* p
   const uint32_t i = static_cast<uint32_t>(first - t0 * per) + threadIdx.x;
   const uint32_t up = i / static_cast<uint32_t>(per);
   const int64_t t = t0 + up, col = static_cast<int64_t>(i - up * static_cast<uint32_t>(per)) * V;
-  if (t >= a.T_) return;
+  if (t >= a.tokens) return;
   const int64_t p = a.list.pos[t];
   float s[V] = {};
   if (p >= 0) {
@@ -572,7 +566,7 @@ template <typename T> void take_common(Space& s, LossP<T>& p) {
 }
 template <typename T> void take_forward(Space& s, LossP<T>& p) {
   take_common(s, p);
-  p.part = s.take<float2>(cdiv(p.V, p.T_ <= kFewTile ? kFewRows : tile_for(p.V, p.T_)) * p.Tp);
+  p.part = s.take<float2>(cdiv(p.V, p.tokens <= kFewTile ? kFewRows : tile_for(p.V, p.tokens)) * p.Tp);
 }
 
 // G of a piece is at most half a GiB, and pieces are alike. dx's contraction is
@@ -611,7 +605,7 @@ template <typename T> BackSpace<T> take_backward(Space& s, LossP<T>& p, const Gr
   take_common(s, p);
   p.list.g = s.take<float>(p.Tp);
   p.list.lse = s.take<float>(p.Tp);
-  p.list.pos = s.take<int32_t>(p.T_);
+  p.list.pos = s.take<int32_t>(p.tokens);
   b.G = s.take<T>(p.Tp * g.Vp);
   b.dx = s.take<float>(g.splits * p.Tp * p.Dp);
   b.rest = s.take<float>(p.Tp * p.Dp);
@@ -625,7 +619,7 @@ template <typename T> LossP<T> loss_sizes(int64_t tokens, int64_t L, int64_t V, 
   p.L = L;
   p.V = V;
   p.D = D;
-  p.T_ = tokens;
+  p.tokens = tokens;
   p.Tp = padded_tokens(tokens);
   p.Dp = padded(D, sizeof(T));
   return p;
@@ -636,17 +630,17 @@ template <typename T> LossP<T> loss_params(const gspn_loss_args& a) {
   p.xb = a.x.batch;
   p.xr = a.x.row;
   p.weight = static_cast<const T*>(a.weight);
-  p.targets = a.targets;
-  p.targets_batch = a.targets_batch;
-  p.targets64 = a.targets64;
+  p.ids = a.targets;
+  p.ids_batch = a.targets_batch;
+  p.ids64 = a.targets64;
   p.lens = a.lens;
   return p;
 }
 
 template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stream, Tracer* tr) {
-  const bool few = !BACK && p.T_ <= kFewTile;
+  const bool few = !BACK && p.tokens <= kFewTile;
   const int wide_x = wide_ok(p.x, 16, sizeof(T), {p.xb, p.xr}) && p.D % (16 / static_cast<int64_t>(sizeof(T))) == 0;
-  tr->before(stream, few ? "loss_few" : "loss_list", p.T_);
+  tr->before(stream, few ? "loss_few" : "loss_list", p.tokens);
   if (few) hipLaunchKernelGGL((loss_few_kernel<T>), dim3(kFewTile), dim3(256), 0, stream, p, wide_x);
   else hipLaunchKernelGGL((loss_list_kernel<LossP<T>, BACK>), dim3(1), dim3(1024), 0, stream, p);
   hipError_t e = hipGetLastError();
@@ -675,9 +669,9 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   take_forward(s, p);
   hipError_t e = gather<T, false>(p, stream, tr);
   if (e != hipSuccess) return e;
-  const bool few = p.T_ <= kFewTile;
-  const int64_t tile = tile_for(p.V, p.T_);
-  const int64_t mt = cdiv(p.V, few ? kFewRows : tile), nt = few ? 1 : cdiv(p.T_, tile);
+  const bool few = p.tokens <= kFewTile;
+  const int64_t tile = tile_for(p.V, p.tokens);
+  const int64_t mt = cdiv(p.V, few ? kFewRows : tile), nt = few ? 1 : cdiv(p.tokens, tile);
   p.part_m = few ? 1 : p.Tp;
   p.part_p = few ? mt : 1;
   tr->before(stream, "loss_logits", p.V);
@@ -691,14 +685,14 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   tr->after(stream);
   if (e != hipSuccess) return e;
   if (few) {
-    tr->before(stream, "loss_join_few", p.T_);
-    hipLaunchKernelGGL((loss_join_few_kernel<T>), dim3(static_cast<unsigned>(p.T_)), dim3(256), 0, stream, p, mt);
+    tr->before(stream, "loss_join_few", p.tokens);
+    hipLaunchKernelGGL((loss_join_few_kernel<T>), dim3(static_cast<unsigned>(p.tokens)), dim3(256), 0, stream, p, mt);
     e = hipGetLastError();
     tr->after(stream);
     return e;
   }
-  tr->before(stream, "loss_join", p.T_);
-  e = in_parts(cdiv(p.T_, 64), [&](int64_t first, unsigned count) {
+  tr->before(stream, "loss_join", p.tokens);
+  e = in_parts(cdiv(p.tokens, 64), [&](int64_t first, unsigned count) {
     p.block0 = first;
     hipLaunchKernelGGL((loss_join_kernel<T>), dim3(count), dim3(512), 0, stream, p, mt);
   });
@@ -711,7 +705,7 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   LossP<T> p = loss_params<T>(a);
   p.glse = g.lse;
   p.gloss = g.grad_loss;
-  const GradPlan plan = grad_plan(p.T_, p.V, p.D, sizeof(T));
+  const GradPlan plan = grad_plan(p.tokens, p.V, p.D, sizeof(T));
   Space s(ws);
   const BackSpace<T> b = take_backward(s, p, plan);
   hipError_t e = gather<T, true>(p, stream, tr);
@@ -719,9 +713,9 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   TokenSort sorted{};
   e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
   if (e != hipSuccess) return e;
-  const int64_t ttiles = cdiv(p.T_, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.T_, plan.gtile);
+  const int64_t ttiles = cdiv(p.tokens, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.tokens, plan.gtile);
   auto launch = [&](const char* name, int64_t blocks, auto&& kernel) {
-    tr->before(stream, name, p.T_);
+    tr->before(stream, name, p.tokens);
     const hipError_t r = in_parts(blocks, [&](int64_t first, unsigned count) {
       p.block0 = first;
       kernel(dim3(count));
@@ -729,7 +723,7 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
     tr->after(stream);
     return r;
   };
-  e = launch("loss_target", cdiv(p.T_, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
+  e = launch("loss_target", cdiv(p.tokens, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
   if (e != hipSuccess) return e;
   // G at the targets times the tokens' rows, summed for each target
   RunSum sum{};
@@ -771,7 +765,7 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   // whole pieces of x's gradient where its rows allow them
   constexpr int kPer = 16 / sizeof(T);
   const bool wide = p.D % kPer == 0 && wide_ok(g.x, 16, sizeof(T), {});
-  return launch("loss_dx", cdiv(p.T_ * (wide ? p.D / kPer : p.D), 256), [&](dim3 n) {
+  return launch("loss_dx", cdiv(p.tokens * (wide ? p.D / kPer : p.D), 256), [&](dim3 n) {
     if (wide) hipLaunchKernelGGL((loss_dx_kernel<T, kPer>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
     else hipLaunchKernelGGL((loss_dx_kernel<T, 1>), n, dim3(256), 0, stream, p, b.dx, plan.splits, static_cast<T*>(g.x));
   });
@@ -779,9 +773,9 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
 
 template <typename T> size_t loss_bytes(int64_t B, int64_t L, int64_t V, int64_t D, bool back) {
   LossP<T> p = loss_sizes<T>(B * L, L, V, D);
-  if (p.T_ == 0 && !back) return 0;
+  if (p.tokens == 0 && !back) return 0;
   Space s(nullptr);
-  if (back) take_backward(s, p, grad_plan(p.T_, V, D, sizeof(T)));
+  if (back) take_backward(s, p, grad_plan(p.tokens, V, D, sizeof(T)));
   else take_forward(s, p);
   return s.used();
 }

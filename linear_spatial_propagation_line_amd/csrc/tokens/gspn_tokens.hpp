@@ -250,4 +250,31 @@ __device__ __forceinline__ int64_t seq_len(const int32_t* lens, int64_t b, int64
   return n < 0 ? 0 : (n > L ? L : n);
 }
 
+// Tokens t, t + apart, ... (a.tokens of them in all, a.L to an entry, ids a.ids with
+// entry stride a.ids_batch, a.ids64 for int64): whether each is a token at all and
+// no padding, and its id, -1 where it is not in 0 .. a.V - 1. All ids are loaded,
+// whatever they are for, so that no load waits for another.
+template <int N, typename P>
+__device__ __forceinline__ void ids_of(const P& a, int64_t t, int64_t apart, bool (&live)[N], int32_t (&id)[N]) {
+  int64_t at[N], v[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t u = t + k * apart;
+    const uint32_t c = static_cast<uint32_t>(u < a.tokens ? u : a.tokens - 1), b = c / static_cast<uint32_t>(a.L);
+    const uint32_t l = c - b * static_cast<uint32_t>(a.L);
+    at[k] = b * a.ids_batch + l;
+    live[k] = u < a.tokens;
+    if (a.lens) live[k] = live[k] && static_cast<int32_t>(l) < a.lens[b];
+  }
+  if (a.ids64) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = static_cast<const int64_t*>(a.ids)[at[k]];
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = static_cast<const int32_t*>(a.ids)[at[k]];
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) id[k] = live[k] && v[k] >= 0 && v[k] < a.V ? static_cast<int32_t>(v[k]) : -1;
+}
+
 }  // namespace gspn

@@ -65,7 +65,7 @@ Deal deal(int64_t rows, int64_t pieces) {
   Deal d{rows, 1, 1};
   const int64_t turns = cdiv(pieces, 64);
   while (rows * d.slices < 8192 && d.slices < turns) ++d.slices;
-  while (d.per < 4 && rows / d.per > 16384) d.per *= 2;
+  while (d.per < 4 && rows / d.per > 65536) d.per *= 2;
   return d;
 }
 int64_t deal_blocks(const Deal& d) { return cdiv(cdiv(d.rows, d.per) * d.slices, kBlock / 64); }

@@ -96,7 +96,7 @@ __device__ __forceinline__ void load_rows(const T* tile, int64_t stride, int64_t
   }
 }
 template <int V, typename T> __device__ __forceinline__ void put_row(T* row, uint32_t off, const float (&y)[V]) {
-  stv<V>(reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off), y);
+  stream_stv<V>(reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off), y);
 }
 
 // zeros in `rows` rows of V values

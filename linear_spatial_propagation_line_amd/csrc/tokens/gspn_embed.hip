@@ -22,21 +22,29 @@ constexpr int kRangeBits = 10;
 constexpr int kMaxRange = 1 << kRangeBits;   // table rows that one sorting workgroup owns, at most
 constexpr int kBlock = 256;
 
-// Tokens of a sorting wavefront: up to a turn of kTurn * 64 in steps of 64, from
-// there on whole turns, to which the rows are padded with -1, so that no load asks
-// where the end is.
+// How a sort is dealt out. A wavefront's share of the tokens: up to a turn of
+// kTurn * 64 in steps of 64, from there on whole turns, to which the rows are
+// padded with -1, so that no load asks where the end is; in up to four parts of
+// whole turns. Table rows of a workgroup: at least a wavefront's worth, so many
+// that there is about one workgroup per compute unit, each of which reads all tokens.
 constexpr int kTurn = 8;
-int64_t sort_share(int64_t tokens) {
-  const int64_t share = cdiv(tokens, kSortWaves * 64) * 64;
-  return share <= kTurn * 64 ? share : cdiv(share, kTurn * 64) * (kTurn * 64);
-}
-
-// Rows per sorting workgroup: about one workgroup per compute unit, each of
-// which reads all ids, at least a wavefront's worth of rows.
-int sort_range(int64_t V) {
-  int r = 64;
-  while (r < kMaxRange && cdiv(V, r) > 256) r *= 2;
-  return r;
+struct SortPlan {
+  int64_t share;    // tokens of a wavefront
+  int parts, range;
+  int64_t blocks;
+  int64_t padded() const { return share * kSortWaves * parts; }
+  bool direct() const { return share <= kTurn * 64 && parts == 1; }
+};
+SortPlan sort_plan(int64_t tokens, int64_t V) {
+  SortPlan s{cdiv(tokens, kSortWaves * 64) * 64, 1, 64, 0};
+  constexpr int64_t turn = kTurn * 64;
+  if (s.share > turn) {
+    s.parts = s.share > 2 * turn ? 4 : 2;
+    s.share = cdiv(cdiv(tokens, s.parts * kSortWaves), turn) * turn;
+  }
+  while (s.range < kMaxRange && cdiv(V, s.range) * s.parts > 256) s.range *= 2;
+  s.blocks = cdiv(V, s.range) * s.parts;
+  return s;
 }
 
 template <typename T> struct EmbedP {
@@ -122,11 +130,13 @@ __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, 
   if (t < padded) rows[t] = row[0];
 }
 
-// Stable counting sort. Workgroup g owns table rows v0 = g * range .. and
-// walks all tokens twice, wavefront w the w-th sixteenth of them: first it
-// counts (per wavefront and row, in LDS; integer counts do not depend on the
-// order of the additions) and finds how many tokens belong to rows below v0,
-// then, with every row's and wavefront's first place known, it places them.
+// Stable counting sort. A workgroup owns table rows v0 = range * (its number / parts)
+// .. and one of `parts` equal parts of the tokens. It counts all tokens of its rows,
+// those of its own part by wavefront (in LDS; integer counts do not depend on
+// the order of the additions), and finds how many tokens belong to rows below v0;
+// then, with every row's and wavefront's first place known, it places those of its
+// own part. Parts, since a few rows hold half of a text's tokens and one workgroup
+// would place them all (32768 tokens, 65536 rows: one part 24 us, four 14).
 // Equal rows among 64 tokens are found by comparing the bits of the row
 // numbers, so that a lane's place is its wavefront's next one plus the lanes
 // of the same row before it. DIRECT: one turn per wavefront, whose rows every
@@ -134,15 +144,17 @@ __global__ __launch_bounds__(kBlock) void embed_rows_kernel(P a, int32_t* rows, 
 // kernel has found once (a launch more, which few tokens would wait for).
 template <bool DIRECT, typename P>
 __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
-    P a, const int32_t* rows, int64_t share, int64_t V, int range, int32_t* start, int2* place_of) {
-  __shared__ int32_t counts[kSortWaves * kMaxRange];   // [wavefront][row]
+    P a, const int32_t* rows, int64_t share, int64_t V, int range, int parts, int32_t* start, int2* place_of) {
+  __shared__ int32_t counts[(kSortWaves + 2) * kMaxRange];   // [wavefront][row], of the parts before, after
   __shared__ int32_t sums[kSortWaves], below[kSortWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int32_t* mine_next = counts + wave * range;
-  const int32_t v0 = static_cast<int32_t>(blockIdx.x) * range;
-  for (int i = threadIdx.x; i < kSortWaves * range; i += kSortWaves * 64) counts[i] = 0;
+  const int64_t block = a.block0 + blockIdx.x;
+  const int part = static_cast<int>(block % parts);
+  const int32_t v0 = static_cast<int32_t>(block / parts) * range;
+  for (int i = threadIdx.x; i < (kSortWaves + 2) * range; i += kSortWaves * 64) counts[i] = 0;
   __syncthreads();
-  const int32_t* own = rows + wave * share;
+  const int32_t* own = rows + (part * kSortWaves + wave) * share;
   int32_t lower = 0;
   uint32_t r[kTurn];
   if constexpr (DIRECT) {
@@ -152,16 +164,20 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) r[k] = 64 * k < share ? own_rows[k] : -1;
   }
-  for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
-    if constexpr (!DIRECT) {
+  for (int q = 0; q < parts; ++q) {
+    const int32_t* from = rows + (q * kSortWaves + wave) * share;
+    int32_t* count = q == part ? mine_next : counts + (kSortWaves + (q < part ? 0 : 1)) * range;
+    for (int64_t turn = 0; turn < share; turn += kTurn * 64) {
+      if constexpr (!DIRECT) {
 #pragma unroll
-      for (int k = 0; k < kTurn; ++k) r[k] = own[turn + 64 * k + lane];
-    }
+        for (int k = 0; k < kTurn; ++k) r[k] = from[turn + 64 * k + lane];
+      }
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) {
-      lower += r[k] < static_cast<uint32_t>(v0) ? 1 : 0;   // -1 is the largest
-      const uint32_t i = r[k] - v0;
-      if (i < static_cast<uint32_t>(range)) atomicAdd(&mine_next[i], 1);
+      for (int k = 0; k < kTurn; ++k) {
+        lower += r[k] < static_cast<uint32_t>(v0) ? 1 : 0;   // -1 is the largest
+        const uint32_t i = r[k] - v0;
+        if (i < static_cast<uint32_t>(range)) atomicAdd(&count[i], 1);
+      }
     }
   }
 #pragma unroll
@@ -173,7 +189,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
   int32_t total = 0;
   if (i < range)
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) total += counts[w * range + i];
+    for (int w = 0; w < kSortWaves + 2; ++w) total += counts[w * range + i];
   int32_t before = total;   // inclusive sum over the wavefront's rows
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) {
@@ -186,8 +202,9 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
 #pragma unroll
   for (int w = 0; w < kSortWaves; ++w) at += below[w] + (w < wave ? sums[w] : 0);
   if (i < range) {
-    if (v0 + static_cast<int64_t>(i) < V) start[v0 + i] = at;
-    if (v0 + static_cast<int64_t>(i) == V - 1) start[V] = at + total;
+    if (part == 0 && v0 + static_cast<int64_t>(i) < V) start[v0 + i] = at;
+    if (part == 0 && v0 + static_cast<int64_t>(i) == V - 1) start[V] = at + total;
+    at += counts[kSortWaves * range + i];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const int32_t n = counts[w * range + i];
@@ -227,7 +244,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(
         const int32_t first = mine_next[i], place = first + __popcll(same & ((uint64_t(1) << lane) - 1));
         __builtin_amdgcn_wave_barrier();
         if ((same >> lane) == 1) mine_next[i] = place + 1;
-        place_of[place] = make_int2(static_cast<int32_t>(wave * share + turn + 64 * k + lane), r[k]);
+        place_of[place] = make_int2(static_cast<int32_t>((part * kSortWaves + wave) * share + turn + 64 * k + lane), r[k]);
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -450,13 +467,15 @@ template <typename T> hipError_t embed_dt(const gspn_embed_args& a, hipStream_t 
 }  // namespace
 
 size_t token_sort_bytes(int64_t tokens, int64_t V) {
-  return up256(static_cast<size_t>(sort_share(tokens)) * kSortWaves * 4) + up256(static_cast<size_t>(tokens) * 8) +
+  return up256(static_cast<size_t>(sort_plan(tokens, V).padded()) * 4) + up256(static_cast<size_t>(tokens) * 8) +
          up256(static_cast<size_t>(V + 1) * 4);
 }
 
 hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int32_t* lens, int64_t B, int64_t L,
                        int64_t V, void* ws, TokenSort* out, hipStream_t stream, Tracer* tr) {
-  const int64_t tokens = B * L, share = sort_share(tokens), padded = share * kSortWaves;
+  const int64_t tokens = B * L;
+  const SortPlan s = sort_plan(tokens, V);
+  const int64_t padded = s.padded();
   const size_t each = up256(static_cast<size_t>(padded) * 4);
   char* w = static_cast<char*>(ws);
   int32_t* rows = reinterpret_cast<int32_t*>(w);
@@ -471,11 +490,8 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
   p.V = V;
   p.tokens = tokens;
   p.ids64 = ids64;
-  const int range = sort_range(V);
-  const dim3 grid(static_cast<unsigned>(cdiv(V, range))), block(kSortWaves * 64);
-  const bool direct = share <= kTurn * 64;
   hipError_t e = hipSuccess;
-  if (!direct) {
+  if (!s.direct()) {
     tr->before(stream, "embed_rows", tokens);
     e = in_parts(cdiv(padded, kBlock), [&](int64_t first, unsigned count) {
       p.block0 = first;
@@ -485,9 +501,16 @@ hipError_t sort_tokens(const void* ids, int ids64, int64_t ids_batch, const int3
     if (e != hipSuccess) return e;
   }
   tr->before(stream, "embed_sort", tokens);
-  if (direct) hipLaunchKernelGGL((embed_sort_kernel<true, EmbedP<bf16_t>>), grid, block, 0, stream, p, rows, share, V, range, start, place);
-  else hipLaunchKernelGGL((embed_sort_kernel<false, EmbedP<bf16_t>>), grid, block, 0, stream, p, rows, share, V, range, start, place);
-  e = hipGetLastError();
+  e = in_parts(s.blocks, [&](int64_t first, unsigned count) {
+    p.block0 = first;
+    const dim3 block(kSortWaves * 64);
+    if (s.direct())
+      hipLaunchKernelGGL((embed_sort_kernel<true, EmbedP<bf16_t>>), dim3(count), block, 0, stream, p, rows, s.share, V,
+                         s.range, s.parts, start, place);
+    else
+      hipLaunchKernelGGL((embed_sort_kernel<false, EmbedP<bf16_t>>), dim3(count), block, 0, stream, p, rows, s.share, V,
+                         s.range, s.parts, start, place);
+  }, kMostBlocks / 2);
   tr->after(stream);
   return e;
 }

@@ -104,9 +104,9 @@ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // parts of at most kMostBlocks (of up to 512 threads): part(first, count), in
 // order; the kernel adds `first`.
 constexpr int64_t kMostBlocks = int64_t(1) << 22;
-template <typename F> hipError_t in_parts(int64_t blocks, F&& part) {
-  for (int64_t first = 0; first < blocks; first += kMostBlocks) {
-    part(first, static_cast<unsigned>(std::min(kMostBlocks, blocks - first)));
+template <typename F> hipError_t in_parts(int64_t blocks, F&& part, int64_t most = kMostBlocks) {
+  for (int64_t first = 0; first < blocks; first += most) {
+    part(first, static_cast<unsigned>(std::min(most, blocks - first)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -172,3 +172,25 @@ def test_binding_refuses():
         with pytest.raises(g.GspnError) as e:
             bad()
         assert e.value.name == "GSPN_E_SHAPE"
+
+
+@pytest.mark.parametrize("T,V", [(8192, 900), (8193, 70), (16384, 5000), (16385, 2), (40000, 300_000)])
+def test_sorts_of_every_size(T, V):
+    """One turn of the sort, the first token past it, two parts, the first past
+    them, more than one turn a part: every token once and in its row (whole
+    numbers), and the same bits whatever the ids' type."""
+    gen = torch.Generator().manual_seed(T)
+    ids = (torch.rand(1, T, generator=gen) ** 3 * V).long().clamp(max=V - 1)
+    ids[0, 5::9] = -1
+    whole = torch.randint(-8, 9, (1, T, 4), generator=gen).float()
+    ref = torch.zeros(V + 1, 4).index_add_(0, ids[0].where(ids[0] >= 0, torch.tensor(V)), whole[0])[:V]
+    assert torch.equal(g.token_embedding_backward(ids.to(DEV), whole.to(DEV), V)["weight"].cpu(), ref)
+    gy = torch.randn(1, T, 4, generator=gen).to(DEV)
+    a = g.token_embedding_backward(ids.to(DEV), gy, V)["weight"]
+    assert torch.equal(a, g.token_embedding_backward(ids.int().to(DEV), gy, V)["weight"])
+    dw, size, count = torch.zeros(3, V, 4, dtype=torch.float64)
+    on = ids[0] >= 0
+    dw.index_add_(0, ids[0][on], gy[0].cpu().double()[on])
+    size.index_add_(0, ids[0][on], gy[0].cpu().double().abs()[on])
+    count.index_add_(0, ids[0][on], torch.ones(int(on.sum()), 4, dtype=torch.float64))
+    plain.within(a, dw, size * (count + 1), 1, "weight")

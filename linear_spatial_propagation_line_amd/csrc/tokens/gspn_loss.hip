@@ -19,7 +19,8 @@
 // the result's own (0.0023 from 64 bits in the norm for 0.00166). So they are 0
 // in the operand; they are found apart, one fp32 value per token, and their
 // products with W's rows and x's are added to dx and dW in fp32. The other
-// entries' rounding is small beside that and independent.
+// entries' rounding is small beside that and independent. With fp32 storage the
+// operand holds them.
 #include "gspn_loss_gemm.hpp"
 
 namespace gspn {
@@ -29,6 +30,9 @@ namespace {
 constexpr int kTile = 256;       // the largest tile: tokens, vocabulary rows or columns
 constexpr int kFewTile = 64;     // tokens of a tile where there are few
 constexpr int kFewRows = 128;    // vocabulary rows of a tile then
+
+// whether G's entries at the targets are kept apart from the operand
+template <typename T> constexpr bool apart() { return sizeof(T) == 2; }
 
 // wavefronts of a square tile
 constexpr int waves_of(int tile) { return tile == 64 ? 4 : 8; }
@@ -170,26 +174,37 @@ __global__ __launch_bounds__(256) void loss_few_kernel(LossP<T> a, int wide) {
 }
 
 // Rows packed to Dp values, 16 bytes per lane, zeros past D and for places
-// without a token. `list` null: rows as they come (the weight).
+// without a token: the tokens', then the weight's (rows as they come).
+template <typename T> struct PackP {
+  const T* x; int64_t xb, xr;
+  const int32_t* token;   // null: rows as they come
+  T* out;
+  int64_t rows, blocks;
+  int wide;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void loss_pack_kernel(const T* x, int64_t xb, int64_t xr, int64_t L, int64_t D,
-                                                        int64_t Dp, int64_t rows, const int32_t* token,
-                                                        const int32_t* count, T* out, int wide, int64_t block0) {
+__global__ __launch_bounds__(256) void loss_pack_kernel(PackP<T> tokens, PackP<T> weight, int64_t L, int64_t D, int64_t Dp,
+                                                        const int32_t* count, int64_t block0) {
   constexpr int kPer = 16 / sizeof(T);
-  const int64_t per = Dp / kPer, i = (block0 + blockIdx.x) * 256 + threadIdx.x;
-  const int64_t p = i / per, at = (i - p * per) * kPer;
-  if (p >= rows) return;
-  const T* src = x + p * xr;
+  int64_t block = block0 + blockIdx.x;
+  const bool second = block >= tokens.blocks;
+  if (second) block -= tokens.blocks;
+  const PackP<T>& k = second ? weight : tokens;
+  const int64_t per = Dp / kPer, first = block * 256, p0 = first / per;
+  const uint32_t i = static_cast<uint32_t>(first - p0 * per) + threadIdx.x, up = i / static_cast<uint32_t>(per);
+  const int64_t p = p0 + up, at = static_cast<int64_t>(i - up * static_cast<uint32_t>(per)) * kPer;
+  if (p >= k.rows) return;
+  const T* src = k.x + p * k.xr;
   bool some = true;
-  if (token) {
+  if (k.token) {
     const int64_t all = *count;
     if (p >= (all + kTile - 1) / kTile * kTile) return;
     some = p < all;
-    const int64_t t = some ? token[p] : 0, b = some ? t / L : 0;
-    src = x + b * xb + (t - b * L) * xr;
+    const int64_t t = some ? k.token[p] : 0, b = some ? static_cast<uint32_t>(t) / static_cast<uint32_t>(L) : 0;
+    src = k.x + b * k.xb + (t - b * L) * k.xr;
   }
-  *reinterpret_cast<u32x4*>(out + p * Dp + at) =
-      load16<T, false>(src, static_cast<int>(at), some ? static_cast<int>(D) : 0, wide);
+  *reinterpret_cast<u32x4*>(k.out + p * Dp + at) =
+      load16<T, false>(src, static_cast<int>(at), some ? static_cast<int>(D) : 0, k.wide);
 }
 
 // ---- forward ----------------------------------------------------------------
@@ -393,7 +408,10 @@ __global__ __launch_bounds__(64 * waves_of(S)) void loss_g_kernel(LossP<T> a, T*
             }
           }
         lds_wave_sync();
-        if (lane < 32 && want >= 0 && want < S / 2) Store<T>::put(reinterpret_cast<T*>(row_out), want, 0.0f);
+        if (lane < 32 && want >= 0 && want < S / 2) {
+          T* target_entry = reinterpret_cast<T*>(row_out) + want;
+          Store<T>::put(target_entry, 0, apart<T>() ? 0.0f : to_f32(*target_entry) - g);
+        }
       }
     }
     lds_barrier();
@@ -462,8 +480,12 @@ __global__ __launch_bounds__(64 * waves_of(S)) void loss_grads_kernel(LossP<T> a
     for (int r = 0; r < 16; ++r) {
       const int64_t v = v0 + m0 + wm + 32 * i + tile_row(r, lane);
       if (v >= a.V) continue;
-      const int64_t s0 = start[v];
-      const bool some = start[v + 1] > s0;
+      int64_t s0 = 0;
+      bool some = false;
+      if constexpr (apart<T>()) {
+        s0 = start[v];
+        some = start[v + 1] > s0;
+      }
 #pragma unroll
       for (int j = 0; j < PW::NI; ++j) {
         const int64_t col = n0 + wn + 32 * j + (lane & 31);
@@ -511,16 +533,18 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(LossP<T> a, const float* p
   const int64_t p = a.list.pos[t];
   float s[V] = {};
   if (p >= 0) {
-    float w[V];
-    ldv<V>(a.w + a.list.target[p] * a.wld + col, w);
     for (int64_t k = 0; k < splits; ++k) {
       float y[V];
       ldv<V>(parts + (k * a.Tp + p) * a.Dp + col, y);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] += y[e];
     }
+    if constexpr (apart<T>()) {
+      float w[V];
+      ldv<V>(a.w + a.list.target[p] * a.wld + col, w);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(a.list.at[p], w[e], s[e]);
+      for (int e = 0; e < V; ++e) s[e] = __builtin_fmaf(a.list.at[p], w[e], s[e]);
+    }
   }
   stv<V>(dx + t * a.D + col, s);
 }
@@ -608,6 +632,7 @@ template <typename T> BackSpace<T> take_backward(Space& s, LossP<T>& p, const Gr
   p.list.pos = s.take<int32_t>(p.tokens);
   b.G = s.take<T>(p.Tp * g.Vp);
   b.dx = s.take<float>(g.splits * p.Tp * p.Dp);
+  if (!apart<T>()) return b;
   b.rest = s.take<float>(p.Tp * p.Dp);
   b.rest_part = reinterpret_cast<float*>(s.take<char>(static_cast<int64_t>(run_part_bytes(p.Tp, p.Dp))));
   b.sort = s.take<char>(static_cast<int64_t>(token_sort_bytes(p.Tp, p.V)));
@@ -646,18 +671,17 @@ template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stre
   hipError_t e = hipGetLastError();
   tr->after(stream);
   if (e != hipSuccess) return e;
-  auto pack = [&](const T* x, int64_t xb, int64_t xr, int64_t rows, const int32_t* token, T* out) {
-    const int wide = wide_ok(x, 16, sizeof(T), {xb, xr}) && p.D % (16 / static_cast<int64_t>(sizeof(T))) == 0;
-    tr->before(stream, "loss_pack", rows);
-    const hipError_t r = in_parts(cdiv(rows * (p.Dp * static_cast<int64_t>(sizeof(T)) / 16), 256), [&](int64_t first, unsigned count) {
-      hipLaunchKernelGGL((loss_pack_kernel<T>), dim3(count), dim3(256), 0, stream, x, xb, xr, p.L, p.D, p.Dp, rows, token,
-                         p.list.count, out, wide, first);
-    });
-    tr->after(stream);
-    return r;
-  };
-  if (!few && (e = pack(p.x, p.xb, p.xr, p.Tp, p.list.token, p.packed)) != hipSuccess) return e;
-  if (p.w != p.weight) e = pack(p.weight, 0, p.D, p.V, nullptr, const_cast<T*>(p.w));
+  const int64_t pieces = p.Dp * static_cast<int64_t>(sizeof(T)) / 16;
+  PackP<T> x{p.x, p.xb, p.xr, p.list.token, p.packed, few ? 0 : p.Tp, 0, wide_x};
+  PackP<T> w{p.weight, 0, p.D, nullptr, const_cast<T*>(p.w), p.w != p.weight ? p.V : 0, 0, 0};
+  x.blocks = cdiv(x.rows * pieces, 256);
+  w.blocks = cdiv(w.rows * pieces, 256);
+  if (x.blocks + w.blocks == 0) return hipSuccess;
+  tr->before(stream, "loss_pack", p.Tp);
+  e = in_parts(x.blocks + w.blocks, [&](int64_t first, unsigned count) {
+    hipLaunchKernelGGL((loss_pack_kernel<T>), dim3(count), dim3(256), 0, stream, x, w, p.L, p.D, p.Dp, p.list.count, first);
+  });
+  tr->after(stream);
   return e;
 }
 
@@ -711,8 +735,6 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
   hipError_t e = gather<T, true>(p, stream, tr);
   if (e != hipSuccess) return e;
   TokenSort sorted{};
-  e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
-  if (e != hipSuccess) return e;
   const int64_t ttiles = cdiv(p.tokens, plan.tile), dtiles = cdiv(p.D, plan.tile), gtiles = cdiv(p.tokens, plan.gtile);
   auto launch = [&](const char* name, int64_t blocks, auto&& kernel) {
     tr->before(stream, name, p.tokens);
@@ -723,23 +745,27 @@ hipError_t loss_bwd(const gspn_loss_args& a, const gspn_loss_grads& g, void* ws,
     tr->after(stream);
     return r;
   };
-  e = launch("loss_target", cdiv(p.tokens, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
-  if (e != hipSuccess) return e;
-  // G at the targets times the tokens' rows, summed for each target
-  RunSum sum{};
-  sum.sort = sorted;
-  sum.dtype = a.dtype;
-  sum.x = p.packed;
-  sum.row = p.Dp;
-  sum.L = sum.tokens = p.Tp;
-  sum.weight = p.list.at;
-  sum.scale = 1.0f;
-  sum.out = b.rest;
-  sum.by_place = 1;
-  sum.part = b.rest_part;
-  sum.V = p.V;
-  sum.D = p.Dp;
-  if ((e = run_sums(sum, stream, tr)) != hipSuccess) return e;
+  if (apart<T>()) {
+    // G at the targets, and times the tokens' rows, summed for each target
+    e = sort_tokens(p.list.target, 0, 0, nullptr, 1, p.Tp, p.V, b.sort, &sorted, stream, tr);
+    if (e != hipSuccess) return e;
+    e = launch("loss_target", cdiv(p.tokens, 4), [&](dim3 n) { hipLaunchKernelGGL((loss_target_kernel<T>), n, dim3(256), 0, stream, p); });
+    if (e != hipSuccess) return e;
+    RunSum sum{};
+    sum.sort = sorted;
+    sum.dtype = a.dtype;
+    sum.x = p.packed;
+    sum.row = p.Dp;
+    sum.L = sum.tokens = p.Tp;
+    sum.weight = p.list.at;
+    sum.scale = 1.0f;
+    sum.out = b.rest;
+    sum.by_place = 1;
+    sum.part = b.rest_part;
+    sum.V = p.V;
+    sum.D = p.Dp;
+    if ((e = run_sums(sum, stream, tr)) != hipSuccess) return e;
+  }
   for (int64_t k = 0; k < plan.pieces; ++k) {
     const int64_t v0 = k * plan.Vp, rows = std::min(plan.Vp, p.V - v0);
     const int64_t mtiles = cdiv(rows, plan.gtile), vtiles = cdiv(rows, plan.tile);

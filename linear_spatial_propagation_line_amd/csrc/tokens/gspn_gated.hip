@@ -39,7 +39,9 @@ constexpr int kChunkB = 64;    // backward: also what the saved states are apart
 constexpr int kWindow = 4;    // chunks that one looks back
 constexpr int kRunF = 16;      // tokens of a wavefront's run, forward
 constexpr int kRunB = 8;       // backward, which keeps twice the values of a token
-constexpr int64_t kShort = 8;  // up to so many tokens a lane walks all of them
+constexpr int64_t kShort = 32;         // where a lane may walk all tokens: so many,
+constexpr int64_t kShortAlone = 12;    // so many with less than
+constexpr int64_t kShortLanes = 65536; // so many lanes
 constexpr uint32_t kAbsent = 0xffffffffu;
 
 template <typename T> struct GatedP {
@@ -122,7 +124,7 @@ __device__ __forceinline__ void publish_state(uint32_t* p, float h) {
 // [k * stride]. Folds forward from the latest published state within the
 // window; comes back when there is one. The place before is asked first, and
 // alone: where there are many chains it is mostly there, and asking costs more than
-// the answer (8 x 2048 x 2304, backward: 144 us; a window
+// the answer (8 x 2048 x 2304, backward, when measured: 144 us; a window
 // of 4 at once 150, of 8 160, of 16 186).
 __device__ __forceinline__ float look_back(const uint64_t* total, const uint32_t* behind, int64_t q, int64_t stride) {
   const uint32_t last = __hip_atomic_load(behind + (q - 1) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -315,6 +317,7 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
     h[v] = a.state ? a.state[b * a.C + c + v] : 0.0f;
     if (a.saved) a.saved[b * a.C + c + v] = h[v];
   }
+  if (!a.out && !a.state_out) return;
   T* o = a.out + b * a.L * a.C + c;
   for (int64_t t = 0; t < a.L; ++t) {
     float y[V] = {};
@@ -604,7 +607,10 @@ hipError_t clear_chain(GatedP<T>& p, int chunk, void* ws, hipStream_t stream, Tr
 
 template <typename T, int V>
 hipError_t gated_fwd(GatedP<T> p, void* ws, hipStream_t stream, Tracer* tr) {
-  if (p.L <= kShort) {
+  // us of 16 tokens by lanes and by chunks: 1152 lanes 7.4 and 6.4, 73728 9.5 and 15.6,
+  // 589824 30 and 93; of 32: 73728 19.1 and 17.6, 147456 22.5 and 28.8, 589824 68 and 101;
+  // of 64: 147456 41 and 35
+  if (p.L <= (p.B * (p.C / V) < kShortLanes ? kShortAlone : kShort)) {
     tr->before(stream, "gated_short", p.B);
     const hipError_t e = in_parts(cdiv(p.B * (p.C / V), 256), [&](int64_t first, unsigned count) {
       p.block0 = first;
@@ -687,7 +693,7 @@ size_t gated_saved_bytes(int64_t B, int64_t L, int64_t C) {
   return static_cast<size_t>(B * std::max<int64_t>(1, cdiv(L, kChunkB)) * C) * 4;
 }
 size_t gated_workspace_bytes(int64_t B, int64_t L, int64_t C) {
-  return L <= kShort ? 0 : chain_space(B, L, C, kChunkB).bytes;   // as the backward pass's chunks need it
+  return chain_space(B, L, C, kChunkB).bytes;   // as the backward pass's chunks need it
 }
 size_t gated_bwd_workspace_bytes(int64_t B, int64_t L, int64_t C) {
   return chain_space(B, L, C, kChunkB).bytes + 2 * up256(gated_saved_bytes(B, L, C));

@@ -38,8 +38,10 @@ CASES = [
     (1, 1, 1, F32, None, False),
     (2, 1, 66, BF16, None, True),
     (3, 4, 130, F32, (4, 0, 2), True),
-    (2, 8, 7, F32, None, True),                        # the last length of the short path
-    (2, 9, 64, BF16, (9, 3), True),                    # the first of the other
+    (2, 8, 7, F32, None, True),                        # a lane walks all tokens
+    (2, 9, 64, BF16, (9, 3), True),
+    (2, 12, 64, BF16, (12, 3), True),                  # the last length of that with few channels
+    (2, 13, 31, F32, (13, 12), True),                  # the first of the other
     (2, 17, 33, BF16, None, False),
     (4, 64, 96, F32, (64, 0, 1, 37), True),            # one whole chunk
     (3, 65, 128, BF16, (65, 64, 63), True),            # one token past it
@@ -113,6 +115,25 @@ def test_gated_gradients(c, keep):
     assert set(got) == set(ref)
     for k in ref:
         plain.within(got[k], ref[k], size[k], 36 * L + 80 + (B * L if k == "A" else 0), "d" + k)
+
+
+@pytest.mark.parametrize("B,L,C,dtype", [(70, 13, 1001, F32), (130, 32, 1010, BF16), (129, 33, 1010, BF16)])
+def test_many_channels_short(B, L, C, dtype):
+    """So many channels that a lane walks all of up to 32 tokens."""
+    lens = tuple((7 * b) % (L + 1) for b in range(B))
+    inp, gy = case(B, L, C, dtype, lens, True, seed=21)
+    args, par = split(dev(inp))
+    end = torch.full((B, C), NAN, device=DEV)
+    saved = g.gated_recurrence_saved(args[0])
+    out = g.gated_recurrence(*args, **par, state_out=end, saved=saved)
+    ref, ref_end = plain.gated(**inp)
+    size, size_end = plain.gated(**inp, absolute=True)
+    plain.within(out, ref, size, 18 * L + 26, "out")
+    plain.within(end, ref_end, size_end, 18 * L + 26, "state")
+    a = g.gated_recurrence_backward(*args, gy.to(DEV), **par, saved=saved)
+    b = g.gated_recurrence_backward(*args, gy.to(DEV), **par)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kTile = 256;       // the largest tile: tokens, vocabulary rows or columns
 constexpr int kFewTile = 64;     // tokens of a tile where there are few
-constexpr int kFewRows = 128;    // vocabulary rows of a tile then
 
 // whether G's entries at the targets are kept apart from the operand
 template <typename T> constexpr bool apart() { return sizeof(T) == 2; }
@@ -583,6 +582,11 @@ int64_t tile_for(int64_t m, int64_t n) {
   return cdiv(m, 128) * cdiv(n, 128) >= 192 ? 128 : 64;
 }
 
+// Vocabulary rows of a tile where there are few tokens: 128, 64 where that leaves
+// each compute unit one tile at most (5003 x 333 fp32 11 us, with 128 15.6; 16384 x 2304
+// bf16 17.0 and 17.6; 50001 x 2304 41.6 and 35.1).
+int64_t few_rows(int64_t V) { return V <= 64 * 256 ? 64 : 128; }
+
 template <typename T> void take_common(Space& s, LossP<T>& p) {
   p.list.count = s.take<int32_t>(1);
   p.list.token = s.take<int32_t>(p.Tp);
@@ -594,7 +598,7 @@ template <typename T> void take_common(Space& s, LossP<T>& p) {
 }
 template <typename T> void take_forward(Space& s, LossP<T>& p) {
   take_common(s, p);
-  p.part = s.take<float2>(cdiv(p.V, p.tokens <= kFewTile ? kFewRows : tile_for(p.V, p.tokens)) * p.Tp);
+  p.part = s.take<float2>(cdiv(p.V, p.tokens <= kFewTile ? few_rows(p.V) : tile_for(p.V, p.tokens)) * p.Tp);
 }
 
 // G of a piece is at most half a GiB, and pieces are alike. dx's contraction is
@@ -698,14 +702,14 @@ template <typename T> hipError_t loss_fwd(const gspn_loss_args& a, void* ws, hip
   hipError_t e = gather<T, false>(p, stream, tr);
   if (e != hipSuccess) return e;
   const bool few = p.tokens <= kFewTile;
-  const int64_t tile = tile_for(p.V, p.tokens);
-  const int64_t mt = cdiv(p.V, few ? kFewRows : tile), nt = few ? 1 : cdiv(p.tokens, tile);
+  const int64_t tile = few ? few_rows(p.V) : tile_for(p.V, p.tokens);
+  const int64_t mt = cdiv(p.V, tile), nt = few ? 1 : cdiv(p.tokens, tile);
   p.part_m = few ? 1 : p.Tp;
   p.part_p = few ? mt : 1;
   tr->before(stream, "loss_logits", p.V);
   e = in_parts(tile_blocks(mt, nt), [&](int64_t first, unsigned count) {
     p.block0 = first;
-    if (few) hipLaunchKernelGGL((loss_logits_kernel<T, kFewRows, kFewTile, 4, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
+    if (few && tile == 128) hipLaunchKernelGGL((loss_logits_kernel<T, 128, kFewTile, 4, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
     else if (tile == 256) hipLaunchKernelGGL((loss_logits_kernel<T, 256, 256, 2, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
     else if (tile == 128) hipLaunchKernelGGL((loss_logits_kernel<T, 128, 128, 2, 8>), dim3(count), dim3(512), 0, stream, p, mt, nt);
     else hipLaunchKernelGGL((loss_logits_kernel<T, 64, 64, 2, 4>), dim3(count), dim3(256), 0, stream, p, mt, nt);

@@ -280,6 +280,11 @@ def test_binding_refuses():
     (999, 3001, 517, F32, False),
     (4097, 700, 200, BF16, True),          # many tokens, few rows
     (65, 9000, 264, BF16, False),          # one token past the kernel for few
+    (2100, 6001, 72, BF16, False),         # logits in tiles of 256
+    (2100, 6000, 40, F32, True),
+    (64, 16_384, 72, BF16, False),         # few tokens, the last vocabulary in tiles of 64 rows
+    (33, 16_385, 40, F32, True),           # the first in tiles of 128
+    (64, 20_001, 136, BF16, True),
 ])
 def test_tiles_of_every_size(T, V, D, dtype, ragged):
     """Tiles that run off every edge, against 64 bits on the GPU, in the norm: the

@@ -194,3 +194,24 @@ def test_sorts_of_every_size(T, V):
     size.index_add_(0, ids[0][on], gy[0].cpu().double().abs()[on])
     count.index_add_(0, ids[0][on], torch.ones(int(on.sum()), 4, dtype=torch.float64))
     plain.within(a, dw, size * (count + 1), 1, "weight")
+
+
+def test_offsets_past_32_bits():
+    """A table, tokens and a gradient of more than 2^31 values each. One row of whole
+    numbers as every token's gradient: a table row's is that row times its tokens, at
+    most 4 x 64, which bf16 holds."""
+    V = T = 950_000
+    D = 2304
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    w = torch.empty(V, D, dtype=BF16, device=DEV).normal_(generator=gen)
+    ids = torch.randint(0, V, (1, T), generator=gen, device=DEV)
+    ids[0, -3:] = torch.tensor([V - 1, 0, V - 1], device=DEV)
+    out = g.token_embedding(ids, w)
+    for t in (slice(0, 2000), slice(T // 2, T // 2 + 2000), slice(T - 2000, T)):
+        assert torch.equal(out[0, t], w[ids[0, t]])
+    row = torch.randint(-4, 5, (1, 1, D), generator=gen, device=DEV).to(BF16)
+    count = torch.bincount(ids[0], minlength=V)
+    assert int(count.max()) <= 64
+    got = g.token_embedding_backward(ids, row.expand(1, T, D), V)["weight"]
+    for v in range(0, V, 50_000):
+        assert torch.equal(got[v:v + 50_000].float(), count[v:v + 50_000, None] * row[0].float())

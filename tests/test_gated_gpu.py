@@ -276,3 +276,44 @@ def test_binding_refuses():
         with pytest.raises(g.GspnError) as e:
             g.gated_recurrence(x, x, x, A, **kw)
         assert e.value.name == name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_broadcast_gates(dtype):
+    """Gates, inputs and grad_out that are one row for all tokens or entries
+    (stride 0): the results and gradients of the written-out ones, bit for bit."""
+    gen = torch.Generator().manual_seed(31)
+    B, L, C = 3, 150, 70
+    x = torch.randn(1, L, C, generator=gen).to(dtype).to(DEV).expand(B, L, C)
+    r = torch.randn(B, 1, C, generator=gen).to(dtype).to(DEV).expand(B, L, C)
+    i = torch.randn(1, 1, C, generator=gen).to(dtype).to(DEV).expand(B, L, C)
+    gy = torch.randn(1, 1, C, generator=gen).to(dtype).to(DEV).expand(B, L, C)
+    A = (-torch.rand(C, generator=gen)).to(DEV)
+    own = [t.contiguous() for t in (x, r, i)]
+    assert torch.equal(g.gated_recurrence(x, r, i, A), g.gated_recurrence(*own, A))
+    a = g.gated_recurrence_backward(x, r, i, A, gy)
+    b = g.gated_recurrence_backward(*own, A, gy.contiguous())
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
+def test_offsets_past_32_bits():
+    """One prompt of more than 2^31 values. The decay is below 2^-9 a token, so the
+    last 100 tokens hang on the 100 before them alone (2^-900): those 200 tokens'
+    roundings bound them."""
+    L, C, n = 950_000, 2304, 200
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.empty(1, L, C, dtype=BF16, device=DEV).normal_(generator=gen)
+    r = (2 + torch.rand(1, 1, C, generator=gen, device=DEV)).to(BF16).expand(1, L, C)
+    i = torch.randn(1, 1, C, generator=gen, device=DEV).to(BF16).expand(1, L, C)
+    gy = torch.randn(1, 1, C, generator=gen, device=DEV).to(BF16).expand(1, L, C)
+    A = torch.full((C,), -8.0, device=DEV)
+    out = g.gated_recurrence(x, r, i, A)
+    tail = dict(x=x[:, -n:].cpu(), r=r[:, -n:].cpu(), i=i[:, -n:].cpu(), A=A.cpu())
+    ref, size = plain.gated(**tail)[0], plain.gated(**tail, absolute=True)[0]
+    plain.within(out[:, -100:], ref[:, -100:], size[:, -100:], 18 * n + 26, "out")
+    got = g.gated_recurrence_backward(x, r, i, A, gy)
+    gyt = gy[:, -n:].cpu()
+    ref, size = plain.gated_grads(**tail, gy=gyt), plain.gated_grads(**tail, gy=gyt, absolute=True)
+    for k in "xri":
+        plain.within(got[k][:, -100:], ref[k][:, -100:], size[k][:, -100:], 36 * n + 80, "d" + k)

@@ -320,3 +320,32 @@ def test_tiles_of_every_size(T, V, D, dtype, ragged):
         assert float((a.double() - b).norm() / b.norm()) <= bound, name
         assert torch.isfinite(a).all()
     assert not got["x"][~on].any()
+
+
+def test_offsets_past_32_bits():
+    """A vocabulary of more than 2^31 weights, targets in its last rows. In the
+    norm, with the bounds of the tests above."""
+    V, D, T = 950_000, 2304, 40
+    gen = torch.Generator(device=DEV).manual_seed(10)
+    w = torch.empty(V, D, dtype=BF16, device=DEV).normal_(0.0, 2 * D ** -0.5, generator=gen)
+    x = torch.randn(1, T, D, generator=gen, device=DEV).to(BF16)
+    t = V - 1 - torch.arange(T, device=DEV)[None]
+    gl = torch.rand(1, T, generator=gen, device=DEV) + 0.5
+    lse = torch.empty(1, T, device=DEV)
+    loss = g.vocab_loss(x, w, t, lse=lse)
+    got = g.vocab_loss_backward(x, w, t, lse, gl)
+    x64, step = x[0].double(), 50_000
+    z = torch.cat([x64 @ w[v:v + step].double().T for v in range(0, V, step)], 1)
+    ref_lse = torch.logsumexp(z, 1)
+    ref = ref_lse - z.gather(1, t.T)[:, 0]
+    for name, a, b in (("lse", lse[0], ref_lse), ("loss", loss[0], ref)):
+        assert float((a.double() - b).norm() / b.norm()) <= 2 * (D ** 0.5 + 30) * S, name
+    G = torch.exp(z - ref_lse[:, None]).scatter_add_(1, t.T, torch.full((T, 1), -1.0, dtype=torch.float64, device=DEV))
+    G *= gl[0].double()[:, None]
+    dx = sum(G[:, v:v + step] @ w[v:v + step].double() for v in range(0, V, step))
+    dw = G[:, V - T:].T @ x64
+    for name, a, b in (("x", got["x"][0], dx), ("weight", got["weight"][V - T:], dw)):
+        own = float((b.to(BF16).double() - b).norm())
+        assert float((a.double() - b).norm()) <= 1.2 * own, name
+    for v in range(0, V, step):
+        assert torch.isfinite(got["weight"][v:v + step]).all()

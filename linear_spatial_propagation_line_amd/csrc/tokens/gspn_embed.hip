@@ -9,6 +9,8 @@
 // thousands, so the work is dealt out by sorted tokens: a wavefront owns kChunk
 // of them, finishes the runs that lie within, and leaves a part of those that do
 // not, which are joined in order. Rows without a token are filled with zeros.
+// 32768 tokens (half of them padding), 65536 rows of 2304 bf16 values: lookup 51 us,
+// 4.4 TB/s; sort 12, sums and zeros 73 (5.2 TB/s), join 10. A large copy: 5.1 TB/s.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 

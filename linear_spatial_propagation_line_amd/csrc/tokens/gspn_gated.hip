@@ -27,6 +27,9 @@
 // word that cannot be torn (4 or 8 bytes, written and read by relaxed
 // device-scope atomics) and says itself whether it is there: the workspace is
 // filled with a pattern that no published value has.
+//
+// 8 x 2048 x 2304 bf16: forward 73 us (4.1 TB/s), backward 137 (3.9 TB/s); one entry of
+// 32768 tokens forward 139 (4.3 TB/s). A large copy: 5.1 TB/s.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
 
@@ -34,9 +37,9 @@ namespace gspn {
 
 namespace {
 
-constexpr int kChunkF = 128;   // tokens of a chunk, forward
+constexpr int kChunkF = 128;   // tokens of a chunk, forward (32768 x 2304 143 us, with 64 157)
 constexpr int kChunkB = 64;    // backward: also what the saved states are apart
-constexpr int kWindow = 4;    // chunks that one looks back
+constexpr int kWindow = 4;     // chunks that one looks back
 constexpr int kRunF = 16;      // tokens of a wavefront's run, forward
 constexpr int kRunB = 8;       // backward, which keeps twice the values of a token
 constexpr int64_t kShort = 32;         // where a lane may walk all tokens: so many,

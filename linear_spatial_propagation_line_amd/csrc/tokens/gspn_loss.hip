@@ -5,7 +5,10 @@
 //   G = g (softmax(z) - onehot(target)),  dx = G W,  dW = G^T x
 //
 // Bound by matrix products: 2 T V D operations forward, 6 T V D backward (the
-// logits are found again). Forward: each tile of logits, 256 vocabulary rows by
+// logits are found again): 8192 x 50001 x 2304 bf16 1510 to 1740 us forward as the
+// card's power allows (1080 to 1250 TFLOP/s), 4800 to 5400 backward; a library product
+// of the logits alone 1603. Few tokens are bound by reading the weight: 32 x 65536 x
+// 2304 bf16 54 us (5.6 TB/s). Forward: each tile of logits, 256 vocabulary rows by
 // 256 tokens, leaves its maximum and sum of every token, which a last kernel
 // joins. Backward, in pieces of the vocabulary: G of the piece goes to the
 // workspace, then one launch takes dW of the piece (complete) and the piece's
@@ -45,7 +48,7 @@ struct TokenList {
   int32_t* target;   // [Tp]
   float* g;          // [Tp] backward: the loss's gradient
   float* lse;        // [Tp]
-  float* at;         // [Tp] forward: the target's logit; backward: G there
+  float* at;         // [Tp] forward: the target's logit; backward, if apart: G there
   int32_t* pos;      // [T] backward: the token's place, -1 without
 };
 
@@ -601,7 +604,8 @@ template <typename T> void take_forward(Space& s, LossP<T>& p) {
   p.part = s.take<float2>(cdiv(p.V, p.tokens <= kFewTile ? few_rows(p.V) : tile_for(p.V, p.tokens)) * p.Tp);
 }
 
-// G of a piece is at most half a GiB, and pieces are alike. dx's contraction is
+// G of a piece is at most half a GiB (pieces of a quarter or a whole GiB take the
+// same time to 5 %: 8192 x 65536 x 1024 bf16 3270, 3110, 2980 us), and pieces are alike. dx's contraction is
 // cut where its tiles alone are fewer than the compute units.
 GradPlan grad_plan(int64_t T, int64_t V, int64_t D, size_t es) {
   GradPlan g;

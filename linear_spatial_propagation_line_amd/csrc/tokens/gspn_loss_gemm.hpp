@@ -11,6 +11,10 @@
 // it lies as it is in memory, [k][BM or BN values], and is read by the
 // transposing LDS read (bf16, runs of 64 bytes swizzled by the row) or value by value (fp32).
 //
+// Matrix units are busy 70 to 78 % of the cycles of tiles of 256 in bf16, and the
+// card's power then holds the clock near 1.6 GHz, which is what bounds it: loads in a
+// row instead of woven in 1825 us against 1589 (8192 x 50001 x 2304).
+//
 // Results are 32 x 32 tiles (v_mfma_f32_32x32x16_bf16, or v_mfma_f32_32x32x2_f32):
 // lane l holds column l % 32 and the rows (i % 4) + 8 (i / 4) + 4 (l / 32), i < 16.
 #pragma once

@@ -377,8 +377,10 @@ size_t gspn_vocab_loss_workspace_bytes(int64_t B, int64_t L, int64_t V, int64_t 
  * (in dtype) given grad_loss = dL/dloss [B, L] (fp32) and the forward call's
  * lse. args as for the forward call (loss and lse of args are not touched).
  * The logits are found again, in pieces of the vocabulary; with bf16 storage
- * their gradients are operands in bf16, those at the targets in fp32. Sums are
- * in fp32, in a fixed order. Workspace:
+ * their gradients are operands in bf16, those at the targets in fp32: results
+ * are further from the exact ones than those rounded are, by a factor of 1.006
+ * for diffuse softmaxes and of up to 1.24 for peaked ones, in the norm. Sums
+ * are in fp32, in a fixed order. Workspace:
  * gspn_vocab_loss_backward_workspace_bytes() bytes, 256-byte aligned.
  */
 typedef struct {

@@ -22,8 +22,13 @@
 // the result's own (0.0023 from 64 bits in the norm for 0.00166). So they are 0
 // in the operand; they are found apart, one fp32 value per token, and their
 // products with W's rows and x's are added to dx and dW in fp32. The other
-// entries' rounding is small beside that and independent. With fp32 storage the
-// operand holds them.
+// entries' rounding stays. They sum to 1 - p(target), so their squares are at most
+// the square of the target's entry and add at most half of the result's own rounding's
+// square: the distance from 64 bits is the result's own rounding times 1.006 where
+// logits have a standard deviation of 2, 1.06 to 1.09 at 4, 1.17 at 8, 1.21 at 16, and
+// 1.24 where a softmax is one entry off the target (32 and more; 512 tokens, 4096 rows).
+// Two bf16 parts would take all of it away for 10 T V D operations instead of 6. With
+// fp32 storage the operand holds the targets as well.
 #include "gspn_loss_gemm.hpp"
 
 namespace gspn {

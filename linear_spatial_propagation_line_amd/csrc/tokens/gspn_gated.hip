@@ -7,8 +7,10 @@
 //   dr = k A s (1 - s),  dA = sum k s,
 //   dx = g beta sigmoid(i),  di = g beta x sigmoid(i) (1 - sigmoid(i)).
 //
-// e = a - 1 is computed before a: 1 - a^2 = -e (2 + e) keeps the digits that an
-// a close to 1 has lost.
+// a and e = a - 1 each have their own digits: 1 - a^2 = -e (2 + e) where a is close to
+// 1, and products of small a, which e has lost (1 + e is off by 2^-25 whatever a is: by
+// 17 % at exp(-16)). What hangs on a times a state, the gradients of r, A and the
+// state among it, keeps them at every A <= 0.
 //
 // Bound by memory, with five or six transcendentals a value close behind
 // (four values moved forward, eight backward): so each value is read once and
@@ -74,6 +76,30 @@ __device__ __forceinline__ void gate_both(float v, float& open, float& shut) {
   const float t = __builtin_amdgcn_exp2f(fminf(v * -kLog2e, 126.0f));
   open = __builtin_amdgcn_rcpf(1.0f + t);
   shut = t * open;
+}
+// a = exp(v) and e = a - 1, v <= 0
+struct Decay {
+  float a, e;
+};
+__device__ __forceinline__ Decay decay_f32(float v) {
+  const float x = __builtin_amdgcn_exp2f(v * kLog2e), p = expm1_series(v);
+  const bool near = fabsf(v) < kExpm1Series;
+  return Decay{near ? 1.0f + p : x, near ? p : x - 1.0f};
+}
+// Both in one word: a, or -|e| where a is above exp(-1/4); a sign says which
+__device__ __forceinline__ float decay_word(const Decay& d) { return d.a > 0.75f ? copysignf(d.e, -1.0f) : d.a; }
+__device__ __forceinline__ Decay word_decay(float w) {
+  const float one = __int_as_float((__float_as_int(w) >> 31) & 0x3f800000);
+  return Decay{w + one, w + (one - 1.0f)};
+}
+// What was derived from the words so far is not kept in registers but derived again
+// (kept, the backward pass in bf16 takes 128 and spills 19; this way 120, and 8 x 2048 x
+// 2304 135 us; with 1 + e, six spilled, 143)
+template <int N, int V> __device__ __forceinline__ void forget(float (&w)[N][V]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) asm("" : "+v"(w[k][v]));
 }
 // 1 - a^2 from e = a - 1 <= 0
 __device__ __forceinline__ float left_f32(float e) { return -e * (2.0f + e); }
@@ -218,9 +244,9 @@ __global__ __launch_bounds__(64 * kChunkF / kRunF, 4) void gated_kernel(GatedP<T
       i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float e = expm1_f32(A[v] * gate_f32(rv[v]));
-        decay[k][v] = 1.0f + e;
-        bu[k][v] = __builtin_amdgcn_sqrtf(left_f32(e)) * gate_f32(iv[v]) * xv[v];
+        const Decay d = decay_f32(A[v] * gate_f32(rv[v]));
+        decay[k][v] = d.a;
+        bu[k][v] = __builtin_amdgcn_sqrtf(left_f32(d.e)) * gate_f32(iv[v]) * xv[v];
       }
     }
     if (live < kRunF) {   // padding leaves the state
@@ -335,8 +361,8 @@ __global__ __launch_bounds__(256) void gated_short_kernel(GatedP<T> a) {
       i.wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float e = expm1_f32(A[v] * gate_f32(rv[v]));
-        h[v] = __builtin_fmaf(1.0f + e, h[v], __builtin_amdgcn_sqrtf(left_f32(e)) * gate_f32(iv[v]) * xv[v]);
+        const Decay d = decay_f32(A[v] * gate_f32(rv[v]));
+        h[v] = __builtin_fmaf(d.a, h[v], __builtin_amdgcn_sqrtf(left_f32(d.e)) * gate_f32(iv[v]) * xv[v]);
         y[v] = h[v];
       }
     }
@@ -380,9 +406,9 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
     }
     return;
   }
-  // kept of every token: e = a - 1, beta sigmoid(i), and the inputs as stored, whose gates are opened
+  // kept of every token: the decay's word, beta sigmoid(i), and the inputs as stored, whose gates are opened
   // again at the end (kept open they would take registers that a second workgroup lives from)
-  float e[kRunB][V], bw[kRunB][V], P[V], H[V], G[V], A[V];
+  float aw[kRunB][V], bw[kRunB][V], P[V], H[V], G[V], A[V];
   Raw<T, V> x[kRunB], gy[kRunB], r[kRunB], i[kRunB];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -402,8 +428,9 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
       i[k].wide(iv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        e[k][v] = expm1_f32(A[v] * gate_f32(rv[v]));
-        bw[k][v] = __builtin_amdgcn_sqrtf(left_f32(e[k][v])) * gate_f32(iv[v]);
+        const Decay d = decay_f32(A[v] * gate_f32(rv[v]));
+        aw[k][v] = decay_word(d);
+        bw[k][v] = __builtin_amdgcn_sqrtf(left_f32(d.e)) * gate_f32(iv[v]);
       }
     }
     if (live < kRunB) {
@@ -412,7 +439,10 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
       for (int k = 0; k < kRunB; ++k)
         if (k >= live) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) e[k][v] = bw[k][v] = 0.0f;
+          for (int v = 0; v < V; ++v) {
+            aw[k][v] = -0.0f;
+            bw[k][v] = 0.0f;
+          }
           gy[k] = Raw<T, V>{};
         }
     }
@@ -422,7 +452,7 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
       x[k].wide(xv);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float av = 1.0f + e[k][v];
+        const float av = word_decay(aw[k][v]).a;
         H[v] = __builtin_fmaf(av, H[v], bw[k][v] * xv[v]);
         P[v] *= av;
       }
@@ -432,7 +462,7 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
       float gv[V];
       gy[k].wide(gv);
 #pragma unroll
-      for (int v = 0; v < V; ++v) G[v] = (1.0f + e[k][v]) * (G[v] + gv[v]);
+      for (int v = 0; v < V; ++v) G[v] = word_decay(aw[k][v]).a * (G[v] + gv[v]);
     }
   }
 #pragma unroll
@@ -486,9 +516,10 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         hp[k][v] = h[v];
-        h[v] = __builtin_fmaf(1.0f + e[k][v], h[v], bw[k][v] * xv[v]);
+        h[v] = __builtin_fmaf(word_decay(aw[k][v]).a, h[v], bw[k][v] * xv[v]);
       }
     }
+    forget(aw);
     int64_t o = to + (kRunB - 1) * a.C;
 #pragma unroll
     for (int k = kRunB - 1; k >= 0; --k) {
@@ -500,7 +531,8 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         // (a^2 / beta) u = a^2 (beta u) / (1 - a^2); 0 where a is 1 to within the smallest normal number
-        const float av = 1.0f + e[k][v], left = left_f32(e[k][v]);
+        const Decay d = word_decay(aw[k][v]);
+        const float av = d.a, left = left_f32(d.e);
         const float inv = left > 1.17549435e-38f ? __builtin_amdgcn_rcpf(left) : 0.0f;
         float s, sshut, w, wshut;
         gate_both(rv[v], s, sshut);

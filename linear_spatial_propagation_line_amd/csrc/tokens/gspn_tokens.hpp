@@ -256,17 +256,21 @@ __device__ __forceinline__ float softplus_f32(float v, float* slope = nullptr) {
   return __builtin_fmaf(2.0f * s, p, fmaxf(v, 0.0f));
 }
 
-// exp(v) - 1: the series where it keeps more digits than the difference
-// (relative error 2e-9 at 1/4)
-__device__ __forceinline__ float expm1_f32(float v) {
+// exp(v) - 1. Below 1/4 its series, cut off at 2e-9 of it and rounded by some two steps
+// of 2^-24; from there on the difference, whose exponential's rounding counts up to
+// four times (5 steps just above 1/4, fewer further on).
+constexpr float kExpm1Series = 0.25f;
+__device__ __forceinline__ float expm1_series(float v) {
   float p = __builtin_fmaf(v, 1.0f / 5040.0f, 1.0f / 720.0f);
   p = __builtin_fmaf(v, p, 1.0f / 120.0f);
   p = __builtin_fmaf(v, p, 1.0f / 24.0f);
   p = __builtin_fmaf(v, p, 1.0f / 6.0f);
   p = __builtin_fmaf(v, p, 0.5f);
-  p = __builtin_fmaf(v, p, 1.0f) * v;
+  return __builtin_fmaf(v, p, 1.0f) * v;
+}
+__device__ __forceinline__ float expm1_f32(float v) {
   const float d = __builtin_amdgcn_exp2f(v * kLog2e) - 1.0f;
-  return fabsf(v) < 0.25f ? p : d;
+  return fabsf(v) < kExpm1Series ? expm1_series(v) : d;
 }
 // length of entry b: lens[b] clamped to 0 .. L, or L
 __device__ __forceinline__ int64_t seq_len(const int32_t* lens, int64_t b, int64_t L) {

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import linear_spatial_propagation_line_amd as g
+import plain_prompt as plain
 from test_vocab_loss_gpu import case as loss_case, check
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +50,101 @@ def test_peaked_softmax_value_by_value():
     c = (2, 20, 300, 64, BF16, torch.int64, (20, 13))
     x, w, t, gl, lens = loss_case(*c, seed=32)
     check(c, x, w * 16, t, gl, lens)
+
+
+# --------------------------------------------------------------------------
+# gated recurrence: decays from next to 1 to next to 0
+# --------------------------------------------------------------------------
+def steps_of_decay(rmax, vmax):
+    """By how many steps of 2^-24 the decay exp(A s) is off, relative to itself,
+    for |r| <= rmax and |A s| <= vmax. exp(-r): r log2(e) is rounded (the product and
+    the constant: 2 |r|, in the exponent) and the exponential is off by 2; the sum
+    by 1, the reciprocal by 2: s by 2 rmax + 5. v = A s by 1 more, so exp(v) by
+    vmax (2 rmax + 6), the product with log2(e) 2 vmax, the exponential 2."""
+    return vmax * (2 * rmax + 8) + 2
+
+
+FLUSH = 1000 * torch.finfo(F32).tiny
+STRONG = [
+    # B, L, C, lens
+    (1, 1, 64, None),
+    (2, 4, 130, (4, 3)),
+    (2, 13, 66, None),         # chunks
+    (1, 13, 7, None),          # single channels a lane
+    (3, 70, 128, (70, 64, 65)),
+    (1, 300, 70, None),
+]
+
+
+def strong_case(B, L, C, lens, dtype=F32):
+    """|A s| between 0.1 and 17, over the channels; every third channel's input gate
+    is shut, so that its state is nothing but a product of decays."""
+    gen = torch.Generator().manual_seed(700 + L)
+    r = torch.rand(B, L, C, generator=gen) * 2 - 1                   # s between 0.27 and 0.73
+    A = -torch.exp(torch.linspace(-1.0, 3.14, C)) if C > 1 else torch.full((1,), -16.0)
+    i = torch.randn(B, L, C, generator=gen)
+    i[..., ::3] = -100.0
+    d = dict(x=torch.randn(B, L, C, generator=gen).to(dtype), r=r.to(dtype), i=i.to(dtype), A=A,
+             state=torch.randn(B, C, generator=gen),
+             lens=None if lens is None else torch.tensor(lens, dtype=torch.int32))
+    return d, torch.randn(B, L, C, generator=gen).to(dtype), torch.randn(B, C, generator=gen)
+
+
+def on(d):
+    return {k: (v.to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in d.items()}
+
+
+def split(d):
+    return (d["x"], d["r"], d["i"], d["A"]), dict(state=d["state"], lens=d["lens"])
+
+
+@pytest.mark.parametrize("c", STRONG)
+@pytest.mark.parametrize("keep", [False, True])
+def test_strong_decays(c, keep):
+    """A decay of exp(-17) is off by no more than its exponent's roundings, so
+    states, gradients of A, r and the state keep the digits that products of such decays
+    have. A token adds a decay's steps and 3 (a product, a sum, the input's own
+    roundings are counted below) to what the state before is off; chunks fold once more.
+    beta sigmoid(i) x by 12 and half of the decay's steps (1 - a^2 = -e (2 + e), and e is
+    off by at most as much as a). The gradients take g and a state (as many each), the
+    decay twice, its slope and up to 8 products: three times as many and 80.
+    What is below the normal range is taken as 0, and enters results times factors (g,
+    A, sums over tokens) below 1000: FLUSH."""
+    B, L, C, lens = c
+    inp, gy, gs = strong_case(*c)
+    d = on(inp)
+    args, par = split(d)
+    n = steps_of_decay(1.0, 17.0)
+    count = 2 * L * (n + 3) + n + 12
+    end = torch.empty(B, C, device=DEV)
+    saved = g.gated_recurrence_saved(args[0]) if keep else None
+    out = g.gated_recurrence(*args, **par, state_out=end, saved=saved)
+    (ref, ref_end), (size, size_end) = plain.gated(**inp), plain.gated(**inp, absolute=True)
+    small = FLUSH / (count * plain.F32_STEP)
+    plain.within(out, ref, size + small, count, "out")
+    plain.within(end, ref_end, size_end + small, count, "state")
+    got = g.gated_recurrence_backward(*args, gy.to(DEV), **par, saved=saved, grad_state=gs.to(DEV))
+    ref = plain.gated_grads(**inp, gy=gy, grad_state=gs)
+    size = plain.gated_grads(**inp, gy=gy, grad_state=gs, absolute=True)
+    for k in ref:
+        plain.within(got[k], ref[k], size[k] + small, 3 * count + 80 + (B * L if k == "A" else 0), "d" + k)
+
+
+@pytest.mark.parametrize("A", [-0.5, -8.0, -16.0, -32.0])
+@pytest.mark.parametrize("C", [64, 63])
+def test_strong_decays_in_the_norm(A, C):
+    """Errors of r's and A's gradients in the norm. Where |A s| is v, the decay is off
+    by some v sqrt(6) + 2 steps as its exponent's roundings fall, and a value's
+    weight falls with the decay, exp(-v): v exp(-v) has its largest value at 1, so the
+    decay's part is below 6 steps whatever A is; 12 products and sums of state
+    and slope fall as 4 more, and the sums of A's gradient over 256 tokens 16: 2^-24 times
+    16 and 32."""
+    gen = torch.Generator().manual_seed(40)
+    B, L = 1, 256
+    x, r, i, gy = torch.randn(4, B, L, C, generator=gen)
+    inp = dict(x=x, r=r, i=i, A=torch.full((C,), A))
+    got = g.gated_recurrence_backward(*(v.to(DEV) for v in inp.values()), gy.to(DEV))
+    ref = plain.gated_grads(**inp, gy=gy)
+    for k, steps in (("r", 16), ("A", 32), ("x", 16), ("i", 16)):
+        err = float((got[k].double().cpu() - ref[k]).norm() / ref[k].norm())
+        assert err <= steps * plain.F32_STEP, (k, err)

@@ -543,8 +543,9 @@ __global__ __launch_bounds__(64 * kChunkB / kRunB, sizeof(T) == 2 || V == 1 ? 4 
         dx[v] = gt * bw[k][v];
         di[v] = dx[v] * xv[v] * wshut;
         dr[v] = ks * A[v] * sshut;
-        if (k < live) dA[v] += ks;   // padding leaves g and has dx = di = 0 already
-        else dr[v] = 0.0f;
+        // padding leaves g; its products are no zeros beside an x or a g that is not finite
+        if (k < live) dA[v] += ks;
+        else dx[v] = dr[v] = di[v] = 0.0f;
         g[v] = ga;
       }
       if (k < rows && mine) {

@@ -148,3 +148,37 @@ def test_strong_decays_in_the_norm(A, C):
     for k, steps in (("r", 16), ("A", 32), ("x", 16), ("i", 16)):
         err = float((got[k].double().cpu() - ref[k]).norm() / ref[k].norm())
         assert err <= steps * plain.F32_STEP, (k, err)
+
+
+# --------------------------------------------------------------------------
+# gated recurrence: infinities beside padding
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("B,L,C,dtype,lens", [
+    (2, 70, 66, BF16, (59, 3)),       # the last token within a run of eight and of sixteen
+    (2, 70, 7, F32, (1, 64)),
+    (2, 20, 130, F32, (13, 9)),
+    (3, 200, 64, BF16, (129, 0, 130)),
+])
+def test_padding_beside_a_last_token_that_is_not_finite(B, L, C, dtype, lens, bad):
+    """The last token's x, its gates and the state's gradient not finite: padding has
+    zeros all the same, in results and gradients."""
+    gen = torch.Generator().manual_seed(41)
+    x, r, i, gy = (torch.randn(B, L, C, generator=gen).to(dtype) for _ in range(4))
+    A, gs = -torch.rand(C, generator=gen) - 0.1, torch.randn(B, C, generator=gen)
+    pad = torch.arange(L)[None] >= torch.tensor(lens)[:, None]
+    for name in ("x", "r", "i", "gy", "gs", "state"):
+        v = {"x": x.clone(), "r": r.clone(), "i": i.clone(), "gy": gy.clone(), "gs": gs.clone(),
+             "state": torch.randn(B, C, generator=gen)}
+        for b, n in enumerate(lens):
+            if name in ("gs", "state"):
+                v[name][b] = bad
+            elif n:
+                v[name][b, n - 1] = bad
+        d = {k: t.to(DEV) for k, t in v.items()}
+        args = (d["x"], d["r"], d["i"], A.to(DEV))
+        par = dict(state=d["state"], lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+        assert not g.gated_recurrence(*args, **par).cpu()[pad].any(), name
+        got = g.gated_recurrence_backward(*args, d["gy"], **par, grad_state=d["gs"])
+        for k in "xri":
+            assert not got[k].cpu()[pad].any(), (name, k)      # NaN counts as any

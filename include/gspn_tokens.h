@@ -347,7 +347,8 @@ size_t gspn_gated_recurrence_backward_workspace_bytes(int64_t B, int64_t L, int6
  * gradient; padding has loss 0 and lse 0 as well.
  *   x [B, L, D], weight [V, D]   in dtype; V, D >= 1. Where D values are whole
  *                       pieces of 16 bytes, weight has to begin on one
- *                       (GSPN_E_ALIGN)
+ *                       (GSPN_E_ALIGN). Where there are no tokens the weight is
+ *                       not read, and may be NULL
  *   targets [B, L], int64 with targets64, else int32; target l of entry b is
  *                       targets[b * targets_batch + l]
  *   loss, lse [B, L] fp32; lse may be NULL

@@ -557,7 +557,8 @@ __global__ __launch_bounds__(256) void loss_dx_kernel(LossP<T> a, const float* p
 }
 
 // ---- host -------------------------------------------------------------------
-bool packs_weight(int64_t D, size_t es) { return D * es % 16 != 0; }
+// rows of no whole pieces, where there are tokens: without one the weight is not read
+bool packs_weight(int64_t tokens, int64_t D, size_t es) { return tokens > 0 && D * es % 16 != 0; }
 int64_t padded(int64_t D, size_t es) { return cdiv(D, 128 / static_cast<int64_t>(es)) * (128 / static_cast<int64_t>(es)); }
 // at least one tile: without a token the weight's gradient is still written
 int64_t padded_tokens(int64_t T) { return std::max<int64_t>(1, cdiv(T, kTile)) * kTile; }
@@ -601,8 +602,9 @@ template <typename T> void take_common(Space& s, LossP<T>& p) {
   p.list.target = s.take<int32_t>(p.Tp);
   p.list.at = s.take<float>(p.Tp);
   p.packed = s.take<T>(p.Tp * p.Dp);
-  p.w = packs_weight(p.D, sizeof(T)) ? s.take<T>(p.V * p.Dp) : p.weight;
-  p.wld = packs_weight(p.D, sizeof(T)) ? p.Dp : p.D;
+  const bool packs = packs_weight(p.tokens, p.D, sizeof(T));
+  p.w = packs ? s.take<T>(p.V * p.Dp) : p.weight;
+  p.wld = packs ? p.Dp : p.D;
 }
 template <typename T> void take_forward(Space& s, LossP<T>& p) {
   take_common(s, p);
@@ -689,7 +691,7 @@ template <typename T, bool BACK> hipError_t gather(LossP<T>& p, hipStream_t stre
   tr->after(stream);
   if (e != hipSuccess) return e;
   const int64_t pieces = p.Dp * static_cast<int64_t>(sizeof(T)) / 16;
-  PackP<T> x{p.x, p.xb, p.xr, p.list.token, p.packed, few ? 0 : p.Tp, 0, wide_x};
+  PackP<T> x{p.x, p.xb, p.xr, p.list.token, p.packed, few || p.tokens == 0 ? 0 : p.Tp, 0, wide_x};
   PackP<T> w{p.weight, 0, p.D, nullptr, const_cast<T*>(p.w), p.w != p.weight ? p.V : 0, 0, 0};
   x.blocks = cdiv(x.rows * pieces, 256);
   w.blocks = cdiv(w.rows * pieces, 256);

@@ -8,6 +8,8 @@ import torch
 
 import linear_spatial_propagation_line_amd as g
 import plain_prompt as plain
+from linear_spatial_propagation_line_amd import tokens
+from test_tokens_edges_gpu import launches
 from test_vocab_loss_gpu import case as loss_case, check
 
 pytestmark = pytest.mark.gpu
@@ -182,3 +184,30 @@ def test_padding_beside_a_last_token_that_is_not_finite(B, L, C, dtype, lens, ba
         got = g.gated_recurrence_backward(*args, d["gy"], **par, grad_state=d["gs"])
         for k in "xri":
             assert not got[k].cpu()[pad].any(), (name, k)      # NaN counts as any
+
+
+# --------------------------------------------------------------------------
+# vocabulary loss: no tokens
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("D,dtype", [(15, F32), (7, BF16), (16, F32), (16, BF16)])
+@pytest.mark.parametrize("B,L", [(0, 4), (3, 0)])
+def test_empty_batch_does_not_read_the_weight(B, L, D, dtype):
+    """Rows of whole pieces and of none, with a weight and without one: the weight's
+    gradient is zeros, and nothing is packed."""
+    V = 700
+    x, w = torch.empty(B, L, D, dtype=dtype, device=DEV), torch.ones(V, D, dtype=dtype, device=DEV)
+    t, no = torch.empty(B, L, dtype=torch.int64, device=DEV), torch.empty(B, L, device=DEV)
+    got, names = launches(lambda: g.vocab_loss_backward(x, w, t, no, no))
+    assert got["x"].shape == (B, L, D) and not got["weight"].any()
+    assert "loss_pack" not in names, names
+    L_ = tokens._lib()
+    code = tokens._CODE[dtype]
+    need = L_.gspn_vocab_loss_backward_workspace_bytes(B, L, V, D, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    dw = torch.full((V, D), float("nan"), dtype=dtype, device=DEV)
+    a = tokens._LOSS.pack(B, L, V, D, code, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L_.gspn_vocab_loss_backward_ws(a, tokens._LOSS_GRADS.pack(0, 0, 0, dw.data_ptr()), ws.data_ptr(), need,
+                                          stream) == 0
+    torch.cuda.synchronize()
+    assert not dw.any()

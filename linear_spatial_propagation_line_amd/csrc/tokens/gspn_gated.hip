@@ -44,9 +44,17 @@ constexpr int kChunkB = 64;    // backward: also what the saved states are apart
 constexpr int kWindow = 4;     // chunks that one looks back
 constexpr int kRunF = 16;      // tokens of a wavefront's run, forward
 constexpr int kRunB = 8;       // backward, which keeps twice the values of a token
-constexpr int64_t kShort = 32;         // where a lane may walk all tokens: so many,
-constexpr int64_t kShortAlone = 12;    // so many with less than
-constexpr int64_t kShortLanes = 65536; // so many lanes
+
+// Up to how many tokens a lane walks all of them, by the number of lanes (of V channels):
+// chunks cost by the rounds in which their workgroups run, a walk by its length. us by
+// lanes and by chunks, bf16, pairs: 1152 lanes 12 tokens 6.0 and 6.3, 16 7.2 and 6.4;
+// 73728 lanes 28 tokens 16.9 and 17.4, 32 18.7 and 17.2; 92160 lanes 32 tokens 18.9 and 20.1,
+// 48 26.6 and 22.2; 589824 lanes 32 tokens 67 and 102. Single channels, whose chunks hold half as
+// much: 80080 lanes 24 tokens 10.8 and 11.5, 28 13.4 and 12.4; 96096 28 tokens 14.8 and 14.6, 32 16.6
+// and 15.5 (the worse of both, by 7 %); 128128 32 tokens 17.2 and 18.2, 48 24.2 and 20.8.
+template <int V> constexpr int64_t short_tokens(int64_t lanes) {
+  return lanes < 65536 ? 12 : (lanes < 90112 ? 20 + 4 * V : 32);
+}
 constexpr uint32_t kAbsent = 0xffffffffu;
 
 template <typename T> struct GatedP {
@@ -643,10 +651,7 @@ hipError_t clear_chain(GatedP<T>& p, int chunk, void* ws, hipStream_t stream, Tr
 
 template <typename T, int V>
 hipError_t gated_fwd(GatedP<T> p, void* ws, hipStream_t stream, Tracer* tr) {
-  // us of 16 tokens by lanes and by chunks: 1152 lanes 7.4 and 6.4, 73728 9.5 and 15.6,
-  // 589824 30 and 93; of 32: 73728 19.1 and 17.6, 147456 22.5 and 28.8, 589824 68 and 101;
-  // of 64: 147456 41 and 35
-  if (p.L <= (p.B * (p.C / V) < kShortLanes ? kShortAlone : kShort)) {
+  if (p.L <= short_tokens<V>(p.B * (p.C / V))) {
     tr->before(stream, "gated_short", p.B);
     const hipError_t e = in_parts(cdiv(p.B * (p.C / V), 256), [&](int64_t first, unsigned count) {
       p.block0 = first;

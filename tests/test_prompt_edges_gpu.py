@@ -211,3 +211,30 @@ def test_empty_batch_does_not_read_the_weight(B, L, D, dtype):
                                           stream) == 0
     torch.cuda.synchronize()
     assert not dw.any()
+
+
+# --------------------------------------------------------------------------
+# gated recurrence: up to how many tokens a lane walks them all
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("B,C,dtype,last", [
+    (16, 130, BF16, 12),        # few lanes
+    (64, 2304, BF16, 28),       # 73728 lanes of two channels
+    (64, 2304, F32, 28),
+    (80, 1001, BF16, 24),       # 80080 of one
+    (80, 2304, BF16, 32),       # 92160 of two
+    (128, 1001, F32, 32),
+])
+def test_a_lane_walks_all_tokens_only_where_chunks_take_longer(B, C, dtype, last):
+    gen = torch.Generator().manual_seed(50)
+    A, state = -torch.rand(C, generator=gen), torch.randn(B, C, generator=gen)
+    for L, want in ((last, "gated_short"), (last + 1, "gated")):
+        x, r, i = (torch.randn(B, L, C, generator=gen).to(dtype) for _ in range(3))
+        end = torch.empty(B, C, device=DEV)
+        out, names = launches(lambda: g.gated_recurrence(x.to(DEV), r.to(DEV), i.to(DEV), A.to(DEV),
+                                                         state=state.to(DEV), state_out=end))
+        assert names[-1] == want, (L, names)
+        few = slice(B - 2, B)
+        inp = dict(x=x[few], r=r[few], i=i[few], A=A, state=state[few])
+        (ref, ref_end), (size, size_end) = plain.gated(**inp), plain.gated(**inp, absolute=True)
+        plain.within(out[few], ref, size, 18 * L + 26, "out")          # |A| <= 1: as in test_gated_gpu.py
+        plain.within(end[few], ref_end, size_end, 18 * L + 26, "state")

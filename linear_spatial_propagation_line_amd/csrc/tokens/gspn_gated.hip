@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * kChunkF / kRunF, 4) void gated_kernel(GatedP<T
     if (at.q == 0) {
       first = a.state && ch < a.C ? a.state[at.b * a.C + ch] : 0.0f;
     } else {
-      if (a.chunks > 1) publish_total(a.total + base + at.q * stride, p, h);
+      publish_total(a.total + base + at.q * stride, p, h);
       first = look_back(a.total + base, a.behind + base, at.q, stride);
     }
     const float last = __builtin_fmaf(p, first, h);
@@ -589,16 +589,16 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(u32x4* marks, int64_t 
   for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < ncounter; i += step) counter[i] = 0;
 }
 
-// The workspace of a chain of chunks: totals, states, counters. Sized for
-// whole tiles of 64 channels, which tiles of 128 fill as well or less.
+// The workspace of a chain of chunks: totals, states, counters. Sized for whole tiles
+// of 128 channels, which tiles of 64 fill as well or less, and counters of tiles of 64.
 struct ChainSpace {
   size_t total, behind, counter, bytes;
 };
 ChainSpace chain_space(int64_t B, int64_t L, int64_t C, int chunk) {
-  const int64_t chunks = cdiv(L, chunk), wide = cdiv(C, 128) * 128, narrow = cdiv(C, 64) * 64;
+  const int64_t chunks = cdiv(L, chunk);
   ChainSpace s{};
   if (chunks <= 1) return s;
-  const size_t n = static_cast<size_t>(B * chunks * std::max(wide, narrow));
+  const size_t n = static_cast<size_t>(B * chunks * cdiv(C, 128) * 128);
   s.total = 0;
   s.behind = n * 8;
   s.counter = s.behind + n * 4;

@@ -166,25 +166,14 @@ template <int V, typename T> __device__ __forceinline__ void stv(T* p, const flo
 // The same past the caches, for results that are written once and read by other
 // calls (gated recurrence 8 x 2048 x 2304: 72.5 us against 77, backward 137 against 146)
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32w4 __attribute__((ext_vector_type(4)));
 template <int V, typename T> __device__ __forceinline__ void stream_stv(T* p, const float* d) {
-  constexpr int kBytes = V * static_cast<int>(sizeof(T));
-  if constexpr (V > 1) {   // single values: rows that begin anywhere, in part lines
-    uint32_t w[kBytes / 4];
-#pragma unroll
-    for (int k = 0; k < kBytes / 4; ++k) {
-      if constexpr (sizeof(T) == 2) w[k] = pack_bf16x2(d[2 * k], d[2 * k + 1]);
-      else w[k] = __float_as_uint(d[k]);
-    }
-    if constexpr (kBytes == 4) __builtin_nontemporal_store(w[0], reinterpret_cast<uint32_t*>(p));
-    else if constexpr (kBytes == 8) __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
-    else {
-#pragma unroll
-      for (int k = 0; k < kBytes / 4; k += 4)
-        __builtin_nontemporal_store(u32w4{w[k], w[k + 1], w[k + 2], w[k + 3]}, reinterpret_cast<u32w4*>(p) + k / 4);
-    }
-  } else {
+  static_assert(V <= 2, "pairs at most");
+  if constexpr (V == 1) {   // rows that begin anywhere, in part lines
     stv<V>(p, d);
+  } else if constexpr (sizeof(T) == 2) {
+    __builtin_nontemporal_store(pack_bf16x2(d[0], d[1]), reinterpret_cast<uint32_t*>(p));
+  } else {
+    __builtin_nontemporal_store(u32x2{__float_as_uint(d[0]), __float_as_uint(d[1])}, reinterpret_cast<u32x2*>(p));
   }
 }
 

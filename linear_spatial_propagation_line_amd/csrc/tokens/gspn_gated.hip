@@ -30,7 +30,7 @@
 // device-scope atomics) and says itself whether it is there: the workspace is
 // filled with a pattern that no published value has.
 //
-// 8 x 2048 x 2304 bf16: forward 73 us (4.1 TB/s), backward 137 (3.9 TB/s); one entry of
+// 8 x 2048 x 2304 bf16: forward 72 us (4.2 TB/s), backward 131 to 137 (3.9 TB/s); one entry of
 // 32768 tokens forward 139 (4.3 TB/s). A large copy: 5.1 TB/s.
 #include "gspn_mfma.hpp"
 #include "gspn_tokens.hpp"
